@@ -21,7 +21,7 @@ import os
 import threading
 
 __all__ = ["attn_fwd", "attn_bwd", "attn_decode", "attn_decode_len", "attn_varlen_fwd", "attn_varlen_bwd", "attn_fwd_ex", "attn_bwd_ex", "attn_rope", "attn_bwd_workspace_size", "attn_decode_workspace_size", "attn_decode_plan",
-           "attn_get_device_status", "attn_selftest_bounded_wait", "attn_kernel_family", "attn_kernel_family_bwd", "attn_fwd_rope", "attn_bwd_rope", "attn_fwd_rope_workspace_size", "attn_bwd_rope_workspace_size", "attn_launch_count", "attn_packed_qkv_fwd", "attn_packed_qkv_bwd", "attn_packed_qkv_workspace_size", "AttnError", "lib",
+           "attn_get_device_status", "attn_selftest_bounded_wait", "attn_kernel_family", "attn_kernel_family_bwd", "attn_fwd_rope", "attn_bwd_rope", "attn_fwd_rope_workspace_size", "attn_bwd_rope_workspace_size", "attn_launch_count", "attn_packed_qkv_fwd", "attn_packed_qkv_bwd", "attn_packed_qkv_workspace_size", "attn_paged_append", "attn_paged_decode", "attn_paged_decode_workspace_size", "attn_paged_gather", "AttnError", "lib",
            "library_path"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -108,6 +108,14 @@ def lib():
         L.attn_bwd_rope.argtypes = [i, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz] + [i] * 6 + [f, i, i, f, i, vp, ll,
                                                                                            i, f, vp]
         L.attn_bwd_rope.restype = i
+        L.attn_paged_append.argtypes = [i, i, vp, ll, vp, ll, vp, ll] + [vp] * 8 + [i] * 8 + [f, vp]
+        L.attn_paged_append.restype = i
+        L.attn_paged_decode_workspace_size.argtypes = [i] * 5
+        L.attn_paged_decode_workspace_size.restype = sz
+        L.attn_paged_decode.argtypes = [i, i] + [vp] * 8 + [sz, vp, vp] + [i] * 8 + [f, i, i, f, vp]
+        L.attn_paged_decode.restype = i
+        L.attn_paged_gather.argtypes = [i, i] + [vp] * 8 + [i] * 7 + [vp]
+        L.attn_paged_gather.restype = i
         L.attn_abi_version.argtypes = []
         L.attn_abi_version.restype = i
         _lib = L
@@ -618,3 +626,187 @@ def attn_packed_qkv_bwd(qkv, do, seq_bounds, *, H, scale=None, window=0, dqkv=No
                                    _stream(stream))
     _check(st, "attn_packed_qkv_bwd")
     return dqkv
+
+
+# ------------------------------------------------------------ paged key/value cache
+_PAGED_DT = {"float16": 1, "bfloat16": 2, "float8_e4m3fn": 3, "float8_e5m2": 4}
+
+
+def _name(dtype) -> str:
+    return str(dtype).replace("torch.", "")
+
+
+class _On:
+    """The device of a call's tensors made current, and the stream that it runs on: the
+    caller's, or the device's current one.  Tensors that the call makes for itself are made
+    on that stream, so that their memory is given back in its order."""
+
+    def __init__(self, device, stream):
+        torch = _torch()
+        if stream is not None and not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        self.guard = None
+        if stream is not None and stream != torch.cuda.current_stream(device):
+            self.guard = torch.cuda.stream(stream)  # makes the stream's device current too
+        elif torch.cuda.current_device() != device.index:
+            self.guard = torch.cuda.device(device)
+        self.stream = torch.cuda.current_stream(device) if stream is None else stream
+        self.handle = ctypes.c_void_p(self.stream.cuda_stream)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
+
+
+def _pools(k_cache, v_cache, k_scale, v_scale, page_table, Hkv, row_dtype):
+    """(cache dtype code, num_pages, page_size, hd, batch, max_pages) of a paged cache whose
+    tensors agree with each other and lie on one GPU."""
+    torch = _torch()
+    dev = k_cache.device
+    if k_cache.dim() != 4 or k_cache.shape[1] != Hkv:
+        raise ValueError("k_cache must be [num_pages, Hkv, page_size, hd] with Hkv = %d (got %s)" % (Hkv, tuple(k_cache.shape)))
+    name = _name(k_cache.dtype)
+    if name not in _PAGED_DT:
+        raise TypeError("unsupported cache dtype %s" % k_cache.dtype)
+    if _name(row_dtype) not in ("float16", "bfloat16"):
+        raise TypeError("the rows of a paged cache are float16 or bfloat16 (got %s)" % row_dtype)
+    if name in ("float16", "bfloat16") and k_cache.dtype != row_dtype:
+        raise ValueError("a 16-bit cache has the rows' dtype %s (got %s)" % (row_dtype, k_cache.dtype))
+    if v_cache.dtype != k_cache.dtype or v_cache.shape != k_cache.shape or v_cache.device != dev:
+        raise ValueError("v_cache must be a %s tensor of shape %s on %s" % (k_cache.dtype, tuple(k_cache.shape), dev))
+    num_pages, _, page_size, hd = k_cache.shape
+    for what, sc in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if name.startswith("float8") and sc is None:
+            raise ValueError("an 8-bit cache needs %s" % what)
+        if sc is not None and (sc.dtype != torch.float32 or tuple(sc.shape) != (num_pages, Hkv) or sc.device != dev):
+            raise ValueError("%s must be an fp32 tensor of shape %s on %s" % (what, (num_pages, Hkv), dev))
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.device != dev:
+        raise ValueError("page_table must be an int32 tensor [batch, max_pages] on %s" % dev)
+    _contig(k_cache, v_cache, k_scale, v_scale, page_table)
+    if dev.type != "cuda":
+        raise ValueError("the library takes CUDA tensors; k_cache is on %s" % dev)
+    return _PAGED_DT[name], num_pages, page_size, hd, page_table.shape[0], page_table.shape[1]
+
+
+def _int_row(what, t, n, device):
+    if t.dtype != _torch().int32 or tuple(t.shape) != (n,) or not t.is_contiguous() or t.device != device:
+        raise ValueError("%s must be a contiguous int32 tensor of shape %s on %s" % (what, (n,), device))
+
+
+def _rows(what, t, n, width, dtype, device):
+    """Row stride of [n, width] rows whose elements are contiguous."""
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != (n, width):
+        raise ValueError("%s must be a %s tensor of shape %s on %s (got %s %s on %s)" % (what, dtype, (n, width), device,
+                                                                                     t.dtype, tuple(t.shape), t.device))
+    if n > 0 and (t.stride(1) != 1 or (n > 1 and t.stride(0) < width)):
+        raise ValueError("%s must have contiguous rows that do not overlap" % what)
+    return t.stride(0) if n > 1 else width
+
+
+def attn_paged_append(k, v, k_cache, v_cache, page_table, lengths, cu_new, *, H, Hkv, k_scale=None, v_scale=None,
+                      q=None, q_out=None, rope_theta=None, stream=None):
+    """Stores new keys and values in a paged cache, the keys turned by their position.
+
+    k, v [rows, Hkv*hd] (rows may be strided: columns of a fused projection) hold the newest
+    tokens of each sequence, sequence b's in rows cu_new[b] .. cu_new[b+1]-1 (int32), at
+    positions up to lengths[b]-1 (int32 [batch], the lengths with the new tokens).  k_cache,
+    v_cache [num_pages, Hkv, page_size, hd] of the rows' dtype, or float8_e4m3fn / float8_e5m2
+    with fp32 k_scale, v_scale [num_pages, Hkv], which are updated; page_table int32
+    [batch, max_pages].  rope_theta None: no turn.  With q [rows, H*hd] the queries are
+    turned too, into q_out (made if not given); returns q_out or None.  Rows in no sequence
+    and rows of a padding slot (length 0) are left alone."""
+    torch = _torch()
+    cd, num_pages, page_size, hd, B, max_pages = _pools(k_cache, v_cache, k_scale, v_scale, page_table, Hkv, k.dtype)
+    dev, n = k_cache.device, k.shape[0]
+    ks, vs = _rows("k", k, n, Hkv * hd, k.dtype, dev), _rows("v", v, n, Hkv * hd, k.dtype, dev)
+    _int_row("lengths", lengths, B, dev)
+    _int_row("cu_new", cu_new, B + 1, dev)
+    qs = 0
+    if q is not None:
+        qs = _rows("q", q, n, H * hd, k.dtype, dev)
+        if q_out is not None and (q_out.dtype != k.dtype or q_out.device != dev or tuple(q_out.shape) != (n, H * hd) or
+                                  not q_out.is_contiguous()):
+            raise ValueError("q_out must be a contiguous %s tensor of shape %s on %s" % (k.dtype, (n, H * hd), dev))
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if rope_theta is not None and not rope_theta > 0:
+        raise ValueError("rope_theta must be positive (None: no turn)")
+    with _On(dev, stream) as handle:
+        if q is not None and q_out is None:
+            q_out = torch.empty((n, H * hd), dtype=k.dtype, device=dev)
+        st = lib().attn_paged_append(_dt(k), cd, _ptr(k), ks, _ptr(v), vs, _ptr(q), qs, _ptr(q_out), _ptr(k_cache),
+                                     _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(cu_new), _ptr(lengths),
+                                     _ptr(page_table), B, n, num_pages, page_size, max_pages, H, Hkv, hd,
+                                     float(rope_theta or 0.0), handle)
+    _check(st, "attn_paged_append")
+    return q_out
+
+
+def attn_paged_decode_workspace_size(B, Lq, H, Hkv, hd) -> int:
+    return int(lib().attn_paged_decode_workspace_size(int(B), int(Lq), int(H), int(Hkv), int(hd)))
+
+
+def attn_paged_decode(q, k_cache, v_cache, page_table, lengths, *, H, Hkv, k_scale=None, v_scale=None, scale=None,
+                      causal=True, window=0, softcap=0.0, o=None, lse=None, want_lse=True, workspace=None,
+                      stream=None):
+    """Attention of q [batch, Lq, H*hd] (Lq <= 16) over the sequences' pages: the rows sit at
+    positions lengths[b]-Lq .. lengths[b]-1.  The cache as for attn_paged_append.  Returns
+    (o, lse).  The launch does not depend on the lengths: a captured graph can be replayed
+    as they, the table and the pages change."""
+    torch = _torch()
+    if q.dim() != 3 or q.shape[2] % H:
+        raise ValueError("q must be [batch, Lq, H*hd]")
+    cd, num_pages, page_size, hd, B, max_pages = _pools(k_cache, v_cache, k_scale, v_scale, page_table, Hkv, q.dtype)
+    dev, Lq = k_cache.device, q.shape[1]
+    if tuple(q.shape) != (B, Lq, H * hd) or q.device != dev:
+        raise ValueError("q must have shape %s on %s (got %s on %s)" % ((B, Lq, H * hd), dev, tuple(q.shape), q.device))
+    _contig(q, o, lse, workspace)
+    _int_row("lengths", lengths, B, dev)
+    _placed(q, like_q=[("o", o)], f32=[("lse", lse, (B, H, Lq))], device=[("workspace", workspace)])
+    with _On(dev, stream) as handle:
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None and want_lse:
+            lse = torch.empty((B, H, Lq), dtype=torch.float32, device=dev)
+        if workspace is None:
+            nbytes = lib().attn_paged_decode_workspace_size(B, Lq, H, Hkv, hd)
+            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        st = lib().attn_paged_decode(_dt(q), cd, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                                     _ptr(o), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                     _ptr(lengths), _ptr(page_table), B, Lq, num_pages, page_size, max_pages, H, Hkv,
+                                     hd, 1.0 / math.sqrt(hd) if scale is None else float(scale), int(bool(causal)),
+                                     int(window), float(softcap), handle)
+    _check(st, "attn_paged_decode")
+    return o, lse
+
+
+def attn_paged_gather(k_cache, v_cache, page_table, cu_seqlens, total, *, Hkv, dtype, k_scale=None, v_scale=None,
+                      k_out=None, v_out=None, stream=None):
+    """Reads a paged cache back: token i of sequence b into row cu_seqlens[b] + i of
+    (k_out, v_out), [total, Hkv*hd] of dtype (torch.float16 or torch.bfloat16), made if not
+    given.  For attention of long query blocks over cached tokens: attn_fwd with q_offset
+    takes one sequence's rows.  Rows in no sequence are left as they were."""
+    torch = _torch()
+    cd, num_pages, page_size, hd, B, max_pages = _pools(k_cache, v_cache, k_scale, v_scale, page_table, Hkv, dtype)
+    dev, total = k_cache.device, int(total)
+    _int_row("cu_seqlens", cu_seqlens, B + 1, dev)
+    for what, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is not None and (t.dtype != dtype or t.device != dev or tuple(t.shape) != (total, Hkv * hd) or
+                              not t.is_contiguous()):
+            raise ValueError("%s must be a contiguous %s tensor of shape %s on %s" % (what, dtype, (total, Hkv * hd), dev))
+    with _On(dev, stream) as handle:
+        if k_out is None:
+            k_out = torch.empty((total, Hkv * hd), dtype=dtype, device=dev)
+        if v_out is None:
+            v_out = torch.empty((total, Hkv * hd), dtype=dtype, device=dev)
+        st = lib().attn_paged_gather(_DT[_name(dtype)], cd, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                                     _ptr(k_out), _ptr(v_out), _ptr(cu_seqlens), _ptr(page_table), B, total, num_pages,
+                                     page_size, max_pages, Hkv, hd, handle)
+    _check(st, "attn_paged_gather")
+    return k_out, v_out

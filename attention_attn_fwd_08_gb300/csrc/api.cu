@@ -788,7 +788,7 @@ attn_status attn_get_device_status(void* stream, unsigned int* detail) {
     const unsigned int zero = 0;
     if (cudaMemcpy(ptr, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess) return ATTN_ERR_CUDA;
     if (detail) *detail = word;
-    if (word & ~(unsigned int)ST_VARLEN_BOUNDS) return ATTN_ERR_TIMEOUT;
+    if (word & ~(unsigned int)(ST_VARLEN_BOUNDS | ST_PAGED_BOUNDS)) return ATTN_ERR_TIMEOUT;
     return word ? ATTN_ERR_INVALID_ARG : ATTN_OK;
 }
 
@@ -990,6 +990,139 @@ attn_status attn_packed_qkv_bwd(attn_dtype dt, const void* qkv, const void* dout
                               cudaMemcpyDeviceToDevice, s) != cudaSuccess)
             return ATTN_ERR_CUDA;
     return ATTN_OK;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------- paged key/value cache
+namespace {
+
+// The rules that the three calls share; fills in the geometry and the pools.
+attn_status paged_params(attn_dtype dt, attn_dtype cache_dt, const void* k_cache, const void* v_cache,
+                         const float* k_scale, const float* v_scale, const int* table, int B, int num_pages,
+                         int page_size, int max_pages, int H, int Hkv, int hd, PagedParams* out, int* cache) {
+    if (dt != ATTN_F32 && dt != ATTN_F16 && dt != ATTN_BF16) return ATTN_ERR_INVALID_ARG;
+    if (cache_dt < ATTN_F32 || cache_dt > ATTN_E5M2) return ATTN_ERR_INVALID_ARG;
+    const bool f8 = cache_dt == ATTN_E4M3 || cache_dt == ATTN_E5M2;
+    if (B < 0 || B > 65535 || num_pages < 0 || max_pages < 0) return ATTN_ERR_INVALID_ARG;
+    if (H <= 0 || Hkv <= 0 || H % Hkv != 0 || H > 65535) return ATTN_ERR_INVALID_ARG;
+    if (dt == ATTN_F32 || cache_dt == ATTN_F32) return ATTN_ERR_UNSUPPORTED;
+    if (!f8 && cache_dt != dt) return ATTN_ERR_INVALID_ARG;
+    if (hd != 64 && hd != 128 && hd != 256) return ATTN_ERR_UNSUPPORTED;
+    if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128 && page_size != 256)
+        return ATTN_ERR_UNSUPPORTED;
+    constexpr long long kMost = INT32_MAX - 511;
+    if ((long long)num_pages * Hkv > kMost / page_size || max_pages > kMost / page_size) return ATTN_ERR_UNSUPPORTED;
+    if (B > 0 && num_pages > 0) {
+        if (!k_cache || !v_cache || !aligned16(k_cache) || !aligned16(v_cache)) return ATTN_ERR_INVALID_ARG;
+        if (f8 && (!k_scale || !v_scale || (reinterpret_cast<uintptr_t>(k_scale) & 3u) ||
+                   (reinterpret_cast<uintptr_t>(v_scale) & 3u)))
+            return ATTN_ERR_INVALID_ARG;
+    }
+    if (B > 0 && max_pages > 0 && (!table || (reinterpret_cast<uintptr_t>(table) & 3u))) return ATTN_ERR_INVALID_ARG;
+    PagedParams p;
+    memset(&p, 0, sizeof(p));
+    p.k_cache = const_cast<void*>(k_cache); p.v_cache = const_cast<void*>(v_cache);
+    p.k_scale = const_cast<float*>(k_scale); p.v_scale = const_cast<float*>(v_scale);
+    p.table = table;
+    p.B = B; p.num_pages = num_pages; p.page_size = page_size; p.max_pages = max_pages;
+    p.H = H; p.Hkv = Hkv; p.G = H / Hkv; p.hd = hd;
+    while ((1 << p.page_shift) < page_size) ++p.page_shift;
+    *cache = cache_dt == ATTN_E4M3 ? CACHE_E4M3 : cache_dt == ATTN_E5M2 ? CACHE_E5M2 : CACHE_16;
+    *out = p;
+    return ATTN_OK;
+}
+
+bool rows_ok(const void* x, long long stride, long long width) {
+    return x && aligned16(x) && stride >= width && stride % 8 == 0;
+}
+bool ints_ok(const int* x) { return x && !(reinterpret_cast<uintptr_t>(x) & 3u); }
+
+}  // namespace
+
+extern "C" {
+
+attn_status attn_paged_append(attn_dtype dt, attn_dtype cache_dt, const void* k, long long k_stride, const void* v,
+                              long long v_stride, const void* q, long long q_stride, void* q_out, void* k_cache,
+                              void* v_cache, float* k_scale, float* v_scale, const int* cu_new, const int* lengths,
+                              const int* page_table, int batch, int total_new, int num_pages, int page_size,
+                              int max_pages, int H, int Hkv, int hd, float rope_theta, void* stream) {
+    PagedParams p;
+    int cache = 0;
+    attn_status st = paged_params(dt, cache_dt, k_cache, v_cache, k_scale, v_scale, page_table, batch, num_pages,
+                                  page_size, max_pages, H, Hkv, hd, &p, &cache);
+    if (st != ATTN_OK) return st;
+    if (total_new < 0 || !(rope_theta >= 0.f) || !isfinite(rope_theta)) return ATTN_ERR_INVALID_ARG;
+    if (batch == 0 || total_new == 0) return ATTN_OK;
+    if (!rows_ok(k, k_stride, (long long)Hkv * hd) || !rows_ok(v, v_stride, (long long)Hkv * hd))
+        return ATTN_ERR_INVALID_ARG;
+    if ((q != nullptr) != (q_out != nullptr)) return ATTN_ERR_INVALID_ARG;
+    if (q && (!rows_ok(q, q_stride, (long long)H * hd) || !aligned16(q_out))) return ATTN_ERR_INVALID_ARG;
+    if (q == q_out && q && q_stride != (long long)H * hd) return ATTN_ERR_INVALID_ARG;
+    if (!ints_ok(cu_new) || !ints_ok(lengths)) return ATTN_ERR_INVALID_ARG;
+    p.status = status_ptr();
+    if (!p.status) return ATTN_ERR_CUDA;
+    p.k = k; p.v = v; p.q = q; p.q_out = q_out;
+    p.k_stride = k_stride; p.v_stride = v_stride; p.q_stride = q_stride;
+    p.cu = cu_new; p.lengths = lengths; p.total = total_new;
+    return counted(launch_paged_append(p, dt == ATTN_BF16, cache, (double)rope_theta, static_cast<cudaStream_t>(stream)),
+                   1);
+}
+
+size_t attn_paged_decode_workspace_size(int B, int Lq, int H, int Hkv, int hd) {
+    if (B <= 0 || Lq <= 0 || Lq > 16 || H <= 0 || Hkv <= 0 || H % Hkv || H / Hkv * Lq > 64 ||
+        (hd != 64 && hd != 128 && hd != 256))
+        return 0;
+    return 16;
+}
+
+attn_status attn_paged_decode(attn_dtype dt, attn_dtype cache_dt, const void* q, const void* k_cache,
+                              const void* v_cache, const float* k_scale, const float* v_scale, void* o, float* lse,
+                              void* workspace, size_t workspace_bytes, const int* lengths, const int* page_table,
+                              int B, int Lq, int num_pages, int page_size, int max_pages, int H, int Hkv, int hd,
+                              float scale, int causal, int window, float softcap, void* stream) {
+    PagedParams p;
+    int cache = 0;
+    attn_status st = paged_params(dt, cache_dt, k_cache, v_cache, k_scale, v_scale, page_table, B, num_pages,
+                                  page_size, max_pages, H, Hkv, hd, &p, &cache);
+    if (st != ATTN_OK) return st;
+    st = check_common(dt, B, Lq, 0, H, Hkv, hd, scale, causal, window, softcap, 0, nullptr, 0, true);
+    if (st != ATTN_OK) return st;
+    if (Lq > 16 || (long long)(H / Hkv) * Lq > 64) return ATTN_ERR_UNSUPPORTED;
+    if (B == 0 || Lq == 0) return ATTN_OK;
+    if (!q || !o || !aligned16(q) || !aligned16(o) || (lse && !aligned16(lse)) || !ints_ok(lengths))
+        return ATTN_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (num_pages == 0 || max_pages == 0)  // no token anywhere
+        return fill_empty(dt, o, (long long)B * Lq * H * hd, lse, lse ? (long long)B * H * Lq : 0, s);
+    if (!workspace || !aligned16(workspace) || workspace_bytes < attn_paged_decode_workspace_size(B, Lq, H, Hkv, hd))
+        return ATTN_ERR_INVALID_ARG;
+    p.status = status_ptr();
+    if (!p.status) return ATTN_ERR_CUDA;
+    p.q = q; p.o = o; p.lse = lse; p.ws = static_cast<float*>(workspace);
+    p.lengths = lengths; p.Lq = Lq;
+    p.scale = scale; p.softcap = softcap;
+    p.wl = window > 0 ? window - 1 : -1;
+    p.wr = causal ? 0 : p.wl;
+    return counted(launch_paged_decode(p, dt == ATTN_BF16, cache, s), 1);
+}
+
+attn_status attn_paged_gather(attn_dtype dt, attn_dtype cache_dt, const void* k_cache, const void* v_cache,
+                              const float* k_scale, const float* v_scale, void* k_out, void* v_out,
+                              const int* cu_seqlens, const int* page_table, int batch, int total, int num_pages,
+                              int page_size, int max_pages, int Hkv, int hd, void* stream) {
+    PagedParams p;
+    int cache = 0;
+    attn_status st = paged_params(dt, cache_dt, k_cache, v_cache, k_scale, v_scale, page_table, batch, num_pages,
+                                  page_size, max_pages, Hkv, Hkv, hd, &p, &cache);
+    if (st != ATTN_OK) return st;
+    if (total < 0) return ATTN_ERR_INVALID_ARG;
+    if (batch == 0 || total == 0) return ATTN_OK;
+    if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out) || !ints_ok(cu_seqlens)) return ATTN_ERR_INVALID_ARG;
+    p.status = status_ptr();
+    if (!p.status) return ATTN_ERR_CUDA;
+    p.k_out = k_out; p.v_out = v_out; p.cu = cu_seqlens; p.total = total;
+    return counted(launch_paged_gather(p, dt == ATTN_BF16, cache, static_cast<cudaStream_t>(stream)), 1);
 }
 
 }  // extern "C"

@@ -56,4 +56,34 @@ cudaError_t launch_rope(const void* src, void* dst, int dt, int B, int T, int H,
 // cosine/sine table of rotary positions pos .. pos+npos-1 for the forward's fused rotation
 cudaError_t launch_rope_table(float* tab, int npos, int hd, int pos, double theta, cudaStream_t s);
 
+// ---- paged key/value cache (paged.cu, paged_decode.cu): fp16 / bf16 rows, hd 64, 128 or 256
+enum : int { CACHE_16 = 0, CACHE_E4M3 = 1, CACHE_E5M2 = 2 };  // element type of the pages (16: that of the rows)
+struct PagedParams {
+    const void* q;  // append: rows to turn, or NULL; decode: [B][Lq][H*hd]
+    const void* k;  // append: new rows
+    const void* v;
+    void* q_out;
+    long long q_stride, k_stride, v_stride;  // elements from row to row
+    void* k_cache;                           // [num_pages][Hkv][page_size][hd]
+    void* v_cache;
+    float* k_scale;  // [num_pages][Hkv], 8-bit pages only
+    float* v_scale;
+    void* k_out;  // gather
+    void* v_out;
+    void* o;  // decode
+    float* lse;
+    float* ws;
+    const int* cu;       // append, gather: packed rows of the sequences
+    const int* lengths;  // append, decode: valid tokens of each sequence
+    const int* table;    // [B][max_pages]
+    int B, Lq, total, num_pages, page_size, page_shift, max_pages, H, Hkv, G, hd;
+    float scale, softcap;
+    int wl, wr;
+    unsigned int* status;
+};
+// bf16: type of the 16-bit rows; theta = 0: nothing is turned
+cudaError_t launch_paged_append(const PagedParams& p, bool bf16, int cache, double theta, cudaStream_t s);
+cudaError_t launch_paged_gather(const PagedParams& p, bool bf16, int cache, cudaStream_t s);
+cudaError_t launch_paged_decode(const PagedParams& p, bool bf16, int cache, cudaStream_t s);
+
 }  // namespace attn

@@ -74,7 +74,8 @@ typedef enum {
     ATTN_ERR_TIMEOUT = 4
 } attn_status;
 
-typedef enum { ATTN_F32 = 0, ATTN_F16 = 1, ATTN_BF16 = 2 } attn_dtype;
+/* ATTN_E4M3 and ATTN_E5M2 (8-bit floating point) are element types of a paged cache only. */
+typedef enum { ATTN_F32 = 0, ATTN_F16 = 1, ATTN_BF16 = 2, ATTN_E4M3 = 3, ATTN_E5M2 = 4 } attn_dtype;
 
 /*
  * Forward.  O = softmax(st) V over the visible keys, LSE saved when lse != NULL.
@@ -414,16 +415,102 @@ ATTN_API attn_status attn_bwd_rope(attn_dtype dt, const void* q, const void* k, 
                         int causal, int window, float softcap, int q_offset, const float* key_mask,
                         long long key_mask_bstride, int rope_pos, float rope_theta, void* stream);
 
+/*
+ * A paged key/value cache: its writer, decode over it, and reading it back.
+ *
+ * The pages lie in two pools, k_cache and v_cache, [num_pages][Hkv][page_size][hd] each;
+ * page_table [B][max_pages] (int32, device) names the pages of sequence b in order, so that
+ * its token t is row t % page_size of page page_table[b][t / page_size].  Entries behind a
+ * sequence's tokens are not read.  lengths [B] (int32, device) are the sequences' valid
+ * tokens, those of the block being appended or attended included (attn_decode_len's
+ * convention), so that one lengths array serves an append and the decode after it.
+ *   dt        : ATTN_F16 or ATTN_BF16, the type of the rows (ATTN_F32: UNSUPPORTED).
+ *   cache_dt  : the pools' type: dt, or ATTN_E4M3 / ATTN_E5M2 with k_scale and v_scale
+ *               [num_pages][Hkv] fp32: an element is its 8-bit value times the scale of its
+ *               page and head.  The scales are not read for 16-bit pools (NULL is fine).
+ *   page_size : 16, 32, 64, 128 or 256.   hd : 64, 128 or 256.   H <= 65535, Hkv divides H.
+ *   num_pages * Hkv * page_size and max_pages * page_size are at most 2^31 - 512.
+ * No access leaves the pools whatever the device arrays hold.  A page number outside
+ * [0, num_pages), a token at or past max_pages * page_size, or a prefix sum that decreases
+ * or leaves [0, total] makes attn_get_device_status() return ATTN_ERR_INVALID_ARG; the
+ * tokens concerned are not stored, not attended, or read back as zeros.
+ * Launch shapes depend on the host arguments alone: a captured graph may be replayed after
+ * lengths, prefix sums, page table, scales or pages changed.
+ *
+ * attn_paged_append stores new keys and values, keys (and, if given, queries) turned by their
+ * position on the way.  Sources: ferrotensor engine/attention.rs, rope / rope_theta (the
+ * rotate-half turn of attn_rope); brotensor ops/flash_attention.h, flash_attention_decode_len
+ * (a cache that grows in place, its valid length on the device).
+ *   k, v      : new rows [total_new][Hkv*hd], rows k_stride / v_stride elements apart (a
+ *               multiple of 8, at least Hkv*hd: columns of a fused projection's rows).
+ *   q, q_out  : NULL, or query rows [total_new][H*hd], q_stride apart, and their output
+ *               [total_new][H*hd] (contiguous); q_out may be q when q_stride = H*hd.
+ *   cu_new    : batch+1 int32 prefix sums: rows [cu_new[b], cu_new[b+1]) are sequence b's
+ *               newest tokens, at positions lengths[b] - n_b .. lengths[b] - 1.  Rows in no
+ *               sequence are ignored, and so are rows at a negative position (a padding slot
+ *               has length 0): nothing is stored for them and their q_out is not written.
+ *   rope_theta: > 0 and finite: pair (x[i], x[i + hd/2]) of a head vector at position p turns
+ *               by p * rope_theta^(-2i/hd), the angle exact at every position; 0: no turn.
+ *   8-bit     : a block (page, head) that holds no earlier token gets the smallest power of
+ *               two s >= 2^-64 with max |x| <= 448 s (57344 s for e5m2) over its new rows; one
+ *               that does keeps its scale unless that is too small for them, and then takes
+ *               the new one, its earlier rows stored again in it.  An element is rounded once,
+ *               to nearest; one that is not finite has no part in the scale, an infinity is
+ *               stored as the largest finite value, NaN as NaN.
+ *   A page that tokens are appended to belongs to one sequence (pages that are only read may
+ *   be shared): two sequences writing one block leave it with unspecified values.
+ */
+ATTN_API attn_status attn_paged_append(attn_dtype dt, attn_dtype cache_dt, const void* k, long long k_stride,
+                        const void* v, long long v_stride, const void* q, long long q_stride, void* q_out,
+                        void* k_cache, void* v_cache, float* k_scale, float* v_scale, const int* cu_new,
+                        const int* lengths, const int* page_table, int batch, int total_new, int num_pages,
+                        int page_size, int max_pages, int H, int Hkv, int hd, float rope_theta, void* stream);
+
+/*
+ * Attention of Lq query rows of each sequence (1 <= Lq <= 16, (H/Hkv)*Lq <= 64) over its
+ * pages.  Source: brotensor ops/flash_attention.h, flash_attention_decode and
+ * flash_attention_decode_len, as for attn_decode_len: L_b = min(max(lengths[b], 0),
+ * max_pages * page_size) tokens are visible, the rows sit at positions L_b - Lq .. L_b - 1,
+ * and a row that sees no key gets O = 0 and LSE = -inf.  What a row does not see has no
+ * effect on it, whatever bytes it holds (rows behind a sequence's end, pages it skips, a
+ * later row's key or value that is not finite).
+ *   q, o      : [B][Lq][H*hd];  lse : [B][H][Lq] fp32, or NULL.
+ *   scale, causal, window, softcap : as for attn_decode.
+ *   workspace : at least attn_paged_decode_workspace_size() bytes of device scratch, 16-byte
+ *               aligned; contents on entry are ignored.  Calls that may run at the same time
+ *               need one each.
+ */
+ATTN_API size_t attn_paged_decode_workspace_size(int B, int Lq, int H, int Hkv, int hd);
+ATTN_API attn_status attn_paged_decode(attn_dtype dt, attn_dtype cache_dt, const void* q, const void* k_cache,
+                        const void* v_cache, const float* k_scale, const float* v_scale, void* o, float* lse,
+                        void* workspace, size_t workspace_bytes, const int* lengths, const int* page_table, int B,
+                        int Lq, int num_pages, int page_size, int max_pages, int H, int Hkv, int hd, float scale,
+                        int causal, int window, float softcap, void* stream);
+
+/*
+ * Reads pages back: token i of sequence b into row cu_seqlens[b] + i of k_out and v_out
+ * [total][Hkv*hd] (type dt), for i < cu_seqlens[b+1] - cu_seqlens[b]; 8-bit elements are
+ * multiplied by their scale and rounded once.  For query blocks longer than the decode's 16
+ * rows (the next chunk of a prompt over its cached prefix): attn_fwd takes the rows of one
+ * sequence as k and v, with q_offset the position of the first query row.  Rows in no
+ * sequence are not written.
+ */
+ATTN_API attn_status attn_paged_gather(attn_dtype dt, attn_dtype cache_dt, const void* k_cache, const void* v_cache,
+                        const float* k_scale, const float* v_scale, void* k_out, void* v_out,
+                        const int* cu_seqlens, const int* page_table, int batch, int total, int num_pages,
+                        int page_size, int max_pages, int Hkv, int hd, void* stream);
+
 /* Human-readable name of a status code (static storage). */
 ATTN_API const char* attn_status_string(attn_status s);
 
 /*
  * Reads and clears the device status word that bounded waits set when they
- * run out (and that packed-sequence calls set when cu_seqlens break their
- * bounds).  Synchronises `stream` first.  Returns ATTN_OK, ATTN_ERR_TIMEOUT (a
- * wait ran out), ATTN_ERR_INVALID_ARG (only the cu_seqlens bit is set) or
- * ATTN_ERR_CUDA.  If `detail` is not NULL it receives the raw word (which wait
- * gave up, as a bit set; bit 9: cu_seqlens out of bounds).
+ * run out (and that packed-sequence and paged calls set when their device arrays
+ * break their bounds).  Synchronises `stream` first.  Returns ATTN_OK,
+ * ATTN_ERR_TIMEOUT (a wait ran out), ATTN_ERR_INVALID_ARG (only bits of broken
+ * bounds are set) or ATTN_ERR_CUDA.  If `detail` is not NULL it receives the raw
+ * word (which wait gave up, as a bit set; bit 9: cu_seqlens out of bounds; bit 10:
+ * a paged call's page, length or prefix sum out of bounds).
  */
 ATTN_API attn_status attn_get_device_status(void* stream, unsigned int* detail);
 

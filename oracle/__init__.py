@@ -386,3 +386,142 @@ def packed_qkv_bwd(qkv, do, seq_bounds, *, H, scale, window=0):
         dk[j] += scale * np.einsum("hj,hd->jhd", ds, q[r])
         dv[j] += np.einsum("hj,hd->jhd", p, do[r])
     return np.concatenate([dq.reshape(L, -1), dk.reshape(L, -1), dv.reshape(L, -1)], axis=1)
+
+
+# ------------------------------------------------------------ paged key/value cache
+F8_TOP = {"e4m3": 448.0, "e5m2": 57344.0}
+
+
+def f8_values(kind):
+    """The 256 values of an 8-bit floating type by code, from the type's definition:
+    sign, exponent (4 bits, bias 7 | 5 bits, bias 15), fraction (3 | 2 bits), subnormals at
+    exponent 0.  e4m3 has no infinity and NaN at 0x7f, 0xff; e5m2 is as IEEE."""
+    eb, fb, bias = (4, 3, 7) if kind == "e4m3" else (5, 2, 15)
+    out = np.zeros(256)
+    for c in range(256):
+        e, f = (c >> fb) & ((1 << eb) - 1), c & ((1 << fb) - 1)
+        x = (f / (1 << fb)) * 2.0 ** (1 - bias) if e == 0 else (1 + f / (1 << fb)) * 2.0 ** (e - bias)
+        if kind == "e4m3" and (c & 0x7f) == 0x7f:
+            x = np.nan
+        if kind == "e5m2" and e == 31:
+            x = np.inf if f == 0 else np.nan
+        out[c] = -x if c & 0x80 else x
+    return out
+
+
+def f8_round(x, kind):
+    """Codes of the nearest values, ties to the even code; beyond the largest finite value
+    (infinities too), the largest; NaN to the code 0x7f."""
+    x = np.asarray(x, np.float64)
+    top = {"e4m3": 0x7e, "e5m2": 0x7b}[kind]
+    pos = f8_values(kind)[:top + 1]  # the finite values from 0 up: codes 0 .. top
+    a = np.minimum(np.abs(np.where(np.isnan(x), 0.0, x)), pos[-1])
+    hi = np.clip(np.searchsorted(pos, a), 1, top)
+    lo = hi - 1
+    dl, dh = a - pos[lo], pos[hi] - a
+    code = np.where((dh < dl) | ((dh == dl) & (hi % 2 == 0)), hi, lo)
+    code = np.where(np.isnan(x), 0x7f, code)
+    return (code + 0x80 * np.signbit(x)).astype(np.uint8)
+
+
+def turn_rows(x, pos, hd, theta):
+    """Rows x [n, heads*hd] with the head vectors of row i turned as rope() does at
+    position pos[i] (all rows at once)."""
+    x = _f64(x)
+    n = x.shape[0]
+    y = x.reshape(n, x.shape[1] // hd, 2, hd // 2)
+    ang = np.asarray(pos, np.float64)[:, None] * float(theta) ** (-2.0 * np.arange(hd // 2) / hd)
+    c, s = np.cos(ang)[:, None], np.sin(ang)[:, None]
+    return np.stack([y[:, :, 0] * c - y[:, :, 1] * s, y[:, :, 1] * c + y[:, :, 0] * s], 2).reshape(x.shape)
+
+
+def paged_tokens(cache, scale, pages, n, kind=None):
+    """Tokens 0 .. n-1 of one sequence as rows [n, Hkv*hd]: token t is row t % page of page
+    pages[t // page] of cache [num_pages, Hkv, page, hd] (values, or codes of `kind` times
+    the scale of their page and head); rows of a page outside the pool are NaN."""
+    P, Hkv, page, hd = cache.shape
+    out = np.full((n, Hkv, hd), np.nan)
+    for t in range(n):
+        pg = int(pages[t // page])
+        if 0 <= pg < P:
+            x = cache[pg, :, t % page]
+            out[t] = x if kind is None else f8_values(kind)[x] * np.asarray(scale, np.float64)[pg][:, None]
+    return out.reshape(n, Hkv * hd)
+
+
+def paged_append(k, v, k_cache, v_cache, k_scale, v_scale, table, lengths, cu, *, Hkv, kind=None, theta=None):
+    """What an append leaves: (k_cache, v_cache, k_scale, v_scale, exact) as new arrays.
+    Rows cu[b] .. cu[b+1]-1 of k, v are sequence b's tokens at positions lengths[b] - n_b ..
+    lengths[b] - 1; rows at a negative position, past the table or in a page outside the
+    pool are dropped.  For 8-bit caches the block rule of the header, and `exact` lists
+    (which, page, row, unrounded values [Hkv, hd] in units of the scale) of every new row."""
+    P, _, page, hd = k_cache.shape
+    out = [np.array(k_cache), np.array(v_cache)]
+    sc = [None if s is None else np.array(s, np.float64) for s in (k_scale, v_scale)]
+    exact = []
+    for b in range(len(lengths)):
+        r0, r1 = int(cu[b]), int(cu[b + 1])
+        first = int(lengths[b]) - (r1 - r0)
+        pos = np.arange(first, int(lengths[b]))
+        rows = [turn_rows(k[r0:r1], pos, hd, theta) if theta else _f64(k[r0:r1]), _f64(v[r0:r1])]
+        for j in sorted({int(p) // page for p in pos if p >= 0}):
+            if j >= table.shape[1] or not 0 <= int(table[b, j]) < P:
+                continue
+            pg = int(table[b, j])
+            lo, hi = max(first, j * page, 0), min(int(lengths[b]), (j + 1) * page)
+            for w in range(2):
+                x = rows[w][lo - first:hi - first].reshape(hi - lo, Hkv, hd).transpose(1, 0, 2)
+                at = lo - j * page
+                if kind is None:
+                    out[w][pg, :, at:at + hi - lo] = x
+                    continue
+                for h in range(Hkv):
+                    mag = np.abs(x[h])
+                    mag = mag[np.isfinite(mag)].max(initial=0.0)
+                    s = 2.0 ** -64
+                    while F8_TOP[kind] * s < mag:
+                        s *= 2.0
+                    if at > 0:
+                        old = sc[w][pg, h]
+                        if old >= s:
+                            s = old
+                        else:
+                            out[w][pg, h, :at] = f8_round(f8_values(kind)[out[w][pg, h, :at]] * (old / s), kind)
+                    sc[w][pg, h] = s
+                    out[w][pg, h, at:at + hi - lo] = f8_round(x[h] / s, kind)
+                for i in range(hi - lo):
+                    exact.append((w, pg, at + i, x[:, i] / sc[w][pg][:, None]))
+    return out[0], out[1], sc[0], sc[1], exact
+
+
+def paged_decode(q, tokens, lengths, *, H, Hkv, scale, causal=True, window=0, softcap=0.0, absolute=False):
+    """O [B, Lq, H*hd] and LSE [B, H, Lq] of Lq rows at positions lengths[b] - Lq ..
+    lengths[b] - 1 over tokens[b] = (k, v), rows [lengths[b], Hkv*hd] (rows of NaN keys are
+    not visible).  With `absolute`, V enters by its magnitude."""
+    q = _f64(q)
+    B, Lq, C = q.shape
+    hd = C // H
+    o, lse = np.zeros_like(q), np.full((B, H, Lq), -np.inf)
+    for b in range(B):
+        n = int(lengths[b])
+        k, v = tokens[b]
+        for i in range(Lq):
+            p = n - Lq + i
+            j = np.arange(n)
+            j = j[~np.isnan(k[:, 0])] if n else j
+            if causal:
+                j = j[j <= p]
+            if window:
+                j = j[np.abs(p - j) < window]
+            if j.size == 0:
+                continue
+            kk, vv = k[j].reshape(-1, Hkv, hd), v[j].reshape(-1, Hkv, hd)
+            vv = np.abs(vv) if absolute else vv
+            for h in range(H):
+                s = scale * (kk[:, h // (H // Hkv)] @ q[b, i, h * hd:(h + 1) * hd])
+                s = softcap * np.tanh(s / softcap) if softcap > 0 else s
+                m = s.max()
+                e = np.exp(s - m)
+                o[b, i, h * hd:(h + 1) * hd] = e @ vv[:, h // (H // Hkv)] / e.sum()
+                lse[b, h, i] = m + np.log(e.sum())
+    return o, lse
