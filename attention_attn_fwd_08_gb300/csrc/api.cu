@@ -1033,6 +1033,24 @@ attn_status paged_params(attn_dtype dt, attn_dtype cache_dt, const void* k_cache
     return ATTN_OK;
 }
 
+// 2-D map over a pool's [rows][hd] elements, boxes of at most 128 bytes by box_rows rows,
+// swizzled by the box's width.
+bool pool_map(CUtensorMap* m, int cache, bool bf16, const void* base, int hd, long long rows, int box_rows) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const int es = cache == CACHE_16 ? 2 : 1, width = hd * es < 128 ? hd : 128 / es;
+    const CUtensorMapDataType t = es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                  : bf16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    cuuint64_t dims[2] = {(cuuint64_t)hd, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)hd * es};
+    cuuint32_t box[2] = {(cuuint32_t)width, (cuuint32_t)box_rows};
+    cuuint32_t one[2] = {1, 1};
+    return enc(m, t, 2, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               width * es == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool rows_ok(const void* x, long long stride, long long width) {
     return x && aligned16(x) && stride >= width && stride % 8 == 0;
 }
@@ -1070,10 +1088,10 @@ attn_status attn_paged_append(attn_dtype dt, attn_dtype cache_dt, const void* k,
 }
 
 size_t attn_paged_decode_workspace_size(int B, int Lq, int H, int Hkv, int hd) {
-    if (B <= 0 || Lq <= 0 || Lq > 16 || H <= 0 || Hkv <= 0 || H % Hkv || H / Hkv * Lq > 64 ||
+    if (B <= 0 || Lq <= 0 || Lq > 16 || H <= 0 || Hkv <= 0 || H % Hkv || (long long)(H / Hkv) * Lq > 64 ||
         (hd != 64 && hd != 128 && hd != 256))
         return 0;
-    return 16;
+    return paged_decode_workspace(H / Hkv * Lq, hd);
 }
 
 attn_status attn_paged_decode(attn_dtype dt, attn_dtype cache_dt, const void* q, const void* k_cache,
@@ -1104,7 +1122,13 @@ attn_status attn_paged_decode(attn_dtype dt, attn_dtype cache_dt, const void* q,
     p.scale = scale; p.softcap = softcap;
     p.wl = window > 0 ? window - 1 : -1;
     p.wr = causal ? 0 : p.wl;
-    return counted(launch_paged_decode(p, dt == ATTN_BF16, cache, s), 1);
+    PagedMaps maps;
+    const long long rows = (long long)num_pages * Hkv * page_size;
+    const int box_rows = page_size < 64 ? page_size : 64;
+    if (!pool_map(&maps.k, cache, dt == ATTN_BF16, k_cache, hd, rows, box_rows) ||
+        !pool_map(&maps.v, cache, dt == ATTN_BF16, v_cache, hd, rows, box_rows))
+        return ATTN_ERR_CUDA;
+    return counted(launch_paged_decode(p, dt == ATTN_BF16, cache, maps, s), 2);
 }
 
 attn_status attn_paged_gather(attn_dtype dt, attn_dtype cache_dt, const void* k_cache, const void* v_cache,

@@ -84,6 +84,19 @@ struct PagedParams {
 // bf16: type of the 16-bit rows; theta = 0: nothing is turned
 cudaError_t launch_paged_append(const PagedParams& p, bool bf16, int cache, double theta, cudaStream_t s);
 cudaError_t launch_paged_gather(const PagedParams& p, bool bf16, int cache, cudaStream_t s);
-cudaError_t launch_paged_decode(const PagedParams& p, bool bf16, int cache, cudaStream_t s);
+// 2-D maps over the pools' rows, boxes of up to 128 bytes by min(page_size, 64) rows
+struct PagedMaps {
+    CUtensorMap k, v;
+};
+size_t paged_decode_workspace(int rows, int hd);
+cudaError_t launch_paged_decode_bf16(const PagedParams& p, bool bf16, const PagedMaps& maps, cudaStream_t s);
+cudaError_t launch_paged_decode_f16(const PagedParams& p, bool bf16, const PagedMaps& maps, cudaStream_t s);
+cudaError_t launch_paged_decode_e4m3(const PagedParams& p, bool bf16, const PagedMaps& maps, cudaStream_t s);
+cudaError_t launch_paged_decode_e5m2(const PagedParams& p, bool bf16, const PagedMaps& maps, cudaStream_t s);
+inline cudaError_t launch_paged_decode(const PagedParams& p, bool bf16, int cache, const PagedMaps& maps, cudaStream_t s) {
+    if (cache == CACHE_E4M3) return launch_paged_decode_e4m3(p, bf16, maps, s);
+    if (cache == CACHE_E5M2) return launch_paged_decode_e5m2(p, bf16, maps, s);
+    return bf16 ? launch_paged_decode_bf16(p, bf16, maps, s) : launch_paged_decode_f16(p, bf16, maps, s);
+}
 
 }  // namespace attn

@@ -1,0 +1,820 @@
+// paged_decode.cuh -- attention of a few query rows of each sequence over a paged cache:
+// the kernels, instantiated per pool type in paged_decode_*.cu.
+//
+// For query row r of a (sequence, KV head) group: O = sum_j p_j v_j / sum_j p_j with
+// p_j = exp(s_j - m), s_j = scale * ks * q . k_j (capped) over the visible keys, m a running
+// maximum, ks and vs the scales of the key's page.
+//
+// Bound by HBM: every visible K and V byte is read once.  What the design does about it:
+//   * The 64-key tiles of all (sequence, KV head) items are numbered in one row and dealt
+//     out in equal stretches to a fixed number of CTAs that are all resident, so that
+//     sequences of unlike lengths, one long sequence, or many short ones load every SM
+//     alike; the numbering is made on the device from the lengths (each CTA sums them), so
+//     the launch depends on none of them.  An item cut by a stretch's end leaves partial
+//     (m, l, O) rows in the workspace, which paged_combine_kernel merges in a fixed order.
+//   * A producer warp keeps a ring of tiles in flight (TMA, 128-byte swizzle, one box for
+//     each run of a page's rows), page numbers and scales fetched 32 groups of 16 keys at a
+//     time, one batch ahead, by the lanes that hold them.
+//   * Four consumer warps split each tile by keys for S = Q K^T (16 each) and by columns of
+//     the head for O += P V: the probabilities go through shared memory, one barrier a
+//     tile, and no warp holds more than a quarter of O, so that three CTAs fit an SM.  Each
+//     warp's probabilities are relative to its own 16 keys' maximum; the factor that brings
+//     them to the row's running maximum, times the page's vs, is applied in fp32 to the
+//     16-key partial product, so a scale of any size costs no precision of P.
+//   * 8-bit pages: codes become fp16 in registers (exact for both types) and the products
+//     run in fp16 with fp32 accumulation.  Q is brought to fp16 by a power of two for each
+//     row (exact for all that matters: 2^-38 of the row's largest element is kept).  A
+//     thread's 32 bits of a K fragment are four neighbouring columns, so the columns of Q
+//     are stored in the order that makes the products match; for V, ldmatrix.trans moves
+//     pairs of columns, and a byte permutation pairs the keys of the even and of the odd one.
+// mma.sync serves the 16 rows that a group usually has; tcgen05's least M (64) would leave
+// three quarters of it idle and need the codes converted through shared memory.
+#pragma once
+
+#include <math.h>
+
+#include <type_traits>
+
+#include "paged.cuh"
+
+namespace attn {
+namespace {
+namespace paged {
+
+constexpr int kKeys = 64;                  // keys of a tile
+constexpr int kDecThreads = 160;           // 4 consumer warps and the producer
+constexpr int kSms = 152;
+constexpr int kMaxCtasPerSm = 3;
+constexpr int kMaxCtas = kSms * kMaxCtasPerSm;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Bytes of workspace: a record for each CTA, then two slots of R partial rows for each (a
+// CTA's stretch can begin in the middle of one item and end in the middle of another).
+__host__ __device__ inline size_t ws_ml_offset() { return (size_t)kMaxCtas * 16; }
+__host__ __device__ inline size_t ws_o_offset(int R) { return ws_ml_offset() + ((size_t)kMaxCtas * 2 * R * 8 + 15) / 16 * 16; }
+inline size_t ws_bytes(int R, int hd) { return ws_o_offset(R) + (size_t)kMaxCtas * 2 * R * hd * 4; }
+
+template <int HD, int CACHE, int RT>
+struct DecShape {
+    static constexpr bool k8 = CACHE != CACHE_16;
+    static constexpr int kEs = k8 ? 1 : 2;
+    static constexpr int kRowBytes = HD * kEs < 128 ? HD * kEs : 128;  // of a box
+    static constexpr int kBoxes = HD * kEs / kRowBytes;                // side by side
+    static constexpr int kTileBytes = kKeys * HD * kEs;                // of K or of V
+    static constexpr int kStageBytes = 2 * kTileBytes;
+    static constexpr int kRows = RT * 16;
+    static constexpr int kQPitch = HD * 2 + 16;  // 16 past a multiple of 128: eight rows' chunks in eight places
+    static constexpr int kPPitch = kKeys * 2 + 16;
+    static constexpr int kQBytes = kRows * kQPitch;
+    static constexpr int kPBytes = 2 * kRows * kPPitch;
+    static constexpr int kMlBytes = 2 * kRows * 4 * 8;  // two buffers of (m, l) by row and warp
+    static constexpr int kFixed = kQBytes + kPBytes + kMlBytes + kRows * 4 + 2048;  // + row scales, alignment, barriers
+    // the most CTAs of an SM whose ring keeps at least three tiles each; the ring's depth
+    static constexpr int stages(int ctas) {
+        const int s = (227 * 1024 / ctas - 1024 - kFixed - 512) / kStageBytes;
+        return s > 8 ? 8 : s;
+    }
+    static constexpr int kCtas = stages(3) >= 3 ? 3 : stages(2) >= 3 ? 2 : 1;
+    static constexpr int kStages = stages(kCtas);
+    static constexpr int kBytes = kStages * kStageBytes + kFixed;
+    // Q fragments stay in registers where they take at most 64
+    static constexpr bool kQReg = RT == 1 || RT * HD <= 128;
+    static constexpr int kN = HD / 32;  // 8-column products of a warp's quarter of the head
+    static_assert(kStages >= 2, "ring too shallow");
+};
+
+// D = A B + 0 and D += A B, m16n8k16 with fp32 accumulation
+template <bool BF16>
+__device__ __forceinline__ void mma_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (BF16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+template <bool BF16>
+__device__ __forceinline__ void mma_add(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (BF16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// the maximum, NaN if either is
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y,
+                                            uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
+        : "memory");
+}
+
+// Sequence b: its visible tokens, the position of its first row, and the tiles that any
+// of its rows sees.
+struct SeqTiles {
+    int len, p0, lo, hi, t0, n;
+};
+__device__ __forceinline__ SeqTiles seq_tiles(const PagedParams& P, int b) {
+    SeqTiles s;
+    s.len = min(max(__ldg(P.lengths + b), 0), P.max_pages << P.page_shift);
+    s.p0 = s.len - P.Lq;
+    key_range(P.wl, P.wr, s.len, s.p0, s.len - 1, &s.lo, &s.hi);
+    s.t0 = s.lo / kKeys;
+    s.n = s.hi > s.lo ? (s.hi + kKeys - 1) / kKeys - s.t0 : 0;
+    return s;
+}
+
+// A CTA's stretch of the tiles: begins at tile `off` of item (b, h), `count` tiles long.
+struct Stretch {
+    int b, h, off;
+    long long count, share;
+};
+
+// Every thread sums its sequences' tiles; the thread whose sequences hold the stretch's
+// first tile finds it.
+__device__ __forceinline__ Stretch find_stretch(const PagedParams& P, Stretch* out, long long* sums) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int per = (P.B + kDecThreads - 1) / kDecThreads;
+    const int b0 = min(P.B, tid * per), b1 = min(P.B, b0 + per);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += seq_tiles(P, b).n;
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+    }
+    if (lane == 31) sums[warp] = incl;
+    if (tid == 0) out->count = 0;
+    __syncthreads();
+    long long before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kDecThreads / 32; ++w) {
+        if (w < warp) before += sums[w];
+        total += sums[w];
+    }
+    const long long all = total * P.Hkv, share = (all + gridDim.x - 1) / gridDim.x;
+    const long long first = (long long)blockIdx.x * share;
+    const long long lo = (before + incl - mine) * P.Hkv, hi = (before + incl) * P.Hkv;
+    if (first < all && first >= lo && first < hi) {
+        long long at = first - lo;
+        int b = b0;
+        for (;; ++b) {
+            const int n = seq_tiles(P, b).n;
+            if (at < (long long)n * P.Hkv) {
+                out->b = b;
+                out->h = (int)(at / n);
+                out->off = (int)(at % n);
+                break;
+            }
+            at -= (long long)n * P.Hkv;
+        }
+        out->count = min(share, all - first);
+    }
+    __syncthreads();
+    Stretch s = *out;
+    s.share = share;
+    return s;
+}
+// the next item with tiles
+__device__ __forceinline__ void next_item(const PagedParams& P, int& b, int& h) {
+    if (++h < P.Hkv) return;
+    h = 0;
+    do ++b;
+    while (b < P.B && seq_tiles(P, b).n == 0);
+}
+
+// kBf: the rows (and 16-bit pools) are bfloat16; over 8-bit pools a run-time choice
+template <int HD, int CACHE, int RT, bool kBf>
+__global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
+    paged_split_kernel(const PagedParams P, const int rows_bf16, const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV) {
+    using S = DecShape<HD, CACHE, RT>;
+    constexpr bool k8 = S::k8;
+    constexpr bool kMmaBf = !k8 && kBf;  // type of the products
+    const bool bf = k8 ? rows_bf16 != 0 : kBf;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* qs = smem + S::kStages * S::kStageBytes;
+    uint8_t* ps = qs + S::kQBytes;
+    float2* mls = reinterpret_cast<float2*>(ps + S::kPBytes);                 // [2][rows][4]
+    float* qscale = reinterpret_cast<float*>(mls + 2 * S::kRows * 4);         // [rows]
+    __shared__ __align__(8) uint64_t bars[2 * S::kStages];
+    __shared__ float2 meta[S::kStages][4];  // scales of the tile's groups of 16 keys
+    __shared__ int there[S::kStages];       // groups that were loaded
+    __shared__ Stretch stretch;
+    __shared__ long long sums[kDecThreads / 32];
+    __shared__ int abort_flag;
+    const uint32_t ring = smem_u32(smem);
+    auto full_bar = [&](int s) { return smem_u32(bars + s); };
+    auto empty_bar = [&](int s) { return smem_u32(bars + S::kStages + s); };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int R = P.G * P.Lq;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S::kStages; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 4);
+        }
+        abort_flag = 0;
+        fence_barrier_init();
+    }
+    const Stretch st = find_stretch(P, &stretch, sums);  // its barriers publish the above
+
+    if (warp == 4) {
+        // ------------------------------------------------------------- producer
+        if (lane == 0) {
+            prefetch_tmap(&tmK);
+            prefetch_tmap(&tmV);
+        }
+        const uint64_t pol = policy_evict_first();  // streamed once
+        const int box_rows = min(P.page_size, kKeys);
+        const int subs = kKeys / box_rows, groups = box_rows / 16;  // boxes down a tile, groups of a box
+        // this lane's box of a tile
+        const int sub = lane % subs, bx = (lane / subs) % S::kBoxes, is_v = lane / subs / S::kBoxes;
+        const bool has_box = is_v < 2;
+        int b = st.b, h = st.h, off = st.off;
+        long long left = st.count;
+        long long it = 0;  // tiles produced
+        bool ok = true;
+        while (left > 0 && ok) {
+            const SeqTiles sq = seq_tiles(P, b);
+            const int n = (int)min(left, (long long)(sq.n - off));
+            // group l of batch k: the 16 keys from (t0 + off) * 64 + (32 k + l) * 16 on
+            const int g0 = (sq.t0 + off) * 4;
+            auto page_at = [&](int batch) {
+                const int g = g0 + batch * 32 + lane;
+                const long long key = (long long)g * 16;
+                if (batch * 8 >= n || batch * 32 + lane >= n * 4 || key >= sq.hi || key + 16 <= sq.lo) return -2;
+                return page_of(P, b, (int)(key >> P.page_shift), true);
+            };
+            auto scales_at = [&](int pg) {
+                float2 s = make_float2(0.f, 0.f);
+                if constexpr (k8) {
+                    if (pg >= 0) {
+                        const long long i = (long long)pg * P.Hkv + h;
+                        s = make_float2(__ldg(P.k_scale + i), __ldg(P.v_scale + i));
+                    }
+                }
+                return s;
+            };
+            int pg = page_at(0), pg_next = page_at(1);
+            float2 sc = scales_at(pg);
+            for (int base = 0; base < n && ok; base += 8) {
+                const float2 sc_next = scales_at(pg_next);
+                const int pg_after = page_at(base / 8 + 2);
+                const int m = min(8, n - base);
+                for (int i = 0; i < m; ++i, ++it) {
+                    const int s = (int)(it % S::kStages);
+                    const long long use = it / S::kStages;
+                    if (use > 0 && !warp_wait(empty_bar(s), (int)(use - 1) & 1, P.status, ST_DEC_WAIT, &abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    const float2 gs = make_float2(__shfl_sync(0xffffffffu, sc.x, i * 4 + (lane & 3)),
+                                                  __shfl_sync(0xffffffffu, sc.y, i * 4 + (lane & 3)));
+                    const int gp = __shfl_sync(0xffffffffu, pg, i * 4 + (lane & 3));
+                    const unsigned have = __ballot_sync(0xffffffffu, gp >= 0) & 0xfu;
+                    if (lane < 4) meta[s][lane] = gs;
+                    if (lane == 0) there[s] = (int)have;
+                    // a box's page: that of any of its groups that is wanted
+                    int page = -1;
+                    for (int e = 0; e < groups; ++e) {
+                        const int x = __shfl_sync(0xffffffffu, pg, i * 4 + (sub * groups + e));
+                        page = max(page, x);
+                    }
+                    const unsigned boxes = __ballot_sync(0xffffffffu, has_box && page >= 0);
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_expect_tx(full_bar(s), (uint32_t)(__popc(boxes) * box_rows * S::kRowBytes));
+                    __syncwarp();
+                    if (has_box && page >= 0) {
+                        const uint32_t dst = ring + (uint32_t)(s * S::kStageBytes + is_v * S::kTileBytes +
+                                                               bx * kKeys * S::kRowBytes + sub * box_rows * S::kRowBytes);
+                        const int row = (int)(((long long)(sq.t0 + off + base + i) * kKeys + sub * box_rows) & (P.page_size - 1));
+                        const int y = ((page * P.Hkv + h) << P.page_shift) + row;
+                        tma_load_2d(dst, is_v ? &tmV : &tmK, full_bar(s), bx * (S::kRowBytes / S::kEs), y, pol);
+                    }
+                }
+                pg = pg_next;
+                sc = sc_next;
+                pg_next = pg_after;
+            }
+            left -= n;
+            off = 0;
+            if (left > 0) next_item(P, b, h);
+        }
+        // no copy is in flight when the CTA ends
+        for (long long i = max(0ll, it - S::kStages); i < it; ++i)
+            mbar_wait(full_bar((int)(i % S::kStages)), (int)(i / S::kStages) & 1, P.status, ST_DEC_WAIT | ST_TEARDOWN,
+                      nullptr);
+        return;
+    }
+
+    // ---------------------------------------------------------------- consumers
+    const int g = lane >> 2, t = lane & 3, mi = lane >> 3, ri = lane & 7;
+    const int tid = threadIdx.x;
+    float* ws_ml = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(P.ws) + ws_ml_offset());
+    float* ws_o = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(P.ws) + ws_o_offset(R));
+    int4 record = make_int4(-1, 0, 0, 0);
+    int b = st.b, h = st.h, off = st.off;
+    long long left = st.count, it = 0;
+    bool ok = true;
+    while (left > 0) {
+        const SeqTiles sq = seq_tiles(P, b);
+        const int n = (int)min(left, (long long)(sq.n - off));
+        // ---- Q of the group into shared memory: row r is (head r / Lq, query row r % Lq)
+        named_bar_sync(1, 128);  // no warp reads the last item's rows any more
+        for (int r = warp; r < S::kRows; r += 4) {
+            constexpr int kPer = HD / 64;  // pairs of a lane
+            const int gg = r / P.Lq, lq = r - gg * P.Lq;
+            const uint32_t* src = reinterpret_cast<const uint32_t*>(
+                static_cast<const uint16_t*>(P.q) + (((long long)b * P.Lq + lq) * P.H + h * P.G + gg) * HD);
+            uint32_t w[kPer];
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) w[e] = r < R ? src[lane + 32 * e] : 0u;
+            if constexpr (k8) {
+                // to fp16 by a power of two that brings the row's largest element to 2^13 .. 2^14
+                float2 f[kPer];
+                float big = 0.f;
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) {
+                    f[e] = bf ? __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&w[e])) : h2_to_f2(w[e]);
+                    big = max_nan(big, max_nan(fabsf(f[e].x), fabsf(f[e].y)));
+                }
+#pragma unroll
+                for (int o = 16; o; o >>= 1) big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, o));
+                int ex = (int)(__float_as_uint(big) >> 23) - 127;
+                ex = big > 0.f && big < INFINITY ? max(ex, -100) : 13;
+                const float mul = __uint_as_float((uint32_t)(13 - ex + 127) << 23);
+                if (lane == 0) qscale[r] = __uint_as_float((uint32_t)(ex - 13 + 127) << 23);
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) {
+                    // columns 4c .. 4c+3 of each 16 go where a fragment's thread c finds them
+                    const int c = 2 * (lane + 32 * e), in = c & 15;
+                    const int at = (c & ~15) + 2 * (in >> 2) + ((in & 2) ? 8 : 0);
+                    *reinterpret_cast<uint32_t*>(qs + r * S::kQPitch + at * 2) = pack2<false>(f[e].x * mul, f[e].y * mul);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < kPer; ++e)
+                    *reinterpret_cast<uint32_t*>(qs + r * S::kQPitch + 4 * (lane + 32 * e)) = w[e];
+            }
+        }
+        named_bar_sync(1, 128);
+        const uint32_t qaddr = smem_u32(qs) + ((mi & 1) * 8 + ri) * S::kQPitch + (mi >> 1) * 16;
+        uint32_t qa[S::kQReg ? RT : 1][S::kQReg ? HD / 16 : 1][4];
+        if constexpr (S::kQReg) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int ks = 0; ks < HD / 16; ++ks)
+                    ldsm_x4(qaddr + rt * 16 * S::kQPitch + ks * 32, qa[rt][ks][0], qa[rt][ks][1], qa[rt][ks][2],
+                            qa[rt][ks][3]);
+        }
+        // this thread's rows 16 rt + g (e < 2) and + 8: visible keys [vlo, vhi), score factor
+        int vlo[RT][2], vhi[RT][2];
+        float qf[RT][2], M[RT][2], L[RT][2];
+        float o[RT][S::kN][4];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = rt * 16 + g + 8 * e, pos = sq.p0 + r % P.Lq;
+                vlo[rt][e] = r < R && P.wl >= 0 ? max(0, pos - P.wl) : 0;
+                vhi[rt][e] = r < R && P.wr >= 0 ? (int)min((long long)sq.len, (long long)pos + P.wr + 1) : sq.len;
+                qf[rt][e] = P.scale * (k8 ? qscale[r] : 1.f) * (P.softcap > 0.f ? 1.f : kLog2e);
+                M[rt][e] = -INFINITY;
+                L[rt][e] = 0.f;
+            }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int i = 0; i < S::kN; ++i) o[rt][i][0] = o[rt][i][1] = o[rt][i][2] = o[rt][i][3] = 0.f;
+
+        for (int i = 0; i < n; ++i, ++it) {
+            const int s = (int)(it % S::kStages), buf = i & 1;
+            ok = ok && mbar_wait(full_bar(s), (int)(it / S::kStages) & 1, P.status, ST_DEC_WAIT, &abort_flag);
+            __syncwarp();
+            const uint32_t kt = ring + (uint32_t)(s * S::kStageBytes), vt = kt + S::kTileBytes;
+            const int j0 = (sq.t0 + off + i) * kKeys;
+            const int have = there[s];
+            const bool full = have == 0xf && tile_full(P.wl, P.wr, sq.len, sq.p0, sq.len - 1, j0, j0 + kKeys);
+            // chunk c (16 bytes) of a tile row
+            auto chunk = [&](uint32_t tile, int row, int c) -> uint32_t {
+                if constexpr (S::kRowBytes == 64) return tile + row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
+                else return tile + (c >> 3) * (kKeys * 128) + sw128(row, c & 7);
+            };
+
+            // ---- S = Q K^T for this warp's 16 keys
+            float sc[RT][2][4];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) sc[rt][x][0] = sc[rt][x][1] = sc[rt][x][2] = sc[rt][x][3] = 0.f;
+            const int key = warp * 16 + (mi & 1) * 8 + ri;
+#pragma unroll
+            for (int ks = 0; ks < HD / 16; ks += 2) {
+                uint32_t kb[2][2][2];  // [step][keys 0-7 | 8-15][fragment half]
+                if constexpr (k8) {
+                    // matrices: (keys 0-7 | 8-15) x (16 columns of step ks | ks + 1)
+                    uint32_t r0, r1, r2, r3;
+                    ldsm_x4(chunk(kt, key, ks + (mi >> 1)), r0, r1, r2, r3);
+                    const uint32_t raw[2][2] = {{r0, r1}, {r2, r3}};
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            kb[x][y][0] = f8x2_to_h2<k8 ? CACHE : CACHE_E4M3>(raw[x][y] & 0xffffu);
+                            kb[x][y][1] = f8x2_to_h2<k8 ? CACHE : CACHE_E4M3>(raw[x][y] >> 16);
+                        }
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        ldsm_x4(chunk(kt, key, 2 * (ks + x) + (mi >> 1)), kb[x][0][0], kb[x][1][0], kb[x][0][1],
+                                kb[x][1][1]);
+                }
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        uint32_t a[4];
+                        if constexpr (S::kQReg) {
+                            a[0] = qa[rt][ks + x][0], a[1] = qa[rt][ks + x][1], a[2] = qa[rt][ks + x][2],
+                            a[3] = qa[rt][ks + x][3];
+                        } else {
+                            ldsm_x4(qaddr + rt * 16 * S::kQPitch + (ks + x) * 32, a[0], a[1], a[2], a[3]);
+                        }
+                        mma_add<kMmaBf>(sc[rt][0], a, kb[x][0][0], kb[x][0][1]);
+                        mma_add<kMmaBf>(sc[rt][1], a, kb[x][1][0], kb[x][1][1]);
+                    }
+            }
+
+            // ---- probabilities of the 16 keys relative to their own maximum
+            const float kscale = k8 ? meta[s][warp].x : 1.f;
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                float mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int r = e >> 1;
+                        float y = sc[rt][x][e] * (qf[rt][r] * kscale);
+                        if (P.softcap > 0.f) y = P.softcap * tanh_accurate(y / P.softcap) * kLog2e;
+                        if (!full) {
+                            const int j = j0 + warp * 16 + x * 8 + 2 * t + (e & 1);
+                            if (j < vlo[rt][r] || j >= vhi[rt][r] || !((have >> warp) & 1)) y = -INFINITY;
+                        }
+                        sc[rt][x][e] = y;
+                        mx[r] = max_nan(mx[r], y);
+                    }
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    mx[r] = max_nan(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+                    mx[r] = max_nan(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+                    const float ref = mx[r] == -INFINITY ? 0.f : mx[r];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float p0 = fast_exp2(sc[rt][x][2 * r] - ref), p1 = fast_exp2(sc[rt][x][2 * r + 1] - ref);
+                        sum[r] += p0 + p1;
+                        *reinterpret_cast<uint32_t*>(ps + (buf * S::kRows + rt * 16 + g + 8 * r) * S::kPPitch +
+                                                     (warp * 16 + x * 8 + 2 * t) * 2) = pack2<kMmaBf>(p0, p1);
+                    }
+                    sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
+                    sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
+                    if (t == 0) mls[(buf * S::kRows + rt * 16 + g + 8 * r) * 4 + warp] = make_float2(mx[r], sum[r]);
+                }
+            }
+            named_bar_sync(1, 128);
+
+            // ---- running maximum and sum; factors of the four groups
+            float f[RT][2][4];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                float alpha[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float4* src = reinterpret_cast<const float4*>(mls + (buf * S::kRows + rt * 16 + g + 8 * r) * 4);
+                    const float4 u = src[0], v = src[1];
+                    const float mw[4] = {u.x, u.z, v.x, v.z}, lw[4] = {u.y, u.w, v.y, v.w};
+                    const float mn = max_nan(M[rt][r], max_nan(max_nan(mw[0], mw[1]), max_nan(mw[2], mw[3])));
+                    alpha[r] = mn == -INFINITY ? 1.f : fast_exp2(M[rt][r] - mn);
+                    M[rt][r] = mn;
+                    float l = L[rt][r] * alpha[r];
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        // a row that sees none of the group takes nothing of it, whatever its scale
+                        const float x = mw[w] == -INFINITY ? 0.f : fast_exp2(mw[w] - mn);
+                        l = fmaf(x, lw[w], l);
+                        f[rt][r][w] = k8 ? (mw[w] == -INFINITY ? 0.f : x * meta[s][w].y) : x;
+                    }
+                    L[rt][r] = l;
+                }
+                if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+                    for (int c = 0; c < S::kN; ++c) {
+                        o[rt][c][0] *= alpha[0], o[rt][c][1] *= alpha[0];
+                        o[rt][c][2] *= alpha[1], o[rt][c][3] *= alpha[1];
+                    }
+                }
+            }
+
+            // ---- O += P V for this warp's quarter of the columns
+            const uint32_t paddr = smem_u32(ps) + (buf * S::kRows + (mi & 1) * 8 + ri) * S::kPPitch + (mi >> 1) * 16;
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+                uint32_t pa[RT][4];
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+                    ldsm_x4(paddr + rt * 16 * S::kPPitch + ks * 32, pa[rt][0], pa[rt][1], pa[rt][2], pa[rt][3]);
+                uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+                if (!full) {
+                    // keys that no row sees: their bytes may be anything
+                    auto seen = [&](int k) {
+                        const int j = j0 + ks * 16 + k;
+                        return j >= sq.lo && j < sq.hi && ((have >> ks) & 1);
+                    };
+                    keep0 = (seen(2 * t) ? 0xffffu : 0u) | (seen(2 * t + 1) ? 0xffff0000u : 0u);
+                    keep1 = (seen(2 * t + 8) ? 0xffffu : 0u) | (seen(2 * t + 9) ? 0xffff0000u : 0u);
+                }
+#pragma unroll
+                for (int c = 0; c < S::kN; c += 2) {
+                    uint32_t vb[2][2];  // [8-column product][fragment half]
+                    const int vrow = ks * 16 + (mi & 1) * 8 + ri;
+                    if constexpr (k8) {
+                        // 16 columns: even ones are product c, odd ones c + 1
+                        uint32_t r0, r1;
+                        const int ch = warp * (HD / 64) + c / 2;
+                        asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];"
+                                     : "=r"(r0), "=r"(r1)
+                                     : "r"(chunk(vt, vrow, ch)));
+                        r0 = __byte_perm(r0, 0, 0x3120);
+                        r1 = __byte_perm(r1, 0, 0x3120);
+                        vb[0][0] = f8x2_to_h2<k8 ? CACHE : CACHE_E4M3>(r0 & 0xffffu);
+                        vb[1][0] = f8x2_to_h2<k8 ? CACHE : CACHE_E4M3>(r0 >> 16);
+                        vb[0][1] = f8x2_to_h2<k8 ? CACHE : CACHE_E4M3>(r1 & 0xffffu);
+                        vb[1][1] = f8x2_to_h2<k8 ? CACHE : CACHE_E4M3>(r1 >> 16);
+                    } else {
+                        ldsm_x4_t(chunk(vt, vrow, warp * (HD / 32) + c + (mi >> 1)), vb[0][0], vb[0][1], vb[1][0],
+                                  vb[1][1]);
+                    }
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        bool apart = false;
+                        if (!full) {
+                            vb[x][0] &= keep0;
+                            vb[x][1] &= keep1;
+                            // a value that is not finite may be one row's and not another's: its key by itself
+                            constexpr uint32_t kInf = kMmaBf ? 0x7f80u : 0x7c00u;
+                            auto wild = [&](uint32_t w) {
+                                return (w & kInf) == kInf || ((w >> 16) & kInf) == kInf;
+                            };
+                            apart = __any_sync(0xffffffffu, wild(vb[x][0]) || wild(vb[x][1]));
+                        }
+                        if (!apart) {
+#pragma unroll
+                            for (int rt = 0; rt < RT; ++rt) {
+                                float d[4];
+                                mma_zero<kMmaBf>(d, pa[rt], vb[x][0], vb[x][1]);
+                                o[rt][c + x][0] = fmaf(f[rt][0][ks], d[0], o[rt][c + x][0]);
+                                o[rt][c + x][1] = fmaf(f[rt][0][ks], d[1], o[rt][c + x][1]);
+                                o[rt][c + x][2] = fmaf(f[rt][1][ks], d[2], o[rt][c + x][2]);
+                                o[rt][c + x][3] = fmaf(f[rt][1][ks], d[3], o[rt][c + x][3]);
+                            }
+                        } else {
+#pragma unroll 1
+                            for (int k = 0; k < 16; ++k) {
+                                const uint32_t one = (k & 1) ? 0xffff0000u : 0xffffu;
+                                const bool mine = ((k & 7) >> 1) == t;
+                                const uint32_t b0 = mine && k < 8 ? vb[x][0] & one : 0u;
+                                const uint32_t b1 = mine && k >= 8 ? vb[x][1] & one : 0u;
+                                const int j = j0 + ks * 16 + k;
+#pragma unroll
+                                for (int rt = 0; rt < RT; ++rt) {
+                                    float d[4];
+                                    mma_zero<kMmaBf>(d, pa[rt], b0, b1);
+#pragma unroll
+                                    for (int r = 0; r < 2; ++r)
+                                        if (j >= vlo[rt][r] && j < vhi[rt][r]) {
+                                            o[rt][c + x][2 * r] = fmaf(f[rt][r][ks], d[2 * r], o[rt][c + x][2 * r]);
+                                            o[rt][c + x][2 * r + 1] =
+                                                fmaf(f[rt][r][ks], d[2 * r + 1], o[rt][c + x][2 * r + 1]);
+                                        }
+                                }
+                            }
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty_bar(s));
+        }
+
+        // ---- the item's rows, whole or partial
+        const bool begins = off == 0, ends = off + n == sq.n;
+        const bool whole = begins && ends;
+        const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
+        if (begins && !ends) {
+            // the CTAs after this one that hold the rest of the item: the stretch ends here
+            const long long rest = sq.n - n;
+            record = make_int4(b, h, (int)((rest + st.share - 1) / st.share), 0);
+        }
+        if (ok) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = rt * 16 + g + 8 * e;
+                    if (r >= R) continue;
+                    const int gg = r / P.Lq, lq = r - gg * P.Lq;
+                    const int hq = h * P.G + gg;
+                    const float inv = M[rt][e] == -INFINITY ? 0.f : 1.f / L[rt][e];
+                    const bool none = M[rt][e] == -INFINITY;
+                    uint16_t* od = static_cast<uint16_t*>(P.o) + (((long long)b * P.Lq + lq) * P.H + hq) * HD;
+                    float* wd = ws_o + ((long long)slot * R + r) * HD;
+                    auto two = [&](float x, float y) { return bf ? pack2<true>(x, y) : pack2<false>(x, y); };
+                    if constexpr (k8) {
+#pragma unroll
+                        for (int c = 0; c < S::kN; c += 2) {
+                            const int d = warp * (HD / 4) + c * 8 + 4 * t;
+                            const float x0 = o[rt][c][2 * e], x1 = o[rt][c + 1][2 * e], x2 = o[rt][c][2 * e + 1],
+                                        x3 = o[rt][c + 1][2 * e + 1];
+                            if (whole)
+                                *reinterpret_cast<uint2*>(od + d) =
+                                    none ? make_uint2(0, 0) : make_uint2(two(x0 * inv, x1 * inv), two(x2 * inv, x3 * inv));
+                            else
+                                *reinterpret_cast<float4*>(wd + d) = make_float4(x0, x1, x2, x3);
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < S::kN; ++c) {
+                            const int d = warp * (HD / 4) + c * 8 + 2 * t;
+                            const float x0 = o[rt][c][2 * e], x1 = o[rt][c][2 * e + 1];
+                            if (whole)
+                                *reinterpret_cast<uint32_t*>(od + d) = none ? 0u : two(x0 * inv, x1 * inv);
+                            else
+                                *reinterpret_cast<float2*>(wd + d) = make_float2(x0, x1);
+                        }
+                    }
+                    if (warp == 0 && t == 0) {
+                        if (whole) {
+                            if (P.lse)
+                                P.lse[((long long)b * P.H + hq) * P.Lq + lq] =
+                                    none ? -INFINITY : (M[rt][e] + log2f(L[rt][e])) * 0.6931471805599453f;
+                        } else {
+                            reinterpret_cast<float2*>(ws_ml)[(long long)slot * R + r] = make_float2(M[rt][e], L[rt][e]);
+                        }
+                    }
+                }
+        }
+        left -= n;
+        off = 0;
+        if (left > 0) next_item(P, b, h);
+    }
+    if (tid == 0) reinterpret_cast<int4*>(P.ws)[blockIdx.x] = record;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // sequences of which no row sees a key
+    for (int e = blockIdx.x; e < P.B; e += gridDim.x) {
+        if (tid == 0 && __ldg(P.lengths + e) > (P.max_pages << P.page_shift)) atomicOr(P.status, ST_PAGED_BOUNDS);
+        if (seq_tiles(P, e).n > 0) continue;
+        uint4* od = reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.o) + (long long)e * P.Lq * P.H * HD);
+        for (int i = tid; i < P.Lq * P.H * HD / 8; i += 128) od[i] = make_uint4(0, 0, 0, 0);
+        if (P.lse)
+            for (int i = tid; i < P.Lq * P.H; i += 128) P.lse[(long long)e * P.Lq * P.H + i] = -INFINITY;
+    }
+}
+
+// Merges the partial rows of the items that stretches cut: CTA (c, y) those of the item
+// that begins in stretch c and does not end in it, eight rows of it (or fewer rows with
+// several warps each).  The order of the sums is that of the stretches.
+template <int HD>
+__global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams P, const int rows_bf16) {
+    constexpr int kPer = HD / 32;  // columns of a lane
+    __shared__ float part[8][HD];
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the split kernel's results are there
+    const int4 rec = reinterpret_cast<const int4*>(P.ws)[blockIdx.x];
+    if (rec.x < 0) return;
+    const int R = P.G * P.Lq;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int wpr = 8;  // warps of a row
+    while (wpr > 1 && 8 / wpr < R) wpr >>= 1;
+    const int r = blockIdx.y * 8 + warp / wpr, w = warp % wpr;
+    const bool live = r < R;
+    const float2* ml = reinterpret_cast<const float2*>(reinterpret_cast<const uint8_t*>(P.ws) + ws_ml_offset());
+    const float* wo = reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(P.ws) + ws_o_offset(R));
+    const int n = rec.z + 1;  // parts: this stretch's end, then the beginnings of the next ones
+    auto at = [&](int i) { return (long long)(2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * R + r; };
+    float M = -INFINITY, L = 0.f;
+    float acc[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+    if (live) {
+        for (int i = lane; i < n; i += 32) M = max_nan(M, ml[at(i)].x);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
+        for (int base = 0; base < n; base += 32) {
+            const int i = base + lane;
+            const float2 x = i < n ? ml[at(i)] : make_float2(-INFINITY, 0.f);
+            const float f = x.x == -INFINITY ? 0.f : fast_exp2(x.x - M);
+            L += f * x.y;
+            const int m = min(32, n - base);
+#pragma unroll 8
+            for (int j = w; j < m; j += wpr) {
+                const float fj = __shfl_sync(0xffffffffu, f, j);
+                const float* src = wo + at(base + j) * HD + lane * kPer;
+                float y[kPer];
+                if constexpr (kPer == 2) {
+                    const float2 v = *reinterpret_cast<const float2*>(src);
+                    y[0] = v.x, y[1] = v.y;
+                } else {
+#pragma unroll
+                    for (int q = 0; q < kPer / 4; ++q) {
+                        const float4 v = reinterpret_cast<const float4*>(src)[q];
+                        y[4 * q] = v.x, y[4 * q + 1] = v.y, y[4 * q + 2] = v.z, y[4 * q + 3] = v.w;
+                    }
+                }
+                // a part whose row saw nothing holds zeros
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) acc[e] = fmaf(fj, y[e], acc[e]);
+            }
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    }
+    if (wpr > 1) {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) part[warp][lane * kPer + e] = acc[e];
+        __syncthreads();
+        if (w == 0)
+            for (int x = 1; x < wpr; ++x)
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) acc[e] += part[warp + x][lane * kPer + e];
+    }
+    if (!live || w != 0) return;
+    const int gg = r / P.Lq, lq = r - gg * P.Lq, hq = rec.y * P.G + gg;
+    const bool none = M == -INFINITY;
+    const float inv = none ? 0.f : 1.f / L;
+    uint32_t* od = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(P.o) +
+                                               (((long long)rec.x * P.Lq + lq) * P.H + hq) * HD + lane * kPer);
+#pragma unroll
+    for (int e = 0; e < kPer; e += 2) {
+        const float x = none ? 0.f : acc[e] * inv, y = none ? 0.f : acc[e + 1] * inv;
+        od[e / 2] = rows_bf16 ? pack2<true>(x, y) : pack2<false>(x, y);
+    }
+    if (P.lse && lane == 0)
+        P.lse[((long long)rec.x * P.H + hq) * P.Lq + lq] = none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+template <int HD, int CACHE, int RT, bool kBf>
+cudaError_t decode_launch(const PagedParams& p, bool bf16, const PagedMaps& maps, cudaStream_t s) {
+    using S = DecShape<HD, CACHE, RT>;
+    auto k = paged_split_kernel<HD, CACHE, RT, kBf>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+    if (e != cudaSuccess) return e;
+    constexpr int kGrid = kSms * S::kCtas;
+    k<<<kGrid, kDecThreads, S::kBytes, s>>>(p, bf16 ? 1 : 0, maps.k, maps.v);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    // launched early: its CTAs come up while the split kernel's last ones run, and wait there
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kGrid, (p.G * p.Lq + 7) / 8);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_combine_kernel<HD>, p, bf16 ? 1 : 0);
+}
+
+template <int HD, int CACHE, bool kBf>
+cudaError_t decode_rows(const PagedParams& p, bool bf16, const PagedMaps& maps, cudaStream_t s) {
+    const int R = p.G * p.Lq;
+    if (R <= 16) return decode_launch<HD, CACHE, 1, kBf>(p, bf16, maps, s);
+    if (R <= 32) return decode_launch<HD, CACHE, 2, kBf>(p, bf16, maps, s);
+    return decode_launch<HD, CACHE, 4, kBf>(p, bf16, maps, s);
+}
+template <int CACHE, bool kBf>
+cudaError_t decode_hd(const PagedParams& p, bool bf16, const PagedMaps& maps, cudaStream_t s) {
+    if (p.hd == 64) return decode_rows<64, CACHE, kBf>(p, bf16, maps, s);
+    if (p.hd == 128) return decode_rows<128, CACHE, kBf>(p, bf16, maps, s);
+    return decode_rows<256, CACHE, kBf>(p, bf16, maps, s);
+}
+
+}  // namespace paged
+}  // namespace
+}  // namespace attn
