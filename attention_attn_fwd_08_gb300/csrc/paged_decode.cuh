@@ -106,6 +106,23 @@ __device__ __forceinline__ void mma_add(float (&d)[4], const uint32_t (&a)[4], u
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// Four codes of a K row (neighbouring columns) as the two halves of a B fragment, and four
+// codes of V (two columns of two keys, as ldmatrix.trans leaves them) as one half of the
+// even column's fragment and of the odd one's.  An e5m2 code is the upper byte of its fp16.
+template <int CACHE>
+__device__ __forceinline__ void codes_k(uint32_t c, uint32_t& h0, uint32_t& h1) {
+    if constexpr (CACHE == CACHE_E4M3)
+        asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+            : "=r"(h0), "=r"(h1)
+            : "r"(c));
+    else
+        h0 = __byte_perm(c, 0, 0x1404), h1 = __byte_perm(c, 0, 0x3424);
+}
+template <int CACHE>
+__device__ __forceinline__ void codes_v(uint32_t c, uint32_t& even, uint32_t& odd) {
+    if constexpr (CACHE == CACHE_E4M3) codes_k<CACHE>(__byte_perm(c, 0, 0x3120), even, odd);
+    else even = __byte_perm(c, 0, 0x2404), odd = __byte_perm(c, 0, 0x3414);
+}
 // the maximum, NaN if either is
 __device__ __forceinline__ float max_nan(float a, float b) {
     float d;
@@ -247,7 +264,8 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
         const bool has_box = is_v < 2;
         int b = st.b, h = st.h, off = st.off;
         long long left = st.count;
-        long long it = 0;  // tiles produced
+        int stage = 0, phase = 1;  // a wait on a fresh barrier's other phase returns at once
+        int made = 0;              // tiles produced, up to the ring's depth
         bool ok = true;
         while (left > 0 && ok) {
             const SeqTiles sq = seq_tiles(P, b);
@@ -276,10 +294,9 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
                 const float2 sc_next = scales_at(pg_next);
                 const int pg_after = page_at(base / 8 + 2);
                 const int m = min(8, n - base);
-                for (int i = 0; i < m; ++i, ++it) {
-                    const int s = (int)(it % S::kStages);
-                    const long long use = it / S::kStages;
-                    if (use > 0 && !warp_wait(empty_bar(s), (int)(use - 1) & 1, P.status, ST_DEC_WAIT, &abort_flag)) {
+                for (int i = 0; i < m; ++i) {
+                    const int s = stage;
+                    if (!warp_wait(empty_bar(s), phase, P.status, ST_DEC_WAIT, &abort_flag)) {
                         ok = false;
                         break;
                     }
@@ -307,6 +324,8 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
                         const int y = ((page * P.Hkv + h) << P.page_shift) + row;
                         tma_load_2d(dst, is_v ? &tmV : &tmK, full_bar(s), bx * (S::kRowBytes / S::kEs), y, pol);
                     }
+                    made = min(made + 1, S::kStages);
+                    if (++stage == S::kStages) stage = 0, phase ^= 1;
                 }
                 pg = pg_next;
                 sc = sc_next;
@@ -317,9 +336,10 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
             if (left > 0) next_item(P, b, h);
         }
         // no copy is in flight when the CTA ends
-        for (long long i = max(0ll, it - S::kStages); i < it; ++i)
-            mbar_wait(full_bar((int)(i % S::kStages)), (int)(i / S::kStages) & 1, P.status, ST_DEC_WAIT | ST_TEARDOWN,
-                      nullptr);
+        for (int i = 0; i < made; ++i) {
+            if (--stage < 0) stage = S::kStages - 1, phase ^= 1;
+            mbar_wait(full_bar(stage), phase ^ 1, P.status, ST_DEC_WAIT | ST_TEARDOWN, nullptr);
+        }
         return;
     }
 
@@ -330,8 +350,23 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
     float* ws_o = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(P.ws) + ws_o_offset(R));
     int4 record = make_int4(-1, 0, 0, 0);
     int b = st.b, h = st.h, off = st.off;
-    long long left = st.count, it = 0;
+    long long left = st.count;
+    int stage = 0, phase = 0;
     bool ok = true;
+    // this thread's places in a tile: its K row's chunk, its V rows' chunks, its rows of P
+    constexpr int kBoxBytes = kKeys * S::kRowBytes;
+    auto chunk = [&](int row, int c) -> uint32_t {  // of 16 bytes, as the swizzle lays them
+        if constexpr (S::kRowBytes == 64) return row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
+        else return (c >> 3) * kBoxBytes + sw128(row, c & 7);
+    };
+    const uint32_t k_off = chunk(warp * 16 + (mi & 1) * 8 + ri, mi >> 1);
+    uint32_t v_off[S::kN / 2];
+#pragma unroll
+    for (int c = 0; c < S::kN; c += 2)
+        v_off[c / 2] = S::kTileBytes + (k8 ? chunk(mi * 8 + ri, warp * (HD / 64) + c / 2)
+                                           : chunk((mi & 1) * 8 + ri, warp * (HD / 32) + c + (mi >> 1)));
+    uint8_t* p_out = ps + g * S::kPPitch + (warp * 16 + 2 * t) * 2;
+    const float cap_inv = P.softcap > 0.f ? 1.f / P.softcap : 0.f;
     while (left > 0) {
         const SeqTiles sq = seq_tiles(P, b);
         const int n = (int)min(left, (long long)(sq.n - off));
@@ -399,24 +434,18 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
                 M[rt][e] = -INFINITY;
                 L[rt][e] = 0.f;
             }
+        // tiles from full_lo to full_hi on are seen whole by every row (tile_full over j0)
+        const int full_lo = P.wl >= 0 ? max(0, sq.len - 1 - P.wl) : 0;
+        const int full_hi = (P.wr >= 0 ? (int)min((long long)sq.len, (long long)sq.p0 + P.wr + 1) : sq.len) - kKeys;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
             for (int i = 0; i < S::kN; ++i) o[rt][i][0] = o[rt][i][1] = o[rt][i][2] = o[rt][i][3] = 0.f;
 
-        for (int i = 0; i < n; ++i, ++it) {
-            const int s = (int)(it % S::kStages), buf = i & 1;
-            ok = ok && mbar_wait(full_bar(s), (int)(it / S::kStages) & 1, P.status, ST_DEC_WAIT, &abort_flag);
-            __syncwarp();
-            const uint32_t kt = ring + (uint32_t)(s * S::kStageBytes), vt = kt + S::kTileBytes;
-            const int j0 = (sq.t0 + off + i) * kKeys;
-            const int have = there[s];
-            const bool full = have == 0xf && tile_full(P.wl, P.wr, sq.len, sq.p0, sq.len - 1, j0, j0 + kKeys);
-            // chunk c (16 bytes) of a tile row
-            auto chunk = [&](uint32_t tile, int row, int c) -> uint32_t {
-                if constexpr (S::kRowBytes == 64) return tile + row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
-                else return tile + (c >> 3) * (kKeys * 128) + sw128(row, c & 7);
-            };
+        // One tile.  kFull: every row sees every key of it, so nothing is masked.
+        auto tile = [&](auto full_c, int j0, int have, int s, int buf) {
+            constexpr bool kFull = decltype(full_c)::value;
+            const uint32_t base = ring + (uint32_t)(s * S::kStageBytes);
 
             // ---- S = Q K^T for this warp's 16 keys
             float sc[RT][2][4];
@@ -424,27 +453,25 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
             for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) sc[rt][x][0] = sc[rt][x][1] = sc[rt][x][2] = sc[rt][x][3] = 0.f;
-            const int key = warp * 16 + (mi & 1) * 8 + ri;
+            const uint32_t kt = base + k_off;
 #pragma unroll
             for (int ks = 0; ks < HD / 16; ks += 2) {
                 uint32_t kb[2][2][2];  // [step][keys 0-7 | 8-15][fragment half]
                 if constexpr (k8) {
                     // matrices: (keys 0-7 | 8-15) x (16 columns of step ks | ks + 1)
-                    uint32_t r0, r1, r2, r3;
-                    ldsm_x4(chunk(kt, key, ks + (mi >> 1)), r0, r1, r2, r3);
-                    const uint32_t raw[2][2] = {{r0, r1}, {r2, r3}};
+                    uint32_t r[2][2];
+                    ldsm_x4((kt ^ ((ks & 7) << 4)) + (ks >> 3) * kBoxBytes, r[0][0], r[0][1], r[1][0], r[1][1]);
 #pragma unroll
                     for (int x = 0; x < 2; ++x)
 #pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            kb[x][y][0] = f8x2_to_h2<k8 ? CACHE : CACHE_E4M3>(raw[x][y] & 0xffffu);
-                            kb[x][y][1] = f8x2_to_h2<k8 ? CACHE : CACHE_E4M3>(raw[x][y] >> 16);
-                        }
+                        for (int y = 0; y < 2; ++y) codes_k<CACHE>(r[x][y], kb[x][y][0], kb[x][y][1]);
                 } else {
 #pragma unroll
-                    for (int x = 0; x < 2; ++x)
-                        ldsm_x4(chunk(kt, key, 2 * (ks + x) + (mi >> 1)), kb[x][0][0], kb[x][1][0], kb[x][0][1],
+                    for (int x = 0; x < 2; ++x) {
+                        const int c = 2 * (ks + x);
+                        ldsm_x4((kt ^ ((c & 7) << 4)) + (c >> 3) * kBoxBytes, kb[x][0][0], kb[x][1][0], kb[x][0][1],
                                 kb[x][1][1]);
+                    }
                 }
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt)
@@ -466,36 +493,45 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
             const float kscale = k8 ? meta[s][warp].x : 1.f;
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-                float mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int r = e >> 1;
-                        float y = sc[rt][x][e] * (qf[rt][r] * kscale);
-                        if (P.softcap > 0.f) y = P.softcap * tanh_accurate(y / P.softcap) * kLog2e;
-                        if (!full) {
-                            const int j = j0 + warp * 16 + x * 8 + 2 * t + (e & 1);
-                            if (j < vlo[rt][r] || j >= vhi[rt][r] || !((have >> warp) & 1)) y = -INFINITY;
-                        }
-                        sc[rt][x][e] = y;
-                        mx[r] = max_nan(mx[r], y);
-                    }
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    mx[r] = max_nan(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-                    mx[r] = max_nan(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-                    const float ref = mx[r] == -INFINITY ? 0.f : mx[r];
+                    const float c = qf[rt][r] * kscale;
+                    sc[rt][0][2 * r] *= c, sc[rt][0][2 * r + 1] *= c, sc[rt][1][2 * r] *= c, sc[rt][1][2 * r + 1] *= c;
+                }
+                if (P.softcap > 0.f) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            sc[rt][x][e] = P.softcap * tanh_accurate(sc[rt][x][e] * cap_inv) * kLog2e;
+                }
+                if constexpr (!kFull) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int r = e >> 1, j = j0 + warp * 16 + x * 8 + 2 * t + (e & 1);
+                            if (j < vlo[rt][r] || j >= vhi[rt][r] || !((have >> warp) & 1)) sc[rt][x][e] = -INFINITY;
+                        }
+                }
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    float mx = max_nan(max_nan(sc[rt][0][2 * r], sc[rt][0][2 * r + 1]),
+                                       max_nan(sc[rt][1][2 * r], sc[rt][1][2 * r + 1]));
+                    mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    const float ref = mx == -INFINITY ? 0.f : mx;
+                    float sum = 0.f;
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         const float p0 = fast_exp2(sc[rt][x][2 * r] - ref), p1 = fast_exp2(sc[rt][x][2 * r + 1] - ref);
-                        sum[r] += p0 + p1;
-                        *reinterpret_cast<uint32_t*>(ps + (buf * S::kRows + rt * 16 + g + 8 * r) * S::kPPitch +
-                                                     (warp * 16 + x * 8 + 2 * t) * 2) = pack2<kMmaBf>(p0, p1);
+                        sum += p0 + p1;
+                        *reinterpret_cast<uint32_t*>(p_out + (buf * S::kRows + rt * 16 + 8 * r) * S::kPPitch + x * 16) =
+                            pack2<kMmaBf>(p0, p1);
                     }
-                    sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
-                    sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
-                    if (t == 0) mls[(buf * S::kRows + rt * 16 + g + 8 * r) * 4 + warp] = make_float2(mx[r], sum[r]);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                    if (t == 0) mls[(buf * S::kRows + rt * 16 + g + 8 * r) * 4 + warp] = make_float2(mx, sum);
                 }
             }
             named_bar_sync(1, 128);
@@ -511,15 +547,20 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
                     const float4 u = src[0], v = src[1];
                     const float mw[4] = {u.x, u.z, v.x, v.z}, lw[4] = {u.y, u.w, v.y, v.w};
                     const float mn = max_nan(M[rt][r], max_nan(max_nan(mw[0], mw[1]), max_nan(mw[2], mw[3])));
-                    alpha[r] = mn == -INFINITY ? 1.f : fast_exp2(M[rt][r] - mn);
+                    const float ref = mn == -INFINITY ? 0.f : mn;
+                    alpha[r] = fast_exp2(M[rt][r] - ref);  // before the first key: 0, of nothing
                     M[rt][r] = mn;
                     float l = L[rt][r] * alpha[r];
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
-                        // a row that sees none of the group takes nothing of it, whatever its scale
-                        const float x = mw[w] == -INFINITY ? 0.f : fast_exp2(mw[w] - mn);
+                        const float x = fast_exp2(mw[w] - ref);
                         l = fmaf(x, lw[w], l);
-                        f[rt][r][w] = k8 ? (mw[w] == -INFINITY ? 0.f : x * meta[s][w].y) : x;
+                        f[rt][r][w] = x;
+                        if constexpr (k8) {
+                            f[rt][r][w] = x * meta[s][w].y;
+                            // a row that sees none of the group takes nothing of it, whatever its scale
+                            if constexpr (!kFull) f[rt][r][w] = mw[w] == -INFINITY ? 0.f : f[rt][r][w];
+                        }
                     }
                     L[rt][r] = l;
                 }
@@ -532,95 +573,105 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
                 }
             }
 
-            // ---- O += P V for this warp's quarter of the columns
+            // ---- O += P V for this warp's quarter of the columns, two groups of 16 keys at a time
             const uint32_t paddr = smem_u32(ps) + (buf * S::kRows + (mi & 1) * 8 + ri) * S::kPPitch + (mi >> 1) * 16;
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-                uint32_t pa[RT][4];
+            for (int kp = 0; kp < 4; kp += 2) {
+                uint32_t pa[2][RT][4], keep[2][2];
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
-                    ldsm_x4(paddr + rt * 16 * S::kPPitch + ks * 32, pa[rt][0], pa[rt][1], pa[rt][2], pa[rt][3]);
-                uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-                if (!full) {
-                    // keys that no row sees: their bytes may be anything
-                    auto seen = [&](int k) {
-                        const int j = j0 + ks * 16 + k;
-                        return j >= sq.lo && j < sq.hi && ((have >> ks) & 1);
-                    };
-                    keep0 = (seen(2 * t) ? 0xffffu : 0u) | (seen(2 * t + 1) ? 0xffff0000u : 0u);
-                    keep1 = (seen(2 * t + 8) ? 0xffffu : 0u) | (seen(2 * t + 9) ? 0xffff0000u : 0u);
+                for (int y = 0; y < 2; ++y) {
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+                        ldsm_x4(paddr + rt * 16 * S::kPPitch + (kp + y) * 32, pa[y][rt][0], pa[y][rt][1], pa[y][rt][2],
+                                pa[y][rt][3]);
+                    if constexpr (!kFull) {
+                        // keys that no row sees: their bytes may be anything
+                        auto seen = [&](int k) {
+                            const int j = j0 + (kp + y) * 16 + k;
+                            return j >= sq.lo && j < sq.hi && ((have >> (kp + y)) & 1);
+                        };
+                        keep[y][0] = (seen(2 * t) ? 0xffffu : 0u) | (seen(2 * t + 1) ? 0xffff0000u : 0u);
+                        keep[y][1] = (seen(2 * t + 8) ? 0xffffu : 0u) | (seen(2 * t + 9) ? 0xffff0000u : 0u);
+                    }
                 }
 #pragma unroll
                 for (int c = 0; c < S::kN; c += 2) {
-                    uint32_t vb[2][2];  // [8-column product][fragment half]
-                    const int vrow = ks * 16 + (mi & 1) * 8 + ri;
+                    uint32_t vb[2][2][2];  // [group][8-column product][fragment half]
                     if constexpr (k8) {
                         // 16 columns: even ones are product c, odd ones c + 1
-                        uint32_t r0, r1;
-                        const int ch = warp * (HD / 64) + c / 2;
-                        asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];"
-                                     : "=r"(r0), "=r"(r1)
-                                     : "r"(chunk(vt, vrow, ch)));
-                        r0 = __byte_perm(r0, 0, 0x3120);
-                        r1 = __byte_perm(r1, 0, 0x3120);
-                        vb[0][0] = f8x2_to_h2<k8 ? CACHE : CACHE_E4M3>(r0 & 0xffffu);
-                        vb[1][0] = f8x2_to_h2<k8 ? CACHE : CACHE_E4M3>(r0 >> 16);
-                        vb[0][1] = f8x2_to_h2<k8 ? CACHE : CACHE_E4M3>(r1 & 0xffffu);
-                        vb[1][1] = f8x2_to_h2<k8 ? CACHE : CACHE_E4M3>(r1 >> 16);
+                        uint32_t r[2][2];
+                        ldsm_x4_t(base + v_off[c / 2] + kp * 16 * S::kRowBytes, r[0][0], r[0][1], r[1][0], r[1][1]);
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+#pragma unroll
+                            for (int z = 0; z < 2; ++z) codes_v<CACHE>(r[y][z], vb[y][0][z], vb[y][1][z]);
                     } else {
-                        ldsm_x4_t(chunk(vt, vrow, warp * (HD / 32) + c + (mi >> 1)), vb[0][0], vb[0][1], vb[1][0],
-                                  vb[1][1]);
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+                            ldsm_x4_t(base + v_off[c / 2] + (kp + y) * 16 * S::kRowBytes, vb[y][0][0], vb[y][0][1],
+                                      vb[y][1][0], vb[y][1][1]);
                     }
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        bool apart = false;
-                        if (!full) {
-                            vb[x][0] &= keep0;
-                            vb[x][1] &= keep1;
-                            // a value that is not finite may be one row's and not another's: its key by itself
-                            constexpr uint32_t kInf = kMmaBf ? 0x7f80u : 0x7c00u;
-                            auto wild = [&](uint32_t w) {
-                                return (w & kInf) == kInf || ((w >> 16) & kInf) == kInf;
-                            };
-                            apart = __any_sync(0xffffffffu, wild(vb[x][0]) || wild(vb[x][1]));
-                        }
-                        if (!apart) {
+                    for (int y = 0; y < 2; ++y)
 #pragma unroll
-                            for (int rt = 0; rt < RT; ++rt) {
-                                float d[4];
-                                mma_zero<kMmaBf>(d, pa[rt], vb[x][0], vb[x][1]);
-                                o[rt][c + x][0] = fmaf(f[rt][0][ks], d[0], o[rt][c + x][0]);
-                                o[rt][c + x][1] = fmaf(f[rt][0][ks], d[1], o[rt][c + x][1]);
-                                o[rt][c + x][2] = fmaf(f[rt][1][ks], d[2], o[rt][c + x][2]);
-                                o[rt][c + x][3] = fmaf(f[rt][1][ks], d[3], o[rt][c + x][3]);
+                        for (int x = 0; x < 2; ++x) {
+                            bool apart = false;
+                            if constexpr (!kFull) {
+                                vb[y][x][0] &= keep[y][0];
+                                vb[y][x][1] &= keep[y][1];
+                                // a value that is not finite may be one row's and not another's: its key by itself
+                                constexpr uint32_t kInf = kMmaBf ? 0x7f80u : 0x7c00u;
+                                auto wild = [&](uint32_t w) {
+                                    return (w & kInf) == kInf || ((w >> 16) & kInf) == kInf;
+                                };
+                                apart = __any_sync(0xffffffffu, wild(vb[y][x][0]) || wild(vb[y][x][1]));
                             }
-                        } else {
-#pragma unroll 1
-                            for (int k = 0; k < 16; ++k) {
-                                const uint32_t one = (k & 1) ? 0xffff0000u : 0xffffu;
-                                const bool mine = ((k & 7) >> 1) == t;
-                                const uint32_t b0 = mine && k < 8 ? vb[x][0] & one : 0u;
-                                const uint32_t b1 = mine && k >= 8 ? vb[x][1] & one : 0u;
-                                const int j = j0 + ks * 16 + k;
+                            if (!apart) {
 #pragma unroll
                                 for (int rt = 0; rt < RT; ++rt) {
                                     float d[4];
-                                    mma_zero<kMmaBf>(d, pa[rt], b0, b1);
+                                    mma_zero<kMmaBf>(d, pa[y][rt], vb[y][x][0], vb[y][x][1]);
+                                    o[rt][c + x][0] = fmaf(f[rt][0][kp + y], d[0], o[rt][c + x][0]);
+                                    o[rt][c + x][1] = fmaf(f[rt][0][kp + y], d[1], o[rt][c + x][1]);
+                                    o[rt][c + x][2] = fmaf(f[rt][1][kp + y], d[2], o[rt][c + x][2]);
+                                    o[rt][c + x][3] = fmaf(f[rt][1][kp + y], d[3], o[rt][c + x][3]);
+                                }
+                            } else {
+#pragma unroll 1
+                                for (int k = 0; k < 16; ++k) {
+                                    const uint32_t one = (k & 1) ? 0xffff0000u : 0xffffu;
+                                    const bool mine = ((k & 7) >> 1) == t;
+                                    const uint32_t b0 = mine && k < 8 ? vb[y][x][0] & one : 0u;
+                                    const uint32_t b1 = mine && k >= 8 ? vb[y][x][1] & one : 0u;
+                                    const int j = j0 + (kp + y) * 16 + k;
 #pragma unroll
-                                    for (int r = 0; r < 2; ++r)
-                                        if (j >= vlo[rt][r] && j < vhi[rt][r]) {
-                                            o[rt][c + x][2 * r] = fmaf(f[rt][r][ks], d[2 * r], o[rt][c + x][2 * r]);
-                                            o[rt][c + x][2 * r + 1] =
-                                                fmaf(f[rt][r][ks], d[2 * r + 1], o[rt][c + x][2 * r + 1]);
-                                        }
+                                    for (int rt = 0; rt < RT; ++rt) {
+                                        float d[4];
+                                        mma_zero<kMmaBf>(d, pa[y][rt], b0, b1);
+#pragma unroll
+                                        for (int r = 0; r < 2; ++r)
+                                            if (j >= vlo[rt][r] && j < vhi[rt][r]) {
+                                                o[rt][c + x][2 * r] = fmaf(f[rt][r][kp + y], d[2 * r], o[rt][c + x][2 * r]);
+                                                o[rt][c + x][2 * r + 1] =
+                                                    fmaf(f[rt][r][kp + y], d[2 * r + 1], o[rt][c + x][2 * r + 1]);
+                                            }
+                                    }
                                 }
                             }
                         }
-                    }
                 }
             }
+        };
+
+        for (int i = 0; i < n; ++i) {
+            ok = ok && mbar_wait(full_bar(stage), phase, P.status, ST_DEC_WAIT, &abort_flag);
             __syncwarp();
-            if (lane == 0) mbar_arrive(empty_bar(s));
+            const int j0 = (sq.t0 + off + i) * kKeys, have = there[stage];
+            if (have == 0xf && j0 >= full_lo && j0 <= full_hi) tile(std::true_type(), j0, have, stage, i & 1);
+            else tile(std::false_type(), j0, have, stage, i & 1);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty_bar(stage));
+            if (++stage == S::kStages) stage = 0, phase ^= 1;
         }
 
         // ---- the item's rows, whole or partial
