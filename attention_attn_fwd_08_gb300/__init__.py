@@ -629,84 +629,93 @@ def attn_packed_qkv_bwd(qkv, do, seq_bounds, *, H, scale=None, window=0, dqkv=No
 
 
 # ------------------------------------------------------------ paged key/value cache
-_PAGED_DT = {"float16": 1, "bfloat16": 2, "float8_e4m3fn": 3, "float8_e5m2": 4}
+# These calls are made once a layer and token: the checks below are written so that a call
+# that passes them costs a few microseconds.
+_paged_dt = {}
 
 
-def _name(dtype) -> str:
-    return str(dtype).replace("torch.", "")
-
-
-class _On:
-    """The device of a call's tensors made current, and the stream that it runs on: the
-    caller's, or the device's current one.  Tensors that the call makes for itself are made
-    on that stream, so that their memory is given back in its order."""
-
-    def __init__(self, device, stream):
+def _paged_codes():
+    """attn_dtype codes by torch dtype: of rows (16-bit floats) and of pools."""
+    if not _paged_dt:
         torch = _torch()
-        if stream is not None and not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=device)
-        self.guard = None
-        if stream is not None and stream != torch.cuda.current_stream(device):
-            self.guard = torch.cuda.stream(stream)  # makes the stream's device current too
-        elif torch.cuda.current_device() != device.index:
-            self.guard = torch.cuda.device(device)
-        self.stream = torch.cuda.current_stream(device) if stream is None else stream
-        self.handle = ctypes.c_void_p(self.stream.cuda_stream)
+        _paged_dt.update({torch.float16: 1, torch.bfloat16: 2, torch.float8_e4m3fn: 3, torch.float8_e5m2: 4})
+    return _paged_dt
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.handle
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-        return False
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _on(device, stream):
+    """(stream handle, context or None) for a call on `device`: the given stream, or the
+    device's current one.  The context makes the device current, and with a stream given
+    that stream, so that what the call allocates for itself is given back in its order."""
+    torch = _torch()
+    if stream is None:
+        at = device.index
+        return torch._C._cuda_getCurrentRawStream(at), None if torch.cuda.current_device() == at else torch.cuda.device(at)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return stream.cuda_stream, torch.cuda.stream(stream)
 
 
 def _pools(k_cache, v_cache, k_scale, v_scale, page_table, Hkv, row_dtype):
-    """(cache dtype code, num_pages, page_size, hd, batch, max_pages) of a paged cache whose
-    tensors agree with each other and lie on one GPU."""
+    """(row dtype code, cache dtype code, num_pages, page_size, hd, batch, max_pages) of a paged
+    cache whose tensors agree with each other and lie on one GPU."""
     torch = _torch()
-    dev = k_cache.device
-    if k_cache.dim() != 4 or k_cache.shape[1] != Hkv:
-        raise ValueError("k_cache must be [num_pages, Hkv, page_size, hd] with Hkv = %d (got %s)" % (Hkv, tuple(k_cache.shape)))
-    name = _name(k_cache.dtype)
-    if name not in _PAGED_DT:
-        raise TypeError("unsupported cache dtype %s" % k_cache.dtype)
-    if _name(row_dtype) not in ("float16", "bfloat16"):
+    codes, dev, shape, dtype = _paged_codes(), k_cache.device, k_cache.shape, k_cache.dtype
+    if len(shape) != 4 or shape[1] != Hkv:
+        raise ValueError("k_cache must be [num_pages, Hkv, page_size, hd] with Hkv = %d (got %s)" % (Hkv, tuple(shape)))
+    code, row = codes.get(dtype), codes.get(row_dtype)
+    if code is None:
+        raise TypeError("unsupported cache dtype %s" % dtype)
+    if row is None or row > 2:
         raise TypeError("the rows of a paged cache are float16 or bfloat16 (got %s)" % row_dtype)
-    if name in ("float16", "bfloat16") and k_cache.dtype != row_dtype:
-        raise ValueError("a 16-bit cache has the rows' dtype %s (got %s)" % (row_dtype, k_cache.dtype))
-    if v_cache.dtype != k_cache.dtype or v_cache.shape != k_cache.shape or v_cache.device != dev:
-        raise ValueError("v_cache must be a %s tensor of shape %s on %s" % (k_cache.dtype, tuple(k_cache.shape), dev))
-    num_pages, _, page_size, hd = k_cache.shape
-    for what, sc in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if name.startswith("float8") and sc is None:
-            raise ValueError("an 8-bit cache needs %s" % what)
-        if sc is not None and (sc.dtype != torch.float32 or tuple(sc.shape) != (num_pages, Hkv) or sc.device != dev):
-            raise ValueError("%s must be an fp32 tensor of shape %s on %s" % (what, (num_pages, Hkv), dev))
+    if code <= 2 and code != row:
+        raise ValueError("a 16-bit cache has the rows' dtype %s (got %s)" % (row_dtype, dtype))
+    if v_cache.dtype != dtype or v_cache.shape != shape or v_cache.device != dev:
+        raise ValueError("v_cache must be a %s tensor of shape %s on %s" % (dtype, tuple(shape), dev))
+    if code > 2 or k_scale is not None or v_scale is not None:
+        for what, sc in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if sc is None:
+                if code > 2:
+                    raise ValueError("an 8-bit cache needs %s" % what)
+            elif sc.dtype != torch.float32 or sc.shape != shape[:2] or sc.device != dev or not sc.is_contiguous():
+                raise ValueError("%s must be a contiguous fp32 tensor of shape %s on %s" % (what, tuple(shape[:2]), dev))
     if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.device != dev:
         raise ValueError("page_table must be an int32 tensor [batch, max_pages] on %s" % dev)
-    _contig(k_cache, v_cache, k_scale, v_scale, page_table)
-    if dev.type != "cuda":
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous() and page_table.is_contiguous()):
+        raise ValueError("tensors must be contiguous")
+    if not k_cache.is_cuda:
         raise ValueError("the library takes CUDA tensors; k_cache is on %s" % dev)
-    return _PAGED_DT[name], num_pages, page_size, hd, page_table.shape[0], page_table.shape[1]
+    B, most = page_table.shape
+    return row, code, shape[0], shape[2], shape[3], B, most
 
 
 def _int_row(what, t, n, device):
-    if t.dtype != _torch().int32 or tuple(t.shape) != (n,) or not t.is_contiguous() or t.device != device:
+    if t.dtype != _torch().int32 or t.shape != (n,) or t.device != device or not t.is_contiguous():
         raise ValueError("%s must be a contiguous int32 tensor of shape %s on %s" % (what, (n,), device))
 
 
 def _rows(what, t, n, width, dtype, device):
     """Row stride of [n, width] rows whose elements are contiguous."""
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != (n, width):
+    if t.dtype != dtype or t.device != device or t.shape != (n, width):
         raise ValueError("%s must be a %s tensor of shape %s on %s (got %s %s on %s)" % (what, dtype, (n, width), device,
                                                                                      t.dtype, tuple(t.shape), t.device))
-    if n > 0 and (t.stride(1) != 1 or (n > 1 and t.stride(0) < width)):
+    if n <= 1:
+        if n and t.stride(1) != 1:
+            raise ValueError("%s must have contiguous rows that do not overlap" % what)
+        return width
+    stride, one = t.stride()
+    if one != 1 or stride < width:
         raise ValueError("%s must have contiguous rows that do not overlap" % what)
-    return t.stride(0) if n > 1 else width
+    return stride
+
+
+def _like(what, t, shape, dtype, device):
+    """Checks an output that the caller gave."""
+    if t is not None and (t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous()):
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s" % (what, dtype, tuple(shape), device))
 
 
 def attn_paged_append(k, v, k_cache, v_cache, page_table, lengths, cu_new, *, H, Hkv, k_scale=None, v_scale=None,
@@ -721,31 +730,35 @@ def attn_paged_append(k, v, k_cache, v_cache, page_table, lengths, cu_new, *, H,
     [batch, max_pages].  rope_theta None: no turn.  With q [rows, H*hd] the queries are
     turned too, into q_out (made if not given); returns q_out or None.  Rows in no sequence
     and rows of a padding slot (length 0) are left alone."""
-    torch = _torch()
-    cd, num_pages, page_size, hd, B, max_pages = _pools(k_cache, v_cache, k_scale, v_scale, page_table, Hkv, k.dtype)
-    dev, n = k_cache.device, k.shape[0]
-    ks, vs = _rows("k", k, n, Hkv * hd, k.dtype, dev), _rows("v", v, n, Hkv * hd, k.dtype, dev)
+    rd, cd, num_pages, page_size, hd, B, max_pages = _pools(k_cache, v_cache, k_scale, v_scale, page_table, Hkv, k.dtype)
+    dev, n, dtype = k_cache.device, k.shape[0], k.dtype
+    ks, vs = _rows("k", k, n, Hkv * hd, dtype, dev), _rows("v", v, n, Hkv * hd, dtype, dev)
     _int_row("lengths", lengths, B, dev)
     _int_row("cu_new", cu_new, B + 1, dev)
     qs = 0
     if q is not None:
-        qs = _rows("q", q, n, H * hd, k.dtype, dev)
-        if q_out is not None and (q_out.dtype != k.dtype or q_out.device != dev or tuple(q_out.shape) != (n, H * hd) or
-                                  not q_out.is_contiguous()):
-            raise ValueError("q_out must be a contiguous %s tensor of shape %s on %s" % (k.dtype, (n, H * hd), dev))
+        qs = _rows("q", q, n, H * hd, dtype, dev)
+        _like("q_out", q_out, (n, H * hd), dtype, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
     if rope_theta is not None and not rope_theta > 0:
         raise ValueError("rope_theta must be positive (None: no turn)")
-    with _On(dev, stream) as handle:
-        if q is not None and q_out is None:
-            q_out = torch.empty((n, H * hd), dtype=k.dtype, device=dev)
-        st = lib().attn_paged_append(_dt(k), cd, _ptr(k), ks, _ptr(v), vs, _ptr(q), qs, _ptr(q_out), _ptr(k_cache),
-                                     _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(cu_new), _ptr(lengths),
-                                     _ptr(page_table), B, n, num_pages, page_size, max_pages, H, Hkv, hd,
-                                     float(rope_theta or 0.0), handle)
+    handle, context = _on(dev, stream)
+
+    def call():
+        out = _torch().empty((n, H * hd), dtype=dtype, device=dev) if q is not None and q_out is None else q_out
+        return out, lib().attn_paged_append(rd, cd, k.data_ptr(), ks, v.data_ptr(), vs, _addr(q), qs, _addr(out),
+                                            k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale),
+                                            cu_new.data_ptr(), lengths.data_ptr(), page_table.data_ptr(), B, n, num_pages,
+                                            page_size, max_pages, H, Hkv, hd, rope_theta or 0.0, handle)
+
+    if context is None:
+        out, st = call()
+    else:
+        with context:
+            out, st = call()
     _check(st, "attn_paged_append")
-    return q_out
+    return out
 
 
 def attn_paged_decode_workspace_size(B, Lq, H, Hkv, hd) -> int:
@@ -760,30 +773,40 @@ def attn_paged_decode(q, k_cache, v_cache, page_table, lengths, *, H, Hkv, k_sca
     (o, lse).  The launch does not depend on the lengths: a captured graph can be replayed
     as they, the table and the pages change."""
     torch = _torch()
-    if q.dim() != 3 or q.shape[2] % H:
-        raise ValueError("q must be [batch, Lq, H*hd]")
-    cd, num_pages, page_size, hd, B, max_pages = _pools(k_cache, v_cache, k_scale, v_scale, page_table, Hkv, q.dtype)
-    dev, Lq = k_cache.device, q.shape[1]
-    if tuple(q.shape) != (B, Lq, H * hd) or q.device != dev:
-        raise ValueError("q must have shape %s on %s (got %s on %s)" % ((B, Lq, H * hd), dev, tuple(q.shape), q.device))
-    _contig(q, o, lse, workspace)
+    rd, cd, num_pages, page_size, hd, B, max_pages = _pools(k_cache, v_cache, k_scale, v_scale, page_table, Hkv, q.dtype)
+    dev = k_cache.device
+    Lq = q.shape[1] if q.dim() == 3 else -1
+    if q.shape != (B, Lq, H * hd) or q.device != dev:
+        raise ValueError("q must have shape [%d, Lq, %d] on %s (got %s on %s)" % (B, H * hd, dev, tuple(q.shape), q.device))
+    if not q.is_contiguous():
+        raise ValueError("tensors must be contiguous")
     _int_row("lengths", lengths, B, dev)
-    _placed(q, like_q=[("o", o)], f32=[("lse", lse, (B, H, Lq))], device=[("workspace", workspace)])
-    with _On(dev, stream) as handle:
-        if o is None:
-            o = torch.empty_like(q)
-        if lse is None and want_lse:
-            lse = torch.empty((B, H, Lq), dtype=torch.float32, device=dev)
-        if workspace is None:
-            nbytes = lib().attn_paged_decode_workspace_size(B, Lq, H, Hkv, hd)
-            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
-        st = lib().attn_paged_decode(_dt(q), cd, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-                                     _ptr(o), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                     _ptr(lengths), _ptr(page_table), B, Lq, num_pages, page_size, max_pages, H, Hkv,
-                                     hd, 1.0 / math.sqrt(hd) if scale is None else float(scale), int(bool(causal)),
-                                     int(window), float(softcap), handle)
+    _like("o", o, q.shape, q.dtype, dev)
+    _like("lse", lse, (B, H, Lq), torch.float32, dev)
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError("workspace must be contiguous and on %s" % dev)
+    handle, context = _on(dev, stream)
+    L = lib()
+
+    def call():
+        out = torch.empty_like(q) if o is None else o
+        sums = torch.empty((B, H, Lq), dtype=torch.float32, device=dev) if lse is None and want_lse else lse
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(L.attn_paged_decode_workspace_size(B, Lq, H, Hkv, hd), dtype=torch.uint8, device=dev)
+        return out, sums, L.attn_paged_decode(rd, cd, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale),
+                                              _addr(v_scale), out.data_ptr(), _addr(sums), ws.data_ptr(), ws.nbytes,
+                                              lengths.data_ptr(), page_table.data_ptr(), B, Lq, num_pages, page_size,
+                                              max_pages, H, Hkv, hd, hd ** -0.5 if scale is None else scale,
+                                              1 if causal else 0, window, softcap, handle)
+
+    if context is None:
+        out, sums, st = call()
+    else:
+        with context:
+            out, sums, st = call()
     _check(st, "attn_paged_decode")
-    return o, lse
+    return out, sums
 
 
 def attn_paged_gather(k_cache, v_cache, page_table, cu_seqlens, total, *, Hkv, dtype, k_scale=None, v_scale=None,
@@ -793,20 +816,25 @@ def attn_paged_gather(k_cache, v_cache, page_table, cu_seqlens, total, *, Hkv, d
     given.  For attention of long query blocks over cached tokens: attn_fwd with q_offset
     takes one sequence's rows.  Rows in no sequence are left as they were."""
     torch = _torch()
-    cd, num_pages, page_size, hd, B, max_pages = _pools(k_cache, v_cache, k_scale, v_scale, page_table, Hkv, dtype)
-    dev, total = k_cache.device, int(total)
+    rd, cd, num_pages, page_size, hd, B, max_pages = _pools(k_cache, v_cache, k_scale, v_scale, page_table, Hkv, dtype)
+    dev, shape = k_cache.device, (int(total), Hkv * hd)
     _int_row("cu_seqlens", cu_seqlens, B + 1, dev)
-    for what, t in (("k_out", k_out), ("v_out", v_out)):
-        if t is not None and (t.dtype != dtype or t.device != dev or tuple(t.shape) != (total, Hkv * hd) or
-                              not t.is_contiguous()):
-            raise ValueError("%s must be a contiguous %s tensor of shape %s on %s" % (what, dtype, (total, Hkv * hd), dev))
-    with _On(dev, stream) as handle:
-        if k_out is None:
-            k_out = torch.empty((total, Hkv * hd), dtype=dtype, device=dev)
-        if v_out is None:
-            v_out = torch.empty((total, Hkv * hd), dtype=dtype, device=dev)
-        st = lib().attn_paged_gather(_DT[_name(dtype)], cd, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-                                     _ptr(k_out), _ptr(v_out), _ptr(cu_seqlens), _ptr(page_table), B, total, num_pages,
-                                     page_size, max_pages, Hkv, hd, handle)
+    _like("k_out", k_out, shape, dtype, dev)
+    _like("v_out", v_out, shape, dtype, dev)
+    handle, context = _on(dev, stream)
+
+    def call():
+        ko = torch.empty(shape, dtype=dtype, device=dev) if k_out is None else k_out
+        vo = torch.empty(shape, dtype=dtype, device=dev) if v_out is None else v_out
+        return ko, vo, lib().attn_paged_gather(rd, cd, k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale),
+                                               _addr(v_scale), ko.data_ptr(), vo.data_ptr(), cu_seqlens.data_ptr(),
+                                               page_table.data_ptr(), B, shape[0], num_pages, page_size, max_pages, Hkv,
+                                               hd, handle)
+
+    if context is None:
+        ko, vo, st = call()
+    else:
+        with context:
+            ko, vo, st = call()
     _check(st, "attn_paged_gather")
-    return k_out, v_out
+    return ko, vo

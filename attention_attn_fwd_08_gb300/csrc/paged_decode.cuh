@@ -33,6 +33,7 @@
 
 #include <math.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "paged.cuh"
@@ -48,10 +49,9 @@ constexpr int kMaxCtasPerSm = 3;
 constexpr int kMaxCtas = kSms * kMaxCtasPerSm;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Bytes of workspace: a record for each CTA, then two slots of R partial rows for each (a
-// CTA's stretch can begin in the middle of one item and end in the middle of another).
-__host__ __device__ inline size_t ws_ml_offset() { return (size_t)kMaxCtas * 16; }
-__host__ __device__ inline size_t ws_o_offset(int R) { return ws_ml_offset() + ((size_t)kMaxCtas * 2 * R * 8 + 15) / 16 * 16; }
+// Bytes of workspace: (m, l), then O, of two slots of R partial rows for each CTA (a stretch
+// can begin in the middle of one item and end in the middle of another).
+__host__ __device__ inline size_t ws_o_offset(int R) { return (size_t)kMaxCtas * 2 * R * 8; }
 inline size_t ws_bytes(int R, int hd) { return ws_o_offset(R) + (size_t)kMaxCtas * 2 * R * hd * 4; }
 
 template <int HD, int CACHE, int RT>
@@ -153,57 +153,52 @@ __device__ __forceinline__ SeqTiles seq_tiles(const PagedParams& P, int b) {
     return s;
 }
 
-// A CTA's stretch of the tiles: begins at tile `off` of item (b, h), `count` tiles long.
-struct Stretch {
-    int b, h, off;
-    long long count, share;
+// How the tiles are dealt out: `all` of them, `share` to a CTA.
+struct Deal {
+    long long all, share;
 };
-
-// Every thread sums its sequences' tiles; the thread whose sequences hold the stretch's
-// first tile finds it.
-__device__ __forceinline__ Stretch find_stretch(const PagedParams& P, Stretch* out, long long* sums) {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int per = (P.B + kDecThreads - 1) / kDecThreads;
-    const int b0 = min(P.B, tid * per), b1 = min(P.B, b0 + per);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += seq_tiles(P, b).n;
-    long long incl = mine;
+// Sums over all sequences, by each warp for itself (no barrier; 32 loads in flight).
+__device__ __forceinline__ Deal deal_tiles(const PagedParams& P, int ctas) {
+    const int lane = threadIdx.x & 31;
+    long long sum = 0;
+#pragma unroll 4
+    for (int b = lane; b < P.B; b += 32) sum += seq_tiles(P, b).n;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
-    }
-    if (lane == 31) sums[warp] = incl;
-    if (tid == 0) out->count = 0;
-    __syncthreads();
-    long long before = 0, total = 0;
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    Deal d;
+    d.all = sum * P.Hkv;
+    d.share = (d.all + ctas - 1) / ctas;
+    return d;
+}
+// Tile number x < all: tile `off` of the `n` of item (b, h).
+struct Place {
+    int b, h, off, n;
+};
+__device__ __forceinline__ Place place_of(const PagedParams& P, long long x) {
+    const int lane = threadIdx.x & 31;
+    for (int base = 0;; base += 32) {
+        const int b = base + lane;
+        const int n = b < P.B ? seq_tiles(P, b).n : 0;
+        long long incl = n;
 #pragma unroll
-    for (int w = 0; w < kDecThreads / 32; ++w) {
-        if (w < warp) before += sums[w];
-        total += sums[w];
-    }
-    const long long all = total * P.Hkv, share = (all + gridDim.x - 1) / gridDim.x;
-    const long long first = (long long)blockIdx.x * share;
-    const long long lo = (before + incl - mine) * P.Hkv, hi = (before + incl) * P.Hkv;
-    if (first < all && first >= lo && first < hi) {
-        long long at = first - lo;
-        int b = b0;
-        for (;; ++b) {
-            const int n = seq_tiles(P, b).n;
-            if (at < (long long)n * P.Hkv) {
-                out->b = b;
-                out->h = (int)(at / n);
-                out->off = (int)(at % n);
-                break;
-            }
-            at -= (long long)n * P.Hkv;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
         }
-        out->count = min(share, all - first);
+        const unsigned after = __ballot_sync(0xffffffffu, incl * P.Hkv > x);
+        if (after) {
+            const int at = __ffs(after) - 1;
+            Place p;
+            p.b = base + at;
+            p.n = __shfl_sync(0xffffffffu, n, at);
+            const long long in = x - (__shfl_sync(0xffffffffu, incl, at) - p.n) * P.Hkv;
+            p.h = (int)(in / p.n);
+            p.off = (int)(in % p.n);
+            return p;
+        }
+        x -= __shfl_sync(0xffffffffu, incl, 31) * P.Hkv;
+        if (base + 32 >= P.B) return Place{0, 0, 0, 0};  // (x was not below all)
     }
-    __syncthreads();
-    Stretch s = *out;
-    s.share = share;
-    return s;
 }
 // the next item with tiles
 __device__ __forceinline__ void next_item(const PagedParams& P, int& b, int& h) {
@@ -231,8 +226,6 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
     __shared__ __align__(8) uint64_t bars[2 * S::kStages];
     __shared__ float2 meta[S::kStages][4];  // scales of the tile's groups of 16 keys
     __shared__ int there[S::kStages];       // groups that were loaded
-    __shared__ Stretch stretch;
-    __shared__ long long sums[kDecThreads / 32];
     __shared__ int abort_flag;
     const uint32_t ring = smem_u32(smem);
     auto full_bar = [&](int s) { return smem_u32(bars + s); };
@@ -242,13 +235,21 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
-            mbar_init(full_bar(s), 1);
+            mbar_init(full_bar(s), k8 ? 2 : 1);  // the tile's bytes; over 8-bit pools, its scales
             mbar_init(empty_bar(s), 4);
         }
         abort_flag = 0;
         fence_barrier_init();
     }
-    const Stretch st = find_stretch(P, &stretch, sums);  // its barriers publish the above
+    const Deal deal = deal_tiles(P, gridDim.x);
+    __syncthreads();  // publishes the barriers
+    // the merging kernel's CTAs may come up from here on (all of this kernel's are running)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const long long first = min(deal.all, (long long)blockIdx.x * deal.share);
+    long long left = min(deal.share, deal.all - first);
+    Place at = {0, 0, 0, 0};
+    if (left > 0) at = place_of(P, first);
+    int b = at.b, h = at.h, off = at.off;
 
     if (warp == 4) {
         // ------------------------------------------------------------- producer
@@ -262,8 +263,6 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
         // this lane's box of a tile
         const int sub = lane % subs, bx = (lane / subs) % S::kBoxes, is_v = lane / subs / S::kBoxes;
         const bool has_box = is_v < 2;
-        int b = st.b, h = st.h, off = st.off;
-        long long left = st.count;
         int stage = 0, phase = 1;  // a wait on a fresh barrier's other phase returns at once
         int made = 0;              // tiles produced, up to the ring's depth
         bool ok = true;
@@ -300,12 +299,8 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
                         ok = false;
                         break;
                     }
-                    const float2 gs = make_float2(__shfl_sync(0xffffffffu, sc.x, i * 4 + (lane & 3)),
-                                                  __shfl_sync(0xffffffffu, sc.y, i * 4 + (lane & 3)));
                     const int gp = __shfl_sync(0xffffffffu, pg, i * 4 + (lane & 3));
                     const unsigned have = __ballot_sync(0xffffffffu, gp >= 0) & 0xfu;
-                    if (lane < 4) meta[s][lane] = gs;
-                    if (lane == 0) there[s] = (int)have;
                     // a box's page: that of any of its groups that is wanted
                     int page = -1;
                     for (int e = 0; e < groups; ++e) {
@@ -313,16 +308,24 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
                         page = max(page, x);
                     }
                     const unsigned boxes = __ballot_sync(0xffffffffu, has_box && page >= 0);
-                    __syncwarp();
-                    if (lane == 0)
+                    if (lane == 0) {
+                        there[s] = (int)have;
                         mbar_expect_tx(full_bar(s), (uint32_t)(__popc(boxes) * box_rows * S::kRowBytes));
+                    }
                     __syncwarp();
                     if (has_box && page >= 0) {
                         const uint32_t dst = ring + (uint32_t)(s * S::kStageBytes + is_v * S::kTileBytes +
                                                                bx * kKeys * S::kRowBytes + sub * box_rows * S::kRowBytes);
-                        const int row = (int)(((long long)(sq.t0 + off + base + i) * kKeys + sub * box_rows) & (P.page_size - 1));
+                        const int row = ((sq.t0 + off + base + i) * kKeys + sub * box_rows) & (P.page_size - 1);
                         const int y = ((page * P.Hkv + h) << P.page_shift) + row;
                         tma_load_2d(dst, is_v ? &tmV : &tmK, full_bar(s), bx * (S::kRowBytes / S::kEs), y, pol);
+                    }
+                    if constexpr (k8) {
+                        const float2 gs = make_float2(__shfl_sync(0xffffffffu, sc.x, i * 4 + (lane & 3)),
+                                                      __shfl_sync(0xffffffffu, sc.y, i * 4 + (lane & 3)));
+                        if (lane < 4) meta[s][lane] = gs;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(full_bar(s));
                     }
                     made = min(made + 1, S::kStages);
                     if (++stage == S::kStages) stage = 0, phase ^= 1;
@@ -346,11 +349,8 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
     // ---------------------------------------------------------------- consumers
     const int g = lane >> 2, t = lane & 3, mi = lane >> 3, ri = lane & 7;
     const int tid = threadIdx.x;
-    float* ws_ml = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(P.ws) + ws_ml_offset());
+    float2* ws_ml = reinterpret_cast<float2*>(P.ws);
     float* ws_o = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(P.ws) + ws_o_offset(R));
-    int4 record = make_int4(-1, 0, 0, 0);
-    int b = st.b, h = st.h, off = st.off;
-    long long left = st.count;
     int stage = 0, phase = 0;
     bool ok = true;
     // this thread's places in a tile: its K row's chunk, its V rows' chunks, its rows of P
@@ -575,58 +575,40 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
 
             // ---- O += P V for this warp's quarter of the columns, two groups of 16 keys at a time
             const uint32_t paddr = smem_u32(ps) + (buf * S::kRows + (mi & 1) * 8 + ri) * S::kPPitch + (mi >> 1) * 16;
-#pragma unroll
-            for (int kp = 0; kp < 4; kp += 2) {
-                uint32_t pa[2][RT][4], keep[2][2];
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
-                        ldsm_x4(paddr + rt * 16 * S::kPPitch + (kp + y) * 32, pa[y][rt][0], pa[y][rt][1], pa[y][rt][2],
-                                pa[y][rt][3]);
-                    if constexpr (!kFull) {
-                        // keys that no row sees: their bytes may be anything
-                        auto seen = [&](int k) {
-                            const int j = j0 + (kp + y) * 16 + k;
-                            return j >= sq.lo && j < sq.hi && ((have >> (kp + y)) & 1);
-                        };
-                        keep[y][0] = (seen(2 * t) ? 0xffffu : 0u) | (seen(2 * t + 1) ? 0xffff0000u : 0u);
-                        keep[y][1] = (seen(2 * t + 8) ? 0xffffu : 0u) | (seen(2 * t + 9) ? 0xffff0000u : 0u);
-                    }
-                }
-#pragma unroll
-                for (int c = 0; c < S::kN; c += 2) {
-                    uint32_t vb[2][2][2];  // [group][8-column product][fragment half]
-                    if constexpr (k8) {
-                        // 16 columns: even ones are product c, odd ones c + 1
-                        uint32_t r[2][2];
-                        ldsm_x4_t(base + v_off[c / 2] + kp * 16 * S::kRowBytes, r[0][0], r[0][1], r[1][0], r[1][1]);
-#pragma unroll
-                        for (int y = 0; y < 2; ++y)
-#pragma unroll
-                            for (int z = 0; z < 2; ++z) codes_v<CACHE>(r[y][z], vb[y][0][z], vb[y][1][z]);
-                    } else {
-#pragma unroll
-                        for (int y = 0; y < 2; ++y)
-                            ldsm_x4_t(base + v_off[c / 2] + (kp + y) * 16 * S::kRowBytes, vb[y][0][0], vb[y][0][1],
-                                      vb[y][1][0], vb[y][1][1]);
-                    }
+            auto load_v = [&](int kp, int c, uint32_t (&vb)[2][2][2]) {  // [group][8-column product][fragment half]
+                if constexpr (k8) {
+                    // 16 columns: even ones are product c, odd ones c + 1
+                    uint32_t r[2][2];
+                    ldsm_x4_t(base + v_off[c / 2] + kp * 16 * S::kRowBytes, r[0][0], r[0][1], r[1][0], r[1][1]);
 #pragma unroll
                     for (int y = 0; y < 2; ++y)
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            bool apart = false;
-                            if constexpr (!kFull) {
-                                vb[y][x][0] &= keep[y][0];
-                                vb[y][x][1] &= keep[y][1];
-                                // a value that is not finite may be one row's and not another's: its key by itself
-                                constexpr uint32_t kInf = kMmaBf ? 0x7f80u : 0x7c00u;
-                                auto wild = [&](uint32_t w) {
-                                    return (w & kInf) == kInf || ((w >> 16) & kInf) == kInf;
-                                };
-                                apart = __any_sync(0xffffffffu, wild(vb[y][x][0]) || wild(vb[y][x][1]));
-                            }
-                            if (!apart) {
+                        for (int z = 0; z < 2; ++z) codes_v<CACHE>(r[y][z], vb[y][0][z], vb[y][1][z]);
+                } else {
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        ldsm_x4_t(base + v_off[c / 2] + (kp + y) * 16 * S::kRowBytes, vb[y][0][0], vb[y][0][1],
+                                  vb[y][1][0], vb[y][1][1]);
+                }
+            };
+            if constexpr (kFull) {
+#pragma unroll
+                for (int kp = 0; kp < 4; kp += 2) {
+                    uint32_t pa[2][RT][4];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt)
+                            ldsm_x4(paddr + rt * 16 * S::kPPitch + (kp + y) * 32, pa[y][rt][0], pa[y][rt][1],
+                                    pa[y][rt][2], pa[y][rt][3]);
+#pragma unroll
+                    for (int c = 0; c < S::kN; c += 2) {
+                        uint32_t vb[2][2][2];
+                        load_v(kp, c, vb);
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x)
 #pragma unroll
                                 for (int rt = 0; rt < RT; ++rt) {
                                     float d[4];
@@ -636,29 +618,81 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
                                     o[rt][c + x][2] = fmaf(f[rt][1][kp + y], d[2], o[rt][c + x][2]);
                                     o[rt][c + x][3] = fmaf(f[rt][1][kp + y], d[3], o[rt][c + x][3]);
                                 }
-                            } else {
+                    }
+                }
+            } else {
+                // Keys that no row sees may hold any bytes: they are masked out of V.  A value
+                // that is not finite may be seen by one row and not by another, whose P of 0 would
+                // not keep it out of a product: such a tile goes through one key of each group at a
+                // time, and a row takes the products of the keys that it sees.
+                auto keep_of = [&](int k, int y) {  // halves of group y's fragment words: keys k + 2t, k + 2t + 1
+                    const int j = j0 + y * 16 + k + 2 * t;
+                    const bool in = (have >> y) & 1;
+                    return (in && j >= sq.lo && j < sq.hi ? 0xffffu : 0u) |
+                           (in && j + 1 >= sq.lo && j + 1 < sq.hi ? 0xffff0000u : 0u);
+                };
+                bool wild = false;
 #pragma unroll 1
-                                for (int k = 0; k < 16; ++k) {
-                                    const uint32_t one = (k & 1) ? 0xffff0000u : 0xffffu;
-                                    const bool mine = ((k & 7) >> 1) == t;
-                                    const uint32_t b0 = mine && k < 8 ? vb[y][x][0] & one : 0u;
-                                    const uint32_t b1 = mine && k >= 8 ? vb[y][x][1] & one : 0u;
-                                    const int j = j0 + (kp + y) * 16 + k;
+                for (int kp = 0; kp < 4; kp += 2) {
+                    const uint32_t keep[2][2] = {{keep_of(0, kp), keep_of(8, kp)}, {keep_of(0, kp + 1), keep_of(8, kp + 1)}};
+#pragma unroll
+                    for (int c = 0; c < S::kN; c += 2) {
+                        uint32_t vb[2][2][2];
+                        load_v(kp, c, vb);
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                                for (int z = 0; z < 2; ++z) {
+                                    constexpr uint32_t kInf = kMmaBf ? 0x7f80u : 0x7c00u;
+                                    const uint32_t w = vb[y][x][z] & keep[y][z];
+                                    wild |= (w & kInf) == kInf || ((w >> 16) & kInf) == kInf;
+                                }
+                    }
+                }
+                wild = __any_sync(0xffffffffu, wild);
+#pragma unroll 1
+                for (int k = wild ? 0 : 16; k < (wild ? 16 : 17); ++k) {
+                    // k = 16: all keys at once; below: key k of each group
+                    const uint32_t one = (k & 1) ? 0xffff0000u : 0xffffu;
+                    const uint32_t lo8 = k == 16 ? 0xffffffffu : (k < 8 && (k >> 1) == t ? one : 0u);
+                    const uint32_t hi8 = k == 16 ? 0xffffffffu : (k >= 8 && ((k - 8) >> 1) == t ? one : 0u);
+#pragma unroll
+                    for (int kp = 0; kp < 4; kp += 2) {
+                        uint32_t pa[2][RT][4];
+                        bool takes[2][RT][2];
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+#pragma unroll
+                            for (int rt = 0; rt < RT; ++rt) {
+                                ldsm_x4(paddr + rt * 16 * S::kPPitch + (kp + y) * 32, pa[y][rt][0], pa[y][rt][1],
+                                        pa[y][rt][2], pa[y][rt][3]);
+                                const int j = j0 + (kp + y) * 16 + k;
+#pragma unroll
+                                for (int r = 0; r < 2; ++r) takes[y][rt][r] = k == 16 || (j >= vlo[rt][r] && j < vhi[rt][r]);
+                            }
+                        const uint32_t keep[2][2] = {{keep_of(0, kp) & lo8, keep_of(8, kp) & hi8},
+                                                     {keep_of(0, kp + 1) & lo8, keep_of(8, kp + 1) & hi8}};
+#pragma unroll
+                        for (int c = 0; c < S::kN; c += 2) {
+                            uint32_t vb[2][2][2];
+                            load_v(kp, c, vb);
+#pragma unroll
+                            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                                for (int x = 0; x < 2; ++x)
 #pragma unroll
                                     for (int rt = 0; rt < RT; ++rt) {
                                         float d[4];
-                                        mma_zero<kMmaBf>(d, pa[y][rt], b0, b1);
+                                        mma_zero<kMmaBf>(d, pa[y][rt], vb[y][x][0] & keep[y][0], vb[y][x][1] & keep[y][1]);
 #pragma unroll
-                                        for (int r = 0; r < 2; ++r)
-                                            if (j >= vlo[rt][r] && j < vhi[rt][r]) {
-                                                o[rt][c + x][2 * r] = fmaf(f[rt][r][kp + y], d[2 * r], o[rt][c + x][2 * r]);
-                                                o[rt][c + x][2 * r + 1] =
-                                                    fmaf(f[rt][r][kp + y], d[2 * r + 1], o[rt][c + x][2 * r + 1]);
-                                            }
+                                        for (int e = 0; e < 4; ++e)
+                                            if (takes[y][rt][e >> 1])
+                                                o[rt][c + x][e] = fmaf(f[rt][e >> 1][kp + y], d[e], o[rt][c + x][e]);
                                     }
-                                }
-                            }
                         }
+                    }
                 }
             }
         };
@@ -678,11 +712,6 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
         const bool begins = off == 0, ends = off + n == sq.n;
         const bool whole = begins && ends;
         const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
-        if (begins && !ends) {
-            // the CTAs after this one that hold the rest of the item: the stretch ends here
-            const long long rest = sq.n - n;
-            record = make_int4(b, h, (int)((rest + st.share - 1) / st.share), 0);
-        }
         if (ok) {
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
@@ -726,7 +755,7 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
                                 P.lse[((long long)b * P.H + hq) * P.Lq + lq] =
                                     none ? -INFINITY : (M[rt][e] + log2f(L[rt][e])) * 0.6931471805599453f;
                         } else {
-                            reinterpret_cast<float2*>(ws_ml)[(long long)slot * R + r] = make_float2(M[rt][e], L[rt][e]);
+                            ws_ml[(long long)slot * R + r] = make_float2(M[rt][e], L[rt][e]);
                         }
                     }
                 }
@@ -735,8 +764,6 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
         off = 0;
         if (left > 0) next_item(P, b, h);
     }
-    if (tid == 0) reinterpret_cast<int4*>(P.ws)[blockIdx.x] = record;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // sequences of which no row sees a key
     for (int e = blockIdx.x; e < P.B; e += gridDim.x) {
@@ -750,43 +777,54 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
 }
 
 // Merges the partial rows of the items that stretches cut: CTA (c, y) those of the item
-// that begins in stretch c and does not end in it, eight rows of it (or fewer rows with
-// several warps each).  The order of the sums is that of the stretches.
+// that begins in stretch c and does not end in it, eight rows of it (fewer rows get several
+// warps each).  It finds its item from the lengths while the split kernel still runs.  The
+// order of the sums is that of the stretches.
 template <int HD>
 __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams P, const int rows_bf16) {
     constexpr int kPer = HD / 32;  // columns of a lane
     __shared__ float part[8][HD];
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the split kernel's results are there
-    const int4 rec = reinterpret_cast<const int4*>(P.ws)[blockIdx.x];
-    if (rec.x < 0) return;
+    const Deal deal = deal_tiles(P, gridDim.x);
+    const long long first = (long long)blockIdx.x * deal.share, last = min(deal.all, first + deal.share) - 1;
+    Place at = {0, 0, 0, 0};
+    if (first <= last) at = place_of(P, last);
+    // Every CTA waits for the split kernel, also those with nothing to merge: this kernel's
+    // end then stands for both.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // no tile, or the last item begins before the stretch, or ends in it
+    if (first > last || at.off > last - first || at.off == at.n - 1) return;
+    const int n = 1 + (int)((at.n - 1 - at.off + deal.share - 1) / deal.share);  // this stretch's end, the next ones' beginnings
     const int R = P.G * P.Lq;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int wpr = 8;  // warps of a row
     while (wpr > 1 && 8 / wpr < R) wpr >>= 1;
     const int r = blockIdx.y * 8 + warp / wpr, w = warp % wpr;
     const bool live = r < R;
-    const float2* ml = reinterpret_cast<const float2*>(reinterpret_cast<const uint8_t*>(P.ws) + ws_ml_offset());
+    const float2* ml = reinterpret_cast<const float2*>(P.ws);
     const float* wo = reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(P.ws) + ws_o_offset(R));
-    const int n = rec.z + 1;  // parts: this stretch's end, then the beginnings of the next ones
-    auto at = [&](int i) { return (long long)(2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * R + r; };
+    auto slot = [&](int i) { return (long long)(2 * ((int)blockIdx.x + i) + (i == 0 ? 1 : 0)) * R + r; };
     float M = -INFINITY, L = 0.f;
     float acc[kPer];
 #pragma unroll
     for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
     if (live) {
-        for (int i = lane; i < n; i += 32) M = max_nan(M, ml[at(i)].x);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
+        // 32 parts at a time, relative to the maximum so far; this warp's every wpr-th of them
         for (int base = 0; base < n; base += 32) {
             const int i = base + lane;
-            const float2 x = i < n ? ml[at(i)] : make_float2(-INFINITY, 0.f);
-            const float f = x.x == -INFINITY ? 0.f : fast_exp2(x.x - M);
-            L += f * x.y;
+            const float2 x = i < n ? ml[slot(i)] : make_float2(-INFINITY, 0.f);
             const int m = min(32, n - base);
-#pragma unroll 8
+            float mx = max_nan(M, x.x);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const float ref = mx == -INFINITY ? 0.f : mx;
+            const float alpha = fast_exp2(M - ref), f = fast_exp2(x.x - ref);
+            M = mx;
+            L = L * alpha + f * x.y;  // of this lane's parts
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) acc[e] *= alpha;
+#pragma unroll 4
             for (int j = w; j < m; j += wpr) {
-                const float fj = __shfl_sync(0xffffffffu, f, j);
-                const float* src = wo + at(base + j) * HD + lane * kPer;
+                const float* src = wo + slot(base + j) * HD + lane * kPer;
                 float y[kPer];
                 if constexpr (kPer == 2) {
                     const float2 v = *reinterpret_cast<const float2*>(src);
@@ -798,6 +836,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams P,
                         y[4 * q] = v.x, y[4 * q + 1] = v.y, y[4 * q + 2] = v.z, y[4 * q + 3] = v.w;
                     }
                 }
+                const float fj = __shfl_sync(0xffffffffu, f, j);
                 // a part whose row saw nothing holds zeros
 #pragma unroll
                 for (int e = 0; e < kPer; ++e) acc[e] = fmaf(fj, y[e], acc[e]);
@@ -816,25 +855,39 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams P,
                 for (int e = 0; e < kPer; ++e) acc[e] += part[warp + x][lane * kPer + e];
     }
     if (!live || w != 0) return;
-    const int gg = r / P.Lq, lq = r - gg * P.Lq, hq = rec.y * P.G + gg;
+    const int gg = r / P.Lq, lq = r - gg * P.Lq, hq = at.h * P.G + gg;
     const bool none = M == -INFINITY;
     const float inv = none ? 0.f : 1.f / L;
     uint32_t* od = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(P.o) +
-                                               (((long long)rec.x * P.Lq + lq) * P.H + hq) * HD + lane * kPer);
+                                               (((long long)at.b * P.Lq + lq) * P.H + hq) * HD + lane * kPer);
 #pragma unroll
     for (int e = 0; e < kPer; e += 2) {
         const float x = none ? 0.f : acc[e] * inv, y = none ? 0.f : acc[e + 1] * inv;
         od[e / 2] = rows_bf16 ? pack2<true>(x, y) : pack2<false>(x, y);
     }
     if (P.lse && lane == 0)
-        P.lse[((long long)rec.x * P.H + hq) * P.Lq + lq] = none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+        P.lse[((long long)at.b * P.H + hq) * P.Lq + lq] = none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+// Dynamic shared memory of a kernel, asked for once on each device.
+template <typename K>
+cudaError_t allow_smem(K k, int bytes, std::atomic<unsigned long long>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 template <int HD, int CACHE, int RT, bool kBf>
 cudaError_t decode_launch(const PagedParams& p, bool bf16, const PagedMaps& maps, cudaStream_t s) {
     using S = DecShape<HD, CACHE, RT>;
     auto k = paged_split_kernel<HD, CACHE, RT, kBf>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+    static std::atomic<unsigned long long> done{0};
+    cudaError_t e = allow_smem(k, S::kBytes, done);
     if (e != cudaSuccess) return e;
     constexpr int kGrid = kSms * S::kCtas;
     k<<<kGrid, kDecThreads, S::kBytes, s>>>(p, bf16 ? 1 : 0, maps.k, maps.v);

@@ -203,7 +203,7 @@ def _on_gpu_shapes(call, c, **kw):
 
     def pools(k_cache, v_cache, k_scale, v_scale, page_table, n, dtype):
         num, _, size, d = k_cache.shape
-        return 2, num, size, d, page_table.shape[0], page_table.shape[1]
+        return 2, 2, num, size, d, page_table.shape[0], page_table.shape[1]
 
     A._pools = pools
     try:
