@@ -48,6 +48,12 @@ constexpr int kSms = 152;
 constexpr int kMaxCtasPerSm = 3;
 constexpr int kMaxCtas = kSms * kMaxCtasPerSm;
 constexpr float kLog2e = 1.4426950408889634f;
+// p = 2^(score - ref) with ref kBias below the largest score when it is set.  In the usual
+// tile p is multiplied by its group's vs / vref before it is rounded: with that ratio at least
+// kRatioLo, fp16's finest step (2^-24) lies 2^-24 or more below the largest p's product, as
+// without a scale; with it at most kRatioHi, scores may pass the reference's by 2^4 before the
+// product leaves fp16's range (2^kTopLog2 is half of its largest value) and the reference moves.
+constexpr float kBias = 6.f, kTopLog2 = 15.f, kRatioLo = 1.f / 64, kRatioHi = 32.f;
 
 // Bytes of workspace: (m, l), then O, of two slots of R partial rows for each CTA (a stretch
 // can begin in the middle of one item and end in the middle of another).
@@ -67,7 +73,7 @@ struct DecShape {
     static constexpr int kPPitch = kKeys * 2 + 16;
     static constexpr int kQBytes = kRows * kQPitch;
     static constexpr int kPBytes = 2 * kRows * kPPitch;
-    static constexpr int kMlBytes = 2 * kRows * 4 * 8;  // two buffers of (m, l) by row and warp
+    static constexpr int kMlBytes = 2 * kRows * 4 * 4;  // two buffers of a number by row and warp
     static constexpr int kFixed = kQBytes + kPBytes + kMlBytes + kRows * 4 + 2048;  // + row scales, alignment, barriers
     // the most CTAs of an SM whose ring keeps at least three tiles each; the ring's depth
     static constexpr int stages(int ctas) {
@@ -221,11 +227,13 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* qs = smem + S::kStages * S::kStageBytes;
     uint8_t* ps = qs + S::kQBytes;
-    float2* mls = reinterpret_cast<float2*>(ps + S::kPBytes);                 // [2][rows][4]
-    float* qscale = reinterpret_cast<float*>(mls + 2 * S::kRows * 4);         // [rows]
+    float* maxima = reinterpret_cast<float*>(ps + S::kPBytes);  // [2][rows][4]
+    float* qscale = maxima + 2 * S::kRows * 4;                  // [rows]
     __shared__ __align__(8) uint64_t bars[2 * S::kStages];
-    __shared__ float2 meta[S::kStages][4];  // scales of the tile's groups of 16 keys
-    __shared__ int there[S::kStages];       // groups that were loaded
+    __shared__ float4 meta[S::kStages][4];  // of the tile's groups of 16 keys: ks, vs / vref, its log2, its inverse
+    __shared__ float vrefs[S::kStages];
+    __shared__ int there[S::kStages];  // bits 0-3: groups that were loaded; bit 4: scales out of the usual
+    __shared__ int raised[2];          // the last tile (as the CTA counts them) with a score too high
     __shared__ int abort_flag;
     const uint32_t ring = smem_u32(smem);
     auto full_bar = [&](int s) { return smem_u32(bars + s); };
@@ -239,6 +247,7 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
             mbar_init(empty_bar(s), 4);
         }
         abort_flag = 0;
+        raised[0] = raised[1] = 0;
         fence_barrier_init();
     }
     const Deal deal = deal_tiles(P, gridDim.x);
@@ -289,27 +298,28 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
             };
             int pg = page_at(0), pg_next = page_at(1);
             float2 sc = scales_at(pg);
+            float vref = 0.f;  // scale of V that the item's O is held in: its first usable one
             for (int base = 0; base < n && ok; base += 8) {
                 const float2 sc_next = scales_at(pg_next);
                 const int pg_after = page_at(base / 8 + 2);
                 const int m = min(8, n - base);
+                const unsigned have = __ballot_sync(0xffffffffu, pg >= 0);
+                // a box's page: that of any of its groups that is wanted
+                int box = pg;
+                if (groups > 1) box = max(box, __shfl_xor_sync(0xffffffffu, box, 1));
+                if (groups > 2) box = max(box, __shfl_xor_sync(0xffffffffu, box, 2));
+                float4 mine = make_float4(0.f, 0.f, 0.f, 0.f);
+                unsigned odd = 0;
                 for (int i = 0; i < m; ++i) {
                     const int s = stage;
                     if (!warp_wait(empty_bar(s), phase, P.status, ST_DEC_WAIT, &abort_flag)) {
                         ok = false;
                         break;
                     }
-                    const int gp = __shfl_sync(0xffffffffu, pg, i * 4 + (lane & 3));
-                    const unsigned have = __ballot_sync(0xffffffffu, gp >= 0) & 0xfu;
-                    // a box's page: that of any of its groups that is wanted
-                    int page = -1;
-                    for (int e = 0; e < groups; ++e) {
-                        const int x = __shfl_sync(0xffffffffu, pg, i * 4 + (sub * groups + e));
-                        page = max(page, x);
-                    }
+                    const int page = __shfl_sync(0xffffffffu, box, i * 4 + sub * groups);
                     const unsigned boxes = __ballot_sync(0xffffffffu, has_box && page >= 0);
                     if (lane == 0) {
-                        there[s] = (int)have;
+                        if constexpr (!k8) there[s] = (int)(have >> (4 * i) & 0xfu);
                         mbar_expect_tx(full_bar(s), (uint32_t)(__popc(boxes) * box_rows * S::kRowBytes));
                     }
                     __syncwarp();
@@ -321,9 +331,22 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
                         tma_load_2d(dst, is_v ? &tmV : &tmK, full_bar(s), bx * (S::kRowBytes / S::kEs), y, pol);
                     }
                     if constexpr (k8) {
-                        const float2 gs = make_float2(__shfl_sync(0xffffffffu, sc.x, i * 4 + (lane & 3)),
-                                                      __shfl_sync(0xffffffffu, sc.y, i * 4 + (lane & 3)));
-                        if (lane < 4) meta[s][lane] = gs;
+                        if (i == 0) {  // the batch's scales, needed only now
+                            if (vref == 0.f) {
+                                const unsigned fit = __ballot_sync(0xffffffffu, pg >= 0 && sc.y > 1e-18f && sc.y < 1e18f);
+                                vref = fit ? __shfl_sync(0xffffffffu, sc.y, __ffs(fit) - 1) : 1.f;
+                            }
+                            const float ratio = sc.y / vref;
+                            // (a scale of 0, as of a block of zeros, has no logarithm: not the usual)
+                            const bool usual = pg < 0 || (sc.x > 0.f && sc.x < 1e30f && ratio >= kRatioLo && ratio <= kRatioHi);
+                            odd = __ballot_sync(0xffffffffu, !usual);
+                            mine = make_float4(sc.x, ratio, usual ? __log2f(ratio) : 0.f, 1.f / ratio);
+                        }
+                        if ((lane >> 2) == i) meta[s][lane & 3] = mine;
+                        if (lane == 0) {
+                            vrefs[s] = vref;
+                            there[s] = (int)((have >> (4 * i) & 0xfu) | ((odd >> (4 * i) & 0xfu) ? 16u : 0u));
+                        }
                         __syncwarp();
                         if (lane == 0) mbar_arrive(full_bar(s));
                     }
@@ -351,8 +374,9 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
     const int tid = threadIdx.x;
     float2* ws_ml = reinterpret_cast<float2*>(P.ws);
     float* ws_o = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(P.ws) + ws_o_offset(R));
-    int stage = 0, phase = 0;
+    int stage = 0, phase = 0, tiles = 0;
     bool ok = true;
+    float vref = 1.f;
     // this thread's places in a tile: its K row's chunk, its V rows' chunks, its rows of P
     constexpr int kBoxBytes = kKeys * S::kRowBytes;
     auto chunk = [&](int row, int c) -> uint32_t {  // of 16 bytes, as the swizzle lays them
@@ -421,7 +445,7 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
         }
         // this thread's rows 16 rt + g (e < 2) and + 8: visible keys [vlo, vhi), score factor
         int vlo[RT][2], vhi[RT][2];
-        float qf[RT][2], M[RT][2], L[RT][2];
+        float qf[RT][2], ref[RT][2];  // and the reference: p = 2^(score - ref)
         float o[RT][S::kN][4];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
@@ -431,8 +455,7 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
                 vlo[rt][e] = r < R && P.wl >= 0 ? max(0, pos - P.wl) : 0;
                 vhi[rt][e] = r < R && P.wr >= 0 ? (int)min((long long)sq.len, (long long)pos + P.wr + 1) : sq.len;
                 qf[rt][e] = P.scale * (k8 ? qscale[r] : 1.f) * (P.softcap > 0.f ? 1.f : kLog2e);
-                M[rt][e] = -INFINITY;
-                L[rt][e] = 0.f;
+                ref[rt][e] = -INFINITY;
             }
         // tiles from full_lo to full_hi on are seen whole by every row (tile_full over j0)
         const int full_lo = P.wl >= 0 ? max(0, sq.len - 1 - P.wl) : 0;
@@ -442,10 +465,16 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
 #pragma unroll
             for (int i = 0; i < S::kN; ++i) o[rt][i][0] = o[rt][i][1] = o[rt][i][2] = o[rt][i][3] = 0.f;
 
-        // One tile.  kFull: every row sees every key of it, so nothing is masked.
-        auto tile = [&](auto full_c, int j0, int have, int s, int buf) {
-            constexpr bool kFull = decltype(full_c)::value;
-            const uint32_t base = ring + (uint32_t)(s * S::kStageBytes);
+        float l[RT][2];  // this thread's part of the sums
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) l[rt][0] = l[rt][1] = 0.f;
+
+        for (int i = 0; i < n; ++i) {
+            ok = ok && mbar_wait(full_bar(stage), phase, P.status, ST_DEC_WAIT, &abort_flag);
+            __syncwarp();
+            const int j0 = (sq.t0 + off + i) * kKeys, have = there[stage], buf = i & 1;
+            const uint32_t base = ring + (uint32_t)(stage * S::kStageBytes);
+            if (k8 && i == 0) vref = vrefs[stage];
 
             // ---- S = Q K^T for this warp's 16 keys
             float sc[RT][2][4];
@@ -489,92 +518,15 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
                     }
             }
 
-            // ---- probabilities of the 16 keys relative to their own maximum
-            const float kscale = k8 ? meta[s][warp].x : 1.f;
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float c = qf[rt][r] * kscale;
-                    sc[rt][0][2 * r] *= c, sc[rt][0][2 * r + 1] *= c, sc[rt][1][2 * r] *= c, sc[rt][1][2 * r + 1] *= c;
-                }
-                if (P.softcap > 0.f) {
-#pragma unroll
-                    for (int x = 0; x < 2; ++x)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            sc[rt][x][e] = P.softcap * tanh_accurate(sc[rt][x][e] * cap_inv) * kLog2e;
-                }
-                if constexpr (!kFull) {
-#pragma unroll
-                    for (int x = 0; x < 2; ++x)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int r = e >> 1, j = j0 + warp * 16 + x * 8 + 2 * t + (e & 1);
-                            if (j < vlo[rt][r] || j >= vhi[rt][r] || !((have >> warp) & 1)) sc[rt][x][e] = -INFINITY;
-                        }
-                }
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    float mx = max_nan(max_nan(sc[rt][0][2 * r], sc[rt][0][2 * r + 1]),
-                                       max_nan(sc[rt][1][2 * r], sc[rt][1][2 * r + 1]));
-                    mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                    mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                    const float ref = mx == -INFINITY ? 0.f : mx;
-                    float sum = 0.f;
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const float p0 = fast_exp2(sc[rt][x][2 * r] - ref), p1 = fast_exp2(sc[rt][x][2 * r + 1] - ref);
-                        sum += p0 + p1;
-                        *reinterpret_cast<uint32_t*>(p_out + (buf * S::kRows + rt * 16 + 8 * r) * S::kPPitch + x * 16) =
-                            pack2<kMmaBf>(p0, p1);
-                    }
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                    if (t == 0) mls[(buf * S::kRows + rt * 16 + g + 8 * r) * 4 + warp] = make_float2(mx, sum);
-                }
-            }
-            named_bar_sync(1, 128);
-
-            // ---- running maximum and sum; factors of the four groups
-            float f[RT][2][4];
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                float alpha[2];
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float4* src = reinterpret_cast<const float4*>(mls + (buf * S::kRows + rt * 16 + g + 8 * r) * 4);
-                    const float4 u = src[0], v = src[1];
-                    const float mw[4] = {u.x, u.z, v.x, v.z}, lw[4] = {u.y, u.w, v.y, v.w};
-                    const float mn = max_nan(M[rt][r], max_nan(max_nan(mw[0], mw[1]), max_nan(mw[2], mw[3])));
-                    const float ref = mn == -INFINITY ? 0.f : mn;
-                    alpha[r] = fast_exp2(M[rt][r] - ref);  // before the first key: 0, of nothing
-                    M[rt][r] = mn;
-                    float l = L[rt][r] * alpha[r];
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const float x = fast_exp2(mw[w] - ref);
-                        l = fmaf(x, lw[w], l);
-                        f[rt][r][w] = x;
-                        if constexpr (k8) {
-                            f[rt][r][w] = x * meta[s][w].y;
-                            // a row that sees none of the group takes nothing of it, whatever its scale
-                            if constexpr (!kFull) f[rt][r][w] = mw[w] == -INFINITY ? 0.f : f[rt][r][w];
-                        }
-                    }
-                    L[rt][r] = l;
-                }
-                if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-#pragma unroll
-                    for (int c = 0; c < S::kN; ++c) {
-                        o[rt][c][0] *= alpha[0], o[rt][c][1] *= alpha[0];
-                        o[rt][c][2] *= alpha[1], o[rt][c][3] *= alpha[1];
-                    }
-                }
-            }
-
-            // ---- O += P V for this warp's quarter of the columns, two groups of 16 keys at a time
+            float4 own = make_float4(1.f, 1.f, 0.f, 1.f);  // this warp's group: ks, vs / vref, its log2, its inverse
+            if constexpr (k8) own = meta[stage][warp];
+            // the score in log2 units, before any mask
+            auto score = [&](float raw, float c) {
+                const float y = raw * c;
+                return P.softcap > 0.f ? P.softcap * tanh_accurate(y * cap_inv) * kLog2e : y;
+            };
             const uint32_t paddr = smem_u32(ps) + (buf * S::kRows + (mi & 1) * 8 + ri) * S::kPPitch + (mi >> 1) * 16;
+            uint8_t* p_to = p_out + buf * S::kRows * S::kPPitch;
             auto load_v = [&](int kp, int c, uint32_t (&vb)[2][2][2]) {  // [group][8-column product][fragment half]
                 if constexpr (k8) {
                     // 16 columns: even ones are product c, odd ones c + 1
@@ -591,36 +543,119 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
                                   vb[y][1][0], vb[y][1][1]);
                 }
             };
-            if constexpr (kFull) {
+
+            // ---- the usual tile: seen whole by every row, scales near the item's first, and no
+            // score so far above the rows' references that p would leave fp16's range
+            bool done = false;
+            ++tiles;
+            const bool unmasked = (have & 0xf) == 0xf && j0 >= full_lo && j0 <= full_hi;
+            if (have == 0xf && unmasked && i > 0) {
+                float part[RT][2];
+                bool high = false;
 #pragma unroll
-                for (int kp = 0; kp < 4; kp += 2) {
-                    uint32_t pa[2][RT][4];
+                for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-                    for (int y = 0; y < 2; ++y)
+                    for (int r = 0; r < 2; ++r) {
+                        const float c = qf[rt][r] * own.x, shift = own.z - ref[rt][r];
+                        float y[4];
 #pragma unroll
-                        for (int rt = 0; rt < RT; ++rt)
-                            ldsm_x4(paddr + rt * 16 * S::kPPitch + (kp + y) * 32, pa[y][rt][0], pa[y][rt][1],
-                                    pa[y][rt][2], pa[y][rt][3]);
+                        for (int e = 0; e < 4; ++e) {
+                            const float raw = sc[rt][e >> 1][2 * r + (e & 1)];
+                            y[e] = P.softcap > 0.f ? score(raw, c) + shift : fmaf(raw, c, shift);
+                            high |= !(y[e] <= kTopLog2);
+                        }
+                        const float p0 = fast_exp2(y[0]), p1 = fast_exp2(y[1]), p2 = fast_exp2(y[2]), p3 = fast_exp2(y[3]);
+                        part[rt][r] = (p0 + p1) + (p2 + p3);
+                        uint8_t* to = p_to + (rt * 16 + 8 * r) * S::kPPitch;
+                        *reinterpret_cast<uint32_t*>(to) = pack2<kMmaBf>(p0, p1);
+                        *reinterpret_cast<uint32_t*>(to + 16) = pack2<kMmaBf>(p2, p3);
+                    }
+                if (high) raised[buf] = tiles;
+                named_bar_sync(1, 128);
+                done = raised[buf] != tiles;
+                if (done) {
 #pragma unroll
-                    for (int c = 0; c < S::kN; c += 2) {
-                        uint32_t vb[2][2][2];
-                        load_v(kp, c, vb);
+                    for (int rt = 0; rt < RT; ++rt) {
+                        l[rt][0] = fmaf(part[rt][0], own.w, l[rt][0]);
+                        l[rt][1] = fmaf(part[rt][1], own.w, l[rt][1]);
+                    }
+#pragma unroll
+                    for (int kp = 0; kp < 4; kp += 2) {
+                        uint32_t pa[2][RT][4];
 #pragma unroll
                         for (int y = 0; y < 2; ++y)
 #pragma unroll
-                            for (int x = 0; x < 2; ++x)
+                            for (int rt = 0; rt < RT; ++rt)
+                                ldsm_x4(paddr + rt * 16 * S::kPPitch + (kp + y) * 32, pa[y][rt][0], pa[y][rt][1],
+                                        pa[y][rt][2], pa[y][rt][3]);
 #pragma unroll
-                                for (int rt = 0; rt < RT; ++rt) {
-                                    float d[4];
-                                    mma_zero<kMmaBf>(d, pa[y][rt], vb[y][x][0], vb[y][x][1]);
-                                    o[rt][c + x][0] = fmaf(f[rt][0][kp + y], d[0], o[rt][c + x][0]);
-                                    o[rt][c + x][1] = fmaf(f[rt][0][kp + y], d[1], o[rt][c + x][1]);
-                                    o[rt][c + x][2] = fmaf(f[rt][1][kp + y], d[2], o[rt][c + x][2]);
-                                    o[rt][c + x][3] = fmaf(f[rt][1][kp + y], d[3], o[rt][c + x][3]);
-                                }
+                        for (int c = 0; c < S::kN; c += 2) {
+                            uint32_t vb[2][2][2];
+                            load_v(kp, c, vb);
+#pragma unroll
+                            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                                    for (int rt = 0; rt < RT; ++rt)
+                                        mma_add<kMmaBf>(o[rt][c + x], pa[y][rt], vb[y][x][0], vb[y][x][1]);
+                        }
                     }
                 }
-            } else {
+            }
+
+            // ---- any other tile: masks, a new reference, a factor for each group of 16 keys
+            if (!done) {
+                float mx[RT][2];
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        mx[rt][r] = -INFINITY;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float& y = sc[rt][e >> 1][2 * r + (e & 1)];
+                            y = score(y, qf[rt][r] * own.x);
+                            const int j = j0 + warp * 16 + (e >> 1) * 8 + 2 * t + (e & 1);
+                            if (!unmasked && (j < vlo[rt][r] || j >= vhi[rt][r] || !((have >> warp) & 1))) y = -INFINITY;
+                            mx[rt][r] = max_nan(mx[rt][r], y);
+                        }
+                        mx[rt][r] = max_nan(mx[rt][r], __shfl_xor_sync(0xffffffffu, mx[rt][r], 1));
+                        mx[rt][r] = max_nan(mx[rt][r], __shfl_xor_sync(0xffffffffu, mx[rt][r], 2));
+                        // relative to the group's own maximum
+                        const float to0 = mx[rt][r] == -INFINITY ? 0.f : mx[rt][r];
+                        float p[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) p[e] = fast_exp2(sc[rt][e >> 1][2 * r + (e & 1)] - to0);
+                        sc[rt][0][2 * r] = (p[0] + p[1]) + (p[2] + p[3]);
+                        uint8_t* to = p_to + (rt * 16 + 8 * r) * S::kPPitch;
+                        *reinterpret_cast<uint32_t*>(to) = pack2<kMmaBf>(p[0], p[1]);
+                        *reinterpret_cast<uint32_t*>(to + 16) = pack2<kMmaBf>(p[2], p[3]);
+                        if (t == 0) maxima[(buf * S::kRows + rt * 16 + g + 8 * r) * 4 + warp] = mx[rt][r];
+                    }
+                named_bar_sync(1, 128);
+                float f[RT][2][4];
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float4 u =
+                            *reinterpret_cast<const float4*>(maxima + (buf * S::kRows + rt * 16 + g + 8 * r) * 4);
+                        const float mw[4] = {u.x, u.y, u.z, u.w};
+                        const float top = max_nan(max_nan(mw[0], mw[1]), max_nan(mw[2], mw[3])) - kBias;
+                        const float next = max_nan(ref[rt][r], top), to0 = next == -INFINITY ? 0.f : next;
+                        const float alpha = fast_exp2(ref[rt][r] - to0);  // 0 before the row's first key
+                        ref[rt][r] = next;
+                        l[rt][r] = fmaf(fast_exp2(mx[rt][r] - to0), sc[rt][0][2 * r], l[rt][r] * alpha);
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            // a row that sees none of the group takes nothing of it, whatever its scale
+                            f[rt][r][w] = fast_exp2(mw[w] - to0);
+                            if constexpr (k8) f[rt][r][w] = mw[w] == -INFINITY ? 0.f : f[rt][r][w] * meta[stage][w].y;
+                        }
+#pragma unroll
+                        for (int c = 0; c < S::kN; ++c) o[rt][c][2 * r] *= alpha, o[rt][c][2 * r + 1] *= alpha;
+                    }
                 // Keys that no row sees may hold any bytes: they are masked out of V.  A value
                 // that is not finite may be seen by one row and not by another, whose P of 0 would
                 // not keep it out of a product: such a tile goes through one key of each group at a
@@ -633,7 +668,7 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
                 };
                 bool wild = false;
 #pragma unroll 1
-                for (int kp = 0; kp < 4; kp += 2) {
+                for (int kp = unmasked ? 4 : 0; kp < 4; kp += 2) {
                     const uint32_t keep[2][2] = {{keep_of(0, kp), keep_of(8, kp)}, {keep_of(0, kp + 1), keep_of(8, kp + 1)}};
 #pragma unroll
                     for (int c = 0; c < S::kN; c += 2) {
@@ -695,18 +730,30 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
                     }
                 }
             }
-        };
-
-        for (int i = 0; i < n; ++i) {
-            ok = ok && mbar_wait(full_bar(stage), phase, P.status, ST_DEC_WAIT, &abort_flag);
-            __syncwarp();
-            const int j0 = (sq.t0 + off + i) * kKeys, have = there[stage];
-            if (have == 0xf && j0 >= full_lo && j0 <= full_hi) tile(std::true_type(), j0, have, stage, i & 1);
-            else tile(std::false_type(), j0, have, stage, i & 1);
             __syncwarp();
             if (lane == 0) mbar_arrive(empty_bar(stage));
             if (++stage == S::kStages) stage = 0, phase ^= 1;
         }
+
+        // ---- the rows' sums: a row's quad, then the four warps
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                l[rt][r] += __shfl_xor_sync(0xffffffffu, l[rt][r], 1);
+                l[rt][r] += __shfl_xor_sync(0xffffffffu, l[rt][r], 2);
+                // (the half of the buffers that the last tile did not use)
+                if (t == 0) maxima[(((n & 1) * S::kRows) + rt * 16 + g + 8 * r) * 4 + warp] = l[rt][r];
+            }
+        named_bar_sync(1, 128);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float4 u =
+                    *reinterpret_cast<const float4*>(maxima + (((n & 1) * S::kRows) + rt * 16 + g + 8 * r) * 4);
+                l[rt][r] = (u.x + u.y) + (u.z + u.w);
+            }
 
         // ---- the item's rows, whole or partial
         const bool begins = off == 0, ends = off + n == sq.n;
@@ -721,8 +768,9 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
                     if (r >= R) continue;
                     const int gg = r / P.Lq, lq = r - gg * P.Lq;
                     const int hq = h * P.G + gg;
-                    const float inv = M[rt][e] == -INFINITY ? 0.f : 1.f / L[rt][e];
-                    const bool none = M[rt][e] == -INFINITY;
+                    const bool none = ref[rt][e] == -INFINITY;
+                    // O / vref in units of 2^ref, l in units of 2^ref
+                    const float mul = whole ? (none ? 0.f : vref / l[rt][e]) : vref;
                     uint16_t* od = static_cast<uint16_t*>(P.o) + (((long long)b * P.Lq + lq) * P.H + hq) * HD;
                     float* wd = ws_o + ((long long)slot * R + r) * HD;
                     auto two = [&](float x, float y) { return bf ? pack2<true>(x, y) : pack2<false>(x, y); };
@@ -730,32 +778,27 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
 #pragma unroll
                         for (int c = 0; c < S::kN; c += 2) {
                             const int d = warp * (HD / 4) + c * 8 + 4 * t;
-                            const float x0 = o[rt][c][2 * e], x1 = o[rt][c + 1][2 * e], x2 = o[rt][c][2 * e + 1],
-                                        x3 = o[rt][c + 1][2 * e + 1];
-                            if (whole)
-                                *reinterpret_cast<uint2*>(od + d) =
-                                    none ? make_uint2(0, 0) : make_uint2(two(x0 * inv, x1 * inv), two(x2 * inv, x3 * inv));
-                            else
-                                *reinterpret_cast<float4*>(wd + d) = make_float4(x0, x1, x2, x3);
+                            const float x0 = o[rt][c][2 * e] * mul, x1 = o[rt][c + 1][2 * e] * mul,
+                                        x2 = o[rt][c][2 * e + 1] * mul, x3 = o[rt][c + 1][2 * e + 1] * mul;
+                            if (whole) *reinterpret_cast<uint2*>(od + d) = make_uint2(two(x0, x1), two(x2, x3));
+                            else *reinterpret_cast<float4*>(wd + d) = make_float4(x0, x1, x2, x3);
                         }
                     } else {
 #pragma unroll
                         for (int c = 0; c < S::kN; ++c) {
                             const int d = warp * (HD / 4) + c * 8 + 2 * t;
-                            const float x0 = o[rt][c][2 * e], x1 = o[rt][c][2 * e + 1];
-                            if (whole)
-                                *reinterpret_cast<uint32_t*>(od + d) = none ? 0u : two(x0 * inv, x1 * inv);
-                            else
-                                *reinterpret_cast<float2*>(wd + d) = make_float2(x0, x1);
+                            const float x0 = o[rt][c][2 * e] * mul, x1 = o[rt][c][2 * e + 1] * mul;
+                            if (whole) *reinterpret_cast<uint32_t*>(od + d) = two(x0, x1);
+                            else *reinterpret_cast<float2*>(wd + d) = make_float2(x0, x1);
                         }
                     }
                     if (warp == 0 && t == 0) {
                         if (whole) {
                             if (P.lse)
                                 P.lse[((long long)b * P.H + hq) * P.Lq + lq] =
-                                    none ? -INFINITY : (M[rt][e] + log2f(L[rt][e])) * 0.6931471805599453f;
+                                    none ? -INFINITY : (ref[rt][e] + log2f(l[rt][e])) * 0.6931471805599453f;
                         } else {
-                            ws_ml[(long long)slot * R + r] = make_float2(M[rt][e], L[rt][e]);
+                            ws_ml[(long long)slot * R + r] = make_float2(ref[rt][e], l[rt][e]);
                         }
                     }
                 }
