@@ -164,13 +164,22 @@ struct Deal {
     long long all, share;
 };
 // Sums over all sequences, by each warp for itself (no barrier; 32 loads in flight).
-__device__ __forceinline__ Deal deal_tiles(const PagedParams& P, int ctas) {
+// (`before`: the tiles of one KV head of the sequences before `upto`)
+__device__ __forceinline__ Deal deal_tiles(const PagedParams& P, int ctas, int upto = 0, long long* before = nullptr) {
     const int lane = threadIdx.x & 31;
-    long long sum = 0;
+    long long sum = 0, part = 0;
 #pragma unroll 4
-    for (int b = lane; b < P.B; b += 32) sum += seq_tiles(P, b).n;
+    for (int b = lane; b < P.B; b += 32) {
+        const int n = seq_tiles(P, b).n;
+        sum += n;
+        if (before && b < upto) part += n;
+    }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int o = 16; o; o >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (before) part += __shfl_xor_sync(0xffffffffu, part, o);
+    }
+    if (before) *before = part;
     Deal d;
     d.all = sum * P.Hkv;
     d.share = (d.all + ctas - 1) / ctas;
@@ -395,15 +404,21 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
         const SeqTiles sq = seq_tiles(P, b);
         const int n = (int)min(left, (long long)(sq.n - off));
         // ---- Q of the group into shared memory: row r is (head r / Lq, query row r % Lq)
-        named_bar_sync(1, 128);  // no warp reads the last item's rows any more
-        for (int r = warp; r < S::kRows; r += 4) {
-            constexpr int kPer = HD / 64;  // pairs of a lane
-            const int gg = r / P.Lq, lq = r - gg * P.Lq;
+        constexpr int kPer = HD / 64;  // pairs of a lane
+        uint32_t qw[S::kRows / 4][kPer];
+#pragma unroll
+        for (int i = 0; i < S::kRows / 4; ++i) {
+            const int r = warp + 4 * i, gg = r / P.Lq, lq = r - gg * P.Lq;
             const uint32_t* src = reinterpret_cast<const uint32_t*>(
                 static_cast<const uint16_t*>(P.q) + (((long long)b * P.Lq + lq) * P.H + h * P.G + gg) * HD);
-            uint32_t w[kPer];
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) w[e] = r < R ? src[lane + 32 * e] : 0u;
+            for (int e = 0; e < kPer; ++e) qw[i][e] = r < R ? __ldg(src + lane + 32 * e) : 0u;
+        }
+        named_bar_sync(1, 128);  // no warp reads the last item's rows any more
+#pragma unroll
+        for (int i = 0; i < S::kRows / 4; ++i) {
+            const int r = warp + 4 * i;
+            uint32_t (&w)[kPer] = qw[i];
             if constexpr (k8) {
                 // to fp16 by a power of two that brings the row's largest element to 2^13 .. 2^14
                 float2 f[kPer];
@@ -477,11 +492,17 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
             if (k8 && i == 0) vref = vrefs[stage];
 
             // ---- S = Q K^T for this warp's 16 keys
-            float sc[RT][2][4];
+            // (one row tile alone: the even and the odd steps' products apart, four chains of them)
+            constexpr int kChains = RT == 1 ? 2 : 1;
+            float sc[RT][2][4], odd[kChains == 2 ? 2 : 1][4];
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) sc[rt][x][0] = sc[rt][x][1] = sc[rt][x][2] = sc[rt][x][3] = 0.f;
+            if constexpr (kChains == 2) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) odd[x][0] = odd[x][1] = odd[x][2] = odd[x][3] = 0.f;
+            }
             const uint32_t kt = base + k_off;
 #pragma unroll
             for (int ks = 0; ks < HD / 16; ks += 2) {
@@ -513,9 +534,20 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
                         } else {
                             ldsm_x4(qaddr + rt * 16 * S::kQPitch + (ks + x) * 32, a[0], a[1], a[2], a[3]);
                         }
-                        mma_add<kMmaBf>(sc[rt][0], a, kb[x][0][0], kb[x][0][1]);
-                        mma_add<kMmaBf>(sc[rt][1], a, kb[x][1][0], kb[x][1][1]);
+                        if (kChains == 2 && x == 1) {
+                            mma_add<kMmaBf>(odd[0], a, kb[x][0][0], kb[x][0][1]);
+                            mma_add<kMmaBf>(odd[kChains - 1], a, kb[x][1][0], kb[x][1][1]);
+                        } else {
+                            mma_add<kMmaBf>(sc[rt][0], a, kb[x][0][0], kb[x][0][1]);
+                            mma_add<kMmaBf>(sc[rt][1], a, kb[x][1][0], kb[x][1][1]);
+                        }
                     }
+            }
+            if constexpr (kChains == 2) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[0][x][e] += odd[x][e];
             }
 
             float4 own = make_float4(1.f, 1.f, 0.f, 1.f);  // this warp's group: ks, vs / vref, its log2, its inverse
@@ -549,7 +581,31 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
             bool done = false;
             ++tiles;
             const bool unmasked = (have & 0xf) == 0xf && j0 >= full_lo && j0 <= full_hi;
-            if (have == 0xf && unmasked && i > 0) {
+            const bool usual = have == 0xf && unmasked;
+            if (usual) {
+                if (i == 0) {
+                    // nothing is summed yet: the rows' references from this tile's maxima
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const float c = qf[rt][r] * own.x;
+                            float m = max_nan(max_nan(score(sc[rt][0][2 * r], c), score(sc[rt][0][2 * r + 1], c)),
+                                              max_nan(score(sc[rt][1][2 * r], c), score(sc[rt][1][2 * r + 1], c)));
+                            m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                            m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                            if (t == 0) maxima[(buf * S::kRows + rt * 16 + g + 8 * r) * 4 + warp] = m;
+                        }
+                    named_bar_sync(1, 128);
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const float4 u =
+                                *reinterpret_cast<const float4*>(maxima + (buf * S::kRows + rt * 16 + g + 8 * r) * 4);
+                            ref[rt][r] = max_nan(max_nan(u.x, u.y), max_nan(u.z, u.w)) - kBias;
+                        }
+                }
                 float part[RT][2];
                 bool high = false;
 #pragma unroll
@@ -588,18 +644,19 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
                             for (int rt = 0; rt < RT; ++rt)
                                 ldsm_x4(paddr + rt * 16 * S::kPPitch + (kp + y) * 32, pa[y][rt][0], pa[y][rt][1],
                                         pa[y][rt][2], pa[y][rt][3]);
+                        // all columns of one group, then of the other: a sum waits for no product before its own
+                        uint32_t vb[S::kN / 2][2][2][2];
 #pragma unroll
-                        for (int c = 0; c < S::kN; c += 2) {
-                            uint32_t vb[2][2][2];
-                            load_v(kp, c, vb);
+                        for (int c = 0; c < S::kN; c += 2) load_v(kp, c, vb[c / 2]);
 #pragma unroll
-                            for (int y = 0; y < 2; ++y)
+                        for (int y = 0; y < 2; ++y)
+#pragma unroll
+                            for (int c = 0; c < S::kN; c += 2)
 #pragma unroll
                                 for (int x = 0; x < 2; ++x)
 #pragma unroll
                                     for (int rt = 0; rt < RT; ++rt)
-                                        mma_add<kMmaBf>(o[rt][c + x], pa[y][rt], vb[y][x][0], vb[y][x][1]);
-                        }
+                                        mma_add<kMmaBf>(o[rt][c + x], pa[y][rt], vb[c / 2][y][x][0], vb[c / 2][y][x][1]);
                     }
                 }
             }
@@ -668,7 +725,7 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
                 };
                 bool wild = false;
 #pragma unroll 1
-                for (int kp = unmasked ? 4 : 0; kp < 4; kp += 2) {
+                for (int kp = unmasked || P.Lq == 1 ? 4 : 0; kp < 4; kp += 2) {  // (rows of one position see alike)
                     const uint32_t keep[2][2] = {{keep_of(0, kp), keep_of(8, kp)}, {keep_of(0, kp + 1), keep_of(8, kp + 1)}};
 #pragma unroll
                     for (int c = 0; c < S::kN; c += 2) {
@@ -819,33 +876,50 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
     }
 }
 
-// Merges the partial rows of the items that stretches cut: CTA (c, y) those of the item
-// that begins in stretch c and does not end in it, eight rows of it (fewer rows get several
-// warps each).  It finds its item from the lengths while the split kernel still runs.  The
+// Merges the partial rows of the items that stretches cut: CTA (x, y) those of the item
+// that begins in stretch x and does not end in it (by_item: of item x; there are then no
+// more items than stretches), rows_per_cta rows of it, several warps to a row.  It finds its item from the lengths while the split kernel still runs.  The
 // order of the sums is that of the stretches.
 template <int HD>
-__global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams P, const int rows_bf16) {
+__global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams P, const int rows_bf16, const int ctas,
+                                                            const int by_item, const int rows_per_cta) {
     constexpr int kPer = HD / 32;  // columns of a lane
     __shared__ float part[8][HD];
-    const Deal deal = deal_tiles(P, gridDim.x);
-    const long long first = (long long)blockIdx.x * deal.share, last = min(deal.all, first + deal.share) - 1;
-    Place at = {0, 0, 0, 0};
-    if (first <= last) at = place_of(P, last);
+    int b, h, cta;      // the item, and the stretch that it begins in
+    int n = 0;          // its parts: that stretch's end, and the beginnings of the next ones
+    if (by_item) {
+        b = blockIdx.x / P.Hkv, h = blockIdx.x % P.Hkv;
+        long long before;
+        const Deal deal = deal_tiles(P, ctas, b, &before);
+        const int tiles = seq_tiles(P, b).n;
+        if (tiles > 0) {
+            const long long first = before * P.Hkv + (long long)h * tiles;
+            cta = (int)(first / deal.share);
+            n = (int)((first + tiles - 1) / deal.share) - cta + 1;
+        }
+    } else {
+        cta = blockIdx.x;
+        const Deal deal = deal_tiles(P, ctas);
+        const long long first = (long long)cta * deal.share, last = min(deal.all, first + deal.share) - 1;
+        if (first <= last) {
+            const Place at = place_of(P, last);
+            b = at.b, h = at.h;
+            // the stretch's last item, if it begins in the stretch
+            if (at.off <= last - first) n = 1 + (int)((at.n - 1 - at.off + deal.share - 1) / deal.share);
+        }
+    }
     // Every CTA waits for the split kernel, also those with nothing to merge: this kernel's
     // end then stands for both.
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    // no tile, or the last item begins before the stretch, or ends in it
-    if (first > last || at.off > last - first || at.off == at.n - 1) return;
-    const int n = 1 + (int)((at.n - 1 - at.off + deal.share - 1) / deal.share);  // this stretch's end, the next ones' beginnings
+    if (n <= 1) return;  // whole in one stretch: written by it
     const int R = P.G * P.Lq;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int wpr = 8;  // warps of a row
-    while (wpr > 1 && 8 / wpr < R) wpr >>= 1;
-    const int r = blockIdx.y * 8 + warp / wpr, w = warp % wpr;
+    const int wpr = 8 / rows_per_cta;  // warps of a row
+    const int r = blockIdx.y * rows_per_cta + warp / wpr, w = warp % wpr;
     const bool live = r < R;
     const float2* ml = reinterpret_cast<const float2*>(P.ws);
     const float* wo = reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(P.ws) + ws_o_offset(R));
-    auto slot = [&](int i) { return (long long)(2 * ((int)blockIdx.x + i) + (i == 0 ? 1 : 0)) * R + r; };
+    auto slot = [&](int i) { return (long long)(2 * (cta + i) + (i == 0 ? 1 : 0)) * R + r; };
     float M = -INFINITY, L = 0.f;
     float acc[kPer];
 #pragma unroll
@@ -898,18 +972,18 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams P,
                 for (int e = 0; e < kPer; ++e) acc[e] += part[warp + x][lane * kPer + e];
     }
     if (!live || w != 0) return;
-    const int gg = r / P.Lq, lq = r - gg * P.Lq, hq = at.h * P.G + gg;
+    const int gg = r / P.Lq, lq = r - gg * P.Lq, hq = h * P.G + gg;
     const bool none = M == -INFINITY;
     const float inv = none ? 0.f : 1.f / L;
     uint32_t* od = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(P.o) +
-                                               (((long long)at.b * P.Lq + lq) * P.H + hq) * HD + lane * kPer);
+                                               (((long long)b * P.Lq + lq) * P.H + hq) * HD + lane * kPer);
 #pragma unroll
     for (int e = 0; e < kPer; e += 2) {
         const float x = none ? 0.f : acc[e] * inv, y = none ? 0.f : acc[e + 1] * inv;
         od[e / 2] = rows_bf16 ? pack2<true>(x, y) : pack2<false>(x, y);
     }
     if (P.lse && lane == 0)
-        P.lse[((long long)at.b * P.H + hq) * P.Lq + lq] = none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+        P.lse[((long long)b * P.H + hq) * P.Lq + lq] = none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
 // Dynamic shared memory of a kernel, asked for once on each device.
@@ -937,7 +1011,12 @@ cudaError_t decode_launch(const PagedParams& p, bool bf16, const PagedMaps& maps
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     // launched early: its CTAs come up while the split kernel's last ones run, and wait there
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kGrid, (p.G * p.Lq + 7) / 8);
+    // by item where there are few; rows to a CTA so that there are not many more CTAs than SMs
+    const int by_item = (long long)p.B * p.Hkv <= kGrid ? 1 : 0, R = p.G * p.Lq;
+    const int x = by_item ? p.B * p.Hkv : kGrid;
+    int per = 1;
+    while (per < 8 && x * ((R + per - 1) / per) > 2 * kSms) per *= 2;
+    cfg.gridDim = dim3(x, (R + per - 1) / per);
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -945,7 +1024,7 @@ cudaError_t decode_launch(const PagedParams& p, bool bf16, const PagedMaps& maps
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_combine_kernel<HD>, p, bf16 ? 1 : 0);
+    return cudaLaunchKernelEx(&cfg, paged_combine_kernel<HD>, p, bf16 ? 1 : 0, kGrid, by_item, per);
 }
 
 template <int HD, int CACHE, bool kBf>
