@@ -15,12 +15,14 @@
 //   * A producer warp keeps a ring of tiles in flight (TMA, 128-byte swizzle, one box for
 //     each run of a page's rows), page numbers and scales fetched 32 groups of 16 keys at a
 //     time, one batch ahead, by the lanes that hold them.
-//   * Four consumer warps split each tile by keys for S = Q K^T (16 each) and by columns of
-//     the head for O += P V: the probabilities go through shared memory, one barrier a
-//     tile, and no warp holds more than a quarter of O, so that three CTAs fit an SM.  Each
-//     warp's probabilities are relative to its own 16 keys' maximum; the factor that brings
-//     them to the row's running maximum, times the page's vs, is applied in fp32 to the
-//     16-key partial product, so a scale of any size costs no precision of P.
+//   * Four consumer warps (eight at hd 256) split each tile by keys for S = Q K^T and by
+//     columns of the head for O += P V: the probabilities go through shared memory, one barrier
+//     a tile, and no warp holds more than its share of O, so that three CTAs fit an SM.
+//   * p is relative to a reference of its row that the warps know alike and that moves only
+//     when a score passes it by far, so that in the usual tile no maximum is exchanged and P V
+//     accumulates in the products themselves; a page's vs enters as an addend of the exponent,
+//     relative to the item's first.  Masked tiles, and scales too unlike for that, take a path
+//     of their own with a factor for each group of 16 keys, applied in fp32.
 //   * 8-bit pages: codes become fp16 in registers (exact for both types) and the products
 //     run in fp16 with fp32 accumulation.  Q is brought to fp16 by a power of two for each
 //     row (exact for all that matters: 2^-38 of the row's largest element is kept).  A
@@ -43,7 +45,6 @@ namespace {
 namespace paged {
 
 constexpr int kKeys = 64;                  // keys of a tile
-constexpr int kDecThreads = 160;           // 4 consumer warps and the producer
 constexpr int kSms = 152;
 constexpr int kMaxCtasPerSm = 3;
 constexpr int kMaxCtas = kSms * kMaxCtasPerSm;
@@ -69,11 +70,19 @@ struct DecShape {
     static constexpr int kTileBytes = kKeys * HD * kEs;                // of K or of V
     static constexpr int kStageBytes = 2 * kTileBytes;
     static constexpr int kRows = RT * 16;
+    // Consumer warps; keys of a tile that each scores; 8-column products of its share of the
+    // head.  At hd 256 the ring leaves room for two CTAs: eight warps each, with half a tile's
+    // work, hide its latencies better than four (e5m2, 32 x 8192 tokens: 95 against 129 us); at
+    // hd 128 three CTAs of four warps do (e4m3, 16 x 32768 tokens: 170 against 277 us).
+    static constexpr int kW = HD == 256 ? 8 : 4;
+    static constexpr int kThreads = kW * 32 + 32;
+    static constexpr int kWk = kKeys / kW, kNt = kWk / 8;
+    static constexpr int kN = HD / 8 / kW;
     static constexpr int kQPitch = HD * 2 + 16;  // 16 past a multiple of 128: eight rows' chunks in eight places
     static constexpr int kPPitch = kKeys * 2 + 16;
     static constexpr int kQBytes = kRows * kQPitch;
     static constexpr int kPBytes = 2 * kRows * kPPitch;
-    static constexpr int kMlBytes = 2 * kRows * 4 * 4;  // two buffers of a number by row and warp
+    static constexpr int kMlBytes = 2 * kRows * kW * 4;  // two buffers of a number by row and warp
     static constexpr int kFixed = kQBytes + kPBytes + kMlBytes + kRows * 4 + 2048;  // + row scales, alignment, barriers
     // the most CTAs of an SM whose ring keeps at least three tiles each; the ring's depth
     static constexpr int stages(int ctas) {
@@ -84,8 +93,7 @@ struct DecShape {
     static constexpr int kStages = stages(kCtas);
     static constexpr int kBytes = kStages * kStageBytes + kFixed;
     // Q fragments stay in registers where they take at most 64
-    static constexpr bool kQReg = RT == 1 || RT * HD <= 128;
-    static constexpr int kN = HD / 32;  // 8-column products of a warp's quarter of the head
+    static constexpr bool kQReg = kW == 4 && (RT == 1 || RT * HD <= 128);
     static_assert(kStages >= 2, "ring too shallow");
 };
 
@@ -225,7 +233,7 @@ __device__ __forceinline__ void next_item(const PagedParams& P, int& b, int& h) 
 
 // kBf: the rows (and 16-bit pools) are bfloat16; over 8-bit pools a run-time choice
 template <int HD, int CACHE, int RT, bool kBf>
-__global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
+__global__ void __launch_bounds__(DecShape<HD, CACHE, RT>::kThreads, DecShape<HD, CACHE, RT>::kCtas)
     paged_split_kernel(const PagedParams P, const int rows_bf16, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV) {
     using S = DecShape<HD, CACHE, RT>;
@@ -236,8 +244,8 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* qs = smem + S::kStages * S::kStageBytes;
     uint8_t* ps = qs + S::kQBytes;
-    float* maxima = reinterpret_cast<float*>(ps + S::kPBytes);  // [2][rows][4]
-    float* qscale = maxima + 2 * S::kRows * 4;                  // [rows]
+    float* maxima = reinterpret_cast<float*>(ps + S::kPBytes);  // [2][rows][warps]
+    float* qscale = maxima + 2 * S::kRows * S::kW;              // [rows]
     __shared__ __align__(8) uint64_t bars[2 * S::kStages];
     __shared__ float4 meta[S::kStages][4];  // of the tile's groups of 16 keys: ks, vs / vref, its log2, its inverse
     __shared__ float vrefs[S::kStages];
@@ -253,7 +261,7 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
             mbar_init(full_bar(s), k8 ? 2 : 1);  // the tile's bytes; over 8-bit pools, its scales
-            mbar_init(empty_bar(s), 4);
+            mbar_init(empty_bar(s), S::kW);
         }
         abort_flag = 0;
         raised[0] = raised[1] = 0;
@@ -269,7 +277,7 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
     if (left > 0) at = place_of(P, first);
     int b = at.b, h = at.h, off = at.off;
 
-    if (warp == 4) {
+    if (warp == S::kW) {
         // ------------------------------------------------------------- producer
         if (lane == 0) {
             prefetch_tmap(&tmK);
@@ -392,32 +400,35 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
         if constexpr (S::kRowBytes == 64) return row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
         else return (c >> 3) * kBoxBytes + sw128(row, c & 7);
     };
-    const uint32_t k_off = chunk(warp * 16 + (mi & 1) * 8 + ri, mi >> 1);
+    // (4 warps: 16 keys by two chunks at a time; 8 warps: 8 keys by four)
+    const uint32_t k_off = S::kNt == 2 ? chunk(warp * 16 + (mi & 1) * 8 + ri, mi >> 1) : chunk(warp * 8 + ri, mi);
+    constexpr int kVc = k8 ? 16 : 8;  // columns of a chunk of V
     uint32_t v_off[S::kN / 2];
 #pragma unroll
-    for (int c = 0; c < S::kN; c += 2)
-        v_off[c / 2] = S::kTileBytes + (k8 ? chunk(mi * 8 + ri, warp * (HD / 64) + c / 2)
-                                           : chunk((mi & 1) * 8 + ri, warp * (HD / 32) + c + (mi >> 1)));
-    uint8_t* p_out = ps + g * S::kPPitch + (warp * 16 + 2 * t) * 2;
+    for (int c = 0; c < S::kN; c += 2) {
+        const int first = (warp * S::kN + c) * 8 / kVc;
+        v_off[c / 2] = S::kTileBytes + (k8 ? chunk(mi * 8 + ri, first) : chunk((mi & 1) * 8 + ri, first + (mi >> 1)));
+    }
+    uint8_t* p_out = ps + g * S::kPPitch + (warp * S::kWk + 2 * t) * 2;
     const float cap_inv = P.softcap > 0.f ? 1.f / P.softcap : 0.f;
     while (left > 0) {
         const SeqTiles sq = seq_tiles(P, b);
         const int n = (int)min(left, (long long)(sq.n - off));
         // ---- Q of the group into shared memory: row r is (head r / Lq, query row r % Lq)
         constexpr int kPer = HD / 64;  // pairs of a lane
-        uint32_t qw[S::kRows / 4][kPer];
+        uint32_t qw[S::kRows / S::kW][kPer];
 #pragma unroll
-        for (int i = 0; i < S::kRows / 4; ++i) {
-            const int r = warp + 4 * i, gg = r / P.Lq, lq = r - gg * P.Lq;
+        for (int i = 0; i < S::kRows / S::kW; ++i) {
+            const int r = warp + S::kW * i, gg = r / P.Lq, lq = r - gg * P.Lq;
             const uint32_t* src = reinterpret_cast<const uint32_t*>(
                 static_cast<const uint16_t*>(P.q) + (((long long)b * P.Lq + lq) * P.H + h * P.G + gg) * HD);
 #pragma unroll
             for (int e = 0; e < kPer; ++e) qw[i][e] = r < R ? __ldg(src + lane + 32 * e) : 0u;
         }
-        named_bar_sync(1, 128);  // no warp reads the last item's rows any more
+        named_bar_sync(1, S::kW * 32);  // no warp reads the last item's rows any more
 #pragma unroll
-        for (int i = 0; i < S::kRows / 4; ++i) {
-            const int r = warp + 4 * i;
+        for (int i = 0; i < S::kRows / S::kW; ++i) {
+            const int r = warp + S::kW * i;
             uint32_t (&w)[kPer] = qw[i];
             if constexpr (k8) {
                 // to fp16 by a power of two that brings the row's largest element to 2^13 .. 2^14
@@ -447,7 +458,7 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
                     *reinterpret_cast<uint32_t*>(qs + r * S::kQPitch + 4 * (lane + 32 * e)) = w[e];
             }
         }
-        named_bar_sync(1, 128);
+        named_bar_sync(1, S::kW * 32);
         const uint32_t qaddr = smem_u32(qs) + ((mi & 1) * 8 + ri) * S::kQPitch + (mi >> 1) * 16;
         uint32_t qa[S::kQReg ? RT : 1][S::kQReg ? HD / 16 : 1][4];
         if constexpr (S::kQReg) {
@@ -491,42 +502,45 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
             const uint32_t base = ring + (uint32_t)(stage * S::kStageBytes);
             if (k8 && i == 0) vref = vrefs[stage];
 
-            // ---- S = Q K^T for this warp's 16 keys
-            // (one row tile alone: the even and the odd steps' products apart, four chains of them)
-            constexpr int kChains = RT == 1 ? 2 : 1;
-            float sc[RT][2][4], odd[kChains == 2 ? 2 : 1][4];
+            // ---- S = Q K^T for this warp's keys, 8 to a column tile
+            // (one row tile alone: the even and the odd steps' products apart, for shorter chains)
+            constexpr int kNt = S::kNt, kChains = RT == 1 ? 2 : 1;
+            float sc[RT][kNt][4], odd[kNt][4];
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
+            for (int x = 0; x < kNt; ++x) {
 #pragma unroll
-                for (int x = 0; x < 2; ++x) sc[rt][x][0] = sc[rt][x][1] = sc[rt][x][2] = sc[rt][x][3] = 0.f;
-            if constexpr (kChains == 2) {
-#pragma unroll
-                for (int x = 0; x < 2; ++x) odd[x][0] = odd[x][1] = odd[x][2] = odd[x][3] = 0.f;
+                for (int rt = 0; rt < RT; ++rt) sc[rt][x][0] = sc[rt][x][1] = sc[rt][x][2] = sc[rt][x][3] = 0.f;
+                odd[x][0] = odd[x][1] = odd[x][2] = odd[x][3] = 0.f;
             }
             const uint32_t kt = base + k_off;
+            // steps of 16 columns that one ldmatrix.x4 (8-bit) or kNt of them (16-bit) serve
+            constexpr int kStep = kNt == 2 || !k8 ? 2 : 4;
 #pragma unroll
-            for (int ks = 0; ks < HD / 16; ks += 2) {
-                uint32_t kb[2][2][2];  // [step][keys 0-7 | 8-15][fragment half]
+            for (int ks = 0; ks < HD / 16; ks += kStep) {
+                uint32_t kb[kStep][kNt][2];  // [step][column tile][fragment half]
                 if constexpr (k8) {
-                    // matrices: (keys 0-7 | 8-15) x (16 columns of step ks | ks + 1)
-                    uint32_t r[2][2];
-                    ldsm_x4((kt ^ ((ks & 7) << 4)) + (ks >> 3) * kBoxBytes, r[0][0], r[0][1], r[1][0], r[1][1]);
+                    uint32_t r[4];
+                    ldsm_x4((kt ^ ((ks & 7) << 4)) + (ks >> 3) * kBoxBytes, r[0], r[1], r[2], r[3]);
 #pragma unroll
-                    for (int x = 0; x < 2; ++x)
+                    for (int x = 0; x < kStep; ++x)
 #pragma unroll
-                        for (int y = 0; y < 2; ++y) codes_k<CACHE>(r[x][y], kb[x][y][0], kb[x][y][1]);
-                } else {
+                        for (int y = 0; y < kNt; ++y) codes_k<CACHE>(r[x * kNt + y], kb[x][y][0], kb[x][y][1]);
+                } else if constexpr (kNt == 2) {
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         const int c = 2 * (ks + x);
                         ldsm_x4((kt ^ ((c & 7) << 4)) + (c >> 3) * kBoxBytes, kb[x][0][0], kb[x][1][0], kb[x][0][1],
                                 kb[x][1][1]);
                     }
+                } else {
+                    const int c = 2 * ks;
+                    ldsm_x4((kt ^ ((c & 7) << 4)) + (c >> 3) * kBoxBytes, kb[0][0][0], kb[0][0][1], kb[1][0][0],
+                            kb[1][0][1]);
                 }
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
+                    for (int x = 0; x < kStep; ++x) {
                         uint32_t a[4];
                         if constexpr (S::kQReg) {
                             a[0] = qa[rt][ks + x][0], a[1] = qa[rt][ks + x][1], a[2] = qa[rt][ks + x][2],
@@ -534,28 +548,36 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
                         } else {
                             ldsm_x4(qaddr + rt * 16 * S::kQPitch + (ks + x) * 32, a[0], a[1], a[2], a[3]);
                         }
-                        if (kChains == 2 && x == 1) {
-                            mma_add<kMmaBf>(odd[0], a, kb[x][0][0], kb[x][0][1]);
-                            mma_add<kMmaBf>(odd[kChains - 1], a, kb[x][1][0], kb[x][1][1]);
-                        } else {
-                            mma_add<kMmaBf>(sc[rt][0], a, kb[x][0][0], kb[x][0][1]);
-                            mma_add<kMmaBf>(sc[rt][1], a, kb[x][1][0], kb[x][1][1]);
+#pragma unroll
+                        for (int y = 0; y < kNt; ++y) {
+                            if (kChains == 2 && (x & 1)) mma_add<kMmaBf>(odd[y], a, kb[x][y][0], kb[x][y][1]);
+                            else mma_add<kMmaBf>(sc[rt][y], a, kb[x][y][0], kb[x][y][1]);
                         }
                     }
             }
             if constexpr (kChains == 2) {
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
+                for (int x = 0; x < kNt; ++x)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) sc[0][x][e] += odd[x][e];
             }
 
-            float4 own = make_float4(1.f, 1.f, 0.f, 1.f);  // this warp's group: ks, vs / vref, its log2, its inverse
-            if constexpr (k8) own = meta[stage][warp];
+            const int grp = warp * S::kWk / 16;               // the group of 16 keys that they lie in
+            float4 own = make_float4(1.f, 1.f, 0.f, 1.f);  // its ks, vs / vref, the log2 of that, its inverse
+            if constexpr (k8) own = meta[stage][grp];
             // the score in log2 units, before any mask
             auto score = [&](float raw, float c) {
                 const float y = raw * c;
                 return P.softcap > 0.f ? P.softcap * tanh_accurate(y * cap_inv) * kLog2e : y;
+            };
+            auto group_maxima = [&](const float* of_row, float (&mw)[4]) {
+                const float4 u = *reinterpret_cast<const float4*>(of_row);
+                if constexpr (S::kW == 4) {
+                    mw[0] = u.x, mw[1] = u.y, mw[2] = u.z, mw[3] = u.w;
+                } else {
+                    const float4 v = *reinterpret_cast<const float4*>(of_row + 4);
+                    mw[0] = max_nan(u.x, u.y), mw[1] = max_nan(u.z, u.w), mw[2] = max_nan(v.x, v.y), mw[3] = max_nan(v.z, v.w);
+                }
             };
             const uint32_t paddr = smem_u32(ps) + (buf * S::kRows + (mi & 1) * 8 + ri) * S::kPPitch + (mi >> 1) * 16;
             uint8_t* p_to = p_out + buf * S::kRows * S::kPPitch;
@@ -590,20 +612,21 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
                             const float c = qf[rt][r] * own.x;
-                            float m = max_nan(max_nan(score(sc[rt][0][2 * r], c), score(sc[rt][0][2 * r + 1], c)),
-                                              max_nan(score(sc[rt][1][2 * r], c), score(sc[rt][1][2 * r + 1], c)));
+                            float m = score(sc[rt][0][2 * r], c);
+#pragma unroll
+                            for (int e = 1; e < 2 * kNt; ++e) m = max_nan(m, score(sc[rt][e >> 1][2 * r + (e & 1)], c));
                             m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
                             m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                            if (t == 0) maxima[(buf * S::kRows + rt * 16 + g + 8 * r) * 4 + warp] = m;
+                            if (t == 0) maxima[(buf * S::kRows + rt * 16 + g + 8 * r) * S::kW + warp] = m;
                         }
-                    named_bar_sync(1, 128);
+                    named_bar_sync(1, S::kW * 32);
 #pragma unroll
                     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
-                            const float4 u =
-                                *reinterpret_cast<const float4*>(maxima + (buf * S::kRows + rt * 16 + g + 8 * r) * 4);
-                            ref[rt][r] = max_nan(max_nan(u.x, u.y), max_nan(u.z, u.w)) - kBias;
+                            float mw[4];
+                            group_maxima(maxima + (buf * S::kRows + rt * 16 + g + 8 * r) * S::kW, mw);
+                            ref[rt][r] = max_nan(max_nan(mw[0], mw[1]), max_nan(mw[2], mw[3])) - kBias;
                         }
                 }
                 float part[RT][2];
@@ -613,21 +636,25 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         const float c = qf[rt][r] * own.x, shift = own.z - ref[rt][r];
-                        float y[4];
+                        float y[2 * kNt];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
+                        for (int e = 0; e < 2 * kNt; ++e) {
                             const float raw = sc[rt][e >> 1][2 * r + (e & 1)];
                             y[e] = P.softcap > 0.f ? score(raw, c) + shift : fmaf(raw, c, shift);
                             high |= !(y[e] <= kTopLog2);
                         }
-                        const float p0 = fast_exp2(y[0]), p1 = fast_exp2(y[1]), p2 = fast_exp2(y[2]), p3 = fast_exp2(y[3]);
-                        part[rt][r] = (p0 + p1) + (p2 + p3);
                         uint8_t* to = p_to + (rt * 16 + 8 * r) * S::kPPitch;
+                        const float p0 = fast_exp2(y[0]), p1 = fast_exp2(y[1]);
                         *reinterpret_cast<uint32_t*>(to) = pack2<kMmaBf>(p0, p1);
-                        *reinterpret_cast<uint32_t*>(to + 16) = pack2<kMmaBf>(p2, p3);
+                        part[rt][r] = p0 + p1;
+                        if constexpr (kNt == 2) {
+                            const float p2 = fast_exp2(y[2]), p3 = fast_exp2(y[3]);
+                            *reinterpret_cast<uint32_t*>(to + 16) = pack2<kMmaBf>(p2, p3);
+                            part[rt][r] += p2 + p3;
+                        }
                     }
                 if (high) raised[buf] = tiles;
-                named_bar_sync(1, 128);
+                named_bar_sync(1, S::kW * 32);
                 done = raised[buf] != tiles;
                 if (done) {
 #pragma unroll
@@ -670,35 +697,50 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
                     for (int r = 0; r < 2; ++r) {
                         mx[rt][r] = -INFINITY;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
+                        for (int e = 0; e < 2 * kNt; ++e) {
                             float& y = sc[rt][e >> 1][2 * r + (e & 1)];
                             y = score(y, qf[rt][r] * own.x);
-                            const int j = j0 + warp * 16 + (e >> 1) * 8 + 2 * t + (e & 1);
-                            if (!unmasked && (j < vlo[rt][r] || j >= vhi[rt][r] || !((have >> warp) & 1))) y = -INFINITY;
+                            const int j = j0 + warp * S::kWk + (e >> 1) * 8 + 2 * t + (e & 1);
+                            if (!unmasked && (j < vlo[rt][r] || j >= vhi[rt][r] || !((have >> grp) & 1))) y = -INFINITY;
                             mx[rt][r] = max_nan(mx[rt][r], y);
                         }
                         mx[rt][r] = max_nan(mx[rt][r], __shfl_xor_sync(0xffffffffu, mx[rt][r], 1));
                         mx[rt][r] = max_nan(mx[rt][r], __shfl_xor_sync(0xffffffffu, mx[rt][r], 2));
-                        // relative to the group's own maximum
-                        const float to0 = mx[rt][r] == -INFINITY ? 0.f : mx[rt][r];
-                        float p[4];
+                        if (t == 0) maxima[(buf * S::kRows + rt * 16 + g + 8 * r) * S::kW + warp] = mx[rt][r];
+                    }
+                if constexpr (kNt == 1) {  // two warps to a group
+                    named_bar_sync(1, S::kW * 32);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) p[e] = fast_exp2(sc[rt][e >> 1][2 * r + (e & 1)] - to0);
-                        sc[rt][0][2 * r] = (p[0] + p[1]) + (p[2] + p[3]);
+                    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r)
+                            mx[rt][r] = max_nan(mx[rt][r], maxima[(buf * S::kRows + rt * 16 + g + 8 * r) * S::kW + (warp ^ 1)]);
+                }
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        // p relative to the group's own maximum
+                        const float to0 = mx[rt][r] == -INFINITY ? 0.f : mx[rt][r];
+                        float p[2 * kNt];
+#pragma unroll
+                        for (int e = 0; e < 2 * kNt; ++e) p[e] = fast_exp2(sc[rt][e >> 1][2 * r + (e & 1)] - to0);
                         uint8_t* to = p_to + (rt * 16 + 8 * r) * S::kPPitch;
                         *reinterpret_cast<uint32_t*>(to) = pack2<kMmaBf>(p[0], p[1]);
-                        *reinterpret_cast<uint32_t*>(to + 16) = pack2<kMmaBf>(p[2], p[3]);
-                        if (t == 0) maxima[(buf * S::kRows + rt * 16 + g + 8 * r) * 4 + warp] = mx[rt][r];
+                        sc[rt][0][2 * r] = p[0] + p[1];
+                        if constexpr (kNt == 2) {
+                            *reinterpret_cast<uint32_t*>(to + 16) = pack2<kMmaBf>(p[2], p[3]);
+                            sc[rt][0][2 * r] += p[2] + p[3];
+                        }
                     }
-                named_bar_sync(1, 128);
+                named_bar_sync(1, S::kW * 32);
                 float f[RT][2][4];
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        const float4 u =
-                            *reinterpret_cast<const float4*>(maxima + (buf * S::kRows + rt * 16 + g + 8 * r) * 4);
-                        const float mw[4] = {u.x, u.y, u.z, u.w};
+                        float mw[4];
+                        group_maxima(maxima + (buf * S::kRows + rt * 16 + g + 8 * r) * S::kW, mw);
                         const float top = max_nan(max_nan(mw[0], mw[1]), max_nan(mw[2], mw[3])) - kBias;
                         const float next = max_nan(ref[rt][r], top), to0 = next == -INFINITY ? 0.f : next;
                         const float alpha = fast_exp2(ref[rt][r] - to0);  // 0 before the row's first key
@@ -800,16 +842,18 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
                 l[rt][r] += __shfl_xor_sync(0xffffffffu, l[rt][r], 1);
                 l[rt][r] += __shfl_xor_sync(0xffffffffu, l[rt][r], 2);
                 // (the half of the buffers that the last tile did not use)
-                if (t == 0) maxima[(((n & 1) * S::kRows) + rt * 16 + g + 8 * r) * 4 + warp] = l[rt][r];
+                if (t == 0) maxima[(((n & 1) * S::kRows) + rt * 16 + g + 8 * r) * S::kW + warp] = l[rt][r];
             }
-        named_bar_sync(1, 128);
+        named_bar_sync(1, S::kW * 32);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const float4 u =
-                    *reinterpret_cast<const float4*>(maxima + (((n & 1) * S::kRows) + rt * 16 + g + 8 * r) * 4);
-                l[rt][r] = (u.x + u.y) + (u.z + u.w);
+                const float4* u =
+                    reinterpret_cast<const float4*>(maxima + (((n & 1) * S::kRows) + rt * 16 + g + 8 * r) * S::kW);
+                l[rt][r] = 0.f;
+#pragma unroll
+                for (int w = 0; w < S::kW / 4; ++w) l[rt][r] += (u[w].x + u[w].y) + (u[w].z + u[w].w);
             }
 
         // ---- the item's rows, whole or partial
@@ -834,7 +878,7 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
                     if constexpr (k8) {
 #pragma unroll
                         for (int c = 0; c < S::kN; c += 2) {
-                            const int d = warp * (HD / 4) + c * 8 + 4 * t;
+                            const int d = (warp * S::kN + c) * 8 + 4 * t;
                             const float x0 = o[rt][c][2 * e] * mul, x1 = o[rt][c + 1][2 * e] * mul,
                                         x2 = o[rt][c][2 * e + 1] * mul, x3 = o[rt][c + 1][2 * e + 1] * mul;
                             if (whole) *reinterpret_cast<uint2*>(od + d) = make_uint2(two(x0, x1), two(x2, x3));
@@ -843,7 +887,7 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
                     } else {
 #pragma unroll
                         for (int c = 0; c < S::kN; ++c) {
-                            const int d = warp * (HD / 4) + c * 8 + 2 * t;
+                            const int d = (warp * S::kN + c) * 8 + 2 * t;
                             const float x0 = o[rt][c][2 * e] * mul, x1 = o[rt][c][2 * e + 1] * mul;
                             if (whole) *reinterpret_cast<uint32_t*>(od + d) = two(x0, x1);
                             else *reinterpret_cast<float2*>(wd + d) = make_float2(x0, x1);
@@ -870,9 +914,9 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<HD, CACHE, RT>::kCtas)
         if (tid == 0 && __ldg(P.lengths + e) > (P.max_pages << P.page_shift)) atomicOr(P.status, ST_PAGED_BOUNDS);
         if (seq_tiles(P, e).n > 0) continue;
         uint4* od = reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.o) + (long long)e * P.Lq * P.H * HD);
-        for (int i = tid; i < P.Lq * P.H * HD / 8; i += 128) od[i] = make_uint4(0, 0, 0, 0);
+        for (int i = tid; i < P.Lq * P.H * HD / 8; i += S::kW * 32) od[i] = make_uint4(0, 0, 0, 0);
         if (P.lse)
-            for (int i = tid; i < P.Lq * P.H; i += 128) P.lse[(long long)e * P.Lq * P.H + i] = -INFINITY;
+            for (int i = tid; i < P.Lq * P.H; i += S::kW * 32) P.lse[(long long)e * P.Lq * P.H + i] = -INFINITY;
     }
 }
 
@@ -1007,7 +1051,7 @@ cudaError_t decode_launch(const PagedParams& p, bool bf16, const PagedMaps& maps
     cudaError_t e = allow_smem(k, S::kBytes, done);
     if (e != cudaSuccess) return e;
     constexpr int kGrid = kSms * S::kCtas;
-    k<<<kGrid, kDecThreads, S::kBytes, s>>>(p, bf16 ? 1 : 0, maps.k, maps.v);
+    k<<<kGrid, S::kThreads, S::kBytes, s>>>(p, bf16 ? 1 : 0, maps.k, maps.v);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     // launched early: its CTAs come up while the split kernel's last ones run, and wait there
     cudaLaunchConfig_t cfg = {};
