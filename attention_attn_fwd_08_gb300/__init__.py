@@ -714,7 +714,7 @@ def _rows(what, t, n, width, dtype, device):
 
 def _like(what, t, shape, dtype, device):
     """Checks an output that the caller gave."""
-    if t is not None and (t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous()):
+    if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of shape %s on %s" % (what, dtype, tuple(shape), device))
 
 
@@ -738,27 +738,26 @@ def attn_paged_append(k, v, k_cache, v_cache, page_table, lengths, cu_new, *, H,
     qs = 0
     if q is not None:
         qs = _rows("q", q, n, H * hd, dtype, dev)
-        _like("q_out", q_out, (n, H * hd), dtype, dev)
+        if q_out is not None:
+            _like("q_out", q_out, (n, H * hd), dtype, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
     if rope_theta is not None and not rope_theta > 0:
         raise ValueError("rope_theta must be positive (None: no turn)")
     handle, context = _on(dev, stream)
-
-    def call():
-        out = _torch().empty((n, H * hd), dtype=dtype, device=dev) if q is not None and q_out is None else q_out
-        return out, lib().attn_paged_append(rd, cd, k.data_ptr(), ks, v.data_ptr(), vs, _addr(q), qs, _addr(out),
-                                            k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale),
-                                            cu_new.data_ptr(), lengths.data_ptr(), page_table.data_ptr(), B, n, num_pages,
-                                            page_size, max_pages, H, Hkv, hd, rope_theta or 0.0, handle)
-
-    if context is None:
-        out, st = call()
-    else:
+    if context is not None:
         with context:
-            out, st = call()
-    _check(st, "attn_paged_append")
-    return out
+            return attn_paged_append(k, v, k_cache, v_cache, page_table, lengths, cu_new, H=H, Hkv=Hkv, k_scale=k_scale,
+                                     v_scale=v_scale, q=q, q_out=q_out, rope_theta=rope_theta)
+    if q is not None and q_out is None:
+        q_out = _torch().empty((n, H * hd), dtype=dtype, device=dev)
+    st = (_lib or lib()).attn_paged_append(rd, cd, k.data_ptr(), ks, v.data_ptr(), vs, _addr(q), qs, _addr(q_out),
+                                           k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale),
+                                           cu_new.data_ptr(), lengths.data_ptr(), page_table.data_ptr(), B, n, num_pages,
+                                           page_size, max_pages, H, Hkv, hd, rope_theta or 0.0, handle)
+    if st != OK:
+        _check(st, "attn_paged_append")
+    return q_out
 
 
 def attn_paged_decode_workspace_size(B, Lq, H, Hkv, hd) -> int:
@@ -781,32 +780,32 @@ def attn_paged_decode(q, k_cache, v_cache, page_table, lengths, *, H, Hkv, k_sca
     if not q.is_contiguous():
         raise ValueError("tensors must be contiguous")
     _int_row("lengths", lengths, B, dev)
-    _like("o", o, q.shape, q.dtype, dev)
-    _like("lse", lse, (B, H, Lq), torch.float32, dev)
+    if o is not None:
+        _like("o", o, q.shape, q.dtype, dev)
+    if lse is not None:
+        _like("lse", lse, (B, H, Lq), torch.float32, dev)
     if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
         raise ValueError("workspace must be contiguous and on %s" % dev)
     handle, context = _on(dev, stream)
-    L = lib()
-
-    def call():
-        out = torch.empty_like(q) if o is None else o
-        sums = torch.empty((B, H, Lq), dtype=torch.float32, device=dev) if lse is None and want_lse else lse
-        ws = workspace
-        if ws is None:
-            ws = torch.empty(L.attn_paged_decode_workspace_size(B, Lq, H, Hkv, hd), dtype=torch.uint8, device=dev)
-        return out, sums, L.attn_paged_decode(rd, cd, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale),
-                                              _addr(v_scale), out.data_ptr(), _addr(sums), ws.data_ptr(), ws.nbytes,
-                                              lengths.data_ptr(), page_table.data_ptr(), B, Lq, num_pages, page_size,
-                                              max_pages, H, Hkv, hd, hd ** -0.5 if scale is None else scale,
-                                              1 if causal else 0, window, softcap, handle)
-
-    if context is None:
-        out, sums, st = call()
-    else:
+    if context is not None:
         with context:
-            out, sums, st = call()
-    _check(st, "attn_paged_decode")
-    return out, sums
+            return attn_paged_decode(q, k_cache, v_cache, page_table, lengths, H=H, Hkv=Hkv, k_scale=k_scale,
+                                     v_scale=v_scale, scale=scale, causal=causal, window=window, softcap=softcap, o=o,
+                                     lse=lse, want_lse=want_lse, workspace=workspace)
+    L = _lib or lib()
+    if o is None:
+        o = torch.empty_like(q)
+    if lse is None and want_lse:
+        lse = torch.empty((B, H, Lq), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(L.attn_paged_decode_workspace_size(B, Lq, H, Hkv, hd), dtype=torch.uint8, device=dev)
+    st = L.attn_paged_decode(rd, cd, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale),
+                             _addr(v_scale), o.data_ptr(), _addr(lse), workspace.data_ptr(), workspace.nbytes,
+                             lengths.data_ptr(), page_table.data_ptr(), B, Lq, num_pages, page_size, max_pages, H, Hkv, hd,
+                             hd ** -0.5 if scale is None else scale, 1 if causal else 0, window, softcap, handle)
+    if st != OK:
+        _check(st, "attn_paged_decode")
+    return o, lse
 
 
 def attn_paged_gather(k_cache, v_cache, page_table, cu_seqlens, total, *, Hkv, dtype, k_scale=None, v_scale=None,
@@ -819,22 +818,23 @@ def attn_paged_gather(k_cache, v_cache, page_table, cu_seqlens, total, *, Hkv, d
     rd, cd, num_pages, page_size, hd, B, max_pages = _pools(k_cache, v_cache, k_scale, v_scale, page_table, Hkv, dtype)
     dev, shape = k_cache.device, (int(total), Hkv * hd)
     _int_row("cu_seqlens", cu_seqlens, B + 1, dev)
-    _like("k_out", k_out, shape, dtype, dev)
-    _like("v_out", v_out, shape, dtype, dev)
+    if k_out is not None:
+        _like("k_out", k_out, shape, dtype, dev)
+    if v_out is not None:
+        _like("v_out", v_out, shape, dtype, dev)
     handle, context = _on(dev, stream)
-
-    def call():
-        ko = torch.empty(shape, dtype=dtype, device=dev) if k_out is None else k_out
-        vo = torch.empty(shape, dtype=dtype, device=dev) if v_out is None else v_out
-        return ko, vo, lib().attn_paged_gather(rd, cd, k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale),
-                                               _addr(v_scale), ko.data_ptr(), vo.data_ptr(), cu_seqlens.data_ptr(),
-                                               page_table.data_ptr(), B, shape[0], num_pages, page_size, max_pages, Hkv,
-                                               hd, handle)
-
-    if context is None:
-        ko, vo, st = call()
-    else:
+    if context is not None:
         with context:
-            ko, vo, st = call()
-    _check(st, "attn_paged_gather")
-    return ko, vo
+            return attn_paged_gather(k_cache, v_cache, page_table, cu_seqlens, total, Hkv=Hkv, dtype=dtype, k_scale=k_scale,
+                                     v_scale=v_scale, k_out=k_out, v_out=v_out)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=dev)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=dev)
+    st = (_lib or lib()).attn_paged_gather(rd, cd, k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale),
+                                           k_out.data_ptr(), v_out.data_ptr(), cu_seqlens.data_ptr(),
+                                           page_table.data_ptr(), B, shape[0], num_pages, page_size, max_pages, Hkv, hd,
+                                           handle)
+    if st != OK:
+        _check(st, "attn_paged_gather")
+    return k_out, v_out

@@ -15,6 +15,8 @@
 // divided by an exact power of two (only codes that become subnormal round again).
 #include <math.h>
 
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace attn {
@@ -53,11 +55,16 @@ __device__ __forceinline__ float2 unpack16(uint32_t w) {
 struct Pairs {
     float lo[8], hi[8];
 };
-template <bool BF16>
-__device__ __forceinline__ void load_pairs(Pairs& x, const void* base, long long elem, int half) {
+struct RawPairs {  // the same as loaded
+    uint4 lo, hi;
+};
+__device__ __forceinline__ RawPairs load_raw(const void* base, long long elem, int half) {
     const uint16_t* p = static_cast<const uint16_t*>(base) + elem;
-    const uint4 a = *reinterpret_cast<const uint4*>(p), b = *reinterpret_cast<const uint4*>(p + half);
-    const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+    return RawPairs{*reinterpret_cast<const uint4*>(p), *reinterpret_cast<const uint4*>(p + half)};
+}
+template <bool BF16>
+__device__ __forceinline__ void unpack_pairs(Pairs& x, const RawPairs& r) {
+    const uint32_t aw[4] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w}, bw[4] = {r.hi.x, r.hi.y, r.hi.z, r.hi.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const float2 u = unpack16<BF16>(aw[e]), v = unpack16<BF16>(bw[e]);
@@ -75,87 +82,128 @@ __device__ __forceinline__ void store_pairs(const Pairs& x, void* base, long lon
     *reinterpret_cast<uint4*>(p + half) = make_uint4(pack2<BF16>(x.hi[0], x.hi[1]), pack2<BF16>(x.hi[2], x.hi[3]),
                                                      pack2<BF16>(x.hi[4], x.hi[5]), pack2<BF16>(x.hi[6], x.hi[7]));
 }
+__device__ __forceinline__ void store_raw(const RawPairs& r, void* base, long long elem, int half) {
+    uint16_t* p = static_cast<uint16_t*>(base) + elem;
+    *reinterpret_cast<uint4*>(p) = r.lo;
+    *reinterpret_cast<uint4*>(p + half) = r.hi;
+}
+// (x.lo, x.hi) turned by the angles whose cosines and sines are cs and sn, as rope_turn does,
+// two pairs to an instruction
 __device__ __forceinline__ void turn_pairs(Pairs& x, const float (&sn)[8], const float (&cs)[8]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        float a, b;
-        rope_turn(x.lo[e], x.hi[e], cs[e], sn[e], a, b);
-        x.lo[e] = a;
-        x.hi[e] = b;
+    for (int e = 0; e < 8; e += 2) {
+        const uint64_t a = f2_make(x.lo[e], x.lo[e + 1]), b = f2_make(x.hi[e], x.hi[e + 1]);
+        const uint64_t s = f2_make(sn[e], sn[e + 1]), c = f2_make(cs[e], cs[e + 1]), m = f2_make(-sn[e], -sn[e + 1]);
+        f2_split(f2_fma(a, c, f2_mul(b, m)), x.lo[e], x.lo[e + 1]);
+        f2_split(f2_fma(b, c, f2_mul(a, s)), x.hi[e], x.hi[e + 1]);
     }
 }
 
-constexpr int kWarps = 8;  // of a CTA, here and below
+constexpr int kWarps = 16;  // of an append's CTA; two CTAs to an SM leave 64 registers to a thread
+constexpr int kSms = 152;
 
 // ------------------------------------------------------- rows in 16 bits
-// One warp per (row, group of heads): lane l owns the 8 pairs of chunk l mod (hd/16) of
-// every head it meets, so that its sines and cosines serve all of them.  The heads are the
-// row's query heads (if they are turned), then, for 16-bit pages, its keys and values.
+// One warp per (row, group of heads): lane l owns the 8 pairs of chunk l mod (hd/16) of every
+// head it meets.  The row's sines and cosines are formed once by the warp, each lane a few,
+// and exchanged through shared memory.  The heads are the row's query heads (if they are
+// turned), then, for 16-bit pages, its keys and values, kAhead at a time; the first ones are
+// loaded before it is known where they go, so that the search and the page's lookup (four
+// dependent reads) overlap the rows' own latency.
 template <bool BF16, int HD>
 __device__ void append_rows(const PagedParams& P, bool kv, bool turn, int steps, int row_block, int group,
                             const TurnFreqs& fr) {
-    constexpr int kChunks = HD / 16, kHeads = 32 / kChunks;  // lanes of a head, heads of a step
+    constexpr int kChunks = HD / 16, kHeads = 32 / kChunks, kAhead = 2;  // lanes of a head, heads of a step
+    __shared__ float2 turns[kWarps][HD / 2 + 4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = row_block * kWarps + warp;
     if (r >= P.total) return;
+    const int c = lane % kChunks;
+    const int nq = P.q ? P.H : 0, heads = nq + (kv ? 2 * P.Hkv : 0);
+    const int h0 = group * steps * kHeads + lane / kChunks, h1 = min(heads, (group + 1) * steps * kHeads);
+    RawPairs raw[kAhead];
+    auto load = [&](int st) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int h = h0 + (st + k) * kHeads;
+            if (h >= h1) continue;
+            const void* from = h < nq ? P.q : h < nq + P.Hkv ? P.k : P.v;
+            const long long stride = h < nq ? P.q_stride : h < nq + P.Hkv ? P.k_stride : P.v_stride;
+            const int hh = h < nq ? h : h < nq + P.Hkv ? h - nq : h - nq - P.Hkv;
+            raw[k] = load_raw(from, r * stride + hh * HD + c * 8, HD / 2);
+        }
+    };
+    load(0);
     const RowSeq sq = row_seq(P, r);
     if (sq.b < 0) return;
     const long long pos = (long long)__ldg(P.lengths + sq.b) - (sq.end - r);
     if (pos < 0) return;  // a padding slot's row
-    const int nq = P.q ? P.H : 0;
-    const int pg = pos <= INT32_MAX ? page_of(P, sq.b, (int)(pos >> P.page_shift), lane == 0)
-                                    : page_of(P, sq.b, -1, lane == 0);
+    const int pg = page_of(P, sq.b, pos <= INT32_MAX ? (int)(pos >> P.page_shift) : -1, lane == 0);
     if (pg < 0) return;
     const int row = (int)pos & (P.page_size - 1);
-    const int c = lane % kChunks;
     float sn[8], cs[8];
     if (turn) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) turn_sincos((unsigned int)pos, fr.f[c * 8 + e], sn[e], cs[e]);
+        for (int i = 0; i < HD / 64; ++i) {
+            float2 t;
+            turn_sincos((unsigned int)pos, fr.f[lane + 32 * i], t.x, t.y);
+            turns[warp][lane + 32 * i] = t;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            const float4 t = *reinterpret_cast<const float4*>(&turns[warp][c * 8 + e]);
+            sn[e] = t.x, cs[e] = t.y, sn[e + 1] = t.z, cs[e + 1] = t.w;
+        }
     }
-    const int heads = nq + (kv ? 2 * P.Hkv : 0);
-#pragma unroll 4
-    for (int st = 0; st < steps; ++st) {
-        const int h = (group * steps + st) * kHeads + lane / kChunks;
-        if (h >= heads) break;
-        Pairs x;
-        if (h < nq) {
-            load_pairs<BF16>(x, P.q, r * P.q_stride + h * HD + c * 8, HD / 2);
-            if (turn) turn_pairs(x, sn, cs);
-            store_pairs<BF16>(x, P.q_out, ((long long)r * P.H + h) * HD + c * 8, HD / 2);
-        } else {
-            const bool is_v = h - nq >= P.Hkv;
+    for (int st = 0; st < steps; st += kAhead) {
+        if (st > 0) load(st);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int h = h0 + (st + k) * kHeads;
+            if (h >= h1) continue;
+            const bool is_v = h >= nq + P.Hkv;
             const int hk = h - nq - (is_v ? P.Hkv : 0);
-            load_pairs<BF16>(x, is_v ? P.v : P.k, r * (is_v ? P.v_stride : P.k_stride) + hk * HD + c * 8, HD / 2);
-            if (turn && !is_v) turn_pairs(x, sn, cs);
-            store_pairs<BF16>(x, is_v ? P.v_cache : P.k_cache, cache_row(P, pg, hk, row) + c * 8, HD / 2);
+            void* to = h < nq ? P.q_out : is_v ? P.v_cache : P.k_cache;
+            const long long at = h < nq ? ((long long)r * P.H + h) * HD + c * 8 : cache_row(P, pg, hk, row) + c * 8;
+            if (turn && !is_v) {
+                Pairs x;
+                unpack_pairs<BF16>(x, raw[k]);
+                turn_pairs(x, sn, cs);
+                store_pairs<BF16>(x, to, at, HD / 2);
+            } else {
+                store_raw(raw[k], to, at, HD / 2);
+            }
         }
     }
 }
 
 // ------------------------------------------------------- blocks in 8 bits
-// One CTA per (sequence's page, KV head, keys or values): the block's scale needs the
-// largest magnitude of all its new rows before the first code can be written.
+// kTeam threads per (sequence's page, keys or values), for some KV heads one after the other:
+// a head's block needs the largest magnitude of all its new rows before its first code can be
+// written, and a thread's 16 elements stay in its registers from the one to the other.  A
+// thread keeps its row and columns from head to head, so its sines and cosines serve them
+// all, and the next head's elements are fetched ahead.  A block of more than 16 kTeam elements
+// (pages of 128 and 256 tokens) is gone through piece by piece, twice.
 //
 // The pages that a call touches are numbered without a pass over the prefix sums:
 // sequence b owns the numbers cu[b]/page + 2b .. cu[b+1]/page + 2b + 1, at least as many
 // as the pages that its rows can touch, so a number finds its sequence by one search.
-template <bool BF16, int HD, int CACHE>
-__device__ void append_block(const PagedParams& P, bool turn, int number, int head, bool is_v, const TurnFreqs& fr) {
+template <bool BF16, int HD, int CACHE, int kTeam>
+__device__ void append_blocks(const PagedParams& P, bool turn, int number, int head0, int head1, bool is_v,
+                              const TurnFreqs& fr) {
     constexpr int kChunks = HD / 16;
-    constexpr int kThreads = kWarps * 32;
-    __shared__ float red[kWarps];
-    const int tid = threadIdx.x, page = P.page_size;
+    __shared__ float red[2][kWarps];
+    const int tid = threadIdx.x % kTeam, team = threadIdx.x / kTeam;
     const int b = warp_last_le(P.B, number,
                                [&](int i) { return (long long)(__ldg(P.cu + i) >> P.page_shift) + 2 * i; });
     if (b < 0) return;
     const int first = __ldg(P.cu + b), end = __ldg(P.cu + b + 1);
+    const long long len = __ldg(P.lengths + b);
     if (first < 0 || end < first || end > P.total) {
         if (tid == 0 && end != first) atomicOr(P.status, ST_PAGED_BOUNDS);
         return;
     }
     if (first == end) return;
-    const long long len = __ldg(P.lengths + b);
     const long long p0 = len - (end - first);  // position of the sequence's first new row
     const long long start = p0 < 0 ? 0 : p0;
     const long long j = (start >> P.page_shift) + (number - ((first >> P.page_shift) + 2 * b));
@@ -164,109 +212,134 @@ __device__ void append_block(const PagedParams& P, bool turn, int number, int he
     const int pg = page_of(P, b, j <= INT32_MAX ? (int)j : -1, tid == 0);
     if (pg < 0) return;
     const int n_old = (int)(lo - (j << P.page_shift));  // rows of the page that an earlier call stored
-    const int rows = (int)(hi - lo);
     const void* src = is_v ? P.v : P.k;
     const long long src_stride = is_v ? P.v_stride : P.k_stride;
-    const long long src_row = first + (lo - p0);
-    uint8_t* cache = static_cast<uint8_t*>(is_v ? P.v_cache : P.k_cache) + cache_row(P, pg, head, 0);
-    float* scale_at = (is_v ? P.v_scale : P.k_scale) + (long long)pg * P.Hkv + head;
+    const long long src_at = (first + (lo - p0)) * src_stride;
     const bool turned = turn && !is_v;
-    (void)page;
+    const int tasks = (int)(hi - lo) * kChunks;  // of 16 elements each
+    const bool once = tasks <= kTeam;
+    const int c = tid % kChunks;
 
-    const int tasks = rows * kChunks;
-    auto load = [&](int t, Pairs& x) {
-        const int i = t / kChunks, c = t % kChunks;
-        load_pairs<BF16>(x, src, (src_row + i) * src_stride + head * HD + c * 8, HD / 2);
-        if (turned) {
-            float sn[8], cs[8];
+    float sn[8], cs[8];
+    auto angles = [&](int t) {
+        if (turned && t < tasks) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) turn_sincos((unsigned int)(lo + i), fr.f[c * 8 + e], sn[e], cs[e]);
-            turn_pairs(x, sn, cs);
+            for (int e = 0; e < 8; ++e) turn_sincos((unsigned int)(lo + t / kChunks), fr.f[c * 8 + e], sn[e], cs[e]);
         }
     };
-    float amax = 0.f;
-    for (int t = tid; t < tasks; t += kThreads) {
-        Pairs x;
-        load(t, x);
+    auto fetch = [&](int h, int t, RawPairs& raw) {
+        if (t < tasks) raw = load_raw(src, src_at + (t / kChunks) * src_stride + h * HD + c * 8, HD / 2);
+    };
+    Pairs x;
+    auto value = [&](int t, const RawPairs& raw) {
+        if (t >= tasks) return;
+        unpack_pairs<BF16>(x, raw);
+        if (turned) turn_pairs(x, sn, cs);
+    };
+    RawPairs raw;
+    fetch(head0, tid, raw);
+    angles(tid);
+    for (int h = head0; h < head1; ++h) {
+        float* scale_at = (is_v ? P.v_scale : P.k_scale) + (long long)pg * P.Hkv + h;
+        const float old = n_old > 0 ? *scale_at : 0.f;
+        float amax = 0.f;
+        for (int t = tid; t - tid < tasks; t += kTeam) {
+            if (!once) {
+                fetch(h, t, raw);
+                angles(t);
+            }
+            value(t, raw);
+            if (t >= tasks) continue;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            // what is not finite has no part in the scale
-            const float a = fabsf(x.lo[e]), d = fabsf(x.hi[e]);
-            amax = fmaxf(amax, a < INFINITY ? a : 0.f);
-            amax = fmaxf(amax, d < INFINITY ? d : 0.f);
-        }
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if ((tid & 31) == 0) red[tid >> 5] = amax;
-    const float old = n_old > 0 ? *scale_at : 0.f;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) amax = fmaxf(amax, red[w]);
-    // smallest power of two s with amax <= 1.75 * 2^kTopExp * s, at least 2^-64
-    const uint32_t bits = __float_as_uint(amax);
-    int ex = (int)(bits >> 23) - 127 - F8<CACHE>::kTopExp + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-    ex = max(ex, -64);
-    float s = __uint_as_float((uint32_t)(ex + 127) << 23);
-    if (n_old > 0) {
-        if (old >= s) {
-            s = old;
-        } else {
-            // the rows that are there, in units of the grown scale
-            const float ratio = old / s;
-            uint32_t* w = reinterpret_cast<uint32_t*>(cache);
-            for (int i = tid; i < n_old * HD / 4; i += kThreads) {
-                const uint32_t x = w[i];
-                const float2 u = h2_to_f2(f8x2_to_h2<CACHE>(x & 0xffffu)), v = h2_to_f2(f8x2_to_h2<CACHE>(x >> 16));
-                w[i] = f8x2_from_f<CACHE>(u.x * ratio, u.y * ratio) |
-                       (f8x2_from_f<CACHE>(v.x * ratio, v.y * ratio) << 16);
+            for (int e = 0; e < 8; ++e) {
+                // what is not finite has no part in the scale
+                const float a = fabsf(x.lo[e]), d = fabsf(x.hi[e]);
+                amax = fmaxf(amax, a < INFINITY ? a : 0.f);
+                amax = fmaxf(amax, d < INFINITY ? d : 0.f);
             }
         }
-    }
-    // a scale of this library is a power of two (its inverse exact); a block that another
-    // program began may have any
-    const bool pow2 = (__float_as_uint(s) & 0x7fffffu) == 0u;
-    const float inv = 1.f / s;
-    for (int t = tid; t < tasks; t += kThreads) {
-        Pairs x;
-        load(t, x);
-        if (pow2) {
+        if (once && h + 1 < head1) fetch(h + 1, tid, raw);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x.lo[e] *= inv, x.hi[e] *= inv;
-        } else {
+        for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        if constexpr (kTeam > 32) {
+            float* mine = red[h & 1] + team * (kTeam / 32);
+            if ((tid & 31) == 0) mine[tid >> 5] = amax;
+            named_bar_sync(1 + team, kTeam);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x.lo[e] /= s, x.hi[e] /= s;
+            for (int w = 0; w < kTeam / 32; ++w) amax = fmaxf(amax, mine[w]);
         }
-        const int i = t / kChunks, c = t % kChunks;
-        uint8_t* out = cache + (n_old + i) * HD + c * 8;
-        auto word = [](const float* y) {
-            return f8x2_from_f<CACHE>(y[0], y[1]) | (f8x2_from_f<CACHE>(y[2], y[3]) << 16);
-        };
-        *reinterpret_cast<uint2*>(out) = make_uint2(word(x.lo), word(x.lo + 4));
-        *reinterpret_cast<uint2*>(out + HD / 2) = make_uint2(word(x.hi), word(x.hi + 4));
+        // smallest power of two s with amax <= 1.75 * 2^kTopExp * s, at least 2^-64
+        const uint32_t bits = __float_as_uint(amax);
+        int ex = (int)(bits >> 23) - 127 - F8<CACHE>::kTopExp + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+        ex = max(ex, -64);
+        float s = __uint_as_float((uint32_t)(ex + 127) << 23);
+        uint8_t* cache = static_cast<uint8_t*>(is_v ? P.v_cache : P.k_cache) + cache_row(P, pg, h, 0);
+        if (n_old > 0) {
+            if (old >= s) {
+                s = old;
+            } else {
+                // the rows that are there, in units of the grown scale
+                const float ratio = old / s;
+                uint32_t* w = reinterpret_cast<uint32_t*>(cache);
+                for (int i = tid; i < n_old * HD / 4; i += kTeam) {
+                    const uint32_t y = w[i];
+                    const float2 u = h2_to_f2(f8x2_to_h2<CACHE>(y & 0xffffu)), v = h2_to_f2(f8x2_to_h2<CACHE>(y >> 16));
+                    w[i] = f8x2_from_f<CACHE>(u.x * ratio, u.y * ratio) |
+                           (f8x2_from_f<CACHE>(v.x * ratio, v.y * ratio) << 16);
+                }
+            }
+        }
+        // a scale of this library is a power of two (its inverse exact); a block that another
+        // program began may have any
+        const bool pow2 = (__float_as_uint(s) & 0x7fffffu) == 0u;
+        const float inv = 1.f / s;
+        for (int t = tid; t < tasks; t += kTeam) {
+            if (!once) {
+                fetch(h, t, raw);
+                angles(t);
+                value(t, raw);
+            }
+            if (pow2) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x.lo[e] *= inv, x.hi[e] *= inv;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x.lo[e] /= s, x.hi[e] /= s;
+            }
+            uint8_t* out = cache + (n_old + t / kChunks) * HD + c * 8;
+            auto word = [](const float* y) {
+                return f8x2_from_f<CACHE>(y[0], y[1]) | (f8x2_from_f<CACHE>(y[2], y[3]) << 16);
+            };
+            *reinterpret_cast<uint2*>(out) = make_uint2(word(x.lo), word(x.lo + 4));
+            *reinterpret_cast<uint2*>(out + HD / 2) = make_uint2(word(x.hi), word(x.hi + 4));
+        }
+        if (tid == 0) *scale_at = s;
     }
-    if (tid == 0) *scale_at = s;
 }
 
-// One launch: CTAs below row_ctas turn rows, the others store 8-bit blocks.
-template <bool BF16, int HD, int CACHE>
-__global__ void __launch_bounds__(kWarps * 32)
-    paged_append_kernel(const PagedParams P, int turn, int steps, int groups, int row_ctas,
+// One launch: CTAs below row_ctas turn rows, the others store 8-bit blocks, `per` heads of a
+// page's keys or values to each team.
+template <bool BF16, int HD, int CACHE, int kTeam>
+__global__ void __launch_bounds__(kWarps * 32, 2)
+    paged_append_kernel(const PagedParams P, int turn, int steps, int groups, int row_ctas, int units, int per,
                         const __grid_constant__ TurnFreqs fr) {
     if ((int)blockIdx.x < row_ctas) {
         append_rows<BF16, HD>(P, CACHE == CACHE_16, turn, steps, blockIdx.x / groups, blockIdx.x % groups, fr);
     } else if constexpr (CACHE != CACHE_16) {
-        const int u = blockIdx.x - row_ctas, per = 2 * P.Hkv;
-        append_block<BF16, HD, CACHE>(P, turn, u / per, (u % per) >> 1, u & 1, fr);
+        const int u = (blockIdx.x - row_ctas) * (kWarps * 32 / kTeam) + threadIdx.x / kTeam;
+        const int parts = (P.Hkv + per - 1) / per, which = u % (2 * parts), h = (which >> 1) * per;
+        if (u < units)
+            append_blocks<BF16, HD, CACHE, kTeam>(P, turn, u / (2 * parts), h, min(P.Hkv, h + per), which & 1, fr);
     }
 }
 
 // --------------------------------------------------------------- reading back
 // One warp per packed row.
+constexpr int kGatherWarps = 8;
 template <bool BF16, int HD, int CACHE>
-__global__ void __launch_bounds__(kWarps * 32) paged_gather_kernel(const PagedParams P) {
+__global__ void __launch_bounds__(kGatherWarps * 32) paged_gather_kernel(const PagedParams P) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int r = blockIdx.x * kWarps + warp;
+    const int r = blockIdx.x * kGatherWarps + warp;
     if (r >= P.total) return;
     const RowSeq sq = row_seq(P, r);
     if (sq.b < 0) return;
@@ -274,53 +347,93 @@ __global__ void __launch_bounds__(kWarps * 32) paged_gather_kernel(const PagedPa
     const int pg = page_of(P, sq.b, pos >> P.page_shift, lane == 0);
     const int row = pos & (P.page_size - 1);
     const int n = P.Hkv * HD / 8;  // 16-byte pieces of an output row
-    for (int i = lane; i < 2 * n; i += 32) {
-        const bool is_v = i >= n;
-        const int e = (is_v ? i - n : i) * 8, h = e / HD, d = e % HD;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (pg >= 0) {
+    constexpr int kAhead = 4;      // pieces of a lane in flight
+    for (int i0 = lane; i0 < 2 * n; i0 += 32 * kAhead) {
+        uint4 raw[kAhead];
+        float scale[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = i0 + 32 * k;
+            if (i >= 2 * n || pg < 0) continue;
+            const bool is_v = i >= n;
+            const int e = (is_v ? i - n : i) * 8, h = e / HD, d = e % HD;
             const long long at = cache_row(P, pg, h, row) + d;
             const void* cache = is_v ? P.v_cache : P.k_cache;
             if constexpr (CACHE == CACHE_16) {
-                w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(cache) + at));
+                raw[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(cache) + at));
             } else {
                 const uint2 x = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(cache) + at));
-                const float s = __ldg((is_v ? P.v_scale : P.k_scale) + (long long)pg * P.Hkv + h);
-                auto two = [&](uint32_t c) {
-                    const float2 f = h2_to_f2(f8x2_to_h2<CACHE>(c));
-                    return pack2<BF16>(f.x * s, f.y * s);
-                };
-                w = make_uint4(two(x.x & 0xffffu), two(x.x >> 16), two(x.y & 0xffffu), two(x.y >> 16));
+                raw[k].x = x.x, raw[k].y = x.y;
+                scale[k] = __ldg((is_v ? P.v_scale : P.k_scale) + (long long)pg * P.Hkv + h);
             }
         }
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(is_v ? P.v_out : P.k_out) + (long long)r * P.Hkv * HD + e) = w;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = i0 + 32 * k;
+            if (i >= 2 * n) continue;
+            const bool is_v = i >= n;
+            uint4 w = make_uint4(0, 0, 0, 0);  // a page outside the pool reads as zeros
+            if (pg >= 0) {
+                if constexpr (CACHE == CACHE_16) {
+                    w = raw[k];
+                } else {
+                    auto two = [&](uint32_t c) {
+                        const float2 f = h2_to_f2(f8x2_to_h2<CACHE>(c));
+                        return pack2<BF16>(f.x * scale[k], f.y * scale[k]);
+                    };
+                    w = make_uint4(two(raw[k].x & 0xffffu), two(raw[k].x >> 16), two(raw[k].y & 0xffffu), two(raw[k].y >> 16));
+                }
+            }
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(is_v ? P.v_out : P.k_out) + (long long)r * P.Hkv * HD +
+                                      (is_v ? i - n : i) * 8) = w;
+        }
     }
 }
 
 template <bool BF16, int HD, int CACHE>
 cudaError_t append_typed(const PagedParams& p, double theta, cudaStream_t s) {
-    constexpr int kHeads = 32 / (HD / 16);
+    constexpr int kPieces = HD / 16, kHeads = 32 / kPieces;
     TurnFreqs fr = {};
     if (theta > 0) fr = turn_freqs(HD, theta);
     const int heads = (p.q ? p.H : 0) + (CACHE == CACHE_16 ? 2 * p.Hkv : 0);
     const long long row_blocks = (p.total + kWarps - 1) / kWarps;
     const int all = (heads + kHeads - 1) / kHeads;
-    int steps = 1;
-    while (steps < 4 && row_blocks * ((all + steps - 1) / steps) > 152 * 8) steps *= 2;
+    // steps of a warp: few where that fills no more than the SMs' warps, else four
+    int steps = 2;
+    if (row_blocks * ((all + 1) / 2) > kSms * 4LL) steps = 4;
     const int groups = (all + steps - 1) / steps;
     const long long row_ctas = row_blocks * groups;
-    long long blocks = 0;
-    if (CACHE != CACHE_16) blocks = ((long long)(p.total >> p.page_shift) + 2LL * p.B) * 2 * p.Hkv;
-    if (row_ctas + blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-    if (row_ctas + blocks == 0) return cudaSuccess;
-    paged_append_kernel<BF16, HD, CACHE><<<(unsigned)(row_ctas + blocks), kWarps * 32, 0, s>>>(
-        p, theta > 0 ? 1 : 0, steps, groups, (int)row_ctas, fr);
-    return cudaGetLastError();
+    long long units = 0, unit_ctas = 0;
+    int per = 1, team = 32;
+    if (CACHE != CACHE_16) {
+        const long long numbers = (long long)(p.total >> p.page_shift) + 2LL * p.B;
+        // threads of a page's block: a warp where the call brings few rows to a sequence,
+        // 128 where a page has no more than 128 pieces of 16 elements, else the CTA
+        const long long tasks = (long long)p.page_size * kPieces;
+        team = (long long)p.total * kPieces <= 64LL * p.B ? 32 : tasks <= 128 ? 128 : 512;
+        // heads of a team: as many as leave every SM some CTAs
+        while (per < 4 && per < p.Hkv && numbers * 2 * (p.Hkv / (2 * per)) * team >= kSms * 4LL * 512) per *= 2;
+        units = numbers * 2 * ((p.Hkv + per - 1) / per);
+        unit_ctas = (units * team + kWarps * 32 - 1) / (kWarps * 32);
+    }
+    if (row_ctas + unit_ctas > INT32_MAX || units > INT32_MAX) return cudaErrorInvalidConfiguration;
+    if (row_ctas + unit_ctas == 0) return cudaSuccess;
+    auto launch = [&](auto t) {
+        paged_append_kernel<BF16, HD, CACHE, decltype(t)::value>
+            <<<(unsigned)(row_ctas + unit_ctas), kWarps * 32, 0, s>>>(p, theta > 0 ? 1 : 0, steps, groups, (int)row_ctas,
+                                                                     (int)units, per, fr);
+        return cudaGetLastError();
+    };
+    if constexpr (CACHE != CACHE_16) {
+        if (team == 32) return launch(std::integral_constant<int, 32>());
+        if (team == 128) return launch(std::integral_constant<int, 128>());
+    }
+    return launch(std::integral_constant<int, 512>());
 }
 
 template <bool BF16, int HD, int CACHE>
 cudaError_t gather_typed(const PagedParams& p, cudaStream_t s) {
-    paged_gather_kernel<BF16, HD, CACHE><<<(p.total + kWarps - 1) / kWarps, kWarps * 32, 0, s>>>(p);
+    paged_gather_kernel<BF16, HD, CACHE><<<(p.total + kGatherWarps - 1) / kGatherWarps, kGatherWarps * 32, 0, s>>>(p);
     return cudaGetLastError();
 }
 
