@@ -398,9 +398,9 @@ cudaError_t append_typed(const PagedParams& p, double theta, cudaStream_t s) {
     const int heads = (p.q ? p.H : 0) + (CACHE == CACHE_16 ? 2 * p.Hkv : 0);
     const long long row_blocks = (p.total + kWarps - 1) / kWarps;
     const int all = (heads + kHeads - 1) / kHeads;
-    // steps of a warp: few where that fills no more than the SMs' warps, else four
+    // steps of a warp: few where that fills no more than the SMs' warps, else eight
     int steps = 2;
-    if (row_blocks * ((all + 1) / 2) > kSms * 4LL) steps = 4;
+    if (row_blocks * ((all + 1) / 2) > kSms * 4LL) steps = 8;
     const int groups = (all + steps - 1) / steps;
     const long long row_ctas = row_blocks * groups;
     long long units = 0, unit_ctas = 0;
