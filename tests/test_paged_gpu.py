@@ -213,6 +213,7 @@ def test_decode_what_a_row_does_not_see_has_no_effect(dt, kind):
     kw = dict(H=4, window=50, **c.kw())
     o0, l0 = A.attn_paged_decode(q, c.k, c.v, c.table_d, i32(lengths), **kw)
     check_decode(c, q, lengths, o0, l0, window=50)
+    tokens = c.tokens(lengths)
     bad = [NAN[kind], 0x7f] if is8(kind) else [float("nan"), float("inf")]
     for w, pool in enumerate((c.k, c.v)):
         raw = pool.view(torch.uint8) if is8(kind) else pool
@@ -222,10 +223,12 @@ def test_decode_what_a_row_does_not_see_has_no_effect(dt, kind):
                 raw[int(c.table[b, t // 16]), :, t % 16] = bad[w]
     o, lse = A.attn_paged_decode(q, c.k, c.v, c.table_d, i32(lengths), **kw)
     status_ok()
-    # the middle row's result is what it was (its sums may run in another order)
-    assert (np.abs(f64(o[:, 1]) - f64(o0[:, 1])) <= 2 * U[dt] * np.abs(f64(o0[:, 1])) + 2.0 ** -16).all()
-    assert (np.abs(f64(lse[:, :, 1]) - f64(l0[:, :, 1])) <= 2.0 ** -18).all()
     assert torch.isnan(o[:, 0]).all() and torch.isnan(o[:, 2]).all()
+    # The middle row sees neither: it is held to the finite tokens' result, with a result's own
+    # tolerance (its P may be rounded relative to another maximum than before, so that it
+    # need not be the same bits).
+    o[:, [0, 2]], lse[:, :, [0, 2]] = o0[:, [0, 2]], l0[:, :, [0, 2]]
+    check_decode(c, q, lengths, o, lse, tokens=tokens, window=50)
 
 
 def test_decode_rows_that_see_nothing():
