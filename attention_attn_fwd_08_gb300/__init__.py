@@ -754,7 +754,7 @@ def attn_paged_append(k, v, k_cache, v_cache, page_table, lengths, cu_new, *, H,
     st = (_lib or lib()).attn_paged_append(rd, cd, k.data_ptr(), ks, v.data_ptr(), vs, _addr(q), qs, _addr(q_out),
                                            k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale),
                                            cu_new.data_ptr(), lengths.data_ptr(), page_table.data_ptr(), B, n, num_pages,
-                                           page_size, max_pages, H, Hkv, hd, rope_theta or 0.0, handle)
+                                           page_size, max_pages, H, Hkv, hd, float(rope_theta or 0.0), handle)
     if st != OK:
         _check(st, "attn_paged_append")
     return q_out
@@ -802,7 +802,7 @@ def attn_paged_decode(q, k_cache, v_cache, page_table, lengths, *, H, Hkv, k_sca
     st = L.attn_paged_decode(rd, cd, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale),
                              _addr(v_scale), o.data_ptr(), _addr(lse), workspace.data_ptr(), workspace.nbytes,
                              lengths.data_ptr(), page_table.data_ptr(), B, Lq, num_pages, page_size, max_pages, H, Hkv, hd,
-                             hd ** -0.5 if scale is None else scale, 1 if causal else 0, window, softcap, handle)
+                             hd ** -0.5 if scale is None else float(scale), 1 if causal else 0, int(window), float(softcap), handle)
     if st != OK:
         _check(st, "attn_paged_decode")
     return o, lse

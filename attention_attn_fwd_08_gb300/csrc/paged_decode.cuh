@@ -49,6 +49,7 @@ constexpr int kSms = 152;
 constexpr int kMaxCtasPerSm = 3;
 constexpr int kMaxCtas = kSms * kMaxCtasPerSm;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kFailed = INT32_MAX;
 // p = 2^(score - ref) with ref kBias below the largest score when it is set.  In the usual
 // tile p is multiplied by its group's vs / vref before it is rounded: with that ratio at least
 // kRatioLo, fp16's finest step (2^-24) lies 2^-24 or more below the largest p's product, as
@@ -177,25 +178,29 @@ __device__ __forceinline__ int item_cost(int tiles) { return tiles > 0 ? tiles +
 struct Deal {
     long long all, share;
 };
-// Sums over all sequences, by each warp for itself (no barrier; 32 loads in flight).
-// (`before`: the cost of one KV head of the sequences before `upto`)
-__device__ __forceinline__ Deal deal_tiles(const PagedParams& P, int ctas, int upto = 0, long long* before = nullptr) {
+// Sums over all sequences, by the whole CTA (`sums`: two shared numbers to a warp; ends after a
+// barrier).  `before`: the cost of one KV head of the sequences before `upto`.
+__device__ __forceinline__ Deal deal_tiles(const PagedParams& P, int ctas, long long (*sums)[2], int upto,
+                                           long long& before) {
     const int lane = threadIdx.x & 31;
     long long sum = 0, part = 0;
 #pragma unroll 4
-    for (int b = lane; b < P.B; b += 32) {
+    for (int b = threadIdx.x; b < P.B; b += blockDim.x) {
         const int n = item_cost(seq_tiles(P, b).n);
         sum += n;
-        if (before && b < upto) part += n;
+        if (b < upto) part += n;
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
         sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (before) part += __shfl_xor_sync(0xffffffffu, part, o);
+        part += __shfl_xor_sync(0xffffffffu, part, o);
     }
-    if (before) *before = part;
+    if (lane == 0) sums[threadIdx.x >> 5][0] = sum, sums[threadIdx.x >> 5][1] = part;
+    __syncthreads();
     Deal d;
-    d.all = sum * P.Hkv;
+    d.all = before = 0;
+    for (int w = 0; w < (int)blockDim.x / 32; ++w) d.all += sums[w][0], before += sums[w][1];
+    d.all *= P.Hkv;
     d.share = (d.all + ctas - 1) / ctas;
     return d;
 }
@@ -237,12 +242,18 @@ __device__ __forceinline__ int stretch_tiles(int tiles, int& off, long long& lef
     off = max(off - kItemCost, 0);
     return max(end - kItemCost - off, 0);
 }
-// the next item with tiles
+// the next item with tiles, by the whole warp: 32 sequences at a time
 __device__ __forceinline__ void next_item(const PagedParams& P, int& b, int& h) {
     if (++h < P.Hkv) return;
     h = 0;
-    do ++b;
-    while (b < P.B && seq_tiles(P, b).n == 0);
+    const int lane = threadIdx.x & 31;
+    for (++b; b < P.B; b += 32) {
+        const unsigned some = __ballot_sync(0xffffffffu, b + lane < P.B && seq_tiles(P, b + lane).n > 0);
+        if (some) {
+            b += __ffs(some) - 1;
+            return;
+        }
+    }
 }
 
 // kBf: the rows (and 16-bit pools) are bfloat16; over 8-bit pools a run-time choice
@@ -264,8 +275,9 @@ __global__ void __launch_bounds__(DecShape<HD, CACHE, RT>::kThreads, DecShape<HD
     __shared__ float4 meta[S::kStages][4];  // of the tile's groups of 16 keys: ks, vs / vref, its log2, its inverse
     __shared__ float vrefs[S::kStages];
     __shared__ int there[S::kStages];  // bits 0-3: groups that were loaded; bit 4: scales out of the usual
-    __shared__ int raised[2];          // the last tile (as the CTA counts them) with a score too high
+    __shared__ int raised[2];  // the last tile (as the CTA counts them) with a score too high; kFailed: a wait ran out
     __shared__ int abort_flag;
+    __shared__ long long sums[S::kThreads / 32][2];
     const uint32_t ring = smem_u32(smem);
     auto full_bar = [&](int s) { return smem_u32(bars + s); };
     auto empty_bar = [&](int s) { return smem_u32(bars + S::kStages + s); };
@@ -281,8 +293,8 @@ __global__ void __launch_bounds__(DecShape<HD, CACHE, RT>::kThreads, DecShape<HD
         raised[0] = raised[1] = 0;
         fence_barrier_init();
     }
-    const Deal deal = deal_tiles(P, gridDim.x);
-    __syncthreads();  // publishes the barriers
+    long long before;
+    const Deal deal = deal_tiles(P, gridDim.x, sums, 0, before);  // (its barrier publishes the ring's)
     // the merging kernel's CTAs may come up from here on (all of this kernel's are running)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const long long first = min(deal.all, (long long)blockIdx.x * deal.share);
@@ -406,7 +418,7 @@ __global__ void __launch_bounds__(DecShape<HD, CACHE, RT>::kThreads, DecShape<HD
     float2* ws_ml = reinterpret_cast<float2*>(P.ws);
     float* ws_o = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(P.ws) + ws_o_offset(R));
     int stage = 0, phase = 0, tiles = 0;
-    bool ok = true;
+    bool failed = false;
     float vref = 1.f;
     // this thread's places in a tile: its K row's chunk, its V rows' chunks, its rows of P
     constexpr int kBoxBytes = kKeys * S::kRowBytes;
@@ -511,8 +523,9 @@ __global__ void __launch_bounds__(DecShape<HD, CACHE, RT>::kThreads, DecShape<HD
         for (int rt = 0; rt < RT; ++rt) l[rt][0] = l[rt][1] = 0.f;
 
         for (int i = 0; i < n; ++i) {
-            ok = ok && mbar_wait(full_bar(stage), phase, P.status, ST_DEC_WAIT, &abort_flag);
-            __syncwarp();
+            // A warp whose wait ran out says so before the tile's first barrier, and all stop there
+            // (another way and some would wait at a barrier that the others never reach).
+            if (!warp_wait(full_bar(stage), phase, P.status, ST_DEC_WAIT, &abort_flag)) atomicMax(&raised[i & 1], kFailed);
             const int j0 = (sq.t0 + off + i) * kKeys, have = there[stage], buf = i & 1;
             const uint32_t base = ring + (uint32_t)(stage * S::kStageBytes);
             if (k8 && i == 0) vref = vrefs[stage];
@@ -635,6 +648,7 @@ __global__ void __launch_bounds__(DecShape<HD, CACHE, RT>::kThreads, DecShape<HD
                             if (t == 0) maxima[(buf * S::kRows + rt * 16 + g + 8 * r) * S::kW + warp] = m;
                         }
                     named_bar_sync(1, S::kW * 32);
+                    if ((failed = raised[buf] == kFailed)) break;
 #pragma unroll
                     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
@@ -668,9 +682,11 @@ __global__ void __launch_bounds__(DecShape<HD, CACHE, RT>::kThreads, DecShape<HD
                             part[rt][r] += p2 + p3;
                         }
                     }
-                if (high) raised[buf] = tiles;
+                if (high) atomicMax(&raised[buf], tiles);
                 named_bar_sync(1, S::kW * 32);
-                done = raised[buf] != tiles;
+                const int last = raised[buf];
+                done = last < tiles;
+                if ((failed = last == kFailed)) break;
                 if (done) {
 #pragma unroll
                     for (int rt = 0; rt < RT; ++rt) {
@@ -725,6 +741,7 @@ __global__ void __launch_bounds__(DecShape<HD, CACHE, RT>::kThreads, DecShape<HD
                     }
                 if constexpr (kNt == 1) {  // two warps to a group
                     named_bar_sync(1, S::kW * 32);
+                    if ((failed = raised[buf] == kFailed)) break;
 #pragma unroll
                     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
@@ -749,6 +766,7 @@ __global__ void __launch_bounds__(DecShape<HD, CACHE, RT>::kThreads, DecShape<HD
                         }
                     }
                 named_bar_sync(1, S::kW * 32);
+                if ((failed = raised[buf] == kFailed)) break;
                 float f[RT][2][4];
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt)
@@ -849,7 +867,9 @@ __global__ void __launch_bounds__(DecShape<HD, CACHE, RT>::kThreads, DecShape<HD
             if (++stage == S::kStages) stage = 0, phase ^= 1;
         }
 
-        // ---- the rows' sums: a row's quad, then the four warps
+        if (failed) break;
+
+        // ---- the rows' sums: a row's quad, then the warps
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
@@ -875,50 +895,48 @@ __global__ void __launch_bounds__(DecShape<HD, CACHE, RT>::kThreads, DecShape<HD
         const bool begins = off == 0, ends = off + n == sq.n;
         const bool whole = begins && ends;
         const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
-        if (ok) {
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
+        for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = rt * 16 + g + 8 * e;
-                    if (r >= R) continue;
-                    const int gg = r / P.Lq, lq = r - gg * P.Lq;
-                    const int hq = h * P.G + gg;
-                    const bool none = ref[rt][e] == -INFINITY;
-                    // O / vref in units of 2^ref, l in units of 2^ref
-                    const float mul = whole ? (none ? 0.f : vref / l[rt][e]) : vref;
-                    uint16_t* od = static_cast<uint16_t*>(P.o) + (((long long)b * P.Lq + lq) * P.H + hq) * HD;
-                    float* wd = ws_o + ((long long)slot * R + r) * HD;
-                    auto two = [&](float x, float y) { return bf ? pack2<true>(x, y) : pack2<false>(x, y); };
-                    if constexpr (k8) {
+            for (int e = 0; e < 2; ++e) {
+                const int r = rt * 16 + g + 8 * e;
+                if (r >= R) continue;
+                const int gg = r / P.Lq, lq = r - gg * P.Lq;
+                const int hq = h * P.G + gg;
+                const bool none = ref[rt][e] == -INFINITY;
+                // O / vref in units of 2^ref, l in units of 2^ref
+                const float mul = whole ? (none ? 0.f : vref / l[rt][e]) : vref;
+                uint16_t* od = static_cast<uint16_t*>(P.o) + (((long long)b * P.Lq + lq) * P.H + hq) * HD;
+                float* wd = ws_o + ((long long)slot * R + r) * HD;
+                auto two = [&](float x, float y) { return bf ? pack2<true>(x, y) : pack2<false>(x, y); };
+                if constexpr (k8) {
 #pragma unroll
-                        for (int c = 0; c < S::kN; c += 2) {
-                            const int d = (warp * S::kN + c) * 8 + 4 * t;
-                            const float x0 = o[rt][c][2 * e] * mul, x1 = o[rt][c + 1][2 * e] * mul,
-                                        x2 = o[rt][c][2 * e + 1] * mul, x3 = o[rt][c + 1][2 * e + 1] * mul;
-                            if (whole) *reinterpret_cast<uint2*>(od + d) = make_uint2(two(x0, x1), two(x2, x3));
-                            else *reinterpret_cast<float4*>(wd + d) = make_float4(x0, x1, x2, x3);
-                        }
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < S::kN; ++c) {
-                            const int d = (warp * S::kN + c) * 8 + 2 * t;
-                            const float x0 = o[rt][c][2 * e] * mul, x1 = o[rt][c][2 * e + 1] * mul;
-                            if (whole) *reinterpret_cast<uint32_t*>(od + d) = two(x0, x1);
-                            else *reinterpret_cast<float2*>(wd + d) = make_float2(x0, x1);
-                        }
+                    for (int c = 0; c < S::kN; c += 2) {
+                        const int d = (warp * S::kN + c) * 8 + 4 * t;
+                        const float x0 = o[rt][c][2 * e] * mul, x1 = o[rt][c + 1][2 * e] * mul,
+                                    x2 = o[rt][c][2 * e + 1] * mul, x3 = o[rt][c + 1][2 * e + 1] * mul;
+                        if (whole) *reinterpret_cast<uint2*>(od + d) = make_uint2(two(x0, x1), two(x2, x3));
+                        else *reinterpret_cast<float4*>(wd + d) = make_float4(x0, x1, x2, x3);
                     }
-                    if (warp == 0 && t == 0) {
-                        if (whole) {
-                            if (P.lse)
-                                P.lse[((long long)b * P.H + hq) * P.Lq + lq] =
-                                    none ? -INFINITY : (ref[rt][e] + log2f(l[rt][e])) * 0.6931471805599453f;
-                        } else {
-                            ws_ml[(long long)slot * R + r] = make_float2(ref[rt][e], l[rt][e]);
-                        }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < S::kN; ++c) {
+                        const int d = (warp * S::kN + c) * 8 + 2 * t;
+                        const float x0 = o[rt][c][2 * e] * mul, x1 = o[rt][c][2 * e + 1] * mul;
+                        if (whole) *reinterpret_cast<uint32_t*>(od + d) = two(x0, x1);
+                        else *reinterpret_cast<float2*>(wd + d) = make_float2(x0, x1);
                     }
                 }
-        }
+                if (warp == 0 && t == 0) {
+                    if (whole) {
+                        if (P.lse)
+                            P.lse[((long long)b * P.H + hq) * P.Lq + lq] =
+                                none ? -INFINITY : (ref[rt][e] + log2f(l[rt][e])) * 0.6931471805599453f;
+                    } else {
+                        ws_ml[(long long)slot * R + r] = make_float2(ref[rt][e], l[rt][e]);
+                    }
+                }
+            }
         off = 0;
         if (left > 0) next_item(P, b, h);
     }
@@ -943,12 +961,13 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams P,
                                                             const int by_item, const int rows_per_cta) {
     constexpr int kPer = HD / 32;  // columns of a lane
     __shared__ float part[8][HD];
+    __shared__ long long sums[8][2];
     int b, h, cta;      // the item, and the stretch that it begins in
     int n = 0;          // its parts: that stretch's end, and the beginnings of the next ones
+    long long before;
+    const Deal deal = deal_tiles(P, ctas, sums, by_item ? blockIdx.x / P.Hkv : 0, before);
     if (by_item) {
         b = blockIdx.x / P.Hkv, h = blockIdx.x % P.Hkv;
-        long long before;
-        const Deal deal = deal_tiles(P, ctas, b, &before);
         const int tiles = seq_tiles(P, b).n;
         if (tiles > 0) {
             const long long first = before * P.Hkv + (long long)h * item_cost(tiles) + kItemCost;  // its first tile
@@ -957,7 +976,6 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams P,
         }
     } else {
         cta = blockIdx.x;
-        const Deal deal = deal_tiles(P, ctas);
         const long long first = (long long)cta * deal.share, last = min(deal.all, first + deal.share) - 1;
         if (first <= last) {
             const Place at = place_of(P, last);

@@ -231,6 +231,101 @@ def test_decode_what_a_row_does_not_see_has_no_effect(dt, kind):
     check_decode(c, q, lengths, o, lse, tokens=tokens, window=50)
 
 
+@pytest.mark.parametrize("kind,Lq", [("bf16", 1), ("f16", 4), ("e4m3", 1), ("e5m2", 4), ("e4m3", 9)])
+@pytest.mark.parametrize("hd", [64, 256])
+@pytest.mark.parametrize("softcap", [0.0, 60.0])
+def test_decode_scores_that_climb(kind, Lq, hd, softcap):
+    """Keys that grow along the sequence: the rows' references have to move again and again, by more
+    than 16 bits of p hold; and some that fall back, whose p are far below the reference's."""
+    lengths = [900, 333]
+    dt = "f16" if kind == "f16" else "bf16"
+    c = Cache(dt, kind, lengths, 2, hd, 16, seed=41)
+    c.fill(lengths, 41, unequal=False)
+    q = torch.randn((2, Lq, 4 * hd), generator=torch.Generator().manual_seed(7)).to(T[dt]).to(DEV)
+    grow = [1.0, 1.0, 4.0, 4.0, 12.0, 30.0, 1.0, 50.0]
+    for b, n in enumerate(lengths):
+        for j in range((n + 15) // 16):
+            m = grow[j % len(grow)] if b else 1.0 + j
+            pg = int(c.table[b, j])
+            if is8(kind):
+                c.ks[pg] *= m
+            else:
+                c.k[pg] *= m
+    kw = dict(scale=0.5 / math.sqrt(hd), softcap=softcap)
+    o, lse = A.attn_paged_decode(q, c.k, c.v, c.table_d, i32(lengths), H=4, **c.kw(), **kw)
+    status_ok()
+    check_decode(c, q, lengths, o, lse, **kw)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("page,Lq", [(16, 1), (16, 3), (64, 1), (128, 5)])
+def test_decode_scales_unlike_each_other(kind, page, Lq):
+    """Scales of zero (blocks of zeros), of the first block alone, of either sign, 2^-40 to 2^20 apart."""
+    lengths = [700, 260, 700, 300]
+    c = Cache("bf16", kind, lengths, 2, 128, page, seed=43)
+    c.fill(lengths, 43)
+    for b in range(4):
+        for j in range((lengths[b] + page - 1) // page):
+            pg = int(c.table[b, j])
+            if b == 0 and j % 3 == 1:
+                c.vs[pg] = 0.0
+            if b == 0 and j % 3 == 2:
+                c.ks[pg, 0], c.ks[pg, 1] = 0.0, -c.ks[pg, 1]
+            if b == 1:
+                c.vs[pg] *= 2.0 ** (20 - 12 * (j % 6))
+            if b == 2 and j == 0:
+                c.vs[pg] = 0.0
+            if b == 3:
+                c.vs[pg, 0] *= -1.0
+    q = torch.randn((4, Lq, 8 * 128), generator=torch.Generator().manual_seed(8)).to(torch.bfloat16).to(DEV)
+    o, lse = A.attn_paged_decode(q, c.k, c.v, c.table_d, i32(lengths), H=8, **c.kw())
+    status_ok()
+    check_decode(c, q, lengths, o, lse)
+
+
+def test_decode_sequences_that_share_pages():
+    """A common prefix: several sequences' tables name the same pages."""
+    c = Cache("bf16", "e4m3", [200, 200, 200], 2, 64, 16, seed=44)
+    c.fill([200, 200, 200], 44)
+    c.table[1, :8] = c.table[0, :8]
+    c.table[2, :5] = c.table[0, :5]
+    c.table_d = i32(c.table)
+    q = torch.randn((3, 1, 4 * 64), generator=torch.Generator().manual_seed(9)).to(torch.bfloat16).to(DEV)
+    o, lse = A.attn_paged_decode(q, c.k, c.v, c.table_d, i32([130, 200, 77]), H=4, **c.kw())
+    status_ok()
+    check_decode(c, q, [130, 200, 77], o, lse)
+
+
+@pytest.mark.parametrize("kind", ["f16", "e4m3"])
+def test_decode_mostly_empty_slots(kind):
+    """A large padded batch: long runs of slots without a token, a few sequences among them."""
+    lengths = [0] * 1500
+    for b, n in ((3, 70), (4, 1), (640, 500), (1111, 64), (1112, 130), (1499, 17)):
+        lengths[b] = n
+    c, q, o, lse = run_decode("f16", kind, lengths, 4, 2, 64, 16, 2, seed=45)
+    assert (o[700:1111] == 0).all()
+
+
+def test_decode_two_calls_at_once():
+    """Two streams, each call with the workspace that the binding makes for it."""
+    calls = []
+    for i, lengths in enumerate(([3000, 17, 900], [64, 2100, 5])):
+        c = Cache("bf16", "e4m3", lengths, 4, 128, 16, seed=46 + i)
+        c.fill(lengths, 46 + i)
+        q = torch.randn((3, 2, 16 * 128), generator=torch.Generator().manual_seed(i)).to(torch.bfloat16).to(DEV)
+        calls.append((c, q, lengths, i32(lengths), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for k, (c, q, lengths, ld, stream) in enumerate(calls):
+            got[k].append(A.attn_paged_decode(q, c.k, c.v, c.table_d, ld, H=16, stream=stream, **c.kw()))
+    status_ok()
+    for k, (c, q, lengths, ld, stream) in enumerate(calls):
+        check_decode(c, q, lengths, *got[k][0])
+        for o, lse in got[k][1:]:
+            np.testing.assert_array_equal(bits(o), bits(got[k][0][0]))
+
+
 def test_decode_rows_that_see_nothing():
     """A block longer than its sequence: the rows at negative positions see nothing."""
     c, q, o, lse = run_decode("bf16", "e4m3", [0, 2, 0], 4, 2, 64, 16, 5, seed=3)
