@@ -85,12 +85,16 @@ struct DecShape {
     static constexpr int kPBytes = 2 * kRows * kPPitch;
     static constexpr int kMlBytes = 2 * kRows * kW * 4;  // two buffers of a number by row and warp
     static constexpr int kFixed = kQBytes + kPBytes + kMlBytes + kRows * 4 + 2048;  // + row scales, alignment, barriers
-    // the most CTAs of an SM whose ring keeps at least three tiles each; the ring's depth
+    // The most CTAs of an SM whose ring keeps at least three tiles each, and whose warps have the
+    // registers that more row tiles need: two with more than one (e4m3, hd 128, 32 rows over
+    // 16 x 32768 tokens: 222 us, three 256; hd 64, 64 rows: 586, three 1019), one with four at
+    // hd 128 over 8-bit pools (64 rows: 523, two 624); and the ring's depth.
+    static constexpr int kMost = RT == 1 ? 3 : RT == 4 && HD == 128 && k8 ? 1 : 2;
     static constexpr int stages(int ctas) {
         const int s = (227 * 1024 / ctas - 1024 - kFixed - 512) / kStageBytes;
         return s > 8 ? 8 : s;
     }
-    static constexpr int kCtas = stages(3) >= 3 ? 3 : stages(2) >= 3 ? 2 : 1;
+    static constexpr int kCtas = kMost == 3 && stages(3) >= 3 ? 3 : kMost >= 2 && stages(2) >= 3 ? 2 : 1;
     static constexpr int kStages = stages(kCtas);
     static constexpr int kBytes = kStages * kStageBytes + kFixed;
     // Q fragments stay in registers where they take at most 64

@@ -174,8 +174,9 @@ def test_decode_groups_and_draft_rows(kind, page, H, Hkv, Lq):
     run_decode("bf16", kind, [3, 129, 300, 1, 16], H, Hkv, 64, page, Lq, seed=H * 31 + Lq + page)
 
 
-@pytest.mark.parametrize("hd,G,Lq", [(128, 8, 8), (256, 4, 16), (128, 1, 1), (256, 2, 9), (128, 5, 7)])
-@pytest.mark.parametrize("kind", ["f16", "e4m3"])
+@pytest.mark.parametrize("hd,G,Lq", [(128, 8, 8), (256, 4, 16), (128, 1, 1), (256, 2, 9), (128, 5, 7), (64, 8, 3), (128, 8, 4),
+                                     (128, 3, 6), (64, 2, 16), (64, 4, 13), (256, 8, 3)])
+@pytest.mark.parametrize("kind", ["f16", "e4m3", "e5m2"])
 def test_decode_many_rows_wide_heads(hd, G, Lq, kind):
     run_decode("f16", kind, [131, 2, 777], 2 * G, 2, hd, 32, Lq, seed=hd + G)
 
