@@ -346,32 +346,34 @@ __global__ void __launch_bounds__(kGatherWarps * 32) paged_gather_kernel(const P
     const int pos = r - sq.first;
     const int pg = page_of(P, sq.b, pos >> P.page_shift, lane == 0);
     const int row = pos & (P.page_size - 1);
-    const int n = P.Hkv * HD / 8;  // 16-byte pieces of an output row
-    constexpr int kAhead = 4;      // pieces of a lane in flight
-    for (int i0 = lane; i0 < 2 * n; i0 += 32 * kAhead) {
+    // Lane l owns 8 elements of every kStep-th head: the row's key heads, then its value heads,
+    // kAhead of its pieces in flight.
+    constexpr int kStep = 256 / HD, kAhead = 4;
+    const int d = lane * 8 % HD, heads = 2 * P.Hkv;
+    const long long head_at = (long long)P.page_size * HD;  // from head to head of a page
+    const long long at = pg < 0 ? 0 : cache_row(P, pg, 0, row) + d, out = (long long)r * P.Hkv * HD + d;
+    const long long scale_at = (long long)max(pg, 0) * P.Hkv;
+#pragma unroll 1
+    for (int x0 = lane * 8 / HD; x0 < heads; x0 += kStep * kAhead) {
         uint4 raw[kAhead];
         float scale[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            const int i = i0 + 32 * k;
-            if (i >= 2 * n || pg < 0) continue;
-            const bool is_v = i >= n;
-            const int e = (is_v ? i - n : i) * 8, h = e / HD, d = e % HD;
-            const long long at = cache_row(P, pg, h, row) + d;
-            const void* cache = is_v ? P.v_cache : P.k_cache;
+            const int x = x0 + k * kStep, h = x < P.Hkv ? x : x - P.Hkv;
+            if (x >= heads || pg < 0) continue;
+            const void* cache = x < P.Hkv ? P.k_cache : P.v_cache;
             if constexpr (CACHE == CACHE_16) {
-                raw[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(cache) + at));
+                raw[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(cache) + at + h * head_at));
             } else {
-                const uint2 x = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(cache) + at));
-                raw[k].x = x.x, raw[k].y = x.y;
-                scale[k] = __ldg((is_v ? P.v_scale : P.k_scale) + (long long)pg * P.Hkv + h);
+                const uint2 y = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(cache) + at + h * head_at));
+                raw[k].x = y.x, raw[k].y = y.y;
+                scale[k] = __ldg((x < P.Hkv ? P.k_scale : P.v_scale) + scale_at + h);
             }
         }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            const int i = i0 + 32 * k;
-            if (i >= 2 * n) continue;
-            const bool is_v = i >= n;
+            const int x = x0 + k * kStep, h = x < P.Hkv ? x : x - P.Hkv;
+            if (x >= heads) continue;
             uint4 w = make_uint4(0, 0, 0, 0);  // a page outside the pool reads as zeros
             if (pg >= 0) {
                 if constexpr (CACHE == CACHE_16) {
@@ -384,8 +386,7 @@ __global__ void __launch_bounds__(kGatherWarps * 32) paged_gather_kernel(const P
                     w = make_uint4(two(raw[k].x & 0xffffu), two(raw[k].x >> 16), two(raw[k].y & 0xffffu), two(raw[k].y >> 16));
                 }
             }
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(is_v ? P.v_out : P.k_out) + (long long)r * P.Hkv * HD +
-                                      (is_v ? i - n : i) * 8) = w;
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(x < P.Hkv ? P.k_out : P.v_out) + out + h * HD) = w;
         }
     }
 }
