@@ -654,8 +654,12 @@ def _on(device, stream):
     if stream is None:
         at = device.index
         return torch._C._cuda_getCurrentRawStream(at), None if torch.cuda.current_device() == at else torch.cuda.device(at)
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if getattr(stream, "device", device) != device:
+        raise ValueError("the stream is of %s, the tensors are on %s" % (stream.device, device))
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        # (torch would take a handle of 0, the default stream's, as a wish for a new one)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
     return stream.cuda_stream, torch.cuda.stream(stream)
 
 

@@ -770,6 +770,22 @@ def test_calls_on_another_stream():
     assert (np.abs(f64(vv)[[299, 376]] - 1) <= U["e4m3"] + 2 * U["bf16"]).all() and torch.isfinite(qo.float()).all()
 
 
+def test_calls_on_the_default_stream_by_its_handle():
+    """A handle of 0 is the default stream, whatever the current one is: the call waits for the lengths."""
+    c = Cache("f16", "f16", [90], 2, 64, 16, seed=20)
+    c.fill([90], 20)
+    q = torch.randn((1, 2, 4 * 64), generator=torch.Generator().manual_seed(2)).to(torch.float16).to(DEV)
+    ld, new = i32([0]), i32([90])
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20000000)
+    ld.copy_(new)
+    with torch.cuda.stream(torch.cuda.Stream()):
+        o, lse = A.attn_paged_decode(q, c.k, c.v, c.table_d, ld, H=4, stream=0, **c.kw())
+    torch.cuda.synchronize()
+    status_ok()
+    check_decode(c, q, [90], o, lse)
+
+
 def test_pages_past_four_gigabytes():
     """Offsets that pass 32 bits, in the pool of each type."""
     for dt, kind, hd in (("bf16", "e4m3", 128), ("f16", "f16", 64)):

@@ -229,3 +229,11 @@ def test_binding_refuses_wrong_decode_tensors(kw, what):
 def test_binding_refuses_wrong_gather_tensors(kw, what):
     with pytest.raises(ValueError, match=what):
         _on_gpu_shapes(call_gather, cache(), **kw)
+
+
+def test_binding_refuses_a_stream_of_another_device():
+    class Stream:
+        cuda_stream, device = 17, torch.device("cuda", 1)
+
+    with pytest.raises(ValueError, match="stream"):
+        A._on(torch.device("cuda", 0), Stream())
