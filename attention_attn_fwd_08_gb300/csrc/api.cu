@@ -1120,7 +1120,9 @@ attn_status attn_paged_decode(attn_dtype dt, attn_dtype cache_dt, const void* q,
     p.q = q; p.o = o; p.lse = lse; p.ws = static_cast<float*>(workspace);
     p.lengths = lengths; p.Lq = Lq;
     p.scale = scale; p.softcap = softcap;
-    p.wl = window > 0 ? window - 1 : -1;
+    // a window that leaves out no token that there can be is none (and a position less it stays an int)
+    const long long most = (long long)max_pages * page_size + Lq;
+    p.wl = window > 0 && window <= most ? window - 1 : -1;
     p.wr = causal ? 0 : p.wl;
     PagedMaps maps;
     const long long rows = (long long)num_pages * Hkv * page_size;

@@ -380,7 +380,9 @@ __global__ void __launch_bounds__(DecShape<HD, CACHE, RT>::kThreads, DecShape<HD
                     if constexpr (k8) {
                         if (i == 0) {  // the batch's scales, needed only now
                             if (vref == 0.f) {
-                                const unsigned fit = __ballot_sync(0xffffffffu, pg >= 0 && sc.y > 1e-18f && sc.y < 1e18f);
+                                // (from 2^-30 on: with a scale of 2^40 elsewhere and 2^31 codes of 2^16, times 2^6
+                                // for p, the sums in its units stay below 2^123)
+                                const unsigned fit = __ballot_sync(0xffffffffu, pg >= 0 && sc.y >= 0x1p-30f && sc.y < 1e18f);
                                 vref = fit ? __shfl_sync(0xffffffffu, sc.y, __ffs(fit) - 1) : 1.f;
                             }
                             const float ratio = sc.y / vref;

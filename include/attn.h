@@ -427,13 +427,16 @@ ATTN_API attn_status attn_bwd_rope(attn_dtype dt, const void* q, const void* k, 
  *   dt        : ATTN_F16 or ATTN_BF16, the type of the rows (ATTN_F32: UNSUPPORTED).
  *   cache_dt  : the pools' type: dt, or ATTN_E4M3 / ATTN_E5M2 with k_scale and v_scale
  *               [num_pages][Hkv] fp32: an element is its 8-bit value times the scale of its
- *               page and head.  The scales are not read for 16-bit pools (NULL is fine).
+ *               page and head.  The scales are not read for 16-bit pools (NULL is fine).  Finite
+ *               scales of magnitude 2^40 or less are meant: with larger ones an
+ *               output may overflow on the way.
  *   page_size : 16, 32, 64, 128 or 256.   hd : 64, 128 or 256.   H <= 65535, Hkv divides H.
  *   num_pages * Hkv * page_size and max_pages * page_size are at most 2^31 - 512.
  * No access leaves the pools whatever the device arrays hold.  A page number outside
  * [0, num_pages), a token at or past max_pages * page_size, or a prefix sum that decreases
  * or leaves [0, total] makes attn_get_device_status() return ATTN_ERR_INVALID_ARG; the
- * tokens concerned are not stored, not attended, or read back as zeros.
+ * tokens concerned are not stored (nor is their q_out written), not attended, or read back
+ * as zeros.  Decode over no page at all (num_pages or max_pages 0) reads no device array.
  * Launch shapes depend on the host arguments alone: a captured graph may be replayed after
  * lengths, prefix sums, page table, scales or pages changed.
  *

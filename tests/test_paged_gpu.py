@@ -189,6 +189,13 @@ def test_decode_masks(kind, flags):
     run_decode("bf16", kind, [300, 5, 64, 66, 1], 4, 2, 128, 16, 4, seed=5, **flags)
 
 
+@pytest.mark.parametrize("window", [2**31 - 1, 2**31 - 8, 640 + 9, 640 + 8, 639])
+@pytest.mark.parametrize("causal", [False, True])
+def test_decode_widest_windows(window, causal):
+    """Rows at negative positions, under windows wider than the cache and just not."""
+    run_decode("f16", "f16", [3, 7, 40, 640], 4, 2, 64, 16, 8, seed=46, window=window, causal=causal)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 def test_decode_long_and_ragged(kind):
     run_decode("bf16", kind, [5000, 1, 0, 2047, 130], 8, 2, 128, 64, 2, seed=8)
@@ -282,6 +289,22 @@ def test_decode_scales_unlike_each_other(kind, page, Lq):
     o, lse = A.attn_paged_decode(q, c.k, c.v, c.table_d, i32(lengths), H=8, **c.kw())
     status_ok()
     check_decode(c, q, lengths, o, lse)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("first", [2.0 ** -58, 2.0 ** -30, 1.0])
+def test_decode_scales_at_the_ends_of_their_range(kind, first):
+    """Small blocks before the largest ones, all codes the largest: no sum leaves fp32 on the way."""
+    n = 4000
+    c = Cache("bf16", kind, [n], 2, 64, 16, seed=47)
+    c.fill([n], 47)
+    c.v.view(torch.uint8).fill_({"e4m3": 0x7E, "e5m2": 0x7B}[kind])
+    c.vs.fill_(2.0 ** 40)
+    c.vs[int(c.table[0, 0])] = first
+    q = torch.randn((1, 2, 4 * 64), generator=torch.Generator().manual_seed(10)).to(torch.bfloat16).to(DEV)
+    o, lse = A.attn_paged_decode(q, c.k, c.v, c.table_d, i32([n]), H=4, **c.kw())
+    status_ok()
+    check_decode(c, q, [n], o, lse)
 
 
 def test_decode_sequences_that_share_pages():
