@@ -15,8 +15,8 @@
 //   * A producer warp keeps a ring of tiles in flight (TMA, 128-byte swizzle, one box for
 //     each run of a page's rows), page numbers and scales fetched 32 groups of 16 keys at a
 //     time, one batch ahead, by the lanes that hold them.
-//   * Four consumer warps (eight at hd 256) split each tile by keys for S = Q K^T and by
-//     columns of the head for O += P V: the probabilities go through shared memory, one barrier
+//   * A team of four consumer warps (eight at hd 256) splits each tile by keys for S = Q K^T and
+//     by columns of the head for O += P V (two teams of four share the tiles of many rows): the probabilities go through shared memory, one barrier
 //     a tile, and no warp holds more than its share of O, so that three CTAs fit an SM.
 //   * p is relative to a reference of its row that the warps know alike and that moves only
 //     when a score passes it by far, so that in the usual tile no maximum is exchanged and P V
@@ -62,7 +62,7 @@ constexpr float kBias = 6.f, kTopLog2 = 15.f, kRatioLo = 1.f / 64, kRatioHi = 32
 __host__ __device__ inline size_t ws_o_offset(int R) { return (size_t)kMaxCtas * 2 * R * 8; }
 inline size_t ws_bytes(int R, int hd) { return ws_o_offset(R) + (size_t)kMaxCtas * 2 * R * hd * 4; }
 
-template <int HD, int CACHE, int RT>
+template <int HD, int CACHE, int kRowTiles>
 struct DecShape {
     static constexpr bool k8 = CACHE != CACHE_16;
     static constexpr int kEs = k8 ? 1 : 2;
@@ -70,26 +70,35 @@ struct DecShape {
     static constexpr int kBoxes = HD * kEs / kRowBytes;                // side by side
     static constexpr int kTileBytes = kKeys * HD * kEs;                // of K or of V
     static constexpr int kStageBytes = 2 * kTileBytes;
+    // Teams of consumer warps that share the ring, each with half of the rows, and row tiles of
+    // 16 of each: two where one team's warps would hold too many rows' state and be too few to
+    // hide their latencies (64 rows over 16 x 32768 tokens, hd 128: 490 us, one team 524 (e4m3)
+    // and 517 (bf16); e5m2, hd 256, 32 x 8192 tokens: 32 rows 142 against 154, 48 rows 310 against
+    // 379); at hd 64 and with fewer rows one team does, whose codes are converted once (64 rows,
+    // hd 64: 586 against 693; 32 rows, hd 128, e4m3: 222 against 357).
+    static constexpr int kTeams = (HD > 64 && kRowTiles == 4) || (HD == 256 && kRowTiles == 2) ? 2 : 1;
+    static constexpr int RT = kRowTiles / kTeams;
     static constexpr int kRows = RT * 16;
-    // Consumer warps; keys of a tile that each scores; 8-column products of its share of the
+    // Warps of a team; keys of a tile that each scores; 8-column products of its share of the
     // head.  At hd 256 the ring leaves room for two CTAs: eight warps each, with half a tile's
     // work, hide its latencies better than four (e5m2, 32 x 8192 tokens: 95 against 129 us); at
     // hd 128 three CTAs of four warps do (e4m3, 16 x 32768 tokens: 170 against 277 us).
-    static constexpr int kW = HD == 256 ? 8 : 4;
-    static constexpr int kThreads = kW * 32 + 32;
+    static constexpr int kW = HD == 256 && kTeams == 1 ? 8 : 4;
+    static constexpr int kConsumers = kTeams * kW * 32;
+    static constexpr int kThreads = kConsumers + 32;
     static constexpr int kWk = kKeys / kW, kNt = kWk / 8;
     static constexpr int kN = HD / 8 / kW;
     static constexpr int kQPitch = HD * 2 + 16;  // 16 past a multiple of 128: eight rows' chunks in eight places
     static constexpr int kPPitch = kKeys * 2 + 16;
-    static constexpr int kQBytes = kRows * kQPitch;
+    static constexpr int kQBytes = kRows * kQPitch;      // of a team, as the next two
     static constexpr int kPBytes = 2 * kRows * kPPitch;
     static constexpr int kMlBytes = 2 * kRows * kW * 4;  // two buffers of a number by row and warp
-    static constexpr int kFixed = kQBytes + kPBytes + kMlBytes + kRows * 4 + 2048;  // + row scales, alignment, barriers
+    static constexpr int kFixed = kTeams * (kQBytes + kPBytes + kMlBytes + kRows * 4) + 2048;  // + row scales, alignment, barriers
     // The most CTAs of an SM whose ring keeps at least three tiles each, and whose warps have the
     // registers that more row tiles need: two with more than one (e4m3, hd 128, 32 rows over
-    // 16 x 32768 tokens: 222 us, three 256; hd 64, 64 rows: 586, three 1019), one with four at
-    // hd 128 over 8-bit pools (64 rows: 523, two 624); and the ring's depth.
-    static constexpr int kMost = RT == 1 ? 3 : RT == 4 && HD == 128 && k8 ? 1 : 2;
+    // 16 x 32768 tokens: 222 us, three 256; hd 64, 64 rows: 586, three 1019), one of two teams;
+    // and the ring's depth.
+    static constexpr int kMost = kTeams == 2 ? 1 : RT == 1 ? 3 : 2;
     static constexpr int stages(int ctas) {
         const int s = (227 * 1024 / ctas - 1024 - kFixed - 512) / kStageBytes;
         return s > 8 ? 8 : s;
@@ -97,8 +106,8 @@ struct DecShape {
     static constexpr int kCtas = kMost == 3 && stages(3) >= 3 ? 3 : kMost >= 2 && stages(2) >= 3 ? 2 : 1;
     static constexpr int kStages = stages(kCtas);
     static constexpr int kBytes = kStages * kStageBytes + kFixed;
-    // Q fragments stay in registers where they take at most 64
-    static constexpr bool kQReg = kW == 4 && (RT == 1 || RT * HD <= 128);
+    // Q fragments stay in registers where they take at most 32
+    static constexpr bool kQReg = kW == 4 && RT * HD <= 128;
     static_assert(kStages >= 2, "ring too shallow");
 };
 
@@ -261,40 +270,38 @@ __device__ __forceinline__ void next_item(const PagedParams& P, int& b, int& h) 
 }
 
 // kBf: the rows (and 16-bit pools) are bfloat16; over 8-bit pools a run-time choice
-template <int HD, int CACHE, int RT, bool kBf>
-__global__ void __launch_bounds__(DecShape<HD, CACHE, RT>::kThreads, DecShape<HD, CACHE, RT>::kCtas)
+template <int HD, int CACHE, int kRowTiles, bool kBf>
+__global__ void __launch_bounds__(DecShape<HD, CACHE, kRowTiles>::kThreads, DecShape<HD, CACHE, kRowTiles>::kCtas)
     paged_split_kernel(const PagedParams P, const int rows_bf16, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV) {
-    using S = DecShape<HD, CACHE, RT>;
+    using S = DecShape<HD, CACHE, kRowTiles>;
+    constexpr int RT = S::RT;
     constexpr bool k8 = S::k8;
     constexpr bool kMmaBf = !k8 && kBf;  // type of the products
     const bool bf = k8 ? rows_bf16 != 0 : kBf;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* qs = smem + S::kStages * S::kStageBytes;
-    uint8_t* ps = qs + S::kQBytes;
-    float* maxima = reinterpret_cast<float*>(ps + S::kPBytes);  // [2][rows][warps]
-    float* qscale = maxima + 2 * S::kRows * S::kW;              // [rows]
     __shared__ __align__(8) uint64_t bars[2 * S::kStages];
     __shared__ float4 meta[S::kStages][4];  // of the tile's groups of 16 keys: ks, vs / vref, its log2, its inverse
     __shared__ float vrefs[S::kStages];
     __shared__ int there[S::kStages];  // bits 0-3: groups that were loaded; bit 4: scales out of the usual
-    __shared__ int raised[2];  // the last tile (as the CTA counts them) with a score too high; kFailed: a wait ran out
+    __shared__ int raised_by[S::kTeams][2];  // the last tile (as the CTA counts them) with a score too high; kFailed: a wait ran out
     __shared__ int abort_flag;
     __shared__ long long sums[S::kThreads / 32][2];
     const uint32_t ring = smem_u32(smem);
     auto full_bar = [&](int s) { return smem_u32(bars + s); };
     auto empty_bar = [&](int s) { return smem_u32(bars + S::kStages + s); };
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31;
     const int R = P.G * P.Lq;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
             mbar_init(full_bar(s), k8 ? 2 : 1);  // the tile's bytes; over 8-bit pools, its scales
-            mbar_init(empty_bar(s), S::kW);
+            mbar_init(empty_bar(s), S::kTeams * S::kW);
         }
         abort_flag = 0;
-        raised[0] = raised[1] = 0;
+        for (int i = 0; i < S::kTeams; ++i) raised_by[i][0] = raised_by[i][1] = 0;
         fence_barrier_init();
     }
     long long before;
@@ -307,7 +314,7 @@ __global__ void __launch_bounds__(DecShape<HD, CACHE, RT>::kThreads, DecShape<HD
     if (left > 0) at = place_of(P, first);
     int b = at.b, h = at.h, off = at.off;
 
-    if (warp == S::kW) {
+    if (threadIdx.x >= S::kConsumers) {
         // ------------------------------------------------------------- producer
         if (lane == 0) {
             prefetch_tmap(&tmK);
@@ -420,7 +427,15 @@ __global__ void __launch_bounds__(DecShape<HD, CACHE, RT>::kThreads, DecShape<HD
 
     // ---------------------------------------------------------------- consumers
     const int g = lane >> 2, t = lane & 3, mi = lane >> 3, ri = lane & 7;
-    const int tid = threadIdx.x;
+    const int team = threadIdx.x / (S::kW * 32), warp = (threadIdx.x >> 5) % S::kW;  // warp of its team
+    const int row0 = team * S::kRows, bar = 1 + team;  // its first row, its barrier
+    qs += team * S::kQBytes;
+    uint8_t* ps = smem + S::kStages * S::kStageBytes + S::kTeams * S::kQBytes + team * S::kPBytes;
+    float* maxima = reinterpret_cast<float*>(smem + S::kStages * S::kStageBytes + S::kTeams * (S::kQBytes + S::kPBytes) +
+                                             team * S::kMlBytes);  // [2][rows][warps]
+    float* qscale = reinterpret_cast<float*>(smem + S::kStages * S::kStageBytes +
+                                             S::kTeams * (S::kQBytes + S::kPBytes + S::kMlBytes)) + row0;  // [rows]
+    int* raised = raised_by[team];
     float2* ws_ml = reinterpret_cast<float2*>(P.ws);
     float* ws_o = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(P.ws) + ws_o_offset(R));
     int stage = 0, phase = 0, tiles = 0;
@@ -452,13 +467,13 @@ __global__ void __launch_bounds__(DecShape<HD, CACHE, RT>::kThreads, DecShape<HD
         uint32_t qw[S::kRows / S::kW][kPer];
 #pragma unroll
         for (int i = 0; i < S::kRows / S::kW; ++i) {
-            const int r = warp + S::kW * i, gg = r / P.Lq, lq = r - gg * P.Lq;
+            const int r = row0 + warp + S::kW * i, gg = r / P.Lq, lq = r - gg * P.Lq;
             const uint32_t* src = reinterpret_cast<const uint32_t*>(
                 static_cast<const uint16_t*>(P.q) + (((long long)b * P.Lq + lq) * P.H + h * P.G + gg) * HD);
 #pragma unroll
             for (int e = 0; e < kPer; ++e) qw[i][e] = r < R ? __ldg(src + lane + 32 * e) : 0u;
         }
-        named_bar_sync(1, S::kW * 32);  // no warp reads the last item's rows any more
+        named_bar_sync(bar, S::kW * 32);  // no warp reads the last item's rows any more
 #pragma unroll
         for (int i = 0; i < S::kRows / S::kW; ++i) {
             const int r = warp + S::kW * i;
@@ -491,7 +506,7 @@ __global__ void __launch_bounds__(DecShape<HD, CACHE, RT>::kThreads, DecShape<HD
                     *reinterpret_cast<uint32_t*>(qs + r * S::kQPitch + 4 * (lane + 32 * e)) = w[e];
             }
         }
-        named_bar_sync(1, S::kW * 32);
+        named_bar_sync(bar, S::kW * 32);
         const uint32_t qaddr = smem_u32(qs) + ((mi & 1) * 8 + ri) * S::kQPitch + (mi >> 1) * 16;
         uint32_t qa[S::kQReg ? RT : 1][S::kQReg ? HD / 16 : 1][4];
         if constexpr (S::kQReg) {
@@ -510,10 +525,10 @@ __global__ void __launch_bounds__(DecShape<HD, CACHE, RT>::kThreads, DecShape<HD
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int r = rt * 16 + g + 8 * e, pos = sq.p0 + r % P.Lq;
+                const int in = rt * 16 + g + 8 * e, r = row0 + in, pos = sq.p0 + r % P.Lq;
                 vlo[rt][e] = r < R && P.wl >= 0 ? max(0, pos - P.wl) : 0;
                 vhi[rt][e] = r < R && P.wr >= 0 ? (int)min((long long)sq.len, (long long)pos + P.wr + 1) : sq.len;
-                qf[rt][e] = P.scale * (k8 ? qscale[r] : 1.f) * (P.softcap > 0.f ? 1.f : kLog2e);
+                qf[rt][e] = P.scale * (k8 ? qscale[in] : 1.f) * (P.softcap > 0.f ? 1.f : kLog2e);
                 ref[rt][e] = -INFINITY;
             }
         // tiles from full_lo to full_hi on are seen whole by every row (tile_full over j0)
@@ -653,7 +668,7 @@ __global__ void __launch_bounds__(DecShape<HD, CACHE, RT>::kThreads, DecShape<HD
                             m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
                             if (t == 0) maxima[(buf * S::kRows + rt * 16 + g + 8 * r) * S::kW + warp] = m;
                         }
-                    named_bar_sync(1, S::kW * 32);
+                    named_bar_sync(bar, S::kW * 32);
                     if ((failed = raised[buf] == kFailed)) break;
 #pragma unroll
                     for (int rt = 0; rt < RT; ++rt)
@@ -689,7 +704,7 @@ __global__ void __launch_bounds__(DecShape<HD, CACHE, RT>::kThreads, DecShape<HD
                         }
                     }
                 if (high) atomicMax(&raised[buf], tiles);
-                named_bar_sync(1, S::kW * 32);
+                named_bar_sync(bar, S::kW * 32);
                 const int last = raised[buf];
                 done = last < tiles;
                 if ((failed = last == kFailed)) break;
@@ -746,7 +761,7 @@ __global__ void __launch_bounds__(DecShape<HD, CACHE, RT>::kThreads, DecShape<HD
                         if (t == 0) maxima[(buf * S::kRows + rt * 16 + g + 8 * r) * S::kW + warp] = mx[rt][r];
                     }
                 if constexpr (kNt == 1) {  // two warps to a group
-                    named_bar_sync(1, S::kW * 32);
+                    named_bar_sync(bar, S::kW * 32);
                     if ((failed = raised[buf] == kFailed)) break;
 #pragma unroll
                     for (int rt = 0; rt < RT; ++rt)
@@ -771,7 +786,7 @@ __global__ void __launch_bounds__(DecShape<HD, CACHE, RT>::kThreads, DecShape<HD
                             sc[rt][0][2 * r] += p[2] + p[3];
                         }
                     }
-                named_bar_sync(1, S::kW * 32);
+                named_bar_sync(bar, S::kW * 32);
                 if ((failed = raised[buf] == kFailed)) break;
                 float f[RT][2][4];
 #pragma unroll
@@ -885,7 +900,7 @@ __global__ void __launch_bounds__(DecShape<HD, CACHE, RT>::kThreads, DecShape<HD
                 // (the half of the buffers that the last tile did not use)
                 if (t == 0) maxima[(((n & 1) * S::kRows) + rt * 16 + g + 8 * r) * S::kW + warp] = l[rt][r];
             }
-        named_bar_sync(1, S::kW * 32);
+        named_bar_sync(bar, S::kW * 32);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
@@ -905,7 +920,7 @@ __global__ void __launch_bounds__(DecShape<HD, CACHE, RT>::kThreads, DecShape<HD
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int r = rt * 16 + g + 8 * e;
+                const int r = row0 + rt * 16 + g + 8 * e;
                 if (r >= R) continue;
                 const int gg = r / P.Lq, lq = r - gg * P.Lq;
                 const int hq = h * P.G + gg;
@@ -949,12 +964,12 @@ __global__ void __launch_bounds__(DecShape<HD, CACHE, RT>::kThreads, DecShape<HD
 
     // sequences of which no row sees a key
     for (int e = blockIdx.x; e < P.B; e += gridDim.x) {
-        if (tid == 0 && __ldg(P.lengths + e) > (P.max_pages << P.page_shift)) atomicOr(P.status, ST_PAGED_BOUNDS);
+        if (threadIdx.x == 0 && __ldg(P.lengths + e) > (P.max_pages << P.page_shift)) atomicOr(P.status, ST_PAGED_BOUNDS);
         if (seq_tiles(P, e).n > 0) continue;
         uint4* od = reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.o) + (long long)e * P.Lq * P.H * HD);
-        for (int i = tid; i < P.Lq * P.H * HD / 8; i += S::kW * 32) od[i] = make_uint4(0, 0, 0, 0);
+        for (int i = threadIdx.x; i < P.Lq * P.H * HD / 8; i += S::kConsumers) od[i] = make_uint4(0, 0, 0, 0);
         if (P.lse)
-            for (int i = tid; i < P.Lq * P.H; i += S::kW * 32) P.lse[(long long)e * P.Lq * P.H + i] = -INFINITY;
+            for (int i = threadIdx.x; i < P.Lq * P.H; i += S::kConsumers) P.lse[(long long)e * P.Lq * P.H + i] = -INFINITY;
     }
 }
 
@@ -1081,10 +1096,10 @@ cudaError_t allow_smem(K k, int bytes, std::atomic<unsigned long long>& done) {
     return e;
 }
 
-template <int HD, int CACHE, int RT, bool kBf>
+template <int HD, int CACHE, int kRowTiles, bool kBf>
 cudaError_t decode_launch(const PagedParams& p, bool bf16, const PagedMaps& maps, cudaStream_t s) {
-    using S = DecShape<HD, CACHE, RT>;
-    auto k = paged_split_kernel<HD, CACHE, RT, kBf>;
+    using S = DecShape<HD, CACHE, kRowTiles>;
+    auto k = paged_split_kernel<HD, CACHE, kRowTiles, kBf>;
     static std::atomic<unsigned long long> done{0};
     cudaError_t e = allow_smem(k, S::kBytes, done);
     if (e != cudaSuccess) return e;
