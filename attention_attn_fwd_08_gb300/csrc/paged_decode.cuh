@@ -16,8 +16,9 @@
 //     each run of a page's rows), page numbers and scales fetched 32 groups of 16 keys at a
 //     time, one batch ahead, by the lanes that hold them.
 //   * A team of four consumer warps (eight at hd 256) splits each tile by keys for S = Q K^T and
-//     by columns of the head for O += P V (two teams of four share the tiles of many rows): the probabilities go through shared memory, one barrier
-//     a tile, and no warp holds more than its share of O, so that three CTAs fit an SM.
+//     by columns of the head for O += P V (two teams of four share the tiles of many rows): the
+//     probabilities go through shared memory, one barrier a tile, and no warp holds more than
+//     its share of O, so that three CTAs fit an SM.
 //   * p is relative to a reference of its row that the warps know alike and that moves only
 //     when a score passes it by far, so that in the usual tile no maximum is exchanged and P V
 //     accumulates in the products themselves; a page's vs enters as an addend of the exponent,
@@ -71,12 +72,13 @@ struct DecShape {
     static constexpr int kTileBytes = kKeys * HD * kEs;                // of K or of V
     static constexpr int kStageBytes = 2 * kTileBytes;
     // Teams of consumer warps that share the ring, each with half of the rows, and row tiles of
-    // 16 of each: two where one team's warps would hold too many rows' state and be too few to
-    // hide their latencies (64 rows over 16 x 32768 tokens, hd 128: 490 us, one team 524 (e4m3)
-    // and 517 (bf16); e5m2, hd 256, 32 x 8192 tokens: 32 rows 142 against 154, 48 rows 310 against
-    // 379); at hd 64 and with fewer rows one team does, whose codes are converted once (64 rows,
-    // hd 64: 586 against 693; 32 rows, hd 128, e4m3: 222 against 357).
-    static constexpr int kTeams = (HD > 64 && kRowTiles == 4) || (HD == 256 && kRowTiles == 2) ? 2 : 1;
+    // 16 of each team: two where one team's warps would hold too many rows' state and be too few
+    // to hide their latencies (16 x 32768 tokens, hd 128, 64 rows: 490 us, one team 524 (e4m3) and
+    // 517 (bf16); 32 rows, bf16: 334 against 346; e5m2, hd 256, 32 x 8192 tokens: 32 rows 142
+    // against 154, 48 rows 310 against 379).  One team converts each code once, which decides for
+    // 32 rows of 8-bit pages at hd 128 (222 against 357) and at hd 64 (64 rows: 586 against 693).
+    static constexpr bool kSplitTwo = HD == 256 || (HD == 128 && !k8);  // with two row tiles
+    static constexpr int kTeams = (HD > 64 && kRowTiles == 4) || (kSplitTwo && kRowTiles == 2) ? 2 : 1;
     static constexpr int RT = kRowTiles / kTeams;
     static constexpr int kRows = RT * 16;
     // Warps of a team; keys of a tile that each scores; 8-column products of its share of the
@@ -95,7 +97,7 @@ struct DecShape {
     static constexpr int kMlBytes = 2 * kRows * kW * 4;  // two buffers of a number by row and warp
     static constexpr int kFixed = kTeams * (kQBytes + kPBytes + kMlBytes + kRows * 4) + 2048;  // + row scales, alignment, barriers
     // The most CTAs of an SM whose ring keeps at least three tiles each, and whose warps have the
-    // registers that more row tiles need: two with more than one (e4m3, hd 128, 32 rows over
+    // registers that more row tiles need: two with more than one tile (e4m3, hd 128, 32 rows over
     // 16 x 32768 tokens: 222 us, three 256; hd 64, 64 rows: 586, three 1019), one of two teams;
     // and the ring's depth.
     static constexpr int kMost = kTeams == 2 ? 1 : RT == 1 ? 3 : 2;
