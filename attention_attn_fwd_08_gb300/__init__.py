@@ -16,6 +16,7 @@ key_mask fp32 [Tk] (shared) or [B, Tk].
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -764,6 +765,7 @@ def attn_paged_append(k, v, k_cache, v_cache, page_table, lengths, cu_new, *, H,
     return q_out
 
 
+@functools.lru_cache(maxsize=256)
 def attn_paged_decode_workspace_size(B, Lq, H, Hkv, hd) -> int:
     return int(lib().attn_paged_decode_workspace_size(int(B), int(Lq), int(H), int(Hkv), int(hd)))
 
@@ -802,7 +804,7 @@ def attn_paged_decode(q, k_cache, v_cache, page_table, lengths, *, H, Hkv, k_sca
     if lse is None and want_lse:
         lse = torch.empty((B, H, Lq), dtype=torch.float32, device=dev)
     if workspace is None:
-        workspace = torch.empty(L.attn_paged_decode_workspace_size(B, Lq, H, Hkv, hd), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(attn_paged_decode_workspace_size(B, Lq, H, Hkv, hd), dtype=torch.uint8, device=dev)
     st = L.attn_paged_decode(rd, cd, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale),
                              _addr(v_scale), o.data_ptr(), _addr(lse), workspace.data_ptr(), workspace.nbytes,
                              lengths.data_ptr(), page_table.data_ptr(), B, Lq, num_pages, page_size, max_pages, H, Hkv, hd,

@@ -13,6 +13,14 @@
 // max|x| <= top * s over the block's rows, so that dividing by it is exact, the code is the
 // only rounding, and a block whose scale grows in a later call has its earlier rows
 // divided by an exact power of two (only codes that become subnormal round again).
+//
+// All three move bytes: each element is read and written once.  What they reach (H32/8, hd 128):
+// four prompts of 2048 tokens into bf16 pages 39 us (201 MB, 5.2 TB/s; the copy rate is 6.8),
+// 12288 tokens in ragged chunks into e4m3 pages 63 us (277 MB, 4.4 TB/s), 32768 e4m3 tokens read
+// back as bf16 37 us (201 MB, 5.4 TB/s).  Between that and the copy rate stand about half of
+// the issue slots (unpacking, turning and packing; gather 74 %) at the 28 warps that an append's
+// registers leave an SM.  A step of one token for each of 64 sequences takes 7.5 us, a launch
+// and four dependent reads.
 #include <math.h>
 
 #include <type_traits>

@@ -30,6 +30,9 @@
 //     thread's 32 bits of a K fragment are four neighbouring columns, so the columns of Q
 //     are stored in the order that makes the products match; for V, ldmatrix.trans moves
 //     pairs of columns, and a byte permutation pairs the keys of the even and of the odd one.
+// It takes (16 x 32768 tokens, H32/8, hd 128) 169 us over e4m3 pages with one query row, 0.93 of
+// the measured copy rate, and 314 us over bf16 pages with four, all of it; 61 sequences of 5 to
+// 9973 tokens 112 us, 0.82.  One short sequence takes 11.7 us, the merge included.
 // mma.sync serves the 16 rows that a group usually has; tcgen05's least M (64) would leave
 // three quarters of it idle and need the codes converted through shared memory.
 #pragma once
