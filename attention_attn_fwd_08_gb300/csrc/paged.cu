@@ -16,7 +16,7 @@
 //
 // All three move bytes: each element is read and written once.  What they reach (H32/8, hd 128):
 // four prompts of 2048 tokens into bf16 pages 39 us (201 MB, 5.2 TB/s; the copy rate is 6.8),
-// 12288 tokens in ragged chunks into e4m3 pages 63 us (277 MB, 4.4 TB/s), 32768 e4m3 tokens read
+// 12288 tokens in ragged chunks into e4m3 pages 57 us (277 MB, 4.9 TB/s), 32768 e4m3 tokens read
 // back as bf16 37 us (201 MB, 5.4 TB/s).  Between that and the copy rate stand about half of
 // the issue slots (unpacking, turning and packing; gather 74 %) at the 28 warps that an append's
 // registers leave an SM.  A step of one token for each of 64 sequences takes 7.5 us, a launch
@@ -325,16 +325,18 @@ __device__ void append_blocks(const PagedParams& P, bool turn, int number, int h
     }
 }
 
-// One launch: CTAs below row_ctas turn rows, the others store 8-bit blocks, `per` heads of a
-// page's keys or values to each team.
+// One launch: the last row_ctas CTAs turn rows, those before them store 8-bit blocks, `per`
+// heads of a page's keys or values to each team (the blocks first: they take longer, and the
+// rows' short CTAs fill the end; the chunks above: 57 us, the rows first 60).
 template <bool BF16, int HD, int CACHE, int kTeam>
 __global__ void __launch_bounds__(kWarps * 32, 2)
     paged_append_kernel(const PagedParams P, int turn, int steps, int groups, int row_ctas, int units, int per,
                         const __grid_constant__ TurnFreqs fr) {
-    if ((int)blockIdx.x < row_ctas) {
-        append_rows<BF16, HD>(P, CACHE == CACHE_16, turn, steps, blockIdx.x / groups, blockIdx.x % groups, fr);
+    const int x = (int)blockIdx.x - ((int)gridDim.x - row_ctas);
+    if (x >= 0) {
+        append_rows<BF16, HD>(P, CACHE == CACHE_16, turn, steps, x / groups, x % groups, fr);
     } else if constexpr (CACHE != CACHE_16) {
-        const int u = (blockIdx.x - row_ctas) * (kWarps * 32 / kTeam) + threadIdx.x / kTeam;
+        const int u = blockIdx.x * (kWarps * 32 / kTeam) + threadIdx.x / kTeam;
         const int parts = (P.Hkv + per - 1) / per, which = u % (2 * parts), h = (which >> 1) * per;
         if (u < units)
             append_blocks<BF16, HD, CACHE, kTeam>(P, turn, u / (2 * parts), h, min(P.Hkv, h + per), which & 1, fr);
@@ -407,21 +409,26 @@ cudaError_t append_typed(const PagedParams& p, double theta, cudaStream_t s) {
     const int heads = (p.q ? p.H : 0) + (CACHE == CACHE_16 ? 2 * p.Hkv : 0);
     const long long row_blocks = (p.total + kWarps - 1) / kWarps;
     const int all = (heads + kHeads - 1) / kHeads;
-    // steps of a warp: few where that fills no more than the SMs' warps, else eight
-    int steps = 2;
-    if (row_blocks * ((all + 1) / 2) > kSms * 4LL) steps = 8;
-    const int groups = (all + steps - 1) / steps;
+    // steps of a warp: two where that fills no more than the SMs' warps, else a row's heads in
+    // equal parts of at most twelve (four: 65 against 63 us for the chunks above, before they
+    // were stored first)
+    const int most = row_blocks * ((all + 1) / 2) > kSms * 4LL ? 12 : 2;
+    const int groups = (all + most - 1) / most;
+    const int steps = groups ? ((all + groups - 1) / groups + 1) / 2 * 2 : 2;  // (even: two are loaded at a time)
     const long long row_ctas = row_blocks * groups;
     long long units = 0, unit_ctas = 0;
     int per = 1, team = 32;
     if (CACHE != CACHE_16) {
         const long long numbers = (long long)(p.total >> p.page_shift) + 2LL * p.B;
-        // threads of a page's block: a warp where the call brings few rows to a sequence,
-        // 128 where a page has no more than 128 pieces of 16 elements, else the CTA
-        const long long tasks = (long long)p.page_size * kPieces;
-        team = (long long)p.total * kPieces <= 64LL * p.B ? 32 : tasks <= 128 ? 128 : 512;
-        // heads of a team: as many as leave every SM some CTAs
-        while (per < 4 && per < p.Hkv && numbers * 2 * (p.Hkv / (2 * per)) * team >= kSms * 4LL * 512) per *= 2;
+        // threads of a page's block: a warp where the call brings few rows to a sequence, else
+        // as many as a page has pieces of 16 elements, up to the CTA
+        const int tasks = p.page_size * kPieces;
+        team = (long long)p.total * kPieces <= 64LL * p.B ? 32 : tasks <= 128 ? 128 : tasks <= 256 ? 256 : 512;
+        // heads of a team, which share its angles and whose loads it overlaps: as many as leave
+        // every SM a CTA (12288 tokens in chunks, hd 64: 33 us, four CTAs 37), or two where a block
+        // is gone through twice (pages of 128 tokens, hd 128: 70 us, one CTA 86, four 74)
+        const long long least = kSms * 512LL * (tasks <= 512 ? 1 : 2);
+        while (per < 8 && per < p.Hkv && numbers * 2 * (p.Hkv / (2 * per)) * team >= least) per *= 2;
         units = numbers * 2 * ((p.Hkv + per - 1) / per);
         unit_ctas = (units * team + kWarps * 32 - 1) / (kWarps * 32);
     }
@@ -436,6 +443,7 @@ cudaError_t append_typed(const PagedParams& p, double theta, cudaStream_t s) {
     if constexpr (CACHE != CACHE_16) {
         if (team == 32) return launch(std::integral_constant<int, 32>());
         if (team == 128) return launch(std::integral_constant<int, 128>());
+        if (team == 256) return launch(std::integral_constant<int, 256>());
     }
     return launch(std::integral_constant<int, 512>());
 }
