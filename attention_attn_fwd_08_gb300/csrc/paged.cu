@@ -16,7 +16,7 @@
 //
 // All three move bytes: each element is read and written once.  What they reach (H32/8, hd 128):
 // four prompts of 2048 tokens into bf16 pages 39 us (201 MB, 5.2 TB/s; the copy rate is 6.8),
-// 12288 tokens in ragged chunks into e4m3 pages 57 us (277 MB, 4.9 TB/s), 32768 e4m3 tokens read
+// 12288 tokens in ragged chunks into e4m3 pages 54 us (277 MB, 5.1 TB/s), 32768 e4m3 tokens read
 // back as bf16 37 us (201 MB, 5.4 TB/s).  Between that and the copy rate stand about half of
 // the issue slots (unpacking, turning and packing; gather 74 %) at the 28 warps that an append's
 // registers leave an SM.  A step of one token for each of 64 sequences takes 7.5 us, a launch
@@ -57,6 +57,15 @@ template <bool BF16>
 __device__ __forceinline__ float2 unpack16(uint32_t w) {
     if constexpr (BF16) return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&w));
     else return __half22float2(*reinterpret_cast<__half2*>(&w));
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // 8 pairs (lo[e], hi[e]) of a head vector, its elements 8c .. and hd/2 + 8c ..
@@ -107,7 +116,10 @@ __device__ __forceinline__ void turn_pairs(Pairs& x, const float (&sn)[8], const
     }
 }
 
-constexpr int kWarps = 16;  // of an append's CTA; two CTAs to an SM leave 64 registers to a thread
+// An append's CTA is as large as its largest team, 512 threads at least: 64 registers to a
+// thread fill an SM.
+constexpr int append_warps(int team) { return team > 512 ? team / 32 : 16; }
+constexpr int blocks_ahead(int team) { return team > 512 ? 1 : 2; }  // heads of a team on their way: 32 KB of a CTA
 constexpr int kSms = 152;
 
 // ------------------------------------------------------- rows in 16 bits
@@ -117,11 +129,11 @@ constexpr int kSms = 152;
 // turned), then, for 16-bit pages, its keys and values, kAhead at a time; the first ones are
 // loaded before it is known where they go, so that the search and the page's lookup (four
 // dependent reads) overlap the rows' own latency.
-template <bool BF16, int HD>
-__device__ void append_rows(const PagedParams& P, bool kv, bool turn, int steps, int row_block, int group,
+template <bool BF16, int HD, int kWarps>
+__device__ void append_rows(uint4* smem, const PagedParams& P, bool kv, bool turn, int steps, int row_block, int group,
                             const TurnFreqs& fr) {
     constexpr int kChunks = HD / 16, kHeads = 32 / kChunks, kAhead = 2;  // lanes of a head, heads of a step
-    __shared__ float2 turns[kWarps][HD / 2 + 4];
+    float2 (*turns)[HD / 2 + 4] = reinterpret_cast<float2 (*)[HD / 2 + 4]>(smem);  // of each warp
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = row_block * kWarps + warp;
     if (r >= P.total) return;
@@ -190,17 +202,19 @@ __device__ void append_rows(const PagedParams& P, bool kv, bool turn, int steps,
 // a head's block needs the largest magnitude of all its new rows before its first code can be
 // written, and a thread's 16 elements stay in its registers from the one to the other.  A
 // thread keeps its row and columns from head to head, so its sines and cosines serve them
-// all, and the next head's elements are fetched ahead.  A block of more than 16 kTeam elements
-// (pages of 128 and 256 tokens) is gone through piece by piece, twice.
+// all, and the next heads' elements are fetched ahead.  A block of more than 16 kTeam elements
+// (pages of 128 and 256 tokens with wide heads) is gone through piece by piece, twice.
 //
 // The pages that a call touches are numbered without a pass over the prefix sums:
 // sequence b owns the numbers cu[b]/page + 2b .. cu[b+1]/page + 2b + 1, at least as many
 // as the pages that its rows can touch, so a number finds its sequence by one search.
 template <bool BF16, int HD, int CACHE, int kTeam>
-__device__ void append_blocks(const PagedParams& P, bool turn, int number, int head0, int head1, bool is_v,
+__device__ void append_blocks(uint4* smem, const PagedParams& P, bool turn, int number, int head0, int head1, bool is_v,
                               const TurnFreqs& fr) {
     constexpr int kChunks = HD / 16;
+    constexpr int kWarps = append_warps(kTeam), kAhead = blocks_ahead(kTeam);
     __shared__ float red[2][kWarps];
+    uint4* ring = smem;
     const int tid = threadIdx.x % kTeam, team = threadIdx.x / kTeam;
     const int b = warp_last_le(P.B, number,
                                [&](int i) { return (long long)(__ldg(P.cu + i) >> P.page_shift) + 2 * i; });
@@ -220,23 +234,34 @@ __device__ void append_blocks(const PagedParams& P, bool turn, int number, int h
     const int pg = page_of(P, b, j <= INT32_MAX ? (int)j : -1, tid == 0);
     if (pg < 0) return;
     const int n_old = (int)(lo - (j << P.page_shift));  // rows of the page that an earlier call stored
-    const void* src = is_v ? P.v : P.k;
-    const long long src_stride = is_v ? P.v_stride : P.k_stride;
-    const long long src_at = (first + (lo - p0)) * src_stride;
     const bool turned = turn && !is_v;
     const int tasks = (int)(hi - lo) * kChunks;  // of 16 elements each
     const bool once = tasks <= kTeam;
-    const int c = tid % kChunks;
+    const int c = tid % kChunks, pos = (int)lo + tid / kChunks;  // of the thread's first row
+    const long long src_stride = is_v ? P.v_stride : P.k_stride;
+    const uint16_t* src = static_cast<const uint16_t*>(is_v ? P.v : P.k) + (first + (pos - p0)) * src_stride + c * 8;
 
     float sn[8], cs[8];
     auto angles = [&](int t) {
         if (turned && t < tasks) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) turn_sincos((unsigned int)(lo + t / kChunks), fr.f[c * 8 + e], sn[e], cs[e]);
+            for (int e = 0; e < 8; ++e) turn_sincos((unsigned int)(pos + (t - tid) / kChunks), fr.f[c * 8 + e], sn[e], cs[e]);
         }
     };
     auto fetch = [&](int h, int t, RawPairs& raw) {
-        if (t < tasks) raw = load_raw(src, src_at + (t / kChunks) * src_stride + h * HD + c * 8, HD / 2);
+        if (t < tasks) raw = load_raw(src, (t - tid) / kChunks * src_stride + h * HD, HD / 2);
+    };
+    // The elements of the next heads are on their way into shared memory, where a thread finds
+    // only its own: what a head costs beside them (the maximum over the team, the stores) would
+    // not cover their latency.
+    const uint32_t mine = smem_u32(&ring[threadIdx.x]);
+    auto stage = [&](int h) {
+        if (tid < tasks && h < head1) {
+            const uint32_t to = mine + (h & (kAhead - 1)) * (uint32_t)(2 * kWarps * 32 * 16);
+            cp_async16(to, src + h * HD);
+            cp_async16(to + kWarps * 32 * 16, src + h * HD + HD / 2);
+        }
+        cp_async_commit();
     };
     Pairs x;
     auto value = [&](int t, const RawPairs& raw) {
@@ -245,9 +270,18 @@ __device__ void append_blocks(const PagedParams& P, bool turn, int number, int h
         if (turned) turn_pairs(x, sn, cs);
     };
     RawPairs raw;
-    fetch(head0, tid, raw);
+    if (once) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) stage(head0 + k);
+    }
     angles(tid);
     for (int h = head0; h < head1; ++h) {
+        if (once) {
+            cp_async_wait<kAhead - 1>();
+            const uint4* at = ring + (h & (kAhead - 1)) * (2 * kWarps * 32) + threadIdx.x;
+            raw.lo = at[0];
+            raw.hi = at[kWarps * 32];
+        }
         float* scale_at = (is_v ? P.v_scale : P.k_scale) + (long long)pg * P.Hkv + h;
         const float old = n_old > 0 ? *scale_at : 0.f;
         float amax = 0.f;
@@ -258,23 +292,29 @@ __device__ void append_blocks(const PagedParams& P, bool turn, int number, int h
             }
             value(t, raw);
             if (t >= tasks) continue;
+            float top = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, fmaxf(fabsf(x.lo[e]), fabsf(x.hi[e])));  // (passes NaN over)
+            if (top == INFINITY) {
                 // what is not finite has no part in the scale
-                const float a = fabsf(x.lo[e]), d = fabsf(x.hi[e]);
-                amax = fmaxf(amax, a < INFINITY ? a : 0.f);
-                amax = fmaxf(amax, d < INFINITY ? d : 0.f);
+                top = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float a = fabsf(x.lo[e]), d = fabsf(x.hi[e]);
+                    top = fmaxf(top, fmaxf(a < INFINITY ? a : 0.f, d < INFINITY ? d : 0.f));
+                }
             }
+            amax = fmaxf(amax, top);
         }
-        if (once && h + 1 < head1) fetch(h + 1, tid, raw);
+        if (once) stage(h + kAhead);  // (the place that was just read)
 #pragma unroll
         for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         if constexpr (kTeam > 32) {
-            float* mine = red[h & 1] + team * (kTeam / 32);
-            if ((tid & 31) == 0) mine[tid >> 5] = amax;
+            float* part = red[h & 1] + team * (kTeam / 32);
+            if ((tid & 31) == 0) part[tid >> 5] = amax;
             named_bar_sync(1 + team, kTeam);
 #pragma unroll
-            for (int w = 0; w < kTeam / 32; ++w) amax = fmaxf(amax, mine[w]);
+            for (int w = 0; w < kTeam / 32; ++w) amax = fmaxf(amax, part[w]);
         }
         // smallest power of two s with amax <= 1.75 * 2^kTopExp * s, at least 2^-64
         const uint32_t bits = __float_as_uint(amax);
@@ -309,7 +349,10 @@ __device__ void append_blocks(const PagedParams& P, bool turn, int number, int h
             }
             if (pow2) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x.lo[e] *= inv, x.hi[e] *= inv;
+                for (int e = 0; e < 8; e += 2) {
+                    f2_split(f2_mul(f2_make(x.lo[e], x.lo[e + 1]), f2_make(inv, inv)), x.lo[e], x.lo[e + 1]);
+                    f2_split(f2_mul(f2_make(x.hi[e], x.hi[e + 1]), f2_make(inv, inv)), x.hi[e], x.hi[e + 1]);
+                }
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x.lo[e] /= s, x.hi[e] /= s;
@@ -329,17 +372,20 @@ __device__ void append_blocks(const PagedParams& P, bool turn, int number, int h
 // heads of a page's keys or values to each team (the blocks first: they take longer, and the
 // rows' short CTAs fill the end; the chunks above: 57 us, the rows first 60).
 template <bool BF16, int HD, int CACHE, int kTeam>
-__global__ void __launch_bounds__(kWarps * 32, 2)
+__global__ void __launch_bounds__(append_warps(kTeam) * 32, 32 / append_warps(kTeam))
     paged_append_kernel(const PagedParams P, int turn, int steps, int groups, int row_ctas, int units, int per,
                         const __grid_constant__ TurnFreqs fr) {
+    constexpr int kWarps = append_warps(kTeam);
+    constexpr int kTurns = kWarps * (HD / 2 + 4) / 2, kRing = CACHE == CACHE_16 ? 0 : blocks_ahead(kTeam) * 2 * kWarps * 32;
+    __shared__ uint4 smem[kTurns > kRing ? kTurns : kRing];
     const int x = (int)blockIdx.x - ((int)gridDim.x - row_ctas);
     if (x >= 0) {
-        append_rows<BF16, HD>(P, CACHE == CACHE_16, turn, steps, x / groups, x % groups, fr);
+        append_rows<BF16, HD, kWarps>(smem, P, CACHE == CACHE_16, turn, steps, x / groups, x % groups, fr);
     } else if constexpr (CACHE != CACHE_16) {
         const int u = blockIdx.x * (kWarps * 32 / kTeam) + threadIdx.x / kTeam;
         const int parts = (P.Hkv + per - 1) / per, which = u % (2 * parts), h = (which >> 1) * per;
         if (u < units)
-            append_blocks<BF16, HD, CACHE, kTeam>(P, turn, u / (2 * parts), h, min(P.Hkv, h + per), which & 1, fr);
+            append_blocks<BF16, HD, CACHE, kTeam>(smem, P, turn, u / (2 * parts), h, min(P.Hkv, h + per), which & 1, fr);
     }
 }
 
@@ -407,7 +453,20 @@ cudaError_t append_typed(const PagedParams& p, double theta, cudaStream_t s) {
     TurnFreqs fr = {};
     if (theta > 0) fr = turn_freqs(HD, theta);
     const int heads = (p.q ? p.H : 0) + (CACHE == CACHE_16 ? 2 * p.Hkv : 0);
-    const long long row_blocks = (p.total + kWarps - 1) / kWarps;
+    const int tasks = p.page_size * kPieces;  // pieces of 16 elements in a page's block
+    const long long numbers = (long long)(p.total >> p.page_shift) + 2LL * p.B;
+    int team = 512;
+    if (CACHE != CACHE_16) {
+        // threads of a block: a warp where the call brings few rows to a sequence, else as many as
+        // it has pieces, up to 512; 1024 where that spares a second pass (12288 tokens in chunks,
+        // hd 256, pages of 64: 121 against 182 us; hd 128, pages of 128: 63 against 67) and there
+        // are some blocks to an SM (one KV head, pages of 128: 27 against 23 us)
+        if ((long long)p.total * kPieces <= 64LL * p.B) team = 32;
+        else if (tasks <= 256) team = tasks <= 128 ? 128 : 256;
+        else if (tasks == 1024 && numbers * 2 * p.Hkv >= kSms * 4LL) team = 1024;
+    }
+    const int warps = append_warps(team);
+    const long long row_blocks = (p.total + warps - 1) / warps;
     const int all = (heads + kHeads - 1) / kHeads;
     // steps of a warp: two where that fills no more than the SMs' warps, else a row's heads in
     // equal parts of at most twelve (four: 65 against 63 us for the chunks above, before they
@@ -417,26 +476,21 @@ cudaError_t append_typed(const PagedParams& p, double theta, cudaStream_t s) {
     const int steps = groups ? ((all + groups - 1) / groups + 1) / 2 * 2 : 2;  // (even: two are loaded at a time)
     const long long row_ctas = row_blocks * groups;
     long long units = 0, unit_ctas = 0;
-    int per = 1, team = 32;
+    int per = 1;
     if (CACHE != CACHE_16) {
-        const long long numbers = (long long)(p.total >> p.page_shift) + 2LL * p.B;
-        // threads of a page's block: a warp where the call brings few rows to a sequence, else
-        // as many as a page has pieces of 16 elements, up to the CTA
-        const int tasks = p.page_size * kPieces;
-        team = (long long)p.total * kPieces <= 64LL * p.B ? 32 : tasks <= 128 ? 128 : tasks <= 256 ? 256 : 512;
         // heads of a team, which share its angles and whose loads it overlaps: as many as leave
-        // every SM a CTA (12288 tokens in chunks, hd 64: 33 us, four CTAs 37), or two where a block
-        // is gone through twice (pages of 128 tokens, hd 128: 70 us, one CTA 86, four 74)
-        const long long least = kSms * 512LL * (tasks <= 512 ? 1 : 2);
+        // every SM 512 threads (the chunks with hd 64: 33 us, four times as many 37), or 1024 where
+        // a CTA has them or goes through a block twice (pages of 128: 70 us, 512 threads 86)
+        const long long least = kSms * (tasks > 512 ? 1024LL : 512LL);
         while (per < 8 && per < p.Hkv && numbers * 2 * (p.Hkv / (2 * per)) * team >= least) per *= 2;
         units = numbers * 2 * ((p.Hkv + per - 1) / per);
-        unit_ctas = (units * team + kWarps * 32 - 1) / (kWarps * 32);
+        unit_ctas = (units * team + warps * 32 - 1) / (warps * 32);
     }
     if (row_ctas + unit_ctas > INT32_MAX || units > INT32_MAX) return cudaErrorInvalidConfiguration;
     if (row_ctas + unit_ctas == 0) return cudaSuccess;
     auto launch = [&](auto t) {
         paged_append_kernel<BF16, HD, CACHE, decltype(t)::value>
-            <<<(unsigned)(row_ctas + unit_ctas), kWarps * 32, 0, s>>>(p, theta > 0 ? 1 : 0, steps, groups, (int)row_ctas,
+            <<<(unsigned)(row_ctas + unit_ctas), warps * 32, 0, s>>>(p, theta > 0 ? 1 : 0, steps, groups, (int)row_ctas,
                                                                      (int)units, per, fr);
         return cudaGetLastError();
     };
@@ -444,6 +498,7 @@ cudaError_t append_typed(const PagedParams& p, double theta, cudaStream_t s) {
         if (team == 32) return launch(std::integral_constant<int, 32>());
         if (team == 128) return launch(std::integral_constant<int, 128>());
         if (team == 256) return launch(std::integral_constant<int, 256>());
+        if (team == 1024) return launch(std::integral_constant<int, 1024>());
     }
     return launch(std::integral_constant<int, 512>());
 }

@@ -509,6 +509,15 @@ def test_append_many_sequences():
     run_append("bf16", "e4m3", [(b * 5) % 40 for b in range(1100)], new, 1, 1, 64, 16, 10000.0, seed=4, turn_q=False)
 
 
+@pytest.mark.parametrize("kind,hd,page,Hkv,theta", [("e4m3", 256, 64, 2, 500.0), ("e5m2", 128, 128, 2, None),
+                                                    ("e4m3", 64, 256, 3, 10000.0), ("e4m3", 64, 64, 12, 10000.0),
+                                                    ("e5m2", 64, 32, 11, 10000.0), ("e4m3", 128, 256, 2, 10000.0)])
+def test_append_blocks_of_every_size(kind, hd, page, Hkv, theta):
+    """Blocks of 128 to 2048 pieces of 16 elements, enough of them for several heads to a team."""
+    new = [(b * 37) % 71 for b in range(80)]
+    run_append("bf16", kind, [(b * 23) % 50 for b in range(80)], new, Hkv, Hkv, hd, page, theta, seed=5 + page, turn_q=hd == 64)
+
+
 def test_append_far_positions_keep_their_angle():
     """Positions of hundreds of thousands: fp32 angles would be off by hundredths."""
     page, far = 256, 700001
