@@ -208,29 +208,41 @@ __device__ void append_rows(uint4* smem, const PagedParams& P, bool kv, bool tur
 // The pages that a call touches are numbered without a pass over the prefix sums:
 // sequence b owns the numbers cu[b]/page + 2b .. cu[b+1]/page + 2b + 1, at least as many
 // as the pages that its rows can touch, so a number finds its sequence by one search.
-template <bool BF16, int HD, int CACHE, int kTeam>
+//
+// A call with few rows to a sequence gives each number a warp, and leaves blocks of more than
+// kFew pieces (a chunk of one sequence's prompt beside the others' single tokens) to teams of
+// 512, which find them by a row (kByRow): of the rows that are the last of kFew / kChunks, one
+// at least lies in such a block, and the first that does stands for it.
+constexpr int kFew = 64;
+template <bool BF16, int HD, int CACHE, int kTeam, bool kByRow>
 __device__ void append_blocks(uint4* smem, const PagedParams& P, bool turn, int number, int head0, int head1, bool is_v,
                               const TurnFreqs& fr) {
-    constexpr int kChunks = HD / 16;
+    constexpr int kChunks = HD / 16, kStride = kFew / kChunks;
     constexpr int kWarps = append_warps(kTeam), kAhead = blocks_ahead(kTeam);
     __shared__ float red[2][kWarps];
     uint4* ring = smem;
     const int tid = threadIdx.x % kTeam, team = threadIdx.x / kTeam;
-    const int b = warp_last_le(P.B, number,
-                               [&](int i) { return (long long)(__ldg(P.cu + i) >> P.page_shift) + 2 * i; });
-    if (b < 0) return;
+    const int row = kByRow ? number * kStride + kStride - 1 : 0;
+    const int b = kByRow ? warp_last_le(P.B + 1, row, [&](int i) { return (long long)__ldg(P.cu + i); })
+                         : warp_last_le(P.B, number, [&](int i) { return (long long)(__ldg(P.cu + i) >> P.page_shift) + 2 * i; });
+    if (b < 0 || b >= P.B) return;
     const int first = __ldg(P.cu + b), end = __ldg(P.cu + b + 1);
     const long long len = __ldg(P.lengths + b);
     if (first < 0 || end < first || end > P.total) {
         if (tid == 0 && end != first) atomicOr(P.status, ST_PAGED_BOUNDS);
         return;
     }
-    if (first == end) return;
+    if (first == end || (kByRow && (row < first || row >= end))) return;
     const long long p0 = len - (end - first);  // position of the sequence's first new row
     const long long start = p0 < 0 ? 0 : p0;
-    const long long j = (start >> P.page_shift) + (number - ((first >> P.page_shift) + 2 * b));
+    const long long at = p0 + (row - first);  // of the row
+    if (kByRow && at < 0) return;
+    const long long j = kByRow ? at >> P.page_shift
+                               : (start >> P.page_shift) + (number - ((first >> P.page_shift) + 2 * b));
     const long long lo = max(start, j << P.page_shift), hi = min(len, (j + 1) << P.page_shift);
     if (lo >= hi) return;
+    if (kTeam == 32 && (hi - lo) * kChunks > kFew) return;
+    if (kByRow && ((hi - lo) * kChunks <= kFew || at - lo >= kStride)) return;
     const int pg = page_of(P, b, j <= INT32_MAX ? (int)j : -1, tid == 0);
     if (pg < 0) return;
     const int n_old = (int)(lo - (j << P.page_shift));  // rows of the page that an earlier call stored
@@ -278,9 +290,9 @@ __device__ void append_blocks(uint4* smem, const PagedParams& P, bool turn, int 
     for (int h = head0; h < head1; ++h) {
         if (once) {
             cp_async_wait<kAhead - 1>();
-            const uint4* at = ring + (h & (kAhead - 1)) * (2 * kWarps * 32) + threadIdx.x;
-            raw.lo = at[0];
-            raw.hi = at[kWarps * 32];
+            const uint4* from = ring + (h & (kAhead - 1)) * (2 * kWarps * 32) + threadIdx.x;
+            raw.lo = from[0];
+            raw.hi = from[kWarps * 32];
         }
         float* scale_at = (is_v ? P.v_scale : P.k_scale) + (long long)pg * P.Hkv + h;
         const float old = n_old > 0 ? *scale_at : 0.f;
@@ -374,7 +386,7 @@ __device__ void append_blocks(uint4* smem, const PagedParams& P, bool turn, int 
 template <bool BF16, int HD, int CACHE, int kTeam>
 __global__ void __launch_bounds__(append_warps(kTeam) * 32, 32 / append_warps(kTeam))
     paged_append_kernel(const PagedParams P, int turn, int steps, int groups, int row_ctas, int units, int per,
-                        const __grid_constant__ TurnFreqs fr) {
+                        int long_ctas, int long_per, const __grid_constant__ TurnFreqs fr) {
     constexpr int kWarps = append_warps(kTeam);
     constexpr int kTurns = kWarps * (HD / 2 + 4) / 2, kRing = CACHE == CACHE_16 ? 0 : blocks_ahead(kTeam) * 2 * kWarps * 32;
     __shared__ uint4 smem[kTurns > kRing ? kTurns : kRing];
@@ -382,10 +394,15 @@ __global__ void __launch_bounds__(append_warps(kTeam) * 32, 32 / append_warps(kT
     if (x >= 0) {
         append_rows<BF16, HD, kWarps>(smem, P, CACHE == CACHE_16, turn, steps, x / groups, x % groups, fr);
     } else if constexpr (CACHE != CACHE_16) {
-        const int u = blockIdx.x * (kWarps * 32 / kTeam) + threadIdx.x / kTeam;
-        const int parts = (P.Hkv + per - 1) / per, which = u % (2 * parts), h = (which >> 1) * per;
-        if (u < units)
-            append_blocks<BF16, HD, CACHE, kTeam>(smem, P, turn, u / (2 * parts), h, min(P.Hkv, h + per), which & 1, fr);
+        const bool by_row = kTeam == 32 && (int)blockIdx.x < long_ctas;
+        const int u = by_row ? blockIdx.x : (blockIdx.x - long_ctas) * (kWarps * 32 / kTeam) + threadIdx.x / kTeam;
+        const int n = by_row ? long_per : per, parts = (P.Hkv + n - 1) / n, which = u % (2 * parts);
+        const int number = u / (2 * parts), h = (which >> 1) * n, h1 = min(P.Hkv, h + n);
+        if (by_row) {
+            if constexpr (kTeam == 32) append_blocks<BF16, HD, CACHE, 512, true>(smem, P, turn, number, h, h1, which & 1, fr);
+        } else if (u < units) {
+            append_blocks<BF16, HD, CACHE, kTeam, false>(smem, P, turn, number, h, h1, which & 1, fr);
+        }
     }
 }
 
@@ -457,11 +474,15 @@ cudaError_t append_typed(const PagedParams& p, double theta, cudaStream_t s) {
     const long long numbers = (long long)(p.total >> p.page_shift) + 2LL * p.B;
     int team = 512;
     if (CACHE != CACHE_16) {
-        // threads of a block: a warp where the call brings few rows to a sequence, else as many as
-        // it has pieces, up to 512; 1024 where that spares a second pass (12288 tokens in chunks,
-        // hd 256, pages of 64: 121 against 182 us; hd 128, pages of 128: 63 against 67) and there
-        // are some blocks to an SM (one KV head, pages of 128: 27 against 23 us)
-        if ((long long)p.total * kPieces <= 64LL * p.B) team = 32;
+        // threads of a block: a warp where the call brings few rows to a sequence (and 512 for the
+        // long blocks of such a call: one token of each of 127 sequences and 700 of another take
+        // 18.5 us, with a warp to every block 32; four times as many rows to a sequence would help
+        // such calls, 575 rows of 64 sequences 14 against 18 us, and cost those of even chunks, 30
+        // rows of each of 100 26 against 18), else as many as it has pieces, up to 512; 1024 where
+        // that spares a second pass (12288 tokens in chunks, hd 256, pages of 64: 121 against 182
+        // us; hd 128, pages of 128: 63 against 67) and there are some blocks to an SM (one KV head,
+        // pages of 128: 27 against 23 us)
+        if ((long long)p.total * kPieces <= (long long)kFew * p.B) team = 32;
         else if (tasks <= 256) team = tasks <= 128 ? 128 : 256;
         else if (tasks == 1024 && numbers * 2 * p.Hkv >= kSms * 4LL) team = 1024;
     }
@@ -475,23 +496,33 @@ cudaError_t append_typed(const PagedParams& p, double theta, cudaStream_t s) {
     const int groups = (all + most - 1) / most;
     const int steps = groups ? ((all + groups - 1) / groups + 1) / 2 * 2 : 2;  // (even: two are loaded at a time)
     const long long row_ctas = row_blocks * groups;
-    long long units = 0, unit_ctas = 0;
-    int per = 1;
+    long long units = 0, unit_ctas = 0, long_ctas = 0;
+    int per = 1, long_per = 1;
     if (CACHE != CACHE_16) {
         // heads of a team, which share its angles and whose loads it overlaps: as many as leave
         // every SM 512 threads (the chunks with hd 64: 33 us, four times as many 37), or 1024 where
         // a CTA has them or goes through a block twice (pages of 128: 70 us, 512 threads 86)
         const long long least = kSms * (tasks > 512 ? 1024LL : 512LL);
-        while (per < 8 && per < p.Hkv && numbers * 2 * (p.Hkv / (2 * per)) * team >= least) per *= 2;
+        auto heads_of_team = [&](long long blocks, int threads) {
+            int n = 1;
+            while (n < 8 && n < p.Hkv && blocks * 2 * (p.Hkv / (2 * n)) * threads >= least) n *= 2;
+            return n;
+        };
+        per = heads_of_team(numbers, team);
+        if (team == 32 && tasks > kFew) {
+            const long long rows = p.total / (kFew / kPieces);  // that may stand for a long block
+            long_per = heads_of_team(rows, 512);
+            long_ctas = rows * 2 * ((p.Hkv + long_per - 1) / long_per);
+        }
         units = numbers * 2 * ((p.Hkv + per - 1) / per);
-        unit_ctas = (units * team + warps * 32 - 1) / (warps * 32);
+        unit_ctas = long_ctas + (units * team + warps * 32 - 1) / (warps * 32);
     }
     if (row_ctas + unit_ctas > INT32_MAX || units > INT32_MAX) return cudaErrorInvalidConfiguration;
     if (row_ctas + unit_ctas == 0) return cudaSuccess;
     auto launch = [&](auto t) {
         paged_append_kernel<BF16, HD, CACHE, decltype(t)::value>
             <<<(unsigned)(row_ctas + unit_ctas), warps * 32, 0, s>>>(p, theta > 0 ? 1 : 0, steps, groups, (int)row_ctas,
-                                                                     (int)units, per, fr);
+                                                                     (int)units, per, (int)long_ctas, long_per, fr);
         return cudaGetLastError();
     };
     if constexpr (CACHE != CACHE_16) {

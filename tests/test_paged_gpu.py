@@ -518,6 +518,18 @@ def test_append_blocks_of_every_size(kind, hd, page, Hkv, theta):
     run_append("bf16", kind, [(b * 23) % 50 for b in range(80)], new, Hkv, Hkv, hd, page, theta, seed=5 + page, turn_q=hd == 64)
 
 
+@pytest.mark.parametrize("kind,hd,page", [("e4m3", 128, 64), ("e5m2", 128, 16), ("e4m3", 64, 16), ("e5m2", 64, 32), ("e4m3", 256, 16),
+                                          ("e4m3", 256, 128), ("bf16", 128, 64)])
+def test_append_chunks_among_single_tokens(kind, hd, page):
+    """Running prompts' chunks beside many sequences with a token each: blocks of 1 row to whole pages."""
+    new = [1] * 100
+    for b, n in ((0, 17), (9, 0), (10, 66), (11, 3), (30, 5), (31, 8), (32, 9), (60, 100), (99, 73)):
+        new[b] = n
+    before = [(b * 31) % 90 for b in range(100)]
+    before[10] = -7  # (rows before the sequence's beginning are not stored)
+    run_append("bf16", kind, before, new, 4, 2, hd, page, 10000.0, seed=6 + page)
+
+
 def test_append_far_positions_keep_their_angle():
     """Positions of hundreds of thousands: fp32 angles would be off by hundredths."""
     page, far = 256, 700001
