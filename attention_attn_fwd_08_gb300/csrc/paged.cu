@@ -19,7 +19,7 @@
 // 12288 tokens in ragged chunks into e4m3 pages 54 us (277 MB, 5.1 TB/s), 32768 e4m3 tokens read
 // back as bf16 37 us (201 MB, 5.4 TB/s).  Between that and the copy rate stand about half of
 // the issue slots (unpacking, turning and packing; gather 74 %) at the 28 warps that an append's
-// registers leave an SM.  A step of one token for each of 64 sequences takes 7.5 us, a launch
+// registers leave an SM.  A step of one token for each of 64 sequences takes 8.2 us, a launch
 // and four dependent reads.
 #include <math.h>
 
