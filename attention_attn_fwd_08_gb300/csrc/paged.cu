@@ -327,6 +327,8 @@ __device__ void append_blocks(uint4* smem, const PagedParams& P, bool turn, int 
             named_bar_sync(1 + team, kTeam);
 #pragma unroll
             for (int w = 0; w < kTeam / 32; ++w) amax = fmaxf(amax, part[w]);
+        } else {
+            __syncwarp();  // as that barrier: all lanes have read the old scale before one stores the new
         }
         // smallest power of two s with amax <= 1.75 * 2^kTopExp * s, at least 2^-64
         const uint32_t bits = __float_as_uint(amax);
