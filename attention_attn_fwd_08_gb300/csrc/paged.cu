@@ -337,8 +337,8 @@ __device__ void append_blocks(uint4* smem, const PagedParams& P, bool turn, int 
         float s = __uint_as_float((uint32_t)(ex + 127) << 23);
         uint8_t* cache = static_cast<uint8_t*>(is_v ? P.v_cache : P.k_cache) + cache_row(P, pg, h, 0);
         if (n_old > 0) {
-            if (old >= s) {
-                s = old;
+            if (fabsf(old) >= s) {
+                s = old;  // (of either sign: another program's block)
             } else {
                 // the rows that are there, in units of the grown scale
                 const float ratio = old / s;

@@ -456,8 +456,9 @@ ATTN_API attn_status attn_bwd_rope(attn_dtype dt, const void* q, const void* k, 
  *               by p * rope_theta^(-2i/hd), the angle exact at every position; 0: no turn.
  *   8-bit     : a block (page, head) that holds no earlier token gets the smallest power of
  *               two s >= 2^-64 with max |x| <= 448 s (57344 s for e5m2) over its new rows; one
- *               that does keeps its scale unless that is too small for them, and then takes
- *               the new one, its earlier rows stored again in it.  An element is rounded once,
+ *               that does keeps its scale (any finite one, of either sign) unless its magnitude is
+ *               below s, and then takes s, its earlier rows stored again in it.  An element is
+ *               rounded once (into a kept scale that is no power of two, its fp32 quotient is),
  *               to nearest; one that is not finite has no part in the scale, an infinity is
  *               stored as the largest finite value, NaN as NaN.
  *   A page that tokens are appended to belongs to one sequence (pages that are only read may

@@ -483,7 +483,7 @@ def paged_append(k, v, k_cache, v_cache, k_scale, v_scale, table, lengths, cu, *
                         s *= 2.0
                     if at > 0:
                         old = sc[w][pg, h]
-                        if old >= s:
+                        if abs(old) >= s:
                             s = old
                         else:
                             out[w][pg, h, :at] = f8_round(f8_values(kind)[out[w][pg, h, :at]] * (old / s), kind)

@@ -70,6 +70,21 @@ def test_a_block_takes_the_smallest_power_of_two_that_fits(oracle, kind):
     assert ks3[0, 0] == ks2[0, 0]
 
 
+@pytest.mark.parametrize("kind", ["e4m3", "e5m2"])
+def test_a_block_keeps_a_large_scale_of_either_sign(oracle, kind):
+    page, hd = 4, 8
+    code = np.full((1, 1, page, hd), oracle.f8_round(2.0, kind), np.uint8)
+    table, rows = np.array([[0]]), np.full((1, hd), 1.0)
+    for old, want in ((-4.0, -4.0), (-2.0 ** -30, 1.0), (0.0, 1.0)):
+        sc = np.full((1, 1), old)
+        x = rows * oracle.F8_TOP[kind]
+        kc, _, ks, _, _ = oracle.paged_append(x, x, code, code, sc, sc, table, [2], [0, 1], Hkv=1, kind=kind)
+        assert ks[0, 0] == want
+        got = oracle.paged_tokens(kc, ks, table[0], 2, kind)
+        np.testing.assert_array_equal(got[1], x[0])
+        np.testing.assert_allclose(got[0], 2.0 * old, atol=2.0 ** -9 * abs(want) if old != want else 0)
+
+
 def test_decode_is_the_dense_oracle_on_the_gathered_tokens(oracle):
     g = np.random.default_rng(11)
     H, Hkv, hd, Lq = 4, 2, 8, 3
