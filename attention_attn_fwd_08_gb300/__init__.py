@@ -747,8 +747,8 @@ def attn_paged_append(k, v, k_cache, v_cache, page_table, lengths, cu_new, *, H,
             _like("q_out", q_out, (n, H * hd), dtype, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    if rope_theta is not None and not rope_theta > 0:
-        raise ValueError("rope_theta must be positive (None: no turn)")
+    if rope_theta is not None and not rope_theta >= 2.0 ** -32:  # (as fp32 a smaller one may be 0, no turn)
+        raise ValueError("rope_theta must be at least 2^-32 (None: no turn)")
     handle, context = _on(dev, stream)
     if context is not None:
         with context:

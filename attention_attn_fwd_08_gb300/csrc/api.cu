@@ -1070,7 +1070,8 @@ attn_status attn_paged_append(attn_dtype dt, attn_dtype cache_dt, const void* k,
     attn_status st = paged_params(dt, cache_dt, k_cache, v_cache, k_scale, v_scale, page_table, batch, num_pages,
                                   page_size, max_pages, H, Hkv, hd, &p, &cache);
     if (st != ATTN_OK) return st;
-    if (total_new < 0 || !(rope_theta >= 0.f) || !isfinite(rope_theta)) return ATTN_ERR_INVALID_ARG;
+    // (below 2^-32 a position's angle would need more turns than the frequencies are held to)
+    if (total_new < 0 || !(rope_theta == 0.f || rope_theta >= 0x1p-32f) || !isfinite(rope_theta)) return ATTN_ERR_INVALID_ARG;
     if (batch == 0 || total_new == 0) return ATTN_OK;
     if (!rows_ok(k, k_stride, (long long)Hkv * hd) || !rows_ok(v, v_stride, (long long)Hkv * hd))
         return ATTN_ERR_INVALID_ARG;

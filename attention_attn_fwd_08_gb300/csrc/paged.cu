@@ -4,10 +4,12 @@
 //
 // Turn: pair (x[i], x[i + hd/2]) of a head vector at position p turns by p * theta^(-2i/hd)
 // (the rotate-half form of rope.cu).  Far positions need more than fp32 for the angle, so
-// the frequency is held in turns as a 64-bit fixed-point fraction f of one turn, and p * f
-// modulo 2^64 is the angle's fraction of a turn, exact to p * 2^-64: two 32-bit multiplies
-// give its upper 32 bits, which become an angle in [-pi, pi) for the hardware sine and
-// cosine (absolute error below 2^-21, under the rounding to 16 or 8 bits that follows).
+// the frequency is held in turns as a 64-bit fixed-point fraction f of one turn (right to its
+// last unit), and p * f modulo 2^64 is the angle's fraction of a turn, right to p * 2^-64: two
+// 32-bit multiplies give its upper 32 bits, which become an angle in [-pi, pi) in fp32 (off by
+// 3e-7 at most, near pi) for the hardware sine and cosine (off by 2^-21.4 and 2^-21.2 at most, by
+// their documentation): 2^-20 in all at every position, under the rounding to 16 or 8 bits that
+// follows.
 //
 // 8-bit pages: the scale of a (page, head) block is a power of two, the smallest s with
 // max|x| <= top * s over the block's rows, so that dividing by it is exact, the code is the
@@ -34,13 +36,38 @@ struct TurnFreqs {
     unsigned long long f[128];  // theta^(-2i/hd) / (2 pi) turns, in units of 2^-64 turns
 };
 
+// A number to about 2^-104 of itself as an unevaluated sum of two doubles (T. J. Dekker, "A
+// floating-point technique for extending the available precision", 1971).  Products that are
+// added to are written as fma(a, b, 0), which no compiler joins with the addition.
+struct Two {
+    double hi, lo;
+};
+Two two_sum(double big, double small) {
+    const double s = big + small;
+    return {s, small - (s - big)};
+}
+Two two_mul(Two a, Two b) {
+    const double p = fma(a.hi, b.hi, 0.0);
+    return two_sum(p, fma(a.hi, b.lo, fma(a.lo, b.hi, fma(a.hi, b.hi, -p))));
+}
+Two two_sqrt(Two a) {  // a Newton step from the double's root
+    const double x = sqrt(a.hi), p = fma(x, x, 0.0);
+    return two_sum(x, ((a.hi - p) - fma(x, x, -p) + a.lo) / (2 * x));
+}
+
 TurnFreqs turn_freqs(int hd, double theta) {
+    // hd / 2 is a power of two: theta^(-2/hd) is 1 / theta's root, that often squared
+    Two r = {1 / theta, 0};
+    r.lo = fma(-theta, r.hi, 1.0) / theta;
+    for (int n = hd / 2; n > 1; n /= 2) r = two_sqrt(r);
+    Two turns = {0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};  // 1 / (2 pi)
     TurnFreqs t;
     for (int i = 0; i < hd / 2; ++i) {
-        // at most 1 / (2 pi) of a turn for theta >= 1; a theta below 1 turns faster than once
-        // a position: only the fraction of a turn counts
-        const double turns = pow(theta, -2.0 * i / hd) / 6.283185307179586476925286766559;
-        t.f[i] = (unsigned long long)ldexp(turns - floor(turns), 64);
+        // At most 1 / (2 pi) of a turn for theta >= 1; a theta below 1 turns faster than once a
+        // position (2^29.4 times for 2^-32, the least): only the fraction of a turn counts, and it
+        // is right to 2^-64 still.
+        t.f[i] = (unsigned long long)ldexp(turns.hi - floor(turns.hi), 64) + (unsigned long long)(long long)rint(ldexp(turns.lo, 64));
+        turns = two_mul(turns, r);
     }
     return t;
 }

@@ -452,8 +452,9 @@ ATTN_API attn_status attn_bwd_rope(attn_dtype dt, const void* q, const void* k, 
  *               newest tokens, at positions lengths[b] - n_b .. lengths[b] - 1.  Rows in no
  *               sequence are ignored, and so are rows at a negative position (a padding slot
  *               has length 0): nothing is stored for them and their q_out is not written.
- *   rope_theta: > 0 and finite: pair (x[i], x[i + hd/2]) of a head vector at position p turns
- *               by p * rope_theta^(-2i/hd), the angle exact at every position; 0: no turn.
+ *   rope_theta: at least 2^-32 and finite: pair (x[i], x[i + hd/2]) of a head vector at position
+ *               p turns by p * rope_theta^(-2i/hd), its sine and cosine right to 2^-20 at every
+ *               position; 0: no turn.
  *   8-bit     : a block (page, head) that holds no earlier token gets the smallest power of
  *               two s >= 2^-64 with max |x| <= 448 s (57344 s for e5m2) over its new rows; one
  *               that does keeps its scale (any finite one, of either sign) unless its magnitude is

@@ -1,11 +1,15 @@
 """Edges of the paged cache on the GPU: block scales, far positions, rotation bases, arrays out of
 range, against the fp64 oracle.  Tolerances as in test_paged_gpu.py."""
+import decimal
+import math
+
 import numpy as np
 import pytest
+import torch
 
 import oracle
 import attention_attn_fwd_08_gb300 as A
-from test_paged_gpu import Cache, run_step
+from test_paged_gpu import DEV, Cache, close, f64, i32, run_step, status_ok
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +54,33 @@ def test_append_to_blocks_of_negative_scale(kind, new):
         after_v = v[got[w][pages[2], :, :7]] * new_scale[:, None, None]
         u, tiny = {"e4m3": (2.0 ** -4, 2.0 ** -10), "e5m2": (2.0 ** -3, 2.0 ** -17)}[kind]
         assert (np.abs(after_v - before_v) <= np.maximum(u * np.abs(before_v), tiny * new_scale[:, None, None])).all()
+
+
+def turned(x, pos, hd, theta):
+    """A row's head vectors turned at one position, the angles from 120 digits."""
+    with decimal.localcontext() as ctx:
+        ctx.prec = 120
+        pi = decimal.Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803482534211706798")
+        base = decimal.Decimal(float(np.float32(theta)))
+        turns = [pos * base ** (decimal.Decimal(-2 * i) / hd) / (2 * pi) for i in range(hd // 2)]
+        ang = 2 * math.pi * np.array([float(t - t.to_integral_value(decimal.ROUND_FLOOR)) for t in turns])
+    y = x.reshape(-1, 2, hd // 2)
+    c, s = np.cos(ang), np.sin(ang)
+    return np.stack([y[:, 0] * c - y[:, 1] * s, y[:, 1] * c + y[:, 0] * s], 1).reshape(x.shape)
+
+
+@pytest.mark.parametrize("theta", [2.0 ** -32, 1e-8, 1e-4, 0.3, 1.0, 10000.0, 5e6, 1e30])
+@pytest.mark.parametrize("far", [3, 1000003])
+@pytest.mark.parametrize("hd", [64, 256])
+def test_append_angles_of_every_base(theta, far, hd):
+    """Bases from 2^-32 on, those below 1 that turn many times a position among them."""
+    page = 256
+    c = Cache("f16", "f16", [3], 2, hd, page, seed=1, most=far // page + 2)
+    c.table[0, far // page] = 0
+    c.table_d = i32(c.table)
+    k = torch.randn((1, 2 * hd), generator=torch.Generator().manual_seed(8)).half().to(DEV)
+    q_out = A.attn_paged_append(k, k, c.k, c.v, c.table_d, i32([far + 1]), i32([0, 1]), H=2, q=k, rope_theta=theta, **c.kw())
+    status_ok()
+    x = turned(f64(k)[0], far, hd, theta).reshape(2, hd)
+    close(f64(q_out).reshape(2, hd), x, "f16")
+    close(f64(c.k[0, :, far % page]), x, "f16")

@@ -237,3 +237,17 @@ def test_binding_refuses_a_stream_of_another_device():
 
     with pytest.raises(ValueError, match="stream"):
         A._on(torch.device("cuda", 0), Stream())
+
+
+@pytest.mark.parametrize("theta", [2.0 ** -33, 1e-12, 1e-38, 1e-45])
+def test_bases_below_the_least_are_refused(theta):
+    assert append(theta=theta) == A.ERR_INVALID_ARG
+    assert append(theta=2.0 ** -32, total=0) == A.OK
+    assert append(theta=0.0, total=0) == A.OK
+
+
+@pytest.mark.parametrize("theta", [1e-12, 1e-46, 5e-324, -0.0])
+def test_binding_refuses_bases_that_fp32_would_lose(theta):
+    """One below fp32's smallest would reach the library as 0, which means no turn."""
+    with pytest.raises(ValueError, match="rope_theta"):
+        _on_gpu_shapes(call_append, cache(), rope_theta=theta)
