@@ -808,7 +808,8 @@ def attn_paged_decode(q, k_cache, v_cache, page_table, lengths, *, H, Hkv, k_sca
     st = L.attn_paged_decode(rd, cd, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale),
                              _addr(v_scale), o.data_ptr(), _addr(lse), workspace.data_ptr(), workspace.nbytes,
                              lengths.data_ptr(), page_table.data_ptr(), B, Lq, num_pages, page_size, max_pages, H, Hkv, hd,
-                             hd ** -0.5 if scale is None else float(scale), 1 if causal else 0, int(window), float(softcap), handle)
+                             hd ** -0.5 if scale is None else float(scale), 1 if causal else 0,
+                             max(-1, min(int(window), 0x7fffffff)), float(softcap), handle)  # (as the C int would wrap it)
     if st != OK:
         _check(st, "attn_paged_decode")
     return o, lse

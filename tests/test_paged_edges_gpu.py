@@ -9,7 +9,7 @@ import torch
 
 import oracle
 import attention_attn_fwd_08_gb300 as A
-from test_paged_gpu import DEV, Cache, close, f64, i32, run_step, status_ok
+from test_paged_gpu import DEV, Cache, check_decode, close, f64, i32, run_step, status_ok
 
 pytestmark = pytest.mark.gpu
 
@@ -84,3 +84,19 @@ def test_append_angles_of_every_base(theta, far, hd):
     x = turned(f64(k)[0], far, hd, theta).reshape(2, hd)
     close(f64(q_out).reshape(2, hd), x, "f16")
     close(f64(c.k[0, :, far % page]), x, "f16")
+
+
+@pytest.mark.parametrize("causal", [False, True])
+def test_decode_windows_past_32_bits(causal):
+    """A window that no 32-bit integer holds leaves out nothing; a negative one is refused."""
+    lengths = [200, 31]
+    c = Cache("f16", "f16", lengths, 2, 64, 16, seed=54)
+    c.fill(lengths, 54)
+    q = torch.randn((2, 3, 4 * 64), generator=torch.Generator().manual_seed(3)).half().to(DEV)
+    for window in (2 ** 31, 2 ** 32, 2 ** 32 + 1, 2 ** 40 + 7):
+        o, lse = A.attn_paged_decode(q, c.k, c.v, c.table_d, i32(lengths), H=4, window=window, causal=causal, **c.kw())
+        status_ok()
+        check_decode(c, q, lengths, o, lse, causal=causal)
+    for window in (-1, -2 ** 32 + 5, -2 ** 32):
+        with pytest.raises(A.AttnError):
+            A.attn_paged_decode(q, c.k, c.v, c.table_d, i32(lengths), H=4, window=window, causal=causal, **c.kw())
