@@ -54,12 +54,18 @@ constexpr int kMaxCtasPerSm = 3;
 constexpr int kMaxCtas = kSms * kMaxCtasPerSm;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kFailed = INT32_MAX;
-// p = 2^(score - ref) with ref kBias below the largest score when it is set.  In the usual
-// tile p is multiplied by its group's vs / vref before it is rounded: with that ratio at least
-// kRatioLo, fp16's finest step (2^-24) lies 2^-24 or more below the largest p's product, as
-// without a scale; with it at most kRatioHi, scores may pass the reference's by 2^4 before the
-// product leaves fp16's range (2^kTopLog2 is half of its largest value) and the reference moves.
-constexpr float kBias = 6.f, kTopLog2 = 15.f, kRatioLo = 1.f / 64, kRatioHi = 32.f;
+// p = 2^(score - ref) with ref `bias` below the largest score when it is set, and moved when a p
+// would pass 2^top (half of fp16's largest value).  In bf16, whose exponent is fp32's, p stays
+// at most 1, so that P V passes fp32's range no sooner than the unweighted sum of V.
+template <bool kBf>
+struct PRange {
+    static constexpr float bias = kBf ? -9.f : 6.f, top = kBf ? 0.f : 15.f;
+};
+// In the usual tile p is multiplied by its group's vs / vref before it is rounded (8-bit pages): with
+// that ratio at least kRatioLo, fp16's finest step (2^-24) lies 2^-24 or more below the largest p's
+// product, as without a scale; with it at most kRatioHi, scores may pass the reference's by 2^4
+// before the product leaves fp16's range and the reference moves.
+constexpr float kRatioLo = 1.f / 64, kRatioHi = 32.f;
 
 // Bytes of workspace: (m, l), then O, of two slots of R partial rows for each CTA (a stretch
 // can begin in the middle of one item and end in the middle of another).
@@ -283,6 +289,7 @@ __global__ void __launch_bounds__(DecShape<HD, CACHE, kRowTiles>::kThreads, DecS
     constexpr int RT = S::RT;
     constexpr bool k8 = S::k8;
     constexpr bool kMmaBf = !k8 && kBf;  // type of the products
+    constexpr PRange<kMmaBf> kRange{};
     const bool bf = k8 ? rows_bf16 != 0 : kBf;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -681,7 +688,7 @@ __global__ void __launch_bounds__(DecShape<HD, CACHE, kRowTiles>::kThreads, DecS
                         for (int r = 0; r < 2; ++r) {
                             float mw[4];
                             group_maxima(maxima + (buf * S::kRows + rt * 16 + g + 8 * r) * S::kW, mw);
-                            ref[rt][r] = max_nan(max_nan(mw[0], mw[1]), max_nan(mw[2], mw[3])) - kBias;
+                            ref[rt][r] = max_nan(max_nan(mw[0], mw[1]), max_nan(mw[2], mw[3])) - kRange.bias;
                         }
                 }
                 float part[RT][2];
@@ -696,7 +703,7 @@ __global__ void __launch_bounds__(DecShape<HD, CACHE, kRowTiles>::kThreads, DecS
                         for (int e = 0; e < 2 * kNt; ++e) {
                             const float raw = sc[rt][e >> 1][2 * r + (e & 1)];
                             y[e] = P.softcap > 0.f ? score(raw, c) + shift : fmaf(raw, c, shift);
-                            high |= !(y[e] <= kTopLog2);
+                            high |= !(y[e] <= kRange.top);
                         }
                         uint8_t* to = p_to + (rt * 16 + 8 * r) * S::kPPitch;
                         const float p0 = fast_exp2(y[0]), p1 = fast_exp2(y[1]);
@@ -800,7 +807,7 @@ __global__ void __launch_bounds__(DecShape<HD, CACHE, kRowTiles>::kThreads, DecS
                     for (int r = 0; r < 2; ++r) {
                         float mw[4];
                         group_maxima(maxima + (buf * S::kRows + rt * 16 + g + 8 * r) * S::kW, mw);
-                        const float top = max_nan(max_nan(mw[0], mw[1]), max_nan(mw[2], mw[3])) - kBias;
+                        const float top = max_nan(max_nan(mw[0], mw[1]), max_nan(mw[2], mw[3])) - kRange.bias;
                         const float next = max_nan(ref[rt][r], top), to0 = next == -INFINITY ? 0.f : next;
                         const float alpha = fast_exp2(ref[rt][r] - to0);  // 0 before the row's first key
                         ref[rt][r] = next;

@@ -100,3 +100,23 @@ def test_decode_windows_past_32_bits(causal):
     for window in (-1, -2 ** 32 + 5, -2 ** 32):
         with pytest.raises(A.AttnError):
             A.attn_paged_decode(q, c.k, c.v, c.table_d, i32(lengths), H=4, window=window, causal=causal, **c.kw())
+
+
+@pytest.mark.parametrize("hd,G,Lq", [(128, 4, 1), (64, 2, 3), (256, 2, 2), (128, 4, 16)])
+@pytest.mark.parametrize("climb", [False, True])
+def test_decode_values_near_the_end_of_bf16(hd, G, Lq, climb):
+    """Values whose weighted mean a bf16 holds easily, and whose products with anything above 1 do not fit in fp32."""
+    lengths = [300, 3000]
+    c = Cache("bf16", "bf16", lengths, 2, hd, 16, seed=55)
+    c.fill(lengths, 55, unequal=False)
+    for b, n in enumerate(lengths):
+        for j in range((n + 15) // 16):
+            pg = int(c.table[b, j])
+            m = min(16, n - 16 * j)
+            c.v[pg, :, :m] = (c.v[pg, :, :m].float().abs().clamp(max=4) * 2.0 ** (117 if b == 0 else 113)).to(torch.bfloat16)
+            if climb:
+                c.k[pg, :, :m] *= 1.0 + j / 8
+    q = torch.randn((2, Lq, 2 * G * hd), generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).to(DEV)
+    o, lse = A.attn_paged_decode(q, c.k, c.v, c.table_d, i32(lengths), H=2 * G, **c.kw())
+    status_ok()
+    check_decode(c, q, lengths, o, lse)
