@@ -9,7 +9,7 @@ import torch
 
 import oracle
 import attention_attn_fwd_08_gb300 as A
-from test_paged_gpu import DEV, Cache, check_decode, close, f64, i32, run_step, status_ok
+from test_paged_gpu import DEV, Cache, check_decode, close, expect_flag, f64, i32, is8, run_step, status_ok
 
 pytestmark = pytest.mark.gpu
 
@@ -120,3 +120,47 @@ def test_decode_values_near_the_end_of_bf16(hd, G, Lq, climb):
     o, lse = A.attn_paged_decode(q, c.k, c.v, c.table_d, i32(lengths), H=2 * G, **c.kw())
     status_ok()
     check_decode(c, q, lengths, o, lse)
+
+
+BAD_ARRAYS = [
+    ([(0, 0, -1), (1, 0, 99), (2, 1, 2 ** 31 - 1), (3, 0, -2 ** 31)], [40, 20, 17, 16]),
+    ([(0, 1, 10 ** 9)], [40, 20, 17, 16]),
+    ([], [80, 20, 17, 16]),                       # the first sequence's last rows lie past its table
+    ([], [40, 2 ** 31 - 1, 17, -2 ** 31]),
+    ([(2, 0, -5)], [40, 60, 9, 16]),
+]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "e5m2"])
+@pytest.mark.parametrize("bad,lengths", BAD_ARRAYS)
+@pytest.mark.parametrize("slots", [0, 60])
+def test_append_stores_what_lies_in_range_and_nothing_else(kind, bad, lengths, slots):
+    """Pages and positions out of range among good ones: pools, scales and turned queries to the last
+    byte, with few rows to a sequence (60 empty slots behind) and with many."""
+    c = Cache("bf16", kind, [40, 20, 17, 16] + [0] * slots, 2, 64, 16, seed=11)
+    for b, j, pg in bad:
+        c.table[b, j] = pg
+    c.table_d = i32(c.table)
+    lengths = lengths + [0] * slots
+    cu = [0, 40, 60, 77, 93] + [93] * slots
+    g = torch.Generator().manual_seed(2)
+    k, v = (torch.randn((97, 128), generator=g).to(torch.bfloat16).to(DEV) for _ in range(2))
+    q = torch.randn((97, 256), generator=g).to(torch.bfloat16).to(DEV)
+    q_out = torch.full((97, 256), 9.0, dtype=torch.bfloat16, device=DEV)
+    host = c.host()
+    A.attn_paged_append(k, v, c.k, c.v, c.table_d, i32(lengths), i32(cu), H=4, q=q, q_out=q_out, **c.kw())
+    expect_flag()
+    want = oracle.paged_append(f64(k), f64(v), *host, c.table, lengths, cu, Hkv=2, kind=kind if is8(kind) else None)
+    for got, ref in zip(c.host(), want):
+        if ref is not None:
+            np.testing.assert_array_equal(got, ref)
+    ref = np.full((97, 256), 9.0)
+    stored = 0
+    for b in range(4):
+        for r in range(cu[b], cu[b + 1]):
+            pos = lengths[b] - (cu[b + 1] - r)
+            if pos >= 0 and pos // 16 < c.most and 0 <= c.table[b, pos // 16] < c.k.shape[0]:
+                ref[r] = f64(q[r])
+                stored += 1
+    assert 0 < stored < 93
+    np.testing.assert_array_equal(f64(q_out), ref)
