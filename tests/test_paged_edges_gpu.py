@@ -9,7 +9,7 @@ import torch
 
 import oracle
 import attention_attn_fwd_08_gb300 as A
-from test_paged_gpu import DEV, Cache, check_decode, close, expect_flag, f64, i32, is8, run_step, status_ok
+from test_paged_gpu import DEV, Cache, check_decode, close, expect_flag, f64, i32, is8, near_steps, run_step, status_ok
 
 pytestmark = pytest.mark.gpu
 
@@ -164,3 +164,57 @@ def test_append_stores_what_lies_in_range_and_nothing_else(kind, bad, lengths, s
                 stored += 1
     assert 0 < stored < 93
     np.testing.assert_array_equal(f64(q_out), ref)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("hd,page,Hkv,new", [
+    (128, 64, 2, [1] * 40),                                    # a warp to each block
+    (64, 32, 2, [70, 33, 64]),                                 # 128 threads, whole pages and their ends
+    (64, 64, 3, [64, 129]),                                    # 256
+    (128, 64, 2, [200, 64]),                                   # 512
+    (128, 64, 2, [1] * 60 + [100] + [1] * 30 + [41]),          # long blocks found by a row
+    (256, 64, 4, [40 + b for b in range(50)]),                 # 1024
+    (128, 128, 1, [300]),                                      # 1024 pieces by 512 threads, twice
+    (256, 128, 2, [131, 128]),                                 # 2048 pieces
+    (128, 256, 1, [256, 5])])
+def test_append_far_positions_into_8_bit_pages(kind, hd, page, Hkv, new):
+    """Keys turned at positions of hundreds of thousands, by every team that stores blocks."""
+    theta, B = 10000.0, len(new)
+    first = [500001 + 977 * b for b in range(B)]
+    first[0] = 700000 // page * page  # (one at a page's beginning)
+    lengths = [a + n for a, n in zip(first, new)]
+    used = [range(a // page, (n - 1) // page + 1) for a, n in zip(first, lengths)]
+    P = sum(len(u) for u in used) + 1
+    c = Cache("bf16", kind, [1] * B, Hkv, hd, page, seed=56, spare=P - B, most=max(lengths) // page + 1)
+    perm = np.random.default_rng(57).permutation(P)
+    c.table[:] = -1
+    at = 0
+    g = torch.Generator().manual_seed(58)
+    for b, u in enumerate(used):
+        c.table[b, u.start:u.stop] = perm[at:at + len(u)]
+        pg, m = int(perm[at]), first[b] % page
+        at += len(u)
+        if m:  # rows of the block that an earlier call stored
+            for pool, sc in ((c.k, c.ks), (c.v, c.vs)):
+                sc[pg] = 2.0 ** -9
+                pool.view(torch.uint8)[pg, :, :m] = torch.randint(0, 0x70, (Hkv, m, hd), generator=g, dtype=torch.uint8).to(DEV)
+    c.table_d = i32(c.table)
+    cu = np.cumsum([0] + list(new))
+    k, v = (torch.randn((int(cu[-1]), Hkv * hd), generator=g).to(torch.bfloat16).to(DEV) for _ in range(2))
+    host = c.host()
+    A.attn_paged_append(k, v, c.k, c.v, c.table_d, i32(lengths), i32(cu), H=Hkv, rope_theta=theta, **c.kw())
+    status_ok()
+    rk, rv, rks, rvs, exact = oracle.paged_append(f64(k), f64(v), *host, c.table, lengths, cu, Hkv=Hkv, kind=kind, theta=theta)
+    gk, gv, gks, gvs = c.host()
+    for got, ref in ((gv, rv), (gks, rks), (gvs, rvs)):
+        np.testing.assert_array_equal(got, ref)
+    fresh = np.zeros(rk.shape, bool)
+    values, top = oracle.f8_values(kind), oracle.F8_TOP[kind]
+    for w, pg, row, x in exact:
+        if w == 0:
+            fresh[pg, :, row] = True
+            pair = np.hypot(x[:, :hd // 2], x[:, hd // 2:])
+            slack = 2.0 ** -20 * np.concatenate([pair, pair], 1)
+            off = np.abs(values[gk[pg, :, row]] - np.clip(x, -top, top))
+            assert (off <= near_steps(np.abs(x) + slack, kind) + slack).all()
+    np.testing.assert_array_equal(gk[~fresh], rk[~fresh])
