@@ -732,7 +732,7 @@ def attn_paged_append(k, v, k_cache, v_cache, page_table, lengths, cu_new, *, H,
     positions up to lengths[b]-1 (int32 [batch], the lengths with the new tokens).  k_cache,
     v_cache [num_pages, Hkv, page_size, hd] of the rows' dtype, or float8_e4m3fn / float8_e5m2
     with fp32 k_scale, v_scale [num_pages, Hkv], which are updated; page_table int32
-    [batch, max_pages].  rope_theta None: no turn.  With q [rows, H*hd] the queries are
+    [batch, max_pages].  rope_theta (at least 2^-32) None: no turn.  With q [rows, H*hd] the queries are
     turned too, into q_out (made if not given); returns q_out or None.  Rows in no sequence
     and rows of a padding slot (length 0) are left alone."""
     rd, cd, num_pages, page_size, hd, B, max_pages = _pools(k_cache, v_cache, k_scale, v_scale, page_table, Hkv, k.dtype)

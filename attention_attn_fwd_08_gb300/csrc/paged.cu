@@ -20,9 +20,10 @@
 // four prompts of 2048 tokens into bf16 pages 39 us (201 MB, 5.2 TB/s; the copy rate is 6.8),
 // 12288 tokens in ragged chunks into e4m3 pages 54 us (277 MB, 5.1 TB/s), 32768 e4m3 tokens read
 // back as bf16 37 us (201 MB, 5.4 TB/s).  Between that and the copy rate stand about half of
-// the issue slots (unpacking, turning and packing; gather 74 %) at the 28 warps that an append's
-// registers leave an SM.  A step of one token for each of 64 sequences takes 8.2 us, a launch
-// and four dependent reads.
+// the issue slots (unpacking, turning and packing; gather 71 %) with 28 warps active on average of
+// the 32 that an append's 64 registers a thread leave an SM.  At hd 256 the same chunks take 119 us
+// (553 MB, 4.6 TB/s): one CTA of 1024 threads to an SM, its next head on the way.  A step of one
+// token for each of 64 sequences takes 8.2 us, a launch and four dependent reads.
 #include <math.h>
 
 #include <type_traits>
@@ -411,7 +412,7 @@ __device__ void append_blocks(uint4* smem, const PagedParams& P, bool turn, int 
 
 // One launch: the last row_ctas CTAs turn rows, those before them store 8-bit blocks, `per`
 // heads of a page's keys or values to each team (the blocks first: they take longer, and the
-// rows' short CTAs fill the end; the chunks above: 57 us, the rows first 60).
+// rows' short CTAs fill the end; the chunks above: 53 us, the rows first 60).
 template <bool BF16, int HD, int CACHE, int kTeam>
 __global__ void __launch_bounds__(append_warps(kTeam) * 32, 32 / append_warps(kTeam))
     paged_append_kernel(const PagedParams P, int turn, int steps, int groups, int row_ctas, int units, int per,
@@ -505,9 +506,11 @@ cudaError_t append_typed(const PagedParams& p, double theta, cudaStream_t s) {
     if (CACHE != CACHE_16) {
         // threads of a block: a warp where the call brings few rows to a sequence (and 512 for the
         // long blocks of such a call: one token of each of 127 sequences and 700 of another take
-        // 18.5 us, with a warp to every block 32; four times as many rows to a sequence would help
-        // such calls, 575 rows of 64 sequences 14 against 18 us, and cost those of even chunks, 30
-        // rows of each of 100 26 against 18), else as many as it has pieces, up to 512; 1024 where
+        // 18.5 us, with a warp to every block 32; a call without such a block pays for teams that
+        // find none, one token of each of 128 10.2 against 8.2; four times as many rows to a
+        // sequence would help such calls, 575 rows of 64 sequences 14 against 18 us, and cost those
+        // of even chunks, 30 rows of each of 100 26 against 18), else as many as it has pieces, up to
+        // 512; 1024 where
         // that spares a second pass (12288 tokens in chunks, hd 256, pages of 64: 121 against 182
         // us; hd 128, pages of 128: 63 against 67) and there are some blocks to an SM (one KV head,
         // pages of 128: 27 against 23 us)
@@ -519,8 +522,8 @@ cudaError_t append_typed(const PagedParams& p, double theta, cudaStream_t s) {
     const long long row_blocks = (p.total + warps - 1) / warps;
     const int all = (heads + kHeads - 1) / kHeads;
     // steps of a warp: two where that fills no more than the SMs' warps, else a row's heads in
-    // equal parts of at most twelve (four: 65 against 63 us for the chunks above, before they
-    // were stored first)
+    // equal parts of at most twelve (of four: the prompts above 41 against 39 us, the chunks 57
+    // against 53)
     const int most = row_blocks * ((all + 1) / 2) > kSms * 4LL ? 12 : 2;
     const int groups = (all + most - 1) / most;
     const int steps = groups ? ((all + groups - 1) / groups + 1) / 2 * 2 : 2;  // (even: two are loaded at a time)

@@ -33,8 +33,16 @@
 // It takes (16 x 32768 tokens, H32/8, hd 128) 169 us over e4m3 pages with one query row, 0.93 of
 // the measured copy rate, and 314 us over bf16 pages with four, all of it; 61 sequences of 5 to
 // 9973 tokens 112 us, 0.82.  One short sequence takes 11.7 us, the merge included.
-// mma.sync serves the 16 rows that a group usually has; tcgen05's least M (64) would leave
-// three quarters of it idle and need the codes converted through shared memory.
+// mma.sync serves the 16 rows that a group usually has: as rows of tcgen05's M (64 at least) they
+// would leave three quarters of it idle.  With 32 or 64 rows keys could be M and rows N, nothing
+// idle, but 8-bit codes would go through shared memory once more; not built: 64 rows over the same
+// cache take 490 us of either type, bound by the latency of a tile's chain at two warps a scheduler.
+//
+// Rounding: P goes into P V in 16 bits, as the tensor cores take it (half a step of each p, of the
+// rows' type over 16-bit pages, of fp16 over 8-bit ones); sums, references, S and O are fp32, and l
+// sums p unrounded.  Relative to 64 bits O is off by 0.0022 over the bf16 cache above, of which 0.0017
+// is its own rounding to bf16, over the e4m3 one by 0.0017, over short fp16 ones by 2.6e-4 of
+// which 2.1e-4 is its own.
 #pragma once
 
 #include <math.h>

@@ -454,7 +454,9 @@ ATTN_API attn_status attn_bwd_rope(attn_dtype dt, const void* q, const void* k, 
  *               has length 0): nothing is stored for them and their q_out is not written.
  *   rope_theta: at least 2^-32 and finite: pair (x[i], x[i + hd/2]) of a head vector at position
  *               p turns by p * rope_theta^(-2i/hd), its sine and cosine right to 2^-20 at every
- *               position; 0: no turn.
+ *               position; 0: no turn.  (attn_rope forms a 16-bit row's angle as an fp32 product, off
+ *               by some 1e-3 rad at position 30000 and by hundredths at 700000: turn the queries of
+ *               cached keys here, by q, rather than there.)
  *   8-bit     : a block (page, head) that holds no earlier token gets the smallest power of
  *               two s >= 2^-64 with max |x| <= 448 s (57344 s for e5m2) over its new rows; one
  *               that does keeps its scale (any finite one, of either sign) unless its magnitude is
