@@ -480,7 +480,8 @@ ATTN_API attn_status attn_paged_append(attn_dtype dt, attn_dtype cache_dt, const
  * max_pages * page_size) tokens are visible, the rows sit at positions L_b - Lq .. L_b - 1,
  * and a row that sees no key gets O = 0 and LSE = -inf.  What a row does not see has no
  * effect on it, whatever bytes it holds (rows behind a sequence's end, pages it skips, a
- * later row's key or value that is not finite).
+ * later row's key or value that is not finite).  Sums are fp32 over weights of at most 1 over
+ * bf16 pages: values whose magnitudes add up past fp32's range may overflow.
  *   q, o      : [B][Lq][H*hd];  lse : [B][H][Lq] fp32, or NULL.
  *   scale, causal, window, softcap : as for attn_decode.
  *   workspace : at least attn_paged_decode_workspace_size() bytes of device scratch, 16-byte

@@ -105,7 +105,7 @@ def test_decode_windows_past_32_bits(causal):
 @pytest.mark.parametrize("hd,G,Lq", [(128, 4, 1), (64, 2, 3), (256, 2, 2), (128, 4, 16)])
 @pytest.mark.parametrize("climb", [False, True])
 def test_decode_values_near_the_end_of_bf16(hd, G, Lq, climb):
-    """Values whose weighted mean a bf16 holds easily, and whose products with anything above 1 do not fit in fp32."""
+    """Values whose weighted mean a bf16 holds easily, and whose sums leave fp32 once they are weighted by more than 1."""
     lengths = [300, 3000]
     c = Cache("bf16", "bf16", lengths, 2, hd, 16, seed=55)
     c.fill(lengths, 55, unequal=False)
