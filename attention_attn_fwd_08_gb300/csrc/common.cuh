@@ -82,7 +82,6 @@ enum : unsigned int {
     ST_SELFTEST = 1u << 7,
     ST_TEARDOWN = 1u << 8,
     ST_VARLEN_BOUNDS = 1u << 9,  // a packed sequence longer than the bound, or cu_seqlens decreasing
-    ST_PAGED_BOUNDS = 1u << 10,  // a paged call's page, length or prefix sum outside its range
 };
 
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s: no wait is ever that long

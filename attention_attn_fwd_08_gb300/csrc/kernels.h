@@ -58,6 +58,8 @@ cudaError_t launch_rope_table(float* tab, int npos, int hd, int pos, double thet
 
 // ---- paged key/value cache (paged.cu, paged_decode.cu): fp16 / bf16 rows, hd 64, 128 or 256
 enum : int { CACHE_16 = 0, CACHE_E4M3 = 1, CACHE_E5M2 = 2 };  // element type of the pages (16: that of the rows)
+// status bit, after those of common.cuh (which the dense kernels' captured figures are tied to, byte by byte)
+enum : unsigned int { ST_PAGED_BOUNDS = 1u << 10 };  // a paged call's page, length or prefix sum outside its range
 struct PagedParams {
     const void* q;  // append: rows to turn, or NULL; decode: [B][Lq][H*hd]
     const void* k;  // append: new rows
