@@ -21,7 +21,7 @@ import math
 import os
 import threading
 
-__all__ = ["attn_fwd", "attn_bwd", "attn_decode", "attn_decode_len", "attn_varlen_fwd", "attn_varlen_bwd", "attn_fwd_ex", "attn_bwd_ex", "attn_rope", "attn_bwd_workspace_size", "attn_decode_workspace_size", "attn_decode_plan",
+__all__ = ["attn_fwd", "attn_bwd", "attn_decode", "attn_decode_len", "attn_varlen_fwd", "attn_varlen_bwd", "attn_fwd_ex", "attn_bwd_ex", "attn_rope", "attn_rope_ex", "attn_rope_freqs", "RopeFreqs", "attn_bwd_workspace_size", "attn_decode_workspace_size", "attn_decode_plan",
            "attn_get_device_status", "attn_selftest_bounded_wait", "attn_kernel_family", "attn_kernel_family_bwd", "attn_fwd_rope", "attn_bwd_rope", "attn_fwd_rope_workspace_size", "attn_bwd_rope_workspace_size", "attn_launch_count", "attn_packed_qkv_fwd", "attn_packed_qkv_bwd", "attn_packed_qkv_workspace_size", "attn_paged_append", "attn_paged_decode", "attn_paged_decode_workspace_size", "attn_paged_gather", "AttnError", "lib",
            "library_path"]
 
@@ -80,6 +80,8 @@ def lib():
         L.attn_bwd_ex.restype = i
         L.attn_rope.argtypes = [i, vp, i, i, i, i, i, f, vp]
         L.attn_rope.restype = i
+        L.attn_rope_ex.argtypes = [i, vp, ll, vp, ll, vp] + [i] * 8 + [ctypes.POINTER(ctypes.c_double), f, i, vp]
+        L.attn_rope_ex.restype = i
         L.attn_varlen_fwd.argtypes = [i] + [vp] * 7 + [i] * 8 + [f, i, i, f, vp]
         L.attn_varlen_fwd.restype = i
         L.attn_varlen_bwd.argtypes = [i] + [vp] * 10 + [sz, vp, vp] + [i] * 8 + [f, i, i, f, vp]
@@ -627,6 +629,134 @@ def attn_packed_qkv_bwd(qkv, do, seq_bounds, *, H, scale=None, window=0, dqkv=No
                                    _stream(stream))
     _check(st, "attn_packed_qkv_bwd")
     return dqkv
+
+
+# ------------------------------------------------------- rotary positions, every form
+class RopeFreqs:
+    """Frequencies of rotary pairs, made once and given to attn_rope_ex: pair i turns by
+    inv_freq[i] from one position to the next and is multiplied by amplitude."""
+
+    __slots__ = ("rotary_dim", "inv_freq", "amplitude", "_doubles")
+
+    def __init__(self, inv_freq, amplitude=1.0):
+        self.inv_freq = tuple(float(f) for f in inv_freq)
+        self.rotary_dim, self.amplitude = 2 * len(self.inv_freq), float(amplitude)
+        if not 1 <= len(self.inv_freq) <= 128 or not all(abs(f) <= 2.0 ** 32 for f in self.inv_freq):
+            raise ValueError("1 to 128 frequencies of magnitude at most 2^32 are needed")
+        if not math.isfinite(self.amplitude):
+            raise ValueError("the amplitude must be finite")
+        self._doubles = (ctypes.c_double * len(self.inv_freq))(*self.inv_freq)
+
+
+def attn_rope_freqs(rotary_dim, theta=10000.0, *, scaling=None, factor=1.0, original_length=None, slow=1.0, fast=None,
+                    amplitude=None) -> RopeFreqs:
+    """The frequencies f_i = theta^(-2i/rotary_dim), i < rotary_dim/2, for attn_rope_ex, scaled for
+    contexts `factor` times as long as the trained one of original_length positions:
+
+      None      f_i
+      "linear"  f_i / factor
+      "base"    theta grown to theta * factor^(rotary_dim/(rotary_dim - 2)): the first pair stays, the last
+                is divided by factor
+      "ramp"    f_i (1 - r_i) + f_i / factor * r_i, r_i rising from 0 to 1 along i between the pairs that make
+                `fast` (32) and `slow` (1) turns in original_length (rounded outwards to whole i);
+                amplitude 0.1 ln(factor) + 1 unless given
+      "bands"   f_i where it makes at least `fast` (4) turns in original_length, f_i / factor where it makes at
+                most `slow` (1), between them (1 - s) f_i / factor + s f_i with s linear in the turns
+
+    A model with other frequencies passes its own: RopeFreqs(inv_freq, amplitude)."""
+    d, theta, factor = int(rotary_dim), float(theta), float(factor)
+    if d != rotary_dim or d < 2 or d > 256 or d % 2:
+        raise ValueError("rotary_dim must be an even number from 2 to 256 (got %s)" % (rotary_dim,))
+    if not (theta > 0 and math.isfinite(theta)) or not (factor > 0 and math.isfinite(factor)):
+        raise ValueError("theta and factor must be positive and finite")
+    if scaling not in (None, "linear", "base", "ramp", "bands"):
+        raise ValueError("scaling must be None, 'linear', 'base', 'ramp' or 'bands' (got %r)" % (scaling,))
+    if scaling is None and factor != 1.0:
+        raise ValueError("a factor needs a scaling")
+    if scaling == "base":
+        if d == 2:
+            raise ValueError("'base' needs two pairs at least")
+        theta *= factor ** (d / (d - 2))
+    f = [theta ** (-2.0 * i / d) for i in range(d // 2)]
+    if scaling == "linear":
+        f = [x / factor for x in f]
+    elif scaling in ("ramp", "bands"):
+        fast = (32.0 if scaling == "ramp" else 4.0) if fast is None else float(fast)
+        if original_length is None or not original_length > 0 or not 0 < slow < fast:
+            raise ValueError("%r needs original_length > 0 and 0 < slow < fast" % scaling)
+        if scaling == "ramp":
+            if not theta > 1:
+                raise ValueError("'ramp' needs theta > 1")
+            # the (fractional) pair that makes t turns in original_length
+            pair = lambda t: d * math.log(original_length / (2 * math.pi * t)) / (2 * math.log(theta))
+            lo, hi = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), d - 1)
+            for i in range(d // 2):
+                r = min(max((i - lo) / max(hi - lo, 0.001), 0.0), 1.0)
+                f[i] = f[i] * (1 - r) + f[i] / factor * r
+            amplitude = 0.1 * math.log(factor) + 1 if amplitude is None and factor > 1 else amplitude
+        else:
+            for i in range(d // 2):
+                s = min(max((original_length * f[i] / (2 * math.pi) - slow) / (fast - slow), 0.0), 1.0)
+                f[i] = (1 - s) * f[i] / factor + s * f[i]
+    return RopeFreqs(f, 1.0 if amplitude is None else amplitude)
+
+
+def _row_stride(what, t):
+    """Distance of the rows of [rows, width] or [B, T, width], whose elements are contiguous."""
+    shape, st = t.shape, t.stride()
+    ok = shape[-1] <= 1 or st[-1] == 1
+    if len(shape) == 3 and shape[0] > 1 and shape[1] > 1:
+        ok = ok and st[0] == shape[1] * st[1]
+    row = st[-2] if shape[-2] > 1 or len(shape) == 2 else st[0]
+    if t.numel() == 0 or t.numel() == shape[-1]:
+        row = shape[-1]
+    if not ok or row < shape[-1]:
+        raise ValueError("%s must have contiguous rows, evenly spaced, that do not overlap" % what)
+    return row
+
+
+def attn_rope_ex(x, freqs, *, H, positions=None, pos=0, layout="half", rotary_start=0, backward=False, out=None, stream=None):
+    """Rotary positions in every form: returns x with a part of each head turned.
+
+    x [rows, H*hd] or [B, T, H*hd] (float32, float16 or bfloat16; rows may be strided: the query and key
+    columns of a fused projection, turned together as H + Hkv heads).  freqs: attn_rope_freqs(...) or
+    RopeFreqs; elements rotary_start .. rotary_start + freqs.rotary_dim - 1 of each head are turned, the
+    others copied.  layout "half" pairs element i of the part with i + rotary_dim/2, "interleaved" 2i with
+    2i + 1.  positions: int32 tensor of x's rows ([rows] or [B, T]); None: row t of each sequence sits at
+    pos + t.  backward: the transposed map, from the gradient of the output to that of x.  out: made if
+    not given; out=x turns in place."""
+    torch = _torch()
+    dev, dtype, shape = x.device, x.dtype, x.shape
+    if len(shape) not in (2, 3) or shape[-1] % H or not shape[-1]:
+        raise ValueError("x must be [rows, H*hd] or [B, T, H*hd] with H = %d (got %s)" % (H, tuple(shape)))
+    if layout not in ("half", "interleaved"):
+        raise ValueError("layout must be 'half' or 'interleaved' (got %r)" % (layout,))
+    dt = _dt(x)
+    hd, rows, period = shape[-1] // H, x.numel() // shape[-1], shape[-2]
+    if rotary_start < 0 or rotary_start + freqs.rotary_dim > hd:
+        raise ValueError("elements %d .. %d are turned of heads of %d" % (rotary_start, rotary_start + freqs.rotary_dim - 1, hd))
+    if positions is not None and (positions.dtype != torch.int32 or positions.shape != shape[:-1] or positions.device != dev or
+                                  not positions.is_contiguous()):
+        raise ValueError("positions must be a contiguous int32 tensor of shape %s on %s" % (tuple(shape[:-1]), dev))
+    if out is not None and (out.dtype != dtype or out.shape != shape or out.device != dev):
+        raise ValueError("out must be a %s tensor of shape %s on %s" % (dtype, tuple(shape), dev))
+    xs = _row_stride("x", x)
+    ys = shape[-1] if out is None else _row_stride("out", out)
+    if not x.is_cuda:
+        raise ValueError("the library takes CUDA tensors; x is on %s" % dev)
+    handle, context = _on(dev, stream)
+    if context is not None:
+        with context:
+            return attn_rope_ex(x, freqs, H=H, positions=positions, pos=pos, layout=layout, rotary_start=rotary_start,
+                                backward=backward, out=out)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    st = (_lib or lib()).attn_rope_ex(dt, x.data_ptr(), xs, out.data_ptr(), ys, _addr(positions), int(pos), period or 1, rows, H,
+                                      hd, freqs.rotary_dim, int(rotary_start), int(layout == "interleaved"), freqs._doubles,
+                                      freqs.amplitude, 1 if backward else 0, handle)
+    if st != OK:
+        _check(st, "attn_rope_ex")
+    return out
 
 
 # ------------------------------------------------------------ paged key/value cache

@@ -533,6 +533,48 @@ attn_status attn_rope(attn_dtype dt, void* x, int B, int T, int H, int hd, int p
         launch_rope(x, x, (int)dt, B, T, H, hd, pos, (double)theta, false, static_cast<cudaStream_t>(stream)), 1);
 }
 
+// Rows of `width` elements, y_stride apart, that share no element with rows x_stride apart: apart as
+// a whole, or columns of their own of the same rows.
+static bool rows_apart(const char* x, long long x_bytes, const char* y, long long y_bytes, long long rows, long long width) {
+    const long long ex = (rows - 1) * x_bytes + width, ey = (rows - 1) * y_bytes + width;
+    if (x + ex <= y || y + ey <= x) return true;
+    if (x_bytes != y_bytes) return false;
+    const long long d = ((y - x) % x_bytes + x_bytes) % x_bytes;
+    return d >= width && d + width <= x_bytes;
+}
+
+attn_status attn_rope_ex(attn_dtype dt, const void* x, long long x_stride, void* y, long long y_stride,
+                         const int* positions, int pos, int period, int rows, int H, int hd, int rotary_dim,
+                         int rotary_start, int interleaved, const double* inv_freq, float amplitude, int backward,
+                         void* stream) {
+    if (dt != ATTN_F32 && dt != ATTN_F16 && dt != ATTN_BF16) return ATTN_ERR_INVALID_ARG;
+    if (rows < 0 || H <= 0 || H > 65535 || hd <= 0) return ATTN_ERR_INVALID_ARG;
+    if (rotary_dim <= 0 || rotary_dim % 2 || rotary_start < 0 || rotary_dim > hd - rotary_start) return ATTN_ERR_INVALID_ARG;
+    if ((interleaved != 0 && interleaved != 1) || (backward != 0 && backward != 1)) return ATTN_ERR_INVALID_ARG;
+    if (!isfinite(amplitude) || !inv_freq) return ATTN_ERR_INVALID_ARG;
+    if (hd > 1024 || rotary_dim > 256 || rows > INT32_MAX - 64) return ATTN_ERR_UNSUPPORTED;
+    for (int i = 0; i < rotary_dim / 2; ++i)
+        if (!(fabs(inv_freq[i]) <= 0x1p32)) return ATTN_ERR_INVALID_ARG;
+    if (!positions && (pos < 0 || period <= 0 || (long long)pos + period > (long long)INT32_MAX + 1)) return ATTN_ERR_INVALID_ARG;
+    const long long width = (long long)H * hd, es = (long long)elem_size(dt);
+    if (x_stride < width || y_stride < width) return ATTN_ERR_INVALID_ARG;
+    if (rows == 0) return ATTN_OK;
+    if (x_stride > (1ll << 46) / rows || y_stride > (1ll << 46) / rows) return ATTN_ERR_INVALID_ARG;  // (no such memory)
+    if (!x || !y || reinterpret_cast<uintptr_t>(x) % es || reinterpret_cast<uintptr_t>(y) % es ||
+        (reinterpret_cast<uintptr_t>(positions) & 3u))
+        return ATTN_ERR_INVALID_ARG;
+    if (x == y ? (x_stride != y_stride && rows > 1)
+               : !rows_apart(static_cast<const char*>(x), x_stride * es, static_cast<const char*>(y), y_stride * es, rows,
+                             width * es))
+        return ATTN_ERR_INVALID_ARG;
+    RopeExCall c;
+    c.x = x; c.y = y; c.x_stride = x_stride; c.y_stride = y_stride;
+    c.positions = positions; c.inv_freq = inv_freq; c.pos = pos; c.period = period;
+    c.rows = rows; c.H = H; c.hd = hd; c.rotary_dim = rotary_dim; c.rotary_start = rotary_start;
+    c.interleaved = interleaved != 0; c.backward = backward != 0; c.amplitude = amplitude;
+    return counted(launch_rope_ex(c, (int)dt, static_cast<cudaStream_t>(stream)), 1);
+}
+
 }  // extern "C"
 
 // --------------------------------------------------- rotary embedding fused

@@ -56,6 +56,19 @@ cudaError_t launch_rope(const void* src, void* dst, int dt, int B, int T, int H,
 // cosine/sine table of rotary positions pos .. pos+npos-1 for the forward's fused rotation
 cudaError_t launch_rope_table(float* tab, int npos, int hd, int pos, double theta, cudaStream_t s);
 
+// rotary positions in every form (rope_ex.cu); fields as attn_rope_ex's arguments
+struct RopeExCall {
+    const void* x;
+    void* y;
+    long long x_stride, y_stride;
+    const int* positions;
+    const double* inv_freq;
+    int pos, period, rows, H, hd, rotary_dim, rotary_start;
+    bool interleaved, backward;
+    float amplitude;
+};
+cudaError_t launch_rope_ex(const RopeExCall& c, int dt, cudaStream_t s);
+
 // ---- paged key/value cache (paged.cu, paged_decode.cu): fp16 / bf16 rows, hd 64, 128 or 256
 enum : int { CACHE_16 = 0, CACHE_E4M3 = 1, CACHE_E5M2 = 2 };  // element type of the pages (16: that of the rows)
 // status bit, after those of common.cuh (which the dense kernels' captured figures are tied to, byte by byte)

@@ -29,56 +29,26 @@
 #include <type_traits>
 
 #include "paged.cuh"
+#include "turns.cuh"
 
 namespace attn {
 namespace {
-
-struct TurnFreqs {
-    unsigned long long f[128];  // theta^(-2i/hd) / (2 pi) turns, in units of 2^-64 turns
-};
-
-// A number to about 2^-104 of itself as an unevaluated sum of two doubles (T. J. Dekker, "A
-// floating-point technique for extending the available precision", 1971).  Products that are
-// added to are written as fma(a, b, 0), which no compiler joins with the addition.
-struct Two {
-    double hi, lo;
-};
-Two two_sum(double big, double small) {
-    const double s = big + small;
-    return {s, small - (s - big)};
-}
-Two two_mul(Two a, Two b) {
-    const double p = fma(a.hi, b.hi, 0.0);
-    return two_sum(p, fma(a.hi, b.lo, fma(a.lo, b.hi, fma(a.hi, b.hi, -p))));
-}
-Two two_sqrt(Two a) {  // a Newton step from the double's root
-    const double x = sqrt(a.hi), p = fma(x, x, 0.0);
-    return two_sum(x, ((a.hi - p) - fma(x, x, -p) + a.lo) / (2 * x));
-}
 
 TurnFreqs turn_freqs(int hd, double theta) {
     // hd / 2 is a power of two: theta^(-2/hd) is 1 / theta's root, that often squared
     Two r = {1 / theta, 0};
     r.lo = fma(-theta, r.hi, 1.0) / theta;
     for (int n = hd / 2; n > 1; n /= 2) r = two_sqrt(r);
-    Two turns = {0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};  // 1 / (2 pi)
+    Two turns = kTurnsPerRadian;
     TurnFreqs t;
     for (int i = 0; i < hd / 2; ++i) {
         // At most 1 / (2 pi) of a turn for theta >= 1; a theta below 1 turns faster than once a
         // position (2^29.4 times for 2^-32, the least): only the fraction of a turn counts, and it
         // is right to 2^-64 still.
-        t.f[i] = (unsigned long long)ldexp(turns.hi - floor(turns.hi), 64) + (unsigned long long)(long long)rint(ldexp(turns.lo, 64));
+        t.f[i] = turn_fraction(turns);
         turns = two_mul(turns, r);
     }
     return t;
-}
-
-__device__ __forceinline__ void turn_sincos(unsigned int p, unsigned long long f, float& s, float& c) {
-    const unsigned int fl = (unsigned int)f, fh = (unsigned int)(f >> 32);
-    const int frac = (int)(__umulhi(p, fl) + p * fh);      // upper half of p * f mod 2^64
-    const float a = (float)frac * 1.46291807926715968e-9f;  // 2 pi / 2^32
-    s = __sinf(a);
-    c = __cosf(a);
 }
 
 template <bool BF16>

@@ -378,6 +378,35 @@ ATTN_API attn_status attn_rope(attn_dtype dt, void* x, int B, int T, int H, int 
                         void* stream);
 
 /*
+ * Rotary embedding in every form: both pair layouts, a part of each head, any frequencies,
+ * any positions, rows inside wider ones, in place or into another buffer, and the gradient.
+ * Sources: ferrotensor engine/attention.rs, rope / rope_theta (the rotate-half turn, which
+ * this contains); the other forms are those of no page: they exist for models trained with
+ * them.
+ *   x, y  : rows [rows][H*hd] of dtype dt, x_stride / y_stride elements apart (at least H*hd),
+ *           aligned to their elements; y may be x (with the same stride), or else shares no
+ *           element with it.  Chunks of 16 bytes are moved where the addresses, the strides, hd,
+ *           rotary_start and the turned part (its halves in the half layout) are multiples of
+ *           them, smaller ones otherwise.
+ *   positions : int32 [rows] on the device, any values, or NULL: row r then sits at pos + r % period
+ *           (pos >= 0, period >= 1: the sequence length of a [B][T] batch).
+ *   rotary_dim, rotary_start : elements [rotary_start, rotary_start + rotary_dim) of each head vector
+ *           are turned (rotary_dim even, at most 256; hd at most 1024); the others are copied as
+ *           they are, in place not touched.
+ *   interleaved : pair i of the part z is (z[2i], z[2i+1]); 0: (z[i], z[i + rotary_dim/2]).
+ *   inv_freq : rotary_dim/2 doubles on the host, read during the call, magnitudes at most 2^32: pair
+ *           i turns by p * inv_freq[i] at position p and is multiplied by amplitude.
+ *   backward : 1: the transposed map (the turn the other way, the same amplitude), which takes
+ *           the gradient of y to that of x.
+ * Sines and cosines are right to 2^-20 for 16-bit elements and to 2^-22 for fp32 ones at every
+ * position; a turned element is rounded once.
+ */
+ATTN_API attn_status attn_rope_ex(attn_dtype dt, const void* x, long long x_stride, void* y, long long y_stride,
+                        const int* positions, int pos, int period, int rows, int H, int hd, int rotary_dim,
+                        int rotary_start, int interleaved, const double* inv_freq, float amplitude, int backward,
+                        void* stream);
+
+/*
  * Attention on rotary-embedded queries and keys, for callers that keep q and k
  * unrotated.  Source: ferrotensor engine/attention.rs, rope / rope_theta (the
  * rotate-half turn applied to q and k before flash attention), with the turn of

@@ -388,6 +388,38 @@ def packed_qkv_bwd(qkv, do, seq_bounds, *, H, scale, window=0):
     return np.concatenate([dq.reshape(L, -1), dk.reshape(L, -1), dv.reshape(L, -1)], axis=1)
 
 
+def turn_part(x, pos, *, H, inv_freq, start=0, interleaved=False, amplitude=1.0, backward=False):
+    """Rows x [n, H*hd] of which the 2*len(inv_freq) elements of each head from `start` on are turned: as
+    complex numbers (first, second element of pair i) times amplitude * exp(+-i pos inv_freq[i]), minus
+    backward (the transposed map).  Half layout, or interleaved pairs; the rest is copied.  The angle's
+    turns are reduced in exact rational arithmetic, so that it is right at every position."""
+    from fractions import Fraction
+
+    x = _f64(x)
+    n, hd, d = x.shape[0], x.shape[1] // H, 2 * len(inv_freq)
+    # 1 / (2 pi) to 2^-200, by Machin's formula for pi in integers
+    one = 1 << 240
+    arctan = lambda k: sum((1 if i % 2 == 0 else -1) * (one // k ** (2 * i + 1) // (2 * i + 1)) for i in range(120))
+    turn = Fraction(one, 2 * 4 * (4 * arctan(5) - arctan(239)))
+    ang = np.empty((n, d // 2))
+    for i, f in enumerate(inv_freq):
+        per = Fraction(float(f)) * turn
+        per = Fraction(round(per * 2 ** 150), 2 ** 150)
+        for r in range(n):
+            t = int(pos[r]) * per
+            ang[r, i] = float(t - round(t)) * 2 * np.pi
+    z = amplitude * np.exp((-1j if backward else 1j) * ang)[:, None, :]
+    out = x.reshape(n, H, hd).copy()
+    part = out[:, :, start:start + d]
+    if interleaved:
+        w = (part[:, :, 0::2] + 1j * part[:, :, 1::2]) * z
+        part[:, :, 0::2], part[:, :, 1::2] = w.real, w.imag
+    else:
+        w = (part[:, :, :d // 2] + 1j * part[:, :, d // 2:]) * z
+        part[:, :, :d // 2], part[:, :, d // 2:] = w.real, w.imag
+    return out.reshape(x.shape)
+
+
 # ------------------------------------------------------------ paged key/value cache
 F8_TOP = {"e4m3": 448.0, "e5m2": 57344.0}
 
