@@ -22,7 +22,7 @@ import os
 import threading
 
 __all__ = ["attn_fwd", "attn_bwd", "attn_decode", "attn_decode_len", "attn_varlen_fwd", "attn_varlen_bwd", "attn_fwd_ex", "attn_bwd_ex", "attn_rope", "attn_rope_ex", "attn_rope_freqs", "RopeFreqs", "attn_bwd_workspace_size", "attn_decode_workspace_size", "attn_decode_plan",
-           "attn_get_device_status", "attn_selftest_bounded_wait", "attn_kernel_family", "attn_kernel_family_bwd", "attn_fwd_rope", "attn_bwd_rope", "attn_fwd_rope_workspace_size", "attn_bwd_rope_workspace_size", "attn_launch_count", "attn_packed_qkv_fwd", "attn_packed_qkv_bwd", "attn_packed_qkv_workspace_size", "attn_paged_append", "attn_paged_decode", "attn_paged_decode_workspace_size", "attn_paged_gather", "AttnError", "lib",
+           "attn_get_device_status", "attn_selftest_bounded_wait", "attn_kernel_family", "attn_kernel_family_bwd", "attn_fwd_rope", "attn_bwd_rope", "attn_fwd_rope_workspace_size", "attn_bwd_rope_workspace_size", "attn_launch_count", "attn_packed_qkv_fwd", "attn_packed_qkv_bwd", "attn_packed_qkv_workspace_size", "attn_paged_append", "attn_paged_decode", "attn_paged_decode_workspace_size", "attn_paged_gather", "attn_paged_prefill", "attn_paged_prefill_workspace_size", "AttnError", "lib",
            "library_path"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -117,6 +117,10 @@ def lib():
         L.attn_paged_decode_workspace_size.restype = sz
         L.attn_paged_decode.argtypes = [i, i] + [vp] * 8 + [sz, vp, vp] + [i] * 8 + [f, i, i, f, vp]
         L.attn_paged_decode.restype = i
+        L.attn_paged_prefill_workspace_size.argtypes = [i] * 5
+        L.attn_paged_prefill_workspace_size.restype = sz
+        L.attn_paged_prefill.argtypes = [i, i, vp, ll] + [vp] * 7 + [sz, vp, vp, vp] + [i] * 8 + [f, i, i, f, vp]
+        L.attn_paged_prefill.restype = i
         L.attn_paged_gather.argtypes = [i, i] + [vp] * 8 + [i] * 7 + [vp]
         L.attn_paged_gather.restype = i
         L.attn_abi_version.argtypes = []
@@ -942,6 +946,56 @@ def attn_paged_decode(q, k_cache, v_cache, page_table, lengths, *, H, Hkv, k_sca
                              max(-1, min(int(window), 0x7fffffff)), float(softcap), handle)  # (as the C int would wrap it)
     if st != OK:
         _check(st, "attn_paged_decode")
+    return o, lse
+
+
+@functools.lru_cache(maxsize=256)
+def attn_paged_prefill_workspace_size(total, batch, H, Hkv, hd) -> int:
+    return int(lib().attn_paged_prefill_workspace_size(int(total), int(batch), int(H), int(Hkv), int(hd)))
+
+
+def attn_paged_prefill(q, k_cache, v_cache, page_table, lengths, cu_new, *, H, Hkv, k_scale=None, v_scale=None, scale=None,
+                       causal=True, window=0, softcap=0.0, o=None, lse=None, want_lse=True, workspace=None, stream=None):
+    """Attention of each sequence's newest tokens over its pages, those tokens' own keys among them
+    (attn_paged_append stores them first).
+
+    q [rows, H*hd] (rows may be strided: columns of a fused projection) holds the tokens' queries, sequence
+    b's in rows cu_new[b] .. cu_new[b+1]-1 (int32), at positions up to lengths[b]-1: any number of them,
+    whole prompts, chunks and single tokens together.  The cache as for attn_paged_append.  Returns
+    (o [rows, H*hd], lse [H, rows]); rows in no sequence are left as they were.  The launch does not
+    depend on the lengths: a captured graph can be replayed as they, the table and the pages change."""
+    torch = _torch()
+    rd, cd, num_pages, page_size, hd, B, max_pages = _pools(k_cache, v_cache, k_scale, v_scale, page_table, Hkv, q.dtype)
+    dev, n = k_cache.device, q.shape[0] if q.dim() else -1
+    qs = _rows("q", q, n, H * hd, q.dtype, dev)
+    _int_row("lengths", lengths, B, dev)
+    _int_row("cu_new", cu_new, B + 1, dev)
+    if o is not None:
+        _like("o", o, (n, H * hd), q.dtype, dev)
+    if lse is not None:
+        _like("lse", lse, (H, n), torch.float32, dev)
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError("workspace must be contiguous and on %s" % dev)
+    handle, context = _on(dev, stream)
+    if context is not None:
+        with context:
+            return attn_paged_prefill(q, k_cache, v_cache, page_table, lengths, cu_new, H=H, Hkv=Hkv, k_scale=k_scale,
+                                      v_scale=v_scale, scale=scale, causal=causal, window=window, softcap=softcap, o=o,
+                                      lse=lse, want_lse=want_lse, workspace=workspace)
+    L = _lib or lib()
+    if o is None:
+        o = torch.empty((n, H * hd), dtype=q.dtype, device=dev)
+    if lse is None and want_lse:
+        lse = torch.empty((H, n), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(attn_paged_prefill_workspace_size(n, B, H, Hkv, hd), dtype=torch.uint8, device=dev)
+    st = L.attn_paged_prefill(rd, cd, q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale),
+                              o.data_ptr(), _addr(lse), workspace.data_ptr(), workspace.nbytes, cu_new.data_ptr(),
+                              lengths.data_ptr(), page_table.data_ptr(), B, n, num_pages, page_size, max_pages, H, Hkv, hd,
+                              hd ** -0.5 if scale is None else float(scale), 1 if causal else 0,
+                              max(-1, min(int(window), 0x7fffffff)), float(softcap), handle)
+    if st != OK:
+        _check(st, "attn_paged_prefill")
     return o, lse
 
 

@@ -1176,6 +1176,64 @@ attn_status attn_paged_decode(attn_dtype dt, attn_dtype cache_dt, const void* q,
     return counted(launch_paged_decode(p, dt == ATTN_BF16, cache, maps, s), 2);
 }
 
+size_t attn_paged_prefill_workspace_size(int total, int batch, int H, int Hkv, int hd) {
+    if (total <= 0 || batch <= 0 || batch > 65535 || H <= 0 || Hkv <= 0 || H % Hkv || H / Hkv > 128 || total > INT32_MAX - 512 ||
+        (hd != 64 && hd != 128 && hd != 256))
+        return 0;
+    return paged_prefill_workspace(total, batch, H / Hkv, hd);
+}
+
+attn_status attn_paged_prefill(attn_dtype dt, attn_dtype cache_dt, const void* q, long long q_stride, const void* k_cache,
+                               const void* v_cache, const float* k_scale, const float* v_scale, void* o, float* lse,
+                               void* workspace, size_t workspace_bytes, const int* cu_new, const int* lengths,
+                               const int* page_table, int batch, int total_new, int num_pages, int page_size,
+                               int max_pages, int H, int Hkv, int hd, float scale, int causal, int window, float softcap,
+                               void* stream) {
+    PagedParams p;
+    int cache = 0;
+    attn_status st = paged_params(dt, cache_dt, k_cache, v_cache, k_scale, v_scale, page_table, batch, num_pages,
+                                  page_size, max_pages, H, Hkv, hd, &p, &cache);
+    if (st != ATTN_OK) return st;
+    if (total_new < 0) return ATTN_ERR_INVALID_ARG;
+    st = check_common(dt, batch, 1, 0, H, Hkv, hd, scale, causal, window, softcap, 0, nullptr, 0, true);
+    if (st != ATTN_OK) return st;
+    if (H / Hkv > 128 || total_new > INT32_MAX - 512) return ATTN_ERR_UNSUPPORTED;
+    if (batch == 0 || total_new == 0) return ATTN_OK;
+    if (!rows_ok(q, q_stride, (long long)H * hd) || q_stride > (1ll << 38) || !o || !aligned16(o) ||
+        (lse && (reinterpret_cast<uintptr_t>(lse) & 3u)) || !ints_ok(cu_new) || !ints_ok(lengths))
+        return ATTN_ERR_INVALID_ARG;
+    if (!workspace || !aligned16(workspace) ||
+        workspace_bytes < attn_paged_prefill_workspace_size(total_new, batch, H, Hkv, hd))
+        return ATTN_ERR_INVALID_ARG;
+    p.status = status_ptr();
+    if (!p.status) return ATTN_ERR_CUDA;
+    p.q = q; p.q_stride = q_stride; p.o = o; p.lse = lse; p.ws = static_cast<float*>(workspace);
+    p.cu = cu_new; p.lengths = lengths; p.total = total_new;
+    if (num_pages == 0) p.max_pages = 0;  // no token anywhere: no key tile, and no map is read
+    p.scale = scale; p.softcap = softcap;
+    // a window that leaves out no token that there can be is none
+    const long long most = (long long)p.max_pages * page_size + total_new;
+    p.wl = window > 0 && window <= most ? window - 1 : -1;
+    p.wr = causal ? 0 : p.wl;
+    PrefillMaps maps;
+    memset(&maps, 0, sizeof(maps));
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return ATTN_ERR_CUDA;
+    const cuuint64_t dims[3] = {(cuuint64_t)hd, (cuuint64_t)H, (cuuint64_t)total_new};
+    const cuuint64_t strides[2] = {(cuuint64_t)hd * 2, (cuuint64_t)q_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)(128 / p.G)}, one[3] = {1, 1, 1};
+    if (enc(&maps.q, dt == ATTN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+            const_cast<void*>(q), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return ATTN_ERR_CUDA;
+    const long long rows = (long long)num_pages * Hkv * page_size;
+    const int box_rows = page_size < 64 ? page_size : 64;
+    if (num_pages > 0 && (!pool_map(&maps.k, cache, dt == ATTN_BF16, k_cache, hd, rows, box_rows) ||
+                          !pool_map(&maps.v, cache, dt == ATTN_BF16, v_cache, hd, rows, box_rows)))
+        return ATTN_ERR_CUDA;
+    return counted(launch_paged_prefill(p, dt == ATTN_BF16, cache, maps, static_cast<cudaStream_t>(stream)), 3);
+}
+
 attn_status attn_paged_gather(attn_dtype dt, attn_dtype cache_dt, const void* k_cache, const void* v_cache,
                               const float* k_scale, const float* v_scale, void* k_out, void* v_out,
                               const int* cu_seqlens, const int* page_table, int batch, int total, int num_pages,

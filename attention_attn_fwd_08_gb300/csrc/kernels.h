@@ -114,4 +114,20 @@ inline cudaError_t launch_paged_decode(const PagedParams& p, bool bf16, int cach
     return bf16 ? launch_paged_decode_bf16(p, bf16, maps, s) : launch_paged_decode_f16(p, bf16, maps, s);
 }
 
+// attention of a chunk of new tokens over the pages (paged_prefill.cuh): q rows packed by cu, q_stride apart
+constexpr int kPrefillCtas = 152;
+struct PrefillMaps {
+    CUtensorMap q;     // [rows][H][hd], boxes of 64 columns by G heads by 128 / G rows
+    CUtensorMap k, v;  // as PagedMaps
+};
+cudaError_t launch_paged_prefill_bf16(const PagedParams& p, int cache, const PrefillMaps& maps, cudaStream_t s);
+cudaError_t launch_paged_prefill_f16(const PagedParams& p, int cache, const PrefillMaps& maps, cudaStream_t s);
+cudaError_t launch_paged_prefill_bf16_f8(const PagedParams& p, int cache, const PrefillMaps& maps, cudaStream_t s);
+cudaError_t launch_paged_prefill_f16_f8(const PagedParams& p, int cache, const PrefillMaps& maps, cudaStream_t s);
+inline cudaError_t launch_paged_prefill(const PagedParams& p, bool bf16, int cache, const PrefillMaps& maps, cudaStream_t s) {
+    if (cache == CACHE_16) return bf16 ? launch_paged_prefill_bf16(p, cache, maps, s) : launch_paged_prefill_f16(p, cache, maps, s);
+    return bf16 ? launch_paged_prefill_bf16_f8(p, cache, maps, s) : launch_paged_prefill_f16_f8(p, cache, maps, s);
+}
+size_t paged_prefill_workspace(int total, int B, int G, int hd);
+
 }  // namespace attn

@@ -1,0 +1,1124 @@
+// paged_prefill.cuh -- attention of a chunk of new tokens of each sequence over its pages: the
+// kernels, instantiated per row and pool type in paged_prefill_*.cu.
+//
+// Row (token i of sequence b's n, query head hq) at position p = L - n + i: O = sum_j p_j v_j / sum_j p_j,
+// p_j = exp(scale * q . k_j (capped)) over the keys j < L that the window lets it see.
+//
+// The rows of a KV head's G query heads share its keys, so a query tile is 128 / G tokens by G heads
+// (rows token * G + head), and an item is two such tiles (one at hd 256) that share every K/V tile: the
+// keys are read once for all heads of the group, and a chunk of a few dozen tokens still fills the 128
+// rows of the tensor cores' M.
+//   paged_plan_kernel lists the items of all sequences (first row, position, key tiles) from the
+//   device's lengths and prefix sums, with the running sum of their key tiles.
+//   paged_prefill_kernel: the key tiles of all (KV head, item) pairs stand in one row that is cut into
+//   equal stretches, one to each of 152 CTAs, so that unlike lengths, one long sequence or few
+//   rows load every SM alike; the launch depends on none of them.  An item cut by a stretch's end leaves
+//   partial (m, l, O) rows in the workspace.
+//   paged_prefill_merge_kernel joins those in a fixed order.
+#pragma once
+
+#include <math.h>
+
+#include <atomic>
+#include <type_traits>
+
+#include "paged.cuh"
+
+namespace attn {
+namespace {
+namespace prefill {
+
+constexpr int kM = 128;  // rows of a query tile
+constexpr float kLog2e = 1.4426950408889634f;
+// What an item costs beside its key tiles, in tiles, dealt out at its beginning.
+constexpr int kItemCost = 2;
+// The least that a stretch holds.
+constexpr int kMinShare = 4;
+
+// p = 2^(x - ref): a row's reference is moved when its largest p would pass 2^top, or, before it has
+// seen anything, when it would stay below 2^(top - 10); it is then put at 2^(top - 8).  fp16 p have room up
+// to 2^8 and no more exponents to lose below; bf16 ones stay at most 1, so that P V passes fp32's range
+// no sooner than the sum of V does.
+template <bool BF16>
+struct PRange {
+    static constexpr float top = BF16 ? 0.f : 8.f;
+};
+
+template <int HD, bool F8>
+struct Cfg {
+    static constexpr int NT = HD == 256 ? 1 : 2;     // query tiles of an item (O in TMEM: NT * HD columns)
+    static constexpr int BN = HD == 256 ? 64 : 128;  // keys of a tile
+    static constexpr int kBoxes = HD / 64;           // 128-byte columns of a 16-bit tile
+    static constexpr int kQBytes = kM * HD * 2, kTileBytes = BN * HD * 2;
+    // K and V tiles in turn go through one ring, 16 bits to an element; 8-bit tiles come into a
+    // ring of their own and are widened into it
+    static constexpr int kRawRow = HD < 128 ? HD : 128, kRawBoxes = HD / kRawRow;
+    static constexpr int kRawBytes = F8 ? BN * HD : 0;
+    static constexpr int kStages = F8 ? (HD == 64 ? 4 : 3) : (HD == 64 ? 8 : 5);
+    static constexpr int kRaw = F8 ? (HD == 64 ? 8 : 4) : 0;
+    static constexpr int kRingOff = NT * kQBytes;
+    static constexpr int kRawOff = kRingOff + kStages * kTileBytes;
+    static constexpr int kBarOff = kRawOff + kRaw * kRawBytes;
+    // barriers, in this order
+    static constexpr int Q_FULL = 0, Q_EMPTY = 2, S_FULL = 4, P_FULL = 6, O_DONE = 8, O_EMPTY = 10, PV_DONE = 12,
+                         V_CHECK = 14, MMA_DONE = 16, FULL = 17, EMPTY = FULL + kStages, RAW_FULL = EMPTY + kStages,
+                         RAW_EMPTY = RAW_FULL + kRaw, kBars = RAW_EMPTY + kRaw;
+    static constexpr int kBytes = kBarOff + kBars * 8 + 16 + 1024;  // (1024: alignment)
+    static_assert(kBytes <= 227 * 1024, "shared memory");
+    // Warpgroups: softmax of tile A; of tile B (at hd 256 the widening warps instead); loads and MMA
+    // issue; the widening warps beside two tiles.
+    static constexpr bool kWideB = F8 && NT == 1, kWide4 = F8 && NT == 2;
+    static constexpr int kThreads = kWide4 ? 512 : 384;
+    static constexpr int kWide0 = kWide4 ? 12 : 4;  // first widening warp
+    // registers: shares of what the launch holds (512 x 128, 384 x 168)
+    static constexpr int kRegsSoftmax = kWide4 ? 200 : 216, kRegsLoad = kWide4 ? 48 : 72, kRegsWide = kWide4 ? 64 : 120;
+    static constexpr int kRegsB = NT == 2 ? kRegsSoftmax : F8 ? kRegsWide : 168;
+    static_assert((kRegsSoftmax + kRegsB + kRegsLoad + (kWide4 ? kRegsWide : 0)) * 128 <= kThreads * (kWide4 ? 128 : 168),
+                  "register split exceeds the launch");
+};
+
+// ------------------------------------------------------------------- the plan
+// An item: `ntok` tokens of a sequence from packed row `row` on, the first at position `pos`; `len` valid
+// keys; key tiles t0 .. t0 + tiles - 1.
+struct Item {
+    int b, row, ntok, pos, len, t0, tiles, pad;
+};
+struct Plan {
+    long long* all;  // sum of one KV head's costs
+    int* count;      // items of one KV head
+    int* base;       // [B + 1] items before a sequence
+    Item* items;
+    long long* cum;  // [count + 1] costs before an item
+    float* part;     // partial rows
+};
+__host__ __device__ __forceinline__ long long plan_items(int total, int B, int tokens) { return (long long)total / tokens + B; }
+__host__ __device__ __forceinline__ size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+// bytes before the partial rows
+__host__ __device__ __forceinline__ size_t plan_bytes(int total, int B, int tokens) {
+    const size_t n = (size_t)plan_items(total, B, tokens);
+    return 256 + round256(((size_t)B + 1) * 4) + round256(n * sizeof(Item)) + round256((n + 1) * 8);
+}
+__device__ __forceinline__ Plan plan_of(const PagedParams& P, int tokens) {
+    uint8_t* w = reinterpret_cast<uint8_t*>(P.ws);
+    const size_t n = (size_t)plan_items(P.total, P.B, tokens);
+    Plan p;
+    p.all = reinterpret_cast<long long*>(w);
+    p.count = reinterpret_cast<int*>(w + 8);
+    w += 256;
+    p.base = reinterpret_cast<int*>(w);
+    w += round256(((size_t)P.B + 1) * 4);
+    p.items = reinterpret_cast<Item*>(w);
+    w += round256(n * sizeof(Item));
+    p.cum = reinterpret_cast<long long*>(w);
+    w += round256((n + 1) * 8);
+    p.part = reinterpret_cast<float*>(w);
+    return p;
+}
+// partial rows: slot s (two to a stretch: 2c for the item that begins before stretch c, 2c + 1 for the one
+// that ends behind it) holds (m, l) of its rows, and all slots' O follow
+constexpr int kSlots = 2 * kPrefillCtas;
+__host__ __device__ __forceinline__ size_t part_bytes(int rows, int hd) { return (size_t)kSlots * rows * (8 + (size_t)hd * 4); }
+__device__ __forceinline__ float2* part_ml(const Plan& p, int slot, int rows) {
+    return reinterpret_cast<float2*>(p.part) + (size_t)slot * rows;
+}
+__device__ __forceinline__ float* part_o(const Plan& p, int slot, int rows, int hd) {
+    return p.part + (size_t)kSlots * rows * 2 + (size_t)slot * rows * hd;
+}
+
+// inclusive sum over the block's 1024 threads; total in *all
+__device__ __forceinline__ long long block_scan(long long x, long long* sums, long long* all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();  // (sums of an earlier scan have been read)
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    long long s = sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
+    }
+    *all = __shfl_sync(0xffffffffu, s, 31);
+    const long long before = __shfl_sync(0xffffffffu, s, max(warp - 1, 0));
+    return x + (warp > 0 ? before : 0);
+}
+
+// new tokens of sequence b: rows first .. first + n - 1 (n = 0 where the prefix sums leave the rows)
+__device__ __forceinline__ int seq_rows(const PagedParams& P, int b, int& first, bool flag) {
+    const int a0 = __ldg(P.cu + b), a1 = __ldg(P.cu + b + 1);
+    first = a0;
+    if (a0 < 0 || a1 < a0 || a1 > P.total) {
+        if (flag) atomicOr(P.status, ST_PAGED_BOUNDS);
+        return 0;
+    }
+    return a1 - a0;
+}
+
+constexpr int kPlanThreads = 1024;
+// tokens: of an item; bn: keys of a tile.  One block: the sums over sequences and items are small.
+__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedParams P, const int tokens, const int bn) {
+    __shared__ long long sums[32];
+    __shared__ int base_s[kPlanThreads + 1];
+    const Plan plan = plan_of(P, tokens);
+    const long long most = plan_items(P.total, P.B, tokens);
+    const bool small = P.B <= kPlanThreads;
+    int* base = small ? base_s : plan.base;
+    long long carry = 0, all;
+    for (int b0 = 0; b0 < P.B; b0 += kPlanThreads) {
+        const int b = b0 + threadIdx.x;
+        int n = 0, first;
+        if (b < P.B) {
+            n = (seq_rows(P, b, first, true) + tokens - 1) / tokens;
+            // (without any page, no length is out of range: nothing is attended)
+            if (P.max_pages > 0 && __ldg(P.lengths + b) > (P.max_pages << P.page_shift)) atomicOr(P.status, ST_PAGED_BOUNDS);
+        }
+        const long long incl = block_scan(n, sums, &all);
+        if (b < P.B) base[b] = (int)min(carry + incl - n, most);
+        carry += all;
+    }
+    // (prefix sums that go back and forth, which are flagged, could name more items than there is room for)
+    const int count = (int)min(carry, most);
+    __syncthreads();
+    // the main kernel's CTAs come up meanwhile
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    carry = 0;
+    for (int e0 = 0; e0 < count; e0 += kPlanThreads) {
+        const int e = e0 + threadIdx.x;
+        Item it = {};
+        long long cost = 0;
+        if (e < count) {
+            int lo = 0, hi = P.B;  // the last b with base[b] <= e lies in [lo, hi)
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (base[mid] <= e) lo = mid;
+                else hi = mid;
+            }
+            int first;
+            const int n = seq_rows(P, lo, first, false), i0 = (e - base[lo]) * tokens;
+            it.b = lo;
+            it.row = first + i0;
+            it.ntok = min(tokens, n - i0);
+            it.len = min(max(__ldg(P.lengths + lo), 0), P.max_pages << P.page_shift);
+            it.pos = it.len - n + i0;
+            int klo, khi;
+            key_range(P.wl, P.wr, it.len, it.pos, it.pos + it.ntok - 1, &klo, &khi);
+            it.t0 = klo / bn;
+            it.tiles = khi > klo ? (khi + bn - 1) / bn - it.t0 : 0;
+            cost = it.tiles + kItemCost;
+            plan.items[e] = it;
+        }
+        const long long incl = block_scan(cost, sums, &all);
+        if (e < count) plan.cum[e] = carry + incl - cost;
+        carry += all;
+    }
+    if (threadIdx.x == 0) {
+        *plan.all = carry;
+        *plan.count = count;
+        plan.cum[count] = carry;
+    }
+}
+
+// ------------------------------------------------------------------- stretches
+struct Deal {
+    long long all, share;  // of all KV heads; of a stretch
+};
+__device__ __forceinline__ Deal deal_of(const PagedParams& P, long long per_head) {
+    Deal d;
+    d.all = per_head * P.Hkv;
+    d.share = max((d.all + kPrefillCtas - 1) / kPrefillCtas, (long long)kMinShare);
+    return d;
+}
+// A CTA's walk along its stretch, the same in every warp: `next` gives the next item of which the stretch
+// holds key tiles (or that has none and ends in it), tiles [begin, end) of it.
+struct Walk {
+    long long left;  // of the stretch
+    long long off;   // where it enters item e
+    int h, e, count;
+};
+struct Part {
+    Item it;
+    int h, begin, end;
+    __device__ bool whole() const { return begin == 0 && end == it.tiles; }
+};
+__device__ __forceinline__ Walk walk_of(const PagedParams& P, const Plan& plan) {
+    Walk w;
+    const long long per_head = *plan.all;
+    const Deal d = deal_of(P, per_head);
+    const long long first = min(d.all, (long long)blockIdx.x * d.share);
+    w.left = min(d.share, d.all - first);
+    w.count = *plan.count;
+    w.h = w.e = 0;
+    w.off = 0;
+    if (w.left > 0) {
+        w.h = (int)(first / per_head);
+        const long long in = first - w.h * per_head;
+        w.e = warp_last_le(w.count, in, [&](int i) { return plan.cum[i]; });
+        w.off = in - plan.cum[w.e];
+    }
+    return w;
+}
+__device__ __forceinline__ bool next_part(const Plan& plan, Walk& w, Part& p) {
+    while (w.left > 0) {
+        p.it = plan.items[w.e];
+        p.h = w.h;
+        const long long cost = p.it.tiles + kItemCost, end = min(cost, w.off + w.left);
+        p.begin = (int)max(w.off - kItemCost, 0ll);
+        p.end = (int)max(end - kItemCost, 0ll);
+        w.left -= end - w.off;
+        w.off = 0;
+        if (++w.e == w.count) w.e = 0, ++w.h;
+        if (p.end > p.begin || (p.it.tiles == 0 && end == cost)) return true;
+    }
+    return false;
+}
+
+// Query tile u of a part: its tokens, and the tiles [t0, t0 + n) of the part that any of its rows sees.
+struct Tiles {
+    int ntok, pos, t0, n;
+};
+template <int BN>
+__device__ __forceinline__ Tiles tiles_of(const PagedParams& P, const Part& p, int u, int tm) {
+    Tiles t;
+    t.ntok = min(max(p.it.ntok - u * tm, 0), tm);
+    t.pos = p.it.pos + u * tm;
+    t.t0 = t.n = 0;
+    if (t.ntok > 0) {
+        int lo, hi;
+        key_range(P.wl, P.wr, p.it.len, t.pos, t.pos + t.ntok - 1, &lo, &hi);
+        const int a = max(lo / BN, p.it.t0 + p.begin), b = min((hi + BN - 1) / BN, p.it.t0 + p.end);
+        if (hi > lo && b > a) t.t0 = a, t.n = b - a;
+    }
+    return t;
+}
+
+__device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+// four codes as two words of two 16-bit values, times s in fp32, rounded once
+template <bool BF16>
+__device__ __forceinline__ void widen4(uint32_t c, bool e4m3, float s, uint32_t& w0, uint32_t& w1) {
+    uint32_t h0, h1;
+    if (e4m3)
+        asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+            : "=r"(h0), "=r"(h1)
+            : "r"(c));
+    else
+        h0 = __byte_perm(c, 0, 0x1404), h1 = __byte_perm(c, 0, 0x3424);  // an e5m2 code is its fp16's upper byte
+    const float2 a = h2_to_f2(h0), b = h2_to_f2(h1);
+    w0 = pack2<BF16>(a.x * s, a.y * s);
+    w1 = pack2<BF16>(b.x * s, b.y * s);
+}
+
+// ------------------------------------------------------------------ the kernel
+// Roles (warps): softmax of tile u, one thread to a row (0-3, 4-7); loads (8); MMA issue of tile u (9 + u); over
+// 8-bit pools, widening (Cfg::kWide0 ...).  Two tiles take turns as in the dense forward: one tile's
+// softmax runs while the tensor cores work on the other's P V and next S; each has one S buffer, and a
+// completed S(n), issued after P(n-1) V(n-1), also means that O stands still.  With one tile (hd 256)
+// there are two S buffers instead, and S(n+1) is issued before P(n) V(n).
+//
+// What a row does not see has no effect on it.  A tile that some row does not see whole is looked over
+// by the softmax warps before its P V: rows of V that no row of the item sees (behind the sequence, in a
+// page that does not exist) become zeros in shared memory; if a value left in it is not finite, the
+// product is made row by row over the keys that the row sees, by the softmax warps, in place of the MMA.
+template <bool BF16, int HD, bool F8, bool CAP>
+__global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
+    paged_prefill_kernel(const PagedParams P, const int e4m3, const __grid_constant__ CUtensorMap tmQ,
+                         const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
+    using C = Cfg<HD, F8>;
+    constexpr int NT = C::NT, BN = C::BN, NS = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
+    const uint32_t bar0 = smem_u32(bars);
+    auto BAR = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+    __shared__ int abort_flag;
+    __shared__ int done_count[2];  // warps that have finished a softmax of tile u
+    __shared__ int bad_tile[2][2]; // the last look-over, by its parity, that met a value that is not finite
+    __shared__ int skip_pv[2][2];  // by the parity of the tile: the softmax warps make this product
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tm = kM / P.G;  // tokens of a query tile
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kBars; ++i) {
+            uint32_t n = 1;
+            if ((i >= C::P_FULL && i < C::P_FULL + 2) || (i >= C::O_EMPTY && i < C::O_EMPTY + 2) ||
+                (i >= C::V_CHECK && i < C::V_CHECK + 2))
+                n = 4;  // softmax warps of a tile
+            if ((i >= C::EMPTY && i < C::EMPTY + NS) || i == C::MMA_DONE) n = NT;  // MMA issuers
+            if (F8 && ((i >= C::FULL && i < C::FULL + NS) || (i >= C::RAW_EMPTY && i < C::RAW_EMPTY + C::kRaw)))
+                n = 4;  // widening warps
+            mbar_init(BAR(i), n);
+        }
+        abort_flag = 0;
+        for (int u = 0; u < 2; ++u) done_count[u] = 0, bad_tile[u][0] = bad_tile[u][1] = 0, skip_pv[u][0] = skip_pv[u][1] = 0;
+        fence_barrier_init();
+    }
+    if (warp == 9) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = *tmem_slot;
+    // the plan is there from here on; the merging kernel's CTAs may come up
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const Plan plan = plan_of(P, NT * tm);
+    // rows of a box of keys, and how many stand below each other in a tile
+    const int box_rows = min(P.page_size, 64), subs = BN / box_rows;
+    // page of the box of keys from `key` on, -1 if it is not there, -2 if no row of [lo, hi) lies in it
+    auto box_page = [&](const Part& p, int key, int lo, int hi, bool flag) {
+        if (key >= hi || key + box_rows <= lo) return -2;
+        return page_of(P, p.it.b, key >> P.page_shift, flag);
+    };
+    auto key_span = [&](const Part& p, int& lo, int& hi) {
+        key_range(P.wl, P.wr, p.it.len, p.it.pos, p.it.pos + p.it.ntok - 1, &lo, &hi);
+    };
+
+    if (warp >= 8 && warp < 12) {
+        regs_dec<C::kRegsLoad>();
+        if (warp == 8) {
+            // ------------------------------------------------------------ loads
+            if (elect_one()) {
+                prefetch_tmap(&tmQ);
+                if (P.max_pages > 0) {  // (there are no other maps without a page)
+                    prefetch_tmap(&tmK);
+                    prefetch_tmap(&tmV);
+                }
+            }
+            constexpr int kCols = F8 ? C::kRawBoxes : C::kBoxes, kRowBytes = F8 ? C::kRawRow : 128;
+            constexpr int kBytes = F8 ? C::kRawBytes : C::kTileBytes, kDepth = F8 ? C::kRaw : NS;
+            constexpr int kFull = F8 ? C::RAW_FULL : C::FULL, kEmpty = F8 ? C::RAW_EMPTY : C::EMPTY;
+            constexpr int kOff = F8 ? C::kRawOff : C::kRingOff;
+            const int sub = lane % subs, col = lane / subs;
+            bool ok = true;
+            int stage = 0, phase = 1, made = 0;  // (a wait on a fresh barrier's other phase returns at once)
+            int qn[2] = {0, 0};
+            Walk w = walk_of(P, plan);
+            Part p;
+            while (ok && next_part(plan, w, p)) {
+                int lo, hi;
+                key_span(p, lo, hi);
+                Tiles tu[2];
+                for (int u = 0; u < NT; ++u) tu[u] = tiles_of<BN>(P, p, u, tm);
+                const int tile0 = p.it.t0 + p.begin, n = p.end - p.begin;
+                int pg = n > 0 && col < kCols ? box_page(p, tile0 * BN + sub * box_rows, lo, hi, true) : -2;
+                for (int u = 0; ok && u < NT; ++u) {
+                    if (tu[u].n == 0) continue;
+                    if (qn[u] > 0 && !warp_wait(BAR(C::Q_EMPTY + u), (qn[u] - 1) & 1, P.status, ST_FWD_PRODUCER, &abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    if (elect_one()) mbar_expect_tx(BAR(C::Q_FULL + u), C::kBoxes * P.G * tm * 128);
+                    for (int bx = 0; bx < C::kBoxes; ++bx)
+                        if (elect_one())
+                            tma_load_3d(sbase + u * C::kQBytes + bx * (kM * 128), &tmQ, BAR(C::Q_FULL + u), bx * 64, p.h * P.G,
+                                        p.it.row + u * tm);
+                    ++qn[u];
+                }
+                for (int i = 0; ok && i < n; ++i) {
+                    const int key = (tile0 + i) * BN + sub * box_rows;
+                    const int next = i + 1 < n && col < kCols ? box_page(p, key + BN, lo, hi, true) : -2;
+                    const bool load = col < kCols && pg >= 0;
+                    const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, load)) * box_rows * kRowBytes);
+                    const int y = load ? ((pg * P.Hkv + p.h) << P.page_shift) + (key & (P.page_size - 1)) : 0;
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        if (!warp_wait(BAR(kEmpty + stage), phase, P.status, ST_FWD_PRODUCER, &abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        if (lane == 0) mbar_expect_tx(BAR(kFull + stage), bytes);
+                        __syncwarp();
+                        if (load)
+                            load_2d(sbase + kOff + stage * kBytes + col * (BN * kRowBytes) + sub * box_rows * kRowBytes,
+                                    kv ? &tmV : &tmK, BAR(kFull + stage), col * (F8 ? kRowBytes : 64), y);
+                        __syncwarp();
+                        made = min(made + 1, kDepth);
+                        if (++stage == kDepth) stage = 0, phase ^= 1;
+                    }
+                    pg = next;
+                }
+            }
+            // every copy in flight lands before the CTA ends
+            for (int u = 0; u < NT; ++u)
+                if (qn[u] > 0) mbar_wait(BAR(C::Q_FULL + u), (qn[u] - 1) & 1, P.status, ST_TEARDOWN, nullptr);
+            for (int i = 0; i < made; ++i) {
+                if (--stage < 0) stage = kDepth - 1, phase ^= 1;
+                mbar_wait(BAR(kFull + stage), phase ^ 1, P.status, ST_TEARDOWN, nullptr);
+            }
+        } else if (warp <= 8 + NT) {
+            // -------------------------------------------------------- MMA issue
+            const int u = warp - 9;
+            constexpr uint32_t idS = idesc_f16(BF16, kM, BN, false, false), idPV = idesc_f16(BF16, kM, HD, false, true);
+            const uint64_t qdesc = sdesc_sw128(sbase + u * C::kQBytes, 16, 1024);
+            const uint32_t tO = tbase + 256 + u * HD;
+            auto wait = [&](int bar, uint32_t parity) { return warp_wait(BAR(bar), parity, P.status, ST_FWD_MMA, &abort_flag); };
+            bool ok = true;
+            unsigned g = 0;            // ring position of the part's first K tile
+            int sc = 0, pc = 0, act = 0;  // S issued, P taken, parts in which this tile was active
+            Walk w = walk_of(P, plan);
+            Part p;
+            while (ok && next_part(plan, w, p)) {
+                const int n = p.end - p.begin, tile0 = p.it.t0 + p.begin;
+                if (n <= 0) continue;
+                const Tiles my = tiles_of<BN>(P, p, u, tm);
+                auto has = [&](int i) { return tile0 + i >= my.t0 && tile0 + i < my.t0 + my.n; };
+                auto kst = [&](int i) { return (g + 2 * i) % NS; };
+                auto kph = [&](int i) { return ((g + 2 * i) / NS) & 1; };
+                auto vst = [&](int i) { return (g + 2 * i + 1) % NS; };
+                auto vph = [&](int i) { return ((g + 2 * i + 1) / NS) & 1; };
+                auto issue_s = [&](int i) {
+                    const uint32_t tS = tbase + (NT == 2 ? u * 128 : (sc & 1) * 64);
+                    const uint64_t kdesc = sdesc_sw128(sbase + C::kRingOff + kst(i) * C::kTileBytes, 16, 1024);
+#pragma unroll
+                    for (int kk = 0; kk < HD / 16; ++kk)
+                        mma_ss_e(tS, qdesc + (((kk >> 2) * (kM * 128) + (kk & 3) * 32) >> 4),
+                                 kdesc + (((kk >> 2) * (BN * 128) + (kk & 3) * 32) >> 4), idS, kk > 0 ? 1u : 0u);
+                    mma_commit_e(BAR(C::S_FULL + (NT == 2 ? u : (sc & 1))));
+                    ++sc;
+                    if (tile0 + i == my.t0 + my.n - 1) mma_commit_e(BAR(C::Q_EMPTY + u));
+                };
+                auto issue_pv = [&](int i, int k) {
+                    const uint32_t tS = tbase + (NT == 2 ? u * 128 : ((pc - 1) & 1) * 64);
+                    const uint64_t vdesc = sdesc_sw128(sbase + C::kRingOff + vst(i) * C::kTileBytes, BN * 128, 1024);
+                    const int skip = *static_cast<volatile int*>(&skip_pv[u][(pc - 1) & 1]);
+                    if (!skip) {
+#pragma unroll
+                        for (int kk = 0; kk < BN / 16; ++kk)
+                            mma_ts_e(tO, tS + kk * 8, vdesc + ((kk * 16 * 128) >> 4), idPV, (k > 0 || kk > 0) ? 1u : 0u);
+                    }
+                    if constexpr (NT == 1) mma_commit_e(BAR(C::PV_DONE));
+                    if (k == my.n - 1) mma_commit_e(BAR(C::O_DONE + u));
+                };
+                // A tile's release is committed only after the wait for its data, also for tiles that
+                // this query tile skips, so that no arrival belongs to a later use of the stage.
+                if (my.n > 0 && !wait(C::Q_FULL + u, act & 1)) break;
+                if (!wait(C::FULL + kst(0), kph(0))) break;
+                tc_fence_after();
+                if (has(0)) issue_s(0);
+                mma_commit_e(BAR(C::EMPTY + kst(0)));
+                for (int i = 0; ok && i < n; ++i) {
+                    const int k = tile0 + i - my.t0;
+                    if constexpr (NT == 1) {
+                        if (i + 1 < n) {
+                            ok = wait(C::FULL + kst(i + 1), kph(i + 1));
+                            if (!ok) break;
+                            tc_fence_after();
+                            if (has(i + 1)) issue_s(i + 1);
+                            mma_commit_e(BAR(C::EMPTY + kst(i + 1)));
+                        }
+                    }
+                    ok = wait(C::FULL + vst(i), vph(i));
+                    if (NT == 2 && ok && i + 1 < n) ok = wait(C::FULL + kst(i + 1), kph(i + 1));
+                    if (ok && has(i)) {
+                        ok = wait(C::P_FULL + u, pc & 1);
+                        ++pc;
+                        // the first product overwrites O: the last part's epilogue must have read it
+                        if (ok && k == 0 && act > 0) ok = wait(C::O_EMPTY + u, (act - 1) & 1);
+                    }
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (has(i)) issue_pv(i, k);
+                    if constexpr (NT == 2) {
+                        if (i + 1 < n && has(i + 1)) issue_s(i + 1);
+                    }
+                    mma_commit_e(BAR(C::EMPTY + vst(i)));
+                    if (NT == 2 && i + 1 < n) mma_commit_e(BAR(C::EMPTY + kst(i + 1)));
+                }
+                g += 2 * n;
+                if (my.n > 0) ++act;
+            }
+            mma_commit_e(BAR(C::MMA_DONE));
+            mbar_wait(BAR(C::MMA_DONE), 0, P.status, ST_TEARDOWN, nullptr);
+        }
+    } else if (F8 && warp >= C::kWide0 && warp < C::kWide0 + 4) {
+        // ---------------------------------------------------------------- widening
+        if constexpr (F8) {
+            regs_dec<C::kRegsWide>();
+            const int ww = warp - C::kWide0;
+            constexpr int kChunks = C::kRawRow / 16;            // 16-byte chunks of a box's row
+            constexpr int kSteps = BN * HD / 16 / 128;          // chunks of a lane, of a tile
+            const int sub = lane % subs;
+            bool ok = true;
+            int stage = 0, phase = 1, raw = 0, raw_phase = 0;
+            auto scales = [&](const Part& p, int pg) {
+                if (pg < 0) return make_float2(0.f, 0.f);
+                const long long i = (long long)pg * P.Hkv + p.h;
+                return make_float2(__ldg(P.k_scale + i), __ldg(P.v_scale + i));
+            };
+            Walk w = walk_of(P, plan);
+            Part p;
+            while (ok && next_part(plan, w, p)) {
+                int lo, hi;
+                key_span(p, lo, hi);
+                const int tile0 = p.it.t0 + p.begin, n = p.end - p.begin;
+                auto page_at = [&](int i) { return i < n ? box_page(p, (tile0 + i) * BN + sub * box_rows, lo, hi, false) : -2; };
+                int pg = page_at(1);
+                float2 sc = scales(p, page_at(0));
+                for (int i = 0; ok && i < n; ++i) {
+                    const float2 sc_next = scales(p, pg);
+                    pg = page_at(i + 2);
+#pragma unroll 1
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const float mine = kv ? sc.y : sc.x;
+                        ok = warp_wait(BAR(C::RAW_FULL + raw), raw_phase, P.status, ST_FWD_PRODUCER, &abort_flag) &&
+                             warp_wait(BAR(C::EMPTY + stage), phase, P.status, ST_FWD_PRODUCER, &abort_flag);
+                        if (!ok) break;
+                        const uint8_t* src = smem + C::kRawOff + raw * C::kRawBytes;
+                        const uint32_t dst = sbase + C::kRingOff + stage * C::kTileBytes;
+#pragma unroll 4
+                        for (int t = 0; t < kSteps; ++t) {
+                            // consecutive lanes: the chunks of a row, then of the next; this warp's rows lie together
+                            const int at = ww * kSteps * 32 + t * 32 + lane;
+                            const int c = at % kChunks, row = at / kChunks % BN, box = at / kChunks / BN;
+                            const uint4 x = *reinterpret_cast<const uint4*>(
+                                src + box * (BN * C::kRawRow) + row * C::kRawRow +
+                                (C::kRawRow == 128 ? (c ^ (row & 7)) << 4 : (c ^ ((row >> 1) & 3)) << 4));
+                            const float s = __shfl_sync(0xffffffffu, mine, row / box_rows);
+                            uint32_t o[8];
+                            widen4<BF16>(x.x, e4m3, s, o[0], o[1]);
+                            widen4<BF16>(x.y, e4m3, s, o[2], o[3]);
+                            widen4<BF16>(x.z, e4m3, s, o[4], o[5]);
+                            widen4<BF16>(x.w, e4m3, s, o[6], o[7]);
+                            // columns 16c .. of the box: two chunks of a 128-byte column of the wide tile.  Lanes of
+                            // either half of a row store them in the other order, so that eight lanes meet no bank twice.
+                            const int wide = box * (kChunks / 4) + (c >> 2), c2 = (2 * c) & 7;
+                            const uint32_t to = dst + wide * (BN * 128) + row * 128;
+                            const bool swap = (c >> 2) & 1;
+                            const uint32_t a0 = to + ((c2 ^ (row & 7)) << 4), a1 = to + (((c2 + 1) ^ (row & 7)) << 4);
+                            st_shared_v4(swap ? a1 : a0, swap ? o[4] : o[0], swap ? o[5] : o[1], swap ? o[6] : o[2], swap ? o[7] : o[3]);
+                            st_shared_v4(swap ? a0 : a1, swap ? o[0] : o[4], swap ? o[1] : o[5], swap ? o[2] : o[6], swap ? o[3] : o[7]);
+                        }
+                        fence_proxy_async_smem();  // the tensor cores read the tile through the async proxy
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(BAR(C::FULL + stage));
+                            mbar_arrive(BAR(C::RAW_EMPTY + raw));
+                        }
+                        if (++stage == NS) stage = 0, phase ^= 1;
+                        if (++raw == C::kRaw) raw = 0, raw_phase ^= 1;
+                    }
+                    sc = sc_next;
+                }
+            }
+        }
+    } else if (warp < 4 * NT) {
+        regs_inc<C::kRegsSoftmax>();
+        // -------------------------------------------------- softmax, epilogue of tile u
+        const int u = warp >> 2, wq = warp & 3, r = wq * 32 + lane;
+        const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
+        const uint32_t tO = tbase + 256 + u * HD + lane_off;
+        const int tok = r / P.G, head = r - tok * P.G;  // of this thread's row
+        const float sl2 = P.scale * kLog2e;
+        const uint64_t sl2_2 = f2_make(sl2, sl2);
+        const float cap_in = P.scale / fmaxf(P.softcap, 1e-30f), cap_out = P.softcap * kLog2e;
+        constexpr float kTop = PRange<BF16>::top;
+        constexpr int NC = BN / 32;
+        auto wait = [&](int bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait(BAR(bar), parity, P.status, ST_FWD_SOFTMAX, &abort_flag));
+        };
+        bool ok = true;
+        int sc = 0, act = 0, vc = 0;  // tiles done, parts in which this tile was active, look-overs
+        int base[2] = {0, 0};         // softmaxes of both tiles in earlier parts
+        unsigned g = 0;               // ring position of the part's first K tile
+        // x = score * log2(e) - m of a pair of raw scores; mode 0: plain; with a softcap 1: the fitted
+        // polynomial, 2: by exp, 3: the short polynomial
+        auto to_x = [&](auto modec, uint64_t rr, uint64_t nm) -> uint64_t {
+            constexpr int kMode = decltype(modec)::value;
+            if constexpr (kMode == 2) {
+                float r0, r1, m0, m1;
+                f2_split(rr, r0, r1);
+                f2_split(nm, m0, m1);
+                // a masked score is -inf, and softcap * tanh(-inf) would be finite
+                return f2_make(r0 == -INFINITY ? -INFINITY : fmaf(cap_out, tanh_accurate(r0 * cap_in), m0),
+                               r1 == -INFINITY ? -INFINITY : fmaf(cap_out, tanh_accurate(r1 * cap_in), m1));
+            } else if constexpr (kMode == 1) {
+                const CapPoly cp = cap_poly(P.scale, P.softcap);
+                const uint64_t uu = f2_mul(rr, rr);
+                uint64_t sp = f2_fma(uu, f2_mul(cp.s3, sl2_2), f2_mul(cp.s2, sl2_2));
+                sp = f2_fma(uu, sp, f2_mul(cp.s1, sl2_2));
+                sp = f2_fma(uu, sp, f2_mul(cp.s0, sl2_2));
+                return f2_fma(rr, f2_fma(uu, sp, sl2_2), nm);
+            } else if constexpr (kMode == 3) {
+                const CapShort cs = cap_short(P.scale, P.softcap);
+                const uint64_t uu = f2_mul(rr, rr);
+                return f2_fma(rr, f2_fma(uu, f2_fma(uu, f2_mul(cs.s1, sl2_2), f2_mul(cs.s0, sl2_2)), sl2_2), nm);
+            } else {
+                return f2_fma(rr, sl2_2, nm);
+            }
+        };
+        using M0 = std::integral_constant<int, 0>;
+        using M1 = std::integral_constant<int, 1>;
+        using M2 = std::integral_constant<int, 2>;
+        using M3 = std::integral_constant<int, 3>;
+        Walk w = walk_of(P, plan);
+        Part p;
+        while (ok && next_part(plan, w, p)) {
+            const int n = p.end - p.begin, tile0 = p.it.t0 + p.begin;
+            const Tiles my = tiles_of<BN>(P, p, u, tm);
+            const Tiles other = NT == 2 ? tiles_of<BN>(P, p, 1 - u, tm) : my;
+            const int nA = u == 0 ? my.n : other.n, nB = u == 0 ? other.n : my.n, bA = base[0], bB = base[1];
+            // (a tile whose keys begin more than one tile before the other's would wait for a turn that needs a
+            // stage of the ring that only its own product frees; 128 rows apart they never do)
+            const bool alt = NT == 2 && abs(my.t0 - other.t0) <= 1;
+            base[0] += nA;
+            base[1] += nB;
+            const unsigned g0 = g;
+            g += 2 * n;
+            if (my.ntok == 0) continue;
+            int lo, hi;  // keys that any row of the item sees
+            key_span(p, lo, hi);
+            const bool row_live = tok < my.ntok;
+            const int pos = my.pos + tok;
+            float m = 8.f - kTop, l = 0.f;
+            const int sub = lane < subs ? lane : 0;
+            int pg = my.n > 0 ? box_page(p, my.t0 * BN + sub * box_rows, lo, hi, false) : -2;
+            for (int k = 0; k < my.n; ++k) {
+                const int j0 = (my.t0 + k) * BN;
+                // boxes of this tile that are there (bit = box)
+                const unsigned there = __ballot_sync(0xffffffffu, lane < subs && pg >= 0);
+                if (k + 1 < my.n) pg = box_page(p, j0 + BN + sub * box_rows, lo, hi, false);
+                const bool full = there == (1u << subs) - 1u &&
+                                  tile_full(P.wl, P.wr, p.it.len, my.pos, my.pos + my.ntok - 1, j0, j0 + BN);
+                const int sbuf = NT == 2 ? u : (sc & 1);
+                const uint32_t tS = tbase + (NT == 2 ? u * 128 : (sc & 1) * 64) + lane_off;
+                if (!wait(C::S_FULL + sbuf, NT == 2 ? sc & 1 : (sc >> 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                uint32_t sv[NC][32];
+#pragma unroll
+                for (int c = 0; c < NC; ++c) tmem_ld32(tS + c * 32, sv[c]);
+                if (alt && (u == 0 ? (k >= 1 && k - 1 < nB) : (k < nA))) {
+                    const int need = 4 * (u == 0 ? bB + k : bA + k + 1);
+                    const bool rr = count_wait(&done_count[u ^ 1], need, P.status, ST_FWD_SOFTMAX, &abort_flag);
+                    if (!__all_sync(0xffffffffu, rr)) {
+                        tmem_ld_wait_only();
+                        ok = false;
+                        break;
+                    }
+                }
+                tmem_ld_wait_only();
+#pragma unroll
+                for (int c = 0; c < NC; ++c) tmem_pin(sv[c]);
+                bool accurate = false, shorter = false;
+                if constexpr (CAP) {
+                    float am[NC];
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        am[c] = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2)
+                            am[c] = max3f(am[c], fabsf(__uint_as_float(sv[c][e])), fabsf(__uint_as_float(sv[c][e + 1])));
+                    }
+                    float amax = fmaxf(am[0], am[1]);
+                    if constexpr (NC == 4) amax = fmaxf(amax, fmaxf(am[2], am[3]));
+                    const CapPoly cp = cap_poly(P.scale, P.softcap);
+                    accurate = __any_sync(0xffffffffu, !(amax <= cp.r_max)) || (!full && !cp.inf_ok);
+                    const CapShort cs = cap_short(P.scale, P.softcap);
+                    shorter = !accurate && __all_sync(0xffffffffu, amax <= cs.r_max) && (full || cs.inf_ok);
+                }
+                uint32_t seen[NC];  // the keys of the tile that this row sees
+                if (!full) {
+                    long long vlo = lo - j0, vhi = hi - j0;
+                    if (P.wl >= 0) vlo = max(vlo, (long long)pos - P.wl - j0);
+                    if (P.wr >= 0) vhi = min(vhi, (long long)pos + P.wr - j0 + 1);
+                    if (!row_live) vhi = vlo;
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        const int a = (int)min(max(vlo - 32 * c, 0ll), 32ll), b = (int)min(max(vhi - 32 * c, 0ll), 32ll);
+                        const uint32_t below_b = b >= 32 ? 0xffffffffu : (1u << b) - 1u;
+                        const uint32_t below_a = a >= 32 ? 0xffffffffu : (1u << a) - 1u;
+                        uint32_t have = 0;  // boxes of 16, 32 or 64 keys
+                        for (int x = 0; x < 32; x += min(box_rows, 32))
+                            if ((there >> ((32 * c + x) / box_rows)) & 1u) have |= (box_rows == 16 ? 0xffffu : 0xffffffffu) << x;
+                        seen[c] = below_b & ~below_a & have;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) sv[c][e] = (seen[c] >> e) & 1u ? sv[c][e] : 0xff800000u;  // -inf
+                    }
+                }
+                // ---- the row's largest score, as x against its reference
+                float rm[NC];
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    rm[c] = -INFINITY;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2)
+                        rm[c] = max3f(rm[c], __uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1]));
+                }
+                float rmax = fmaxf(rm[0], rm[1]);
+                if constexpr (NC == 4) rmax = fmaxf(rmax, fmaxf(rm[2], rm[3]));
+                float xm, xm_;
+                {
+                    const uint64_t r2 = f2_make(rmax, rmax), n2 = f2_make(-m, -m);
+                    uint64_t x2;
+                    if (!CAP) x2 = to_x(M0(), r2, n2);
+                    else if (shorter) x2 = to_x(M3(), r2, n2);
+                    else if (!accurate) x2 = to_x(M1(), r2, n2);
+                    else x2 = to_x(M2(), r2, n2);
+                    f2_split(x2, xm, xm_);
+                }
+                if (rmax == -INFINITY) xm = -INFINITY;
+                const bool move = xm > kTop || (l == 0.f && xm < kTop - 10.f && xm != -INFINITY);
+                bool o_stands = NT == 2;  // the product of the tile before is complete
+                if (__any_sync(0xffffffffu, move)) {
+                    // rows that have seen nothing hold O = 0: their reference may move by any amount
+                    const float by = xm - (kTop - 8.f);
+                    const float alpha = fast_exp2(move && l > 0.f ? -by : 0.f);
+                    if (move) {
+                        m += by;
+                        l *= alpha;
+                    }
+                    if (k > 0) {
+                        if (!o_stands) {
+                            if (!wait(C::PV_DONE, (sc - 1) & 1)) {
+                                ok = false;
+                                break;
+                            }
+                            o_stands = true;
+                            tc_fence_after();
+                        }
+#pragma unroll 1
+                        for (int c = 0; c < HD / 32; ++c) {
+                            uint32_t orr[32];
+                            tmem_ld32(tO + c * 32, orr);
+                            tmem_ld_wait(orr);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * alpha);
+                            tmem_st32(tO + c * 32, orr);
+                        }
+                    }
+                }
+                // ---- p, chunk by chunk over S
+                auto p_pass = [&](auto modec) {
+                    const uint64_t nm = f2_make(-m, -m);
+                    uint64_t rs[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float x0, x1;
+                            f2_split(to_x(modec, f2_make(__uint_as_float(sv[c][2 * e]), __uint_as_float(sv[c][2 * e + 1])), nm), x0, x1);
+                            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);  // 2^-inf = 0
+                            rs[e & 1] = f2_add(rs[e & 1], f2_make(p0, p1));
+                            pk[e] = pack2<BF16>(p0, p1);
+                        }
+                        tmem_st16(tS + c * 16, pk);
+                    }
+                    float a0, a1, b0, b1;
+                    f2_split(rs[0], a0, a1);
+                    f2_split(rs[1], b0, b1);
+                    l += (a0 + b0) + (a1 + b1);
+                };
+                if (!CAP) p_pass(M0());
+                else if (shorter) p_pass(M3());
+                else if (!accurate) p_pass(M1());
+                else p_pass(M2());
+                // ---- a tile that is not whole: V looked over
+                bool by_row = false;
+                if (!full) {
+                    const int i = my.t0 + k - tile0;  // its place in the part
+                    const unsigned gv = g0 + 2 * i + 1;
+                    if (!wait(C::FULL + gv % NS, (gv / NS) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* vt = smem + C::kRingOff + (gv % NS) * C::kTileBytes;
+                    bool bad = false;
+                    // a lane takes 16-byte chunks of rows r, r + 32, ...: eight lanes a row's
+#pragma unroll 4
+                    for (int x = r; x < BN * 8 * C::kBoxes; x += kM) {
+                        const int row = (x >> 3) % BN, j = j0 + row;
+                        uint4* at = reinterpret_cast<uint4*>(vt + x * 16);
+                        if (j < lo || j >= hi || !((there >> (row / box_rows)) & 1u)) {
+                            *at = make_uint4(0, 0, 0, 0);
+                        } else {
+                            const uint4 v = *at;
+                            constexpr uint32_t kExp = BF16 ? 0x7f807f80u : 0x7c007c00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
+                            // an exponent of all ones carries into its sign's place
+                            const uint32_t c = ((v.x & kExp) + kOne) | ((v.y & kExp) + kOne) | ((v.z & kExp) + kOne) | ((v.w & kExp) + kOne);
+                            bad = bad || (c & 0x80008000u);
+                        }
+                    }
+                    ++vc;
+                    if (bad) *static_cast<volatile int*>(&bad_tile[u][vc & 1]) = vc;
+                    fence_proxy_async_smem();  // the zeros, before the product
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(BAR(C::V_CHECK + u));
+                    if (!wait(C::V_CHECK + u, (vc - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    by_row = *static_cast<volatile int*>(&bad_tile[u][vc & 1]) == vc;
+                    if (by_row) {
+                        tmem_st_wait();
+                        if (!o_stands && k > 0) {
+                            if (!wait(C::PV_DONE, (sc - 1) & 1)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                        }
+#pragma unroll 1
+                        for (int c = 0; c < HD / 32; ++c) {
+                            uint32_t orr[32];
+                            if (k > 0) {
+                                tmem_ld32(tO + c * 32, orr);
+                                tmem_ld_wait(orr);
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) orr[e] = 0u;
+                            }
+                            const uint8_t* col = vt + (c >> 1) * (BN * 128);
+#pragma unroll 1
+                            for (int j = 0; j < BN; ++j) {
+                                uint32_t pw;
+                                asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(pw) : "r"(tS + (j >> 1)));
+                                asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(pw)::"memory");
+                                float p0, p1;
+                                if constexpr (BF16) {
+                                    p0 = __uint_as_float(pw << 16);
+                                    p1 = __uint_as_float(pw & 0xffff0000u);
+                                } else {
+                                    const float2 f = h2_to_f2(pw);
+                                    p0 = f.x, p1 = f.y;
+                                }
+                                const float pj = (j & 1) ? p1 : p0;
+                                uint32_t sw = 0;
+#pragma unroll
+                                for (int x = 0; x < NC; ++x) sw = (j >> 5) == x ? seen[x] : sw;
+                                const bool see = (sw >> (j & 31)) & 1u;
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    const uint4 v = *reinterpret_cast<const uint4*>(col + j * 128 + ((((c & 1) * 4 + q) ^ (j & 7)) << 4));
+                                    const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        float v0, v1;
+                                        if constexpr (BF16) {
+                                            v0 = __uint_as_float(vw[e] << 16);
+                                            v1 = __uint_as_float(vw[e] & 0xffff0000u);
+                                        } else {
+                                            const float2 f = h2_to_f2(vw[e]);
+                                            v0 = f.x, v1 = f.y;
+                                        }
+                                        uint32_t& o0 = orr[8 * q + 2 * e];
+                                        uint32_t& o1 = orr[8 * q + 2 * e + 1];
+                                        if (see) {
+                                            o0 = __float_as_uint(fmaf(pj, v0, __uint_as_float(o0)));
+                                            o1 = __float_as_uint(fmaf(pj, v1, __uint_as_float(o1)));
+                                        }
+                                    }
+                                }
+                            }
+                            tmem_st32(tO + c * 32, orr);
+                        }
+                    }
+                }
+                if (wq == 0 && lane == 0) *static_cast<volatile int*>(&skip_pv[u][sc & 1]) = by_row ? 1 : 0;
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(BAR(C::P_FULL + u));
+                    if constexpr (NT == 2) atomicAdd(&done_count[u], 1);
+                }
+                ++sc;
+            }
+            // ------------------------------------------------------------ epilogue
+            const bool have_o = ok && my.n > 0 && wait(C::O_DONE + u, act & 1);
+            if (my.n > 0) ++act;
+            if (!ok || (my.n > 0 && !have_o)) {
+                ok = false;
+                break;
+            }
+            if (have_o) tc_fence_after();
+            const bool whole = p.whole();
+            const bool none = l == 0.f;
+            const float inv = none ? 0.f : 1.f / l;
+            const int slot = 2 * blockIdx.x + (p.begin == 0 ? 1 : 0), rows = NT * kM;
+            const long long orow = (long long)(p.it.row + u * tm + tok);
+            uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.o) + (orow * P.H + p.h * P.G + head) * HD);
+            float4* part = reinterpret_cast<float4*>(part_o(plan, slot, rows, HD) + (size_t)(u * kM + r) * HD);
+#pragma unroll 1
+            for (int c = 0; c < HD / 32; ++c) {
+                uint32_t orr[32];
+                if (have_o) {
+                    tmem_ld32(tO + c * 32, orr);
+                    tmem_ld_wait(orr);
+                }
+                if (row_live && whole) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t pk[4] = {0, 0, 0, 0};
+                        if (!none)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                pk[e] = pack2<BF16>(__uint_as_float(orr[8 * q + 2 * e]) * inv, __uint_as_float(orr[8 * q + 2 * e + 1]) * inv);
+                        out[c * 4 + q] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    }
+                } else if (row_live && !none) {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        part[c * 8 + q] = make_float4(__uint_as_float(orr[4 * q]), __uint_as_float(orr[4 * q + 1]),
+                                                      __uint_as_float(orr[4 * q + 2]), __uint_as_float(orr[4 * q + 3]));
+                }
+                __syncwarp();
+            }
+            // O is in registers or out: the next part's first product may overwrite it
+            if (have_o) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(BAR(C::O_EMPTY + u));
+            }
+            if (row_live) {
+                if (!whole) part_ml(plan, slot, rows)[u * kM + r] = make_float2(m, l);
+                else if (P.lse)
+                    P.lse[(long long)(p.h * P.G + head) * P.total + orow] = none ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tbase, 512);
+    }
+}
+
+// ------------------------------------------------------------------- the merge
+// Joins the partial rows of the items that stretches cut: CTA (c, y) those of the item that begins in
+// stretch c and ends behind it, a warp to a row, in the order of the stretches.
+template <int HD>
+__global__ void __launch_bounds__(256) paged_prefill_merge_kernel(const PagedParams P, const int bf16, const int bn) {
+    constexpr int NT = HD == 256 ? 1 : 2, rows = NT * kM, kPer = HD / 32;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int tm = kM / P.G, c = blockIdx.x;
+    const Plan plan = plan_of(P, NT * tm);
+    const long long per_head = *plan.all;
+    const Deal d = deal_of(P, per_head);
+    const long long last = min(d.all, (c + 1) * d.share) - 1;
+    if (last < c * d.share) return;  // nothing in the stretch
+    const int h = (int)(last / per_head);
+    const int e = warp_last_le(*plan.count, last - h * per_head, [&](int i) { return plan.cum[i]; });
+    const Item it = plan.items[e];
+    const long long first = h * per_head + plan.cum[e] + kItemCost;  // its first tile
+    if (it.tiles == 0 || first / d.share != c) return;
+    const int n = (int)((first + it.tiles - 1) / d.share) - c + 1;  // its parts
+    if (n <= 1) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int live = it.ntok;  // tokens
+    for (int x = blockIdx.y * 8 + warp; x < live * P.G; x += gridDim.y * 8) {
+        const int t = x / P.G, head = x - t * P.G, u = t / tm, r = u * kM + (t - u * tm) * P.G + head;
+        auto slot = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); };
+        float M = -INFINITY, L = 0.f;
+        float acc[kPer];
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) acc[q] = 0.f;
+        for (int base = 0; base < n; base += 32) {
+            const int i = base + lane;
+            const float2 ml = i < n ? part_ml(plan, slot(i), rows)[r] : make_float2(0.f, 0.f);
+            const bool some = ml.y != 0.f;  // a part whose row saw nothing holds no O
+            float mx = some ? ml.x : -INFINITY;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const unsigned use = __ballot_sync(0xffffffffu, some);
+            if (use == 0) continue;
+            const float ref = fmaxf(M, mx), alpha = M == -INFINITY ? 0.f : fast_exp2(M - ref);
+            const float f = some ? fast_exp2(ml.x - ref) : 0.f;
+            M = ref;
+            L = L * alpha + (some ? f * ml.y : 0.f);  // of this lane's parts
+#pragma unroll
+            for (int q = 0; q < kPer; ++q) acc[q] *= alpha;
+            for (int j = 0; j < min(32, n - base); ++j) {
+                if (!((use >> j) & 1u)) continue;
+                const float* src = part_o(plan, slot(base + j), rows, HD) + (size_t)r * HD + lane * kPer;
+                const float fj = __shfl_sync(0xffffffffu, f, j);
+#pragma unroll
+                for (int q = 0; q < kPer; q += 2) {
+                    const float2 v = *reinterpret_cast<const float2*>(src + q);
+                    acc[q] = fmaf(fj, v.x, acc[q]);
+                    acc[q + 1] = fmaf(fj, v.y, acc[q + 1]);
+                }
+            }
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        const bool none = M == -INFINITY;
+        const float inv = none ? 0.f : 1.f / L;
+        const long long orow = it.row + t;
+        const int hq = h * P.G + head;
+        uint32_t* od = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(P.o) + (orow * P.H + hq) * HD + lane * kPer);
+#pragma unroll
+        for (int q = 0; q < kPer; q += 2)
+            od[q / 2] = bf16 ? pack2<true>(acc[q] * inv, acc[q + 1] * inv) : pack2<false>(acc[q] * inv, acc[q + 1] * inv);
+        if (P.lse && lane == 0) P.lse[(long long)hq * P.total + orow] = none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    }
+}
+
+// Dynamic shared memory of a kernel, asked for once on each device.
+template <typename K>
+cudaError_t allow_smem(K k, int bytes, std::atomic<unsigned long long>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+inline void early(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* at) {
+    at->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at->val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+}
+
+template <bool BF16, int HD, bool F8, bool CAP>
+cudaError_t launch_one(const PagedParams& p, int cache, const PrefillMaps& maps, cudaStream_t s) {
+    using C = Cfg<HD, F8>;
+    auto k = paged_prefill_kernel<BF16, HD, F8, CAP>;
+    static std::atomic<unsigned long long> done{0};
+    cudaError_t e = allow_smem(k, C::kBytes, done);
+    if (e != cudaSuccess) return e;
+    paged_plan_kernel<<<1, kPlanThreads, 0, s>>>(p, C::NT * (kM / p.G), C::BN);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    cfg.gridDim = dim3(kPrefillCtas);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kBytes;
+    cfg.stream = s;
+    early(cfg, at);
+    if ((e = cudaLaunchKernelEx(&cfg, k, p, cache == CACHE_E4M3 ? 1 : 0, maps.q, maps.k, maps.v)) != cudaSuccess) return e;
+    cfg.gridDim = dim3(kPrefillCtas, 8);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, paged_prefill_merge_kernel<HD>, p, BF16 ? 1 : 0, C::BN);
+}
+template <bool BF16, bool F8>
+cudaError_t launch_hd(const PagedParams& p, int cache, const PrefillMaps& m, cudaStream_t s) {
+    const bool cap = p.softcap > 0.f;
+    if (p.hd == 64) return cap ? launch_one<BF16, 64, F8, true>(p, cache, m, s) : launch_one<BF16, 64, F8, false>(p, cache, m, s);
+    if (p.hd == 128) return cap ? launch_one<BF16, 128, F8, true>(p, cache, m, s) : launch_one<BF16, 128, F8, false>(p, cache, m, s);
+    return cap ? launch_one<BF16, 256, F8, true>(p, cache, m, s) : launch_one<BF16, 256, F8, false>(p, cache, m, s);
+}
+
+}  // namespace prefill
+}  // namespace
+}  // namespace attn

@@ -1,0 +1,8 @@
+// paged_prefill_f16_f8.cu -- instantiations of paged_prefill.cuh.
+#include "paged_prefill.cuh"
+
+namespace attn {
+cudaError_t launch_paged_prefill_f16_f8(const PagedParams& p, int cache, const PrefillMaps& maps, cudaStream_t s) {
+    return prefill::launch_hd<false, true>(p, cache, maps, s);
+}
+}  // namespace attn

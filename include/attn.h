@@ -525,6 +525,34 @@ ATTN_API attn_status attn_paged_decode(attn_dtype dt, attn_dtype cache_dt, const
                         int causal, int window, float softcap, void* stream);
 
 /*
+ * Attention of a chunk of new tokens of each sequence over its pages, the chunk's own tokens among
+ * them (attn_paged_append stores them first): prompts served whole or in chunks, follow-ups of any
+ * length, prompts beside single tokens.  Source: brotensor ops/flash_attention.h, flash_attention_decode_len
+ * (query rows at the end of a cache of device-held length), without a limit on the rows.
+ *   q         : packed rows [total_new][H*hd], q_stride elements apart (a multiple of 8, at least
+ *               H*hd).  o : [total_new][H*hd] (contiguous).  lse : [H][total_new] fp32, or NULL.
+ *   cu_new, lengths, page_table : as for attn_paged_append: rows [cu_new[b], cu_new[b+1]) are sequence b's
+ *               last tokens, at positions L_b - n_b .. L_b - 1, L_b = min(max(lengths[b], 0), max_pages *
+ *               page_size).  A row that sees no key (one at a negative position under the causal mask)
+ *               gets O = 0 and LSE = -inf; rows in no sequence are not written.
+ *   scale, causal, window, softcap : as for attn_decode.  H/Hkv is at most 128.
+ *   workspace : at least attn_paged_prefill_workspace_size() bytes of device scratch, 16-byte
+ *               aligned; contents on entry are ignored.  Calls that may run at the same time
+ *               need one each.
+ * What a row does not see has no effect on it, whatever bytes it holds.  Table entries of which no row
+ * sees a token (behind a sequence, before every row's window) are not read.  Over 8-bit pages an
+ * element is read as attn_paged_gather reads it, its product with its scale rounded once to dt (exact
+ * for scales that are powers of two, while the product stays in dt's range).  Sums are fp32, over
+ * weights of at most 1 in bf16 and 2^8 in fp16.
+ */
+ATTN_API size_t attn_paged_prefill_workspace_size(int total_new, int batch, int H, int Hkv, int hd);
+ATTN_API attn_status attn_paged_prefill(attn_dtype dt, attn_dtype cache_dt, const void* q, long long q_stride,
+                        const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale, void* o,
+                        float* lse, void* workspace, size_t workspace_bytes, const int* cu_new, const int* lengths,
+                        const int* page_table, int batch, int total_new, int num_pages, int page_size, int max_pages,
+                        int H, int Hkv, int hd, float scale, int causal, int window, float softcap, void* stream);
+
+/*
  * Reads pages back: token i of sequence b into row cu_seqlens[b] + i of k_out and v_out
  * [total][Hkv*hd] (type dt), for i < cu_seqlens[b+1] - cu_seqlens[b]; 8-bit elements are
  * multiplied by their scale and rounded once.  For query blocks longer than the decode's 16

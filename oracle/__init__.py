@@ -557,3 +557,37 @@ def paged_decode(q, tokens, lengths, *, H, Hkv, scale, causal=True, window=0, so
                 o[b, i, h * hd:(h + 1) * hd] = e @ vv[:, h // (H // Hkv)] / e.sum()
                 lse[b, h, i] = m + np.log(e.sum())
     return o, lse
+
+
+def paged_prefill(q, tokens, lengths, cu, *, H, Hkv, scale, causal=True, window=0, softcap=0.0, absolute=False):
+    """O [rows, H*hd] and LSE [H, rows] of packed rows: rows cu[b] .. cu[b+1]-1 are sequence b's last tokens,
+    at positions lengths[b] - n_b .. lengths[b] - 1 over tokens[b] = (k, v), rows [lengths[b], Hkv*hd] (rows of
+    NaN keys are not visible).  Rows in no sequence are NaN.  With `absolute`, V enters by its magnitude."""
+    q = _f64(q)
+    hd = q.shape[1] // H
+    o, lse = np.full_like(q, np.nan), np.full((H, q.shape[0]), np.nan)
+    for b in range(len(lengths)):
+        r0, r1, n = int(cu[b]), int(cu[b + 1]), int(lengths[b])
+        k, v = (np.asarray(x, np.float64).reshape(n, Hkv, hd) for x in tokens[b])
+        p, j = (n - (r1 - r0) + np.arange(r1 - r0))[:, None], np.arange(n)[None, :]
+        seen = np.broadcast_to(~np.isnan(k[:, 0, 0])[None, :], (r1 - r0, n))
+        if causal:
+            seen = seen & (j <= p)
+        if window:
+            seen = seen & (np.abs(p - j) < window)
+        # (what no row sees may be anything)
+        k = np.where(seen.any(0)[:, None, None], k, 0.0) if n else k
+        v = np.where(seen.any(0)[:, None, None], v, 0.0) if n else v
+        v = np.abs(v) if absolute else v
+        for h in range(H):
+            c = slice(h * hd, (h + 1) * hd)
+            s = scale * (q[r0:r1, c] @ k[:, h // (H // Hkv)].T)
+            s = softcap * np.tanh(s / softcap) if softcap > 0 else s
+            s = np.where(seen, s, -np.inf)
+            m = s.max(axis=1, initial=-np.inf)
+            e = np.exp(s - np.where(np.isneginf(m), 0.0, m)[:, None])
+            l = e.sum(1)
+            o[r0:r1, c] = np.where(l[:, None] > 0, e @ v[:, h // (H // Hkv)] / np.where(l > 0, l, 1.0)[:, None], 0.0)
+            with np.errstate(divide="ignore"):
+                lse[h, r0:r1] = np.where(l > 0, m + np.log(l), -np.inf)
+    return o, lse
