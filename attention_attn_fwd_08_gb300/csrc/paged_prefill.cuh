@@ -322,7 +322,8 @@ __device__ __forceinline__ void widen4(uint32_t c, bool e4m3, float s, uint32_t&
 // 8-bit pools, widening (Cfg::kWide0 ...).  Two tiles take turns as in the dense forward: one tile's
 // softmax runs while the tensor cores work on the other's P V and next S; each has one S buffer, and a
 // completed S(n), issued after P(n-1) V(n-1), also means that O stands still.  With one tile (hd 256)
-// there are two S buffers instead, and S(n+1) is issued before P(n) V(n).
+// there are two S buffers instead, S(n+1) is issued before P(n) V(n), and the softmax may be done with P(n+1)
+// before that product is issued: S, P and the product have a barrier for each buffer.
 //
 // What a row does not see has no effect on it.  A tile that some row does not see whole is looked over
 // by the softmax warps before its P V: rows of V that no row of the item sees (behind the sequence, in a
@@ -499,7 +500,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                         for (int kk = 0; kk < BN / 16; ++kk)
                             mma_ts_e(tO, tS + kk * 8, vdesc + ((kk * 16 * 128) >> 4), idPV, (k > 0 || kk > 0) ? 1u : 0u);
                     }
-                    if constexpr (NT == 1) mma_commit_e(BAR(C::PV_DONE));
+                    if constexpr (NT == 1) mma_commit_e(BAR(C::PV_DONE + ((pc - 1) & 1)));
                     if (k == my.n - 1) mma_commit_e(BAR(C::O_DONE + u));
                 };
                 // A tile's release is committed only after the wait for its data, also for tiles that
@@ -523,7 +524,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                     ok = wait(C::FULL + vst(i), vph(i));
                     if (NT == 2 && ok && i + 1 < n) ok = wait(C::FULL + kst(i + 1), kph(i + 1));
                     if (ok && has(i)) {
-                        ok = wait(C::P_FULL + u, pc & 1);
+                        ok = NT == 2 ? wait(C::P_FULL + u, pc & 1) : wait(C::P_FULL + (pc & 1), (pc >> 1) & 1);
                         ++pc;
                         // the first product overwrites O: the last part's epilogue must have read it
                         if (ok && k == 0 && act > 0) ok = wait(C::O_EMPTY + u, (act - 1) & 1);
@@ -631,6 +632,9 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
         };
         bool ok = true;
         int sc = 0, act = 0, vc = 0;  // tiles done, parts in which this tile was active, look-overs
+        // (one tile) the product of the tile before this one is complete.  At most that one can still be on
+        // its way, since this tile's S was issued after the one before it, and it cannot be overtaken.
+        auto wait_pv = [&]() { return wait(C::PV_DONE + ((sc - 1) & 1), ((sc - 1) >> 1) & 1); };
         int base[2] = {0, 0};         // softmaxes of both tiles in earlier parts
         unsigned g = 0;               // ring position of the part's first K tile
         // x = score * log2(e) - m of a pair of raw scores; mode 0: plain; with a softcap 1: the fitted
@@ -784,7 +788,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                     }
                     if (k > 0) {
                         if (!o_stands) {
-                            if (!wait(C::PV_DONE, (sc - 1) & 1)) {
+                            if (!wait_pv()) {
                                 ok = false;
                                 break;
                             }
@@ -867,7 +871,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                     if (by_row) {
                         tmem_st_wait();
                         if (!o_stands && k > 0) {
-                            if (!wait(C::PV_DONE, (sc - 1) & 1)) {
+                            if (!wait_pv()) {
                                 ok = false;
                                 break;
                             }
@@ -934,7 +938,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(BAR(C::P_FULL + u));
+                    mbar_arrive(BAR(C::P_FULL + (NT == 2 ? u : (sc & 1))));
                     if constexpr (NT == 2) atomicAdd(&done_count[u], 1);
                 }
                 ++sc;
