@@ -61,7 +61,7 @@ struct Cfg {
     static constexpr int kBarOff = kRawOff + kRaw * kRawBytes;
     // barriers, in this order
     static constexpr int Q_FULL = 0, Q_EMPTY = 2, S_FULL = 4, P_FULL = 6, O_DONE = 8, O_EMPTY = 10, PV_DONE = 12,
-                         V_CHECK = 14, MMA_DONE = 16, FULL = 17, EMPTY = FULL + kStages, RAW_FULL = EMPTY + kStages,
+                         MMA_DONE = 14, FULL = 15, EMPTY = FULL + kStages, V_OK = EMPTY + kStages, RAW_FULL = V_OK + kStages,
                          RAW_EMPTY = RAW_FULL + kRaw, kBars = RAW_EMPTY + kRaw;
     static constexpr int kBytes = kBarOff + kBars * 8 + 16 + 1024;  // (1024: alignment)
     static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -89,6 +89,7 @@ struct Plan {
     int* base;       // [B + 1] items before a sequence
     Item* items;
     long long* cum;  // [count + 1] costs before an item
+    int4* split;     // of a stretch: the item that begins in it and does not end in it: its first row, tokens, KV head, parts
     float* part;     // partial rows
 };
 __host__ __device__ __forceinline__ long long plan_items(int total, int B, int tokens) { return (long long)total / tokens + B; }
@@ -96,7 +97,7 @@ __host__ __device__ __forceinline__ size_t round256(size_t n) { return (n + 255)
 // bytes before the partial rows
 __host__ __device__ __forceinline__ size_t plan_bytes(int total, int B, int tokens) {
     const size_t n = (size_t)plan_items(total, B, tokens);
-    return 256 + round256(((size_t)B + 1) * 4) + round256(n * sizeof(Item)) + round256((n + 1) * 8);
+    return 256 + round256(kPrefillCtas * sizeof(int4)) + round256(((size_t)B + 1) * 4) + round256(n * sizeof(Item)) + round256((n + 1) * 8);
 }
 __device__ __forceinline__ Plan plan_of(const PagedParams& P, int tokens) {
     uint8_t* w = reinterpret_cast<uint8_t*>(P.ws);
@@ -105,6 +106,8 @@ __device__ __forceinline__ Plan plan_of(const PagedParams& P, int tokens) {
     p.all = reinterpret_cast<long long*>(w);
     p.count = reinterpret_cast<int*>(w + 8);
     w += 256;
+    p.split = reinterpret_cast<int4*>(w);
+    w += round256(kPrefillCtas * sizeof(int4));
     p.base = reinterpret_cast<int*>(w);
     w += round256(((size_t)P.B + 1) * 4);
     p.items = reinterpret_cast<Item*>(w);
@@ -235,8 +238,9 @@ __device__ __forceinline__ Deal deal_of(const PagedParams& P, long long per_head
 // A CTA's walk along its stretch, the same in every warp: `next` gives the next item of which the stretch
 // holds key tiles (or that has none and ends in it), tiles [begin, end) of it.
 struct Walk {
-    long long left;  // of the stretch
-    long long off;   // where it enters item e
+    int left;   // of the stretch (a stretch of 2^31 tiles would take days)
+    int share;
+    int off;    // where it enters item e
     int h, e, count;
 };
 struct Part {
@@ -249,7 +253,8 @@ __device__ __forceinline__ Walk walk_of(const PagedParams& P, const Plan& plan) 
     const long long per_head = *plan.all;
     const Deal d = deal_of(P, per_head);
     const long long first = min(d.all, (long long)blockIdx.x * d.share);
-    w.left = min(d.share, d.all - first);
+    w.share = (int)min(d.share, (long long)INT32_MAX);
+    w.left = (int)min((long long)w.share, d.all - first);
     w.count = *plan.count;
     w.h = w.e = 0;
     w.off = 0;
@@ -257,7 +262,7 @@ __device__ __forceinline__ Walk walk_of(const PagedParams& P, const Plan& plan) 
         w.h = (int)(first / per_head);
         const long long in = first - w.h * per_head;
         w.e = warp_last_le(w.count, in, [&](int i) { return plan.cum[i]; });
-        w.off = in - plan.cum[w.e];
+        w.off = (int)(in - plan.cum[w.e]);
     }
     return w;
 }
@@ -265,10 +270,10 @@ __device__ __forceinline__ bool next_part(const Plan& plan, Walk& w, Part& p) {
     while (w.left > 0) {
         p.it = plan.items[w.e];
         p.h = w.h;
-        const long long cost = p.it.tiles + kItemCost, end = min(cost, w.off + w.left);
-        p.begin = (int)max(w.off - kItemCost, 0ll);
-        p.end = (int)max(end - kItemCost, 0ll);
-        w.left -= end - w.off;
+        const int cost = p.it.tiles + kItemCost, take = min(cost - w.off, w.left), end = w.off + take;
+        p.begin = max(w.off - kItemCost, 0);
+        p.end = max(end - kItemCost, 0);
+        w.left -= take;
         w.off = 0;
         if (++w.e == w.count) w.e = 0, ++w.h;
         if (p.end > p.begin || (p.it.tiles == 0 && end == cost)) return true;
@@ -303,10 +308,10 @@ __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, ui
 }
 
 // four codes as two words of two 16-bit values, times s in fp32, rounded once
-template <bool BF16>
-__device__ __forceinline__ void widen4(uint32_t c, bool e4m3, float s, uint32_t& w0, uint32_t& w1) {
+template <bool BF16, bool E4M3>
+__device__ __forceinline__ void widen4(uint32_t c, float s, uint32_t& w0, uint32_t& w1) {
     uint32_t h0, h1;
-    if (e4m3)
+    if constexpr (E4M3)
         asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
             : "=r"(h0), "=r"(h1)
             : "r"(c));
@@ -317,18 +322,32 @@ __device__ __forceinline__ void widen4(uint32_t c, bool e4m3, float s, uint32_t&
     w1 = pack2<BF16>(b.x * s, b.y * s);
 }
 
+// n bits from bit i on (i + n <= 32)
+__device__ __forceinline__ uint32_t bit_range(int i, int n) {
+    uint32_t m;
+    asm("bmsk.clamp.b32 %0, %1, %2;" : "=r"(m) : "r"(i), "r"(n));
+    return m;
+}
+// 32 bytes to global memory, aligned to them
+__device__ __forceinline__ void store_32(void* at, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // ------------------------------------------------------------------ the kernel
-// Roles (warps): softmax of tile u, one thread to a row (0-3, 4-7); loads (8); MMA issue of tile u (9 + u); over
-// 8-bit pools, widening (Cfg::kWide0 ...).  Two tiles take turns as in the dense forward: one tile's
+// Roles (warps): softmax of tile u, one thread to a row (0-3, 4-7); loads (8); MMA issue of tile u (9 + u); looking
+// V over (11); over 8-bit pools, widening (Cfg::kWide0 ...).  Two tiles take turns as in the dense forward: one tile's
 // softmax runs while the tensor cores work on the other's P V and next S; each has one S buffer, and a
 // completed S(n), issued after P(n-1) V(n-1), also means that O stands still.  With one tile (hd 256)
 // there are two S buffers instead, S(n+1) is issued before P(n) V(n), and the softmax may be done with P(n+1)
 // before that product is issued: S, P and the product have a barrier for each buffer.
 //
-// What a row does not see has no effect on it.  A tile that some row does not see whole is looked over
-// by the softmax warps before its P V: rows of V that no row of the item sees (behind the sequence, in a
-// page that does not exist) become zeros in shared memory; if a value left in it is not finite, the
-// product is made row by row over the keys that the row sees, by the softmax warps, in place of the MMA.
+// What a row does not see has no effect on it.  Warp 11 looks over each tile of V before its product is
+// issued: rows of V that no row of the item sees (behind the sequence, in a page that does not exist) become
+// zeros in shared memory, and of those that some rows see it notes whether a value is not finite; if so, the
+// softmax warps of a tile that does not see all of it make its product themselves, row by row over the
+// keys that the row sees, in place of the MMA.
 template <bool BF16, int HD, bool F8, bool CAP>
 __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
     paged_prefill_kernel(const PagedParams P, const int e4m3, const __grid_constant__ CUtensorMap tmQ,
@@ -344,7 +363,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
     auto BAR = [&](int i) { return bar0 + 8u * (uint32_t)i; };
     __shared__ int abort_flag;
     __shared__ int done_count[2];  // warps that have finished a softmax of tile u
-    __shared__ int bad_tile[2][2]; // the last look-over, by its parity, that met a value that is not finite
+    __shared__ int bad_v[NS];      // of V tile n, at n mod NS, as its barrier: a value that not every row sees is not finite
     __shared__ int skip_pv[2][2];  // by the parity of the tile: the softmax warps make this product
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tm = kM / P.G;  // tokens of a query tile
@@ -352,8 +371,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kBars; ++i) {
             uint32_t n = 1;
-            if ((i >= C::P_FULL && i < C::P_FULL + 2) || (i >= C::O_EMPTY && i < C::O_EMPTY + 2) ||
-                (i >= C::V_CHECK && i < C::V_CHECK + 2))
+            if ((i >= C::P_FULL && i < C::P_FULL + 2) || (i >= C::O_EMPTY && i < C::O_EMPTY + 2))
                 n = 4;  // softmax warps of a tile
             if ((i >= C::EMPTY && i < C::EMPTY + NS) || i == C::MMA_DONE) n = NT;  // MMA issuers
             if (F8 && ((i >= C::FULL && i < C::FULL + NS) || (i >= C::RAW_EMPTY && i < C::RAW_EMPTY + C::kRaw)))
@@ -361,7 +379,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
             mbar_init(BAR(i), n);
         }
         abort_flag = 0;
-        for (int u = 0; u < 2; ++u) done_count[u] = 0, bad_tile[u][0] = bad_tile[u][1] = 0, skip_pv[u][0] = skip_pv[u][1] = 0;
+        for (int u = 0; u < 2; ++u) done_count[u] = 0, skip_pv[u][0] = skip_pv[u][1] = 0;
         fence_barrier_init();
     }
     if (warp == 9) {
@@ -377,12 +395,14 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Plan plan = plan_of(P, NT * tm);
     // rows of a box of keys, and how many stand below each other in a tile
-    const int box_rows = min(P.page_size, 64), subs = BN / box_rows;
-    // page of the box of keys from `key` on, -1 if it is not there, -2 if no row of [lo, hi) lies in it
-    auto box_page = [&](const Part& p, int key, int lo, int hi, bool flag) {
-        if (key >= hi || key + box_rows <= lo) return -2;
-        return page_of(P, p.it.b, key >> P.page_shift, flag);
+    const int box_shift = min(P.page_shift, 6), box_rows = 1 << box_shift, subs = BN >> box_shift;
+    // The table's entry for the box of keys from `key` on, -1 if no row of [lo, hi) lies in it; what is no page is told
+    // by page_ok, later, so that nothing waits for the entry when it is asked for.
+    auto box_page = [&](const Part& p, int key, int lo, int hi) {
+        if (key >= hi || key + box_rows <= lo) return -1;
+        return __ldg(P.table + (long long)p.it.b * P.max_pages + (key >> P.page_shift));
     };
+    auto page_ok = [&](int pg) { return (unsigned)pg < (unsigned)P.num_pages; };
     auto key_span = [&](const Part& p, int& lo, int& hi) {
         key_range(P.wl, P.wr, p.it.len, p.it.pos, p.it.pos + p.it.ntok - 1, &lo, &hi);
     };
@@ -414,7 +434,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                 Tiles tu[2];
                 for (int u = 0; u < NT; ++u) tu[u] = tiles_of<BN>(P, p, u, tm);
                 const int tile0 = p.it.t0 + p.begin, n = p.end - p.begin;
-                int pg = n > 0 && col < kCols ? box_page(p, tile0 * BN + sub * box_rows, lo, hi, true) : -2;
+                int pg = n > 0 && col < kCols ? box_page(p, tile0 * BN + sub * box_rows, lo, hi) : -1;
                 for (int u = 0; ok && u < NT; ++u) {
                     if (tu[u].n == 0) continue;
                     if (qn[u] > 0 && !warp_wait(BAR(C::Q_EMPTY + u), (qn[u] - 1) & 1, P.status, ST_FWD_PRODUCER, &abort_flag)) {
@@ -430,8 +450,9 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                 }
                 for (int i = 0; ok && i < n; ++i) {
                     const int key = (tile0 + i) * BN + sub * box_rows;
-                    const int next = i + 1 < n && col < kCols ? box_page(p, key + BN, lo, hi, true) : -2;
-                    const bool load = col < kCols && pg >= 0;
+                    const int next = i + 1 < n && col < kCols ? box_page(p, key + BN, lo, hi) : -1;
+                    const bool load = page_ok(pg);
+                    if (!load && col < kCols && key < hi && key + box_rows > lo) atomicOr(P.status, ST_PAGED_BOUNDS);
                     const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, load)) * box_rows * kRowBytes);
                     const int y = load ? ((pg * P.Hkv + p.h) << P.page_shift) + (key & (P.page_size - 1)) : 0;
 #pragma unroll
@@ -479,7 +500,6 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                 auto kst = [&](int i) { return (g + 2 * i) % NS; };
                 auto kph = [&](int i) { return ((g + 2 * i) / NS) & 1; };
                 auto vst = [&](int i) { return (g + 2 * i + 1) % NS; };
-                auto vph = [&](int i) { return ((g + 2 * i + 1) / NS) & 1; };
                 auto issue_s = [&](int i) {
                     const uint32_t tS = tbase + (NT == 2 ? u * 128 : (sc & 1) * 64);
                     const uint64_t kdesc = sdesc_sw128(sbase + C::kRingOff + kst(i) * C::kTileBytes, 16, 1024);
@@ -521,7 +541,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                             mma_commit_e(BAR(C::EMPTY + kst(i + 1)));
                         }
                     }
-                    ok = wait(C::FULL + vst(i), vph(i));
+                    ok = wait(C::V_OK + (g / 2 + i) % NS, ((g / 2 + i) / NS) & 1);
                     if (NT == 2 && ok && i + 1 < n) ok = wait(C::FULL + kst(i + 1), kph(i + 1));
                     if (ok && has(i)) {
                         ok = NT == 2 ? wait(C::P_FULL + u, pc & 1) : wait(C::P_FULL + (pc & 1), (pc >> 1) & 1);
@@ -543,6 +563,80 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
             }
             mma_commit_e(BAR(C::MMA_DONE));
             mbar_wait(BAR(C::MMA_DONE), 0, P.status, ST_TEARDOWN, nullptr);
+        } else if (warp == 11) {
+            // ------------------------------------------------------ V looked over
+            const int sub = lane < subs ? lane : 0;
+            bool ok = true;
+            unsigned g = 0;  // ring position of the part's first K tile
+            Walk w = walk_of(P, plan);
+            Part p;
+            int4 split = make_int4(0, 0, 0, 0);
+            while (ok && next_part(plan, w, p)) {
+                const int n = p.end - p.begin, tile0 = p.it.t0 + p.begin;
+                if (p.begin == 0 && p.end < p.it.tiles)  // the item goes on in the next stretches
+                    split = make_int4(p.it.row, p.it.ntok, p.h, 1 + (p.it.tiles - p.end - 1) / w.share + 1);
+                int lo, hi;
+                key_span(p, lo, hi);
+                // keys that every row of the item sees
+                const long long last = (long long)p.it.pos + p.it.ntok - 1;
+                const int all_lo = P.wl >= 0 ? (int)max(0ll, last - P.wl) : 0;
+                const int all_hi = P.wr >= 0 ? (int)max(min((long long)p.it.len, (long long)p.it.pos + P.wr + 1), 0ll) : p.it.len;
+                int pg = n > 0 ? box_page(p, tile0 * BN + sub * box_rows, lo, hi) : -1;
+                for (int i = 0; ok && i < n; ++i) {
+                    const int j0 = (tile0 + i) * BN;
+                    const unsigned there = __ballot_sync(0xffffffffu, lane < subs && page_ok(pg));
+                    if (i + 1 < n) pg = box_page(p, j0 + BN + sub * box_rows, lo, hi);
+                    // (the K tile too, though it is not looked at: a stage's uses are waited for one by one, since a
+                    // phase that has not begun looks like one that is over)
+                    const unsigned gk = g + 2 * i, gv = gk + 1, stage = gv % NS;
+                    ok = warp_wait(BAR(C::FULL + gk % NS), (gk / NS) & 1, P.status, ST_FWD_PRODUCER, &abort_flag) &&
+                         warp_wait(BAR(C::FULL + stage), (gv / NS) & 1, P.status, ST_FWD_PRODUCER, &abort_flag);
+                    if (!ok) break;
+                    bool bad = false;
+                    if (j0 < all_lo || j0 + BN > all_hi || there != (1u << subs) - 1u) {
+                        uint8_t* vt = smem + C::kRingOff + stage * C::kTileBytes;
+                        auto zero_rows = [&](int r0, int r1) {
+                            for (int x = r0 * 8 + lane; x < r1 * 8; x += 32)
+#pragma unroll
+                                for (int bx = 0; bx < C::kBoxes; ++bx)
+                                    *reinterpret_cast<uint4*>(vt + bx * (BN * 128) + x * 16) = make_uint4(0, 0, 0, 0);
+                        };
+                        auto check_rows = [&](int r0, int r1) {
+#pragma unroll 2
+                            for (int x = r0 * 8 + lane; x < r1 * 8; x += 32)
+#pragma unroll
+                                for (int bx = 0; bx < C::kBoxes; ++bx) {
+                                    const uint4 v = *reinterpret_cast<const uint4*>(vt + bx * (BN * 128) + x * 16);
+                                    // an exponent of all ones carries into its sign's place
+                                    constexpr uint32_t kExp = BF16 ? 0x7f807f80u : 0x7c007c00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
+                                    const uint32_t c = ((v.x & kExp) + kOne) | ((v.y & kExp) + kOne) | ((v.z & kExp) + kOne) | ((v.w & kExp) + kOne);
+                                    bad = bad || (c & 0x80008000u);
+                                }
+                        };
+                        auto in_tile = [&](int j) { return min(max(j - j0, 0), BN); };
+                        const int a = in_tile(lo), b = in_tile(hi);
+                        zero_rows(0, a);
+                        zero_rows(b, BN);
+                        if (there != (1u << subs) - 1u)
+                            for (int x = 0; x < subs; ++x)
+                                if (!((there >> x) & 1u)) zero_rows(max(x * box_rows, a), min((x + 1) * box_rows, b));
+                        __syncwarp();
+                        const int c = min(max(in_tile(all_lo), a), b), d = max(min(in_tile(all_hi), b), c);
+                        check_rows(a, c);
+                        check_rows(d, b);
+                        fence_proxy_async_smem();  // the zeros, before the product
+                    }
+                    bad = __any_sync(0xffffffffu, bad);
+                    if (lane == 0) {
+                        const unsigned v = (g / 2 + i) % NS;
+                        bad_v[v] = bad ? 1 : 0;
+                        mbar_arrive(BAR(C::V_OK + v));
+                    }
+                    __syncwarp();
+                }
+                g += 2 * n;
+            }
+            if (lane == 0) plan.split[blockIdx.x] = split;
         }
     } else if (F8 && warp >= C::kWide0 && warp < C::kWide0 + 4) {
         // ---------------------------------------------------------------- widening
@@ -555,7 +649,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
             bool ok = true;
             int stage = 0, phase = 1, raw = 0, raw_phase = 0;
             auto scales = [&](const Part& p, int pg) {
-                if (pg < 0) return make_float2(0.f, 0.f);
+                if (!page_ok(pg)) return make_float2(0.f, 0.f);
                 const long long i = (long long)pg * P.Hkv + p.h;
                 return make_float2(__ldg(P.k_scale + i), __ldg(P.v_scale + i));
             };
@@ -565,7 +659,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                 int lo, hi;
                 key_span(p, lo, hi);
                 const int tile0 = p.it.t0 + p.begin, n = p.end - p.begin;
-                auto page_at = [&](int i) { return i < n ? box_page(p, (tile0 + i) * BN + sub * box_rows, lo, hi, false) : -2; };
+                auto page_at = [&](int i) { return i < n ? box_page(p, (tile0 + i) * BN + sub * box_rows, lo, hi) : -1; };
                 int pg = page_at(1);
                 float2 sc = scales(p, page_at(0));
                 for (int i = 0; ok && i < n; ++i) {
@@ -579,20 +673,28 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                         if (!ok) break;
                         const uint8_t* src = smem + C::kRawOff + raw * C::kRawBytes;
                         const uint32_t dst = sbase + C::kRingOff + stage * C::kTileBytes;
-#pragma unroll 4
+                        auto widen = [&](auto e4m3c) {
+                        constexpr bool kE4m3 = decltype(e4m3c)::value;
+                        // consecutive lanes: the chunks of a row, then of the next; this warp's rows lie together
+                        uint4 x[kSteps];
+#pragma unroll
                         for (int t = 0; t < kSteps; ++t) {
-                            // consecutive lanes: the chunks of a row, then of the next; this warp's rows lie together
                             const int at = ww * kSteps * 32 + t * 32 + lane;
                             const int c = at % kChunks, row = at / kChunks % BN, box = at / kChunks / BN;
-                            const uint4 x = *reinterpret_cast<const uint4*>(
+                            x[t] = *reinterpret_cast<const uint4*>(
                                 src + box * (BN * C::kRawRow) + row * C::kRawRow +
                                 (C::kRawRow == 128 ? (c ^ (row & 7)) << 4 : (c ^ ((row >> 1) & 3)) << 4));
-                            const float s = __shfl_sync(0xffffffffu, mine, row / box_rows);
+                        }
+#pragma unroll
+                        for (int t = 0; t < kSteps; ++t) {
+                            const int at = ww * kSteps * 32 + t * 32 + lane;
+                            const int c = at % kChunks, row = at / kChunks % BN, box = at / kChunks / BN;
+                            const float s = __shfl_sync(0xffffffffu, mine, row >> box_shift);
                             uint32_t o[8];
-                            widen4<BF16>(x.x, e4m3, s, o[0], o[1]);
-                            widen4<BF16>(x.y, e4m3, s, o[2], o[3]);
-                            widen4<BF16>(x.z, e4m3, s, o[4], o[5]);
-                            widen4<BF16>(x.w, e4m3, s, o[6], o[7]);
+                            widen4<BF16, kE4m3>(x[t].x, s, o[0], o[1]);
+                            widen4<BF16, kE4m3>(x[t].y, s, o[2], o[3]);
+                            widen4<BF16, kE4m3>(x[t].z, s, o[4], o[5]);
+                            widen4<BF16, kE4m3>(x[t].w, s, o[6], o[7]);
                             // columns 16c .. of the box: two chunks of a 128-byte column of the wide tile.  Lanes of
                             // either half of a row store them in the other order, so that eight lanes meet no bank twice.
                             const int wide = box * (kChunks / 4) + (c >> 2), c2 = (2 * c) & 7;
@@ -602,6 +704,9 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                             st_shared_v4(swap ? a1 : a0, swap ? o[4] : o[0], swap ? o[5] : o[1], swap ? o[6] : o[2], swap ? o[7] : o[3]);
                             st_shared_v4(swap ? a0 : a1, swap ? o[0] : o[4], swap ? o[1] : o[5], swap ? o[2] : o[6], swap ? o[3] : o[7]);
                         }
+                        };
+                        if (e4m3) widen(std::true_type());
+                        else widen(std::false_type());
                         fence_proxy_async_smem();  // the tensor cores read the tile through the async proxy
                         __syncwarp();
                         if (lane == 0) {
@@ -631,7 +736,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
             return __all_sync(0xffffffffu, mbar_wait(BAR(bar), parity, P.status, ST_FWD_SOFTMAX, &abort_flag));
         };
         bool ok = true;
-        int sc = 0, act = 0, vc = 0;  // tiles done, parts in which this tile was active, look-overs
+        int sc = 0, act = 0;  // tiles done, parts in which this tile was active
         // (one tile) the product of the tile before this one is complete.  At most that one can still be on
         // its way, since this tile's S was issued after the one before it, and it cannot be overtaken.
         auto wait_pv = [&]() { return wait(C::PV_DONE + ((sc - 1) & 1), ((sc - 1) >> 1) & 1); };
@@ -688,12 +793,12 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
             const int pos = my.pos + tok;
             float m = 8.f - kTop, l = 0.f;
             const int sub = lane < subs ? lane : 0;
-            int pg = my.n > 0 ? box_page(p, my.t0 * BN + sub * box_rows, lo, hi, false) : -2;
+            int pg = my.n > 0 ? box_page(p, my.t0 * BN + sub * box_rows, lo, hi) : -1;
             for (int k = 0; k < my.n; ++k) {
                 const int j0 = (my.t0 + k) * BN;
                 // boxes of this tile that are there (bit = box)
-                const unsigned there = __ballot_sync(0xffffffffu, lane < subs && pg >= 0);
-                if (k + 1 < my.n) pg = box_page(p, j0 + BN + sub * box_rows, lo, hi, false);
+                const unsigned there = __ballot_sync(0xffffffffu, lane < subs && page_ok(pg));
+                if (k + 1 < my.n) pg = box_page(p, j0 + BN + sub * box_rows, lo, hi);
                 const bool full = there == (1u << subs) - 1u &&
                                   tile_full(P.wl, P.wr, p.it.len, my.pos, my.pos + my.ntok - 1, j0, j0 + BN);
                 const int sbuf = NT == 2 ? u : (sc & 1);
@@ -740,19 +845,27 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                     long long vlo = lo - j0, vhi = hi - j0;
                     if (P.wl >= 0) vlo = max(vlo, (long long)pos - P.wl - j0);
                     if (P.wr >= 0) vhi = min(vhi, (long long)pos + P.wr - j0 + 1);
-                    if (!row_live) vhi = vlo;
+                    const int a = (int)min(max(vlo, 0ll), (long long)BN), b = row_live ? (int)min(max(vhi, (long long)a), (long long)BN) : a;
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
-                        const int a = (int)min(max(vlo - 32 * c, 0ll), 32ll), b = (int)min(max(vhi - 32 * c, 0ll), 32ll);
-                        const uint32_t below_b = b >= 32 ? 0xffffffffu : (1u << b) - 1u;
-                        const uint32_t below_a = a >= 32 ? 0xffffffffu : (1u << a) - 1u;
-                        uint32_t have = 0;  // boxes of 16, 32 or 64 keys
-                        for (int x = 0; x < 32; x += min(box_rows, 32))
-                            if ((there >> ((32 * c + x) / box_rows)) & 1u) have |= (box_rows == 16 ? 0xffffu : 0xffffffffu) << x;
-                        seen[c] = below_b & ~below_a & have;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) sv[c][e] = (seen[c] >> e) & 1u ? sv[c][e] : 0xff800000u;  // -inf
+                        const int c0 = min(max(a - 32 * c, 0), 32), c1 = min(max(b - 32 * c, 0), 32);
+                        seen[c] = bit_range(c0, c1 - c0);
                     }
+                    if (there != (1u << subs) - 1u) {
+#pragma unroll
+                        for (int c = 0; c < NC; ++c) {  // boxes of 16, 32 or 64 keys
+                            const int x = 32 * c / box_rows;
+                            uint32_t have = ((there >> x) & 1u) ? 0xffffffffu : 0u;
+                            if (box_rows == 16) have = (have & 0xffffu) | (((there >> (x + 1)) & 1u) ? 0xffff0000u : 0u);
+                            seen[c] &= have;
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < NC; ++c)
+                        if (!__all_sync(0xffffffffu, seen[c] == 0xffffffffu)) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) sv[c][e] = (seen[c] >> e) & 1u ? sv[c][e] : 0xff800000u;  // -inf
+                        }
                 }
                 // ---- the row's largest score, as x against its reference
                 float rm[NC];
@@ -832,42 +945,17 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                 else if (shorter) p_pass(M3());
                 else if (!accurate) p_pass(M1());
                 else p_pass(M2());
-                // ---- a tile that is not whole: V looked over
+                // ---- a tile that is not whole: is all of V finite that some row does not see
                 bool by_row = false;
                 if (!full) {
                     const int i = my.t0 + k - tile0;  // its place in the part
-                    const unsigned gv = g0 + 2 * i + 1;
-                    if (!wait(C::FULL + gv % NS, (gv / NS) & 1)) {
+                    const unsigned gv = g0 + 2 * i + 1, vn = g0 / 2 + i;
+                    if (!wait(C::V_OK + vn % NS, (vn / NS) & 1)) {
                         ok = false;
                         break;
                     }
-                    uint8_t* vt = smem + C::kRingOff + (gv % NS) * C::kTileBytes;
-                    bool bad = false;
-                    // a lane takes 16-byte chunks of rows r, r + 32, ...: eight lanes a row's
-#pragma unroll 4
-                    for (int x = r; x < BN * 8 * C::kBoxes; x += kM) {
-                        const int row = (x >> 3) % BN, j = j0 + row;
-                        uint4* at = reinterpret_cast<uint4*>(vt + x * 16);
-                        if (j < lo || j >= hi || !((there >> (row / box_rows)) & 1u)) {
-                            *at = make_uint4(0, 0, 0, 0);
-                        } else {
-                            const uint4 v = *at;
-                            constexpr uint32_t kExp = BF16 ? 0x7f807f80u : 0x7c007c00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
-                            // an exponent of all ones carries into its sign's place
-                            const uint32_t c = ((v.x & kExp) + kOne) | ((v.y & kExp) + kOne) | ((v.z & kExp) + kOne) | ((v.w & kExp) + kOne);
-                            bad = bad || (c & 0x80008000u);
-                        }
-                    }
-                    ++vc;
-                    if (bad) *static_cast<volatile int*>(&bad_tile[u][vc & 1]) = vc;
-                    fence_proxy_async_smem();  // the zeros, before the product
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(BAR(C::V_CHECK + u));
-                    if (!wait(C::V_CHECK + u, (vc - 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    by_row = *static_cast<volatile int*>(&bad_tile[u][vc & 1]) == vc;
+                    const uint8_t* vt = smem + C::kRingOff + (gv % NS) * C::kTileBytes;
+                    by_row = *static_cast<volatile int*>(&bad_v[vn % NS]) != 0;
                     if (by_row) {
                         tmem_st_wait();
                         if (!o_stands && k > 0) {
@@ -952,7 +1040,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
             }
             if (have_o) tc_fence_after();
             const bool whole = p.whole();
-            const bool none = l == 0.f;
+            const bool none = l == 0.f, o32 = (reinterpret_cast<uintptr_t>(P.o) & 31u) == 0;
             const float inv = none ? 0.f : 1.f / l;
             const int slot = 2 * blockIdx.x + (p.begin == 0 ? 1 : 0), rows = NT * kM;
             const long long orow = (long long)(p.it.row + u * tm + tok);
@@ -966,20 +1054,27 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                     tmem_ld_wait(orr);
                 }
                 if (row_live && whole) {
+                    uint32_t pk[2][8];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t pk[4] = {0, 0, 0, 0};
-                        if (!none)
+                    for (int e = 0; e < 16; ++e)
+                        pk[e >> 3][e & 7] = none ? 0u : pack2<BF16>(__uint_as_float(orr[2 * e]) * inv, __uint_as_float(orr[2 * e + 1]) * inv);
+                    // (a row's sector at a time, where O is aligned to them)
+                    if (o32) {
+                        store_32(out + c * 4, pk[0]);
+                        store_32(out + c * 4 + 2, pk[1]);
+                    } else {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                pk[e] = pack2<BF16>(__uint_as_float(orr[8 * q + 2 * e]) * inv, __uint_as_float(orr[8 * q + 2 * e + 1]) * inv);
-                        out[c * 4 + q] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                        for (int q = 0; q < 4; ++q)
+                            out[c * 4 + q] = make_uint4(pk[q >> 1][4 * (q & 1)], pk[q >> 1][4 * (q & 1) + 1], pk[q >> 1][4 * (q & 1) + 2],
+                                                        pk[q >> 1][4 * (q & 1) + 3]);
                     }
                 } else if (row_live && !none) {
 #pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        part[c * 8 + q] = make_float4(__uint_as_float(orr[4 * q]), __uint_as_float(orr[4 * q + 1]),
-                                                      __uint_as_float(orr[4 * q + 2]), __uint_as_float(orr[4 * q + 3]));
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t f[8] = {orr[8 * q], orr[8 * q + 1], orr[8 * q + 2], orr[8 * q + 3],
+                                               orr[8 * q + 4], orr[8 * q + 5], orr[8 * q + 6], orr[8 * q + 7]};
+                        store_32(part + c * 8 + q * 2, f);
+                    }
                 }
                 __syncwarp();
             }
@@ -1005,29 +1100,40 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
 }
 
 // ------------------------------------------------------------------- the merge
-// Joins the partial rows of the items that stretches cut: CTA (c, y) those of the item that begins in
-// stretch c and ends behind it, a warp to a row, in the order of the stretches.
+// Joins the partial rows of the items that stretches cut, a warp to a row, in the order of the stretches.
+constexpr int kMergeCtas = 8 * kPrefillCtas;
 template <int HD>
-__global__ void __launch_bounds__(256) paged_prefill_merge_kernel(const PagedParams P, const int bf16, const int bn) {
+__global__ void __launch_bounds__(256) paged_prefill_merge_kernel(const PagedParams P, const int bf16) {
     constexpr int NT = HD == 256 ? 1 : 2, rows = NT * kM, kPer = HD / 32;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int tm = kM / P.G, c = blockIdx.x;
+    static_assert(kPrefillCtas <= 256, "a thread to a stretch");
+    __shared__ int4 split_s[kPrefillCtas];
+    __shared__ int before_s[kPrefillCtas];  // rows of the items that earlier stretches cut
+    __shared__ int sums[8];
+    const int tm = kM / P.G, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Plan plan = plan_of(P, NT * tm);
-    const long long per_head = *plan.all;
-    const Deal d = deal_of(P, per_head);
-    const long long last = min(d.all, (c + 1) * d.share) - 1;
-    if (last < c * d.share) return;  // nothing in the stretch
-    const int h = (int)(last / per_head);
-    const int e = warp_last_le(*plan.count, last - h * per_head, [&](int i) { return plan.cum[i]; });
-    const Item it = plan.items[e];
-    const long long first = h * per_head + plan.cum[e] + kItemCost;  // its first tile
-    if (it.tiles == 0 || first / d.share != c) return;
-    const int n = (int)((first + it.tiles - 1) / d.share) - c + 1;  // its parts
-    if (n <= 1) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int live = it.ntok;  // tokens
-    for (int x = blockIdx.y * 8 + warp; x < live * P.G; x += gridDim.y * 8) {
-        const int t = x / P.G, head = x - t * P.G, u = t / tm, r = u * kM + (t - u * tm) * P.G + head;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 mine = threadIdx.x < kPrefillCtas ? plan.split[threadIdx.x] : make_int4(0, 0, 0, 0);
+    const int count = mine.y * P.G;  // (no tokens: nothing is cut)
+    int incl = count;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    int all = 0;
+    for (int i = 0; i < 8; ++i) {
+        if (i < warp) incl += sums[i];
+        all += sums[i];
+    }
+    if (threadIdx.x < kPrefillCtas) split_s[threadIdx.x] = mine, before_s[threadIdx.x] = incl - count;
+    __syncthreads();
+    for (int x = blockIdx.x * 8 + warp; x < all; x += kMergeCtas * 8) {
+        const int c = warp_last_le(kPrefillCtas, x, [&](int i) { return (long long)before_s[i]; });
+        const int4 it = split_s[c];
+        const int y = x - before_s[c], n = it.w;
+        const int t = y / P.G, head = y - t * P.G, u = t / tm, r = u * kM + (t - u * tm) * P.G + head;
         auto slot = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); };
         float M = -INFINITY, L = 0.f;
         float acc[kPer];
@@ -1048,15 +1154,17 @@ __global__ void __launch_bounds__(256) paged_prefill_merge_kernel(const PagedPar
             L = L * alpha + (some ? f * ml.y : 0.f);  // of this lane's parts
 #pragma unroll
             for (int q = 0; q < kPer; ++q) acc[q] *= alpha;
-            for (int j = 0; j < min(32, n - base); ++j) {
-                if (!((use >> j) & 1u)) continue;
+            const int m = min(32, n - base);
+#pragma unroll 4
+            for (int j = 0; j < m; ++j) {
                 const float* src = part_o(plan, slot(base + j), rows, HD) + (size_t)r * HD + lane * kPer;
                 const float fj = __shfl_sync(0xffffffffu, f, j);
+                const bool has = (use >> j) & 1u;
 #pragma unroll
                 for (int q = 0; q < kPer; q += 2) {
                     const float2 v = *reinterpret_cast<const float2*>(src + q);
-                    acc[q] = fmaf(fj, v.x, acc[q]);
-                    acc[q + 1] = fmaf(fj, v.y, acc[q + 1]);
+                    acc[q] = has ? fmaf(fj, v.x, acc[q]) : acc[q];
+                    acc[q + 1] = has ? fmaf(fj, v.y, acc[q + 1]) : acc[q + 1];
                 }
             }
         }
@@ -1064,8 +1172,8 @@ __global__ void __launch_bounds__(256) paged_prefill_merge_kernel(const PagedPar
         for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
         const bool none = M == -INFINITY;
         const float inv = none ? 0.f : 1.f / L;
-        const long long orow = it.row + t;
-        const int hq = h * P.G + head;
+        const long long orow = it.x + t;
+        const int hq = it.z * P.G + head;
         uint32_t* od = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(P.o) + (orow * P.H + hq) * HD + lane * kPer);
 #pragma unroll
         for (int q = 0; q < kPer; q += 2)
@@ -1110,10 +1218,10 @@ cudaError_t launch_one(const PagedParams& p, int cache, const PrefillMaps& maps,
     cfg.stream = s;
     early(cfg, at);
     if ((e = cudaLaunchKernelEx(&cfg, k, p, cache == CACHE_E4M3 ? 1 : 0, maps.q, maps.k, maps.v)) != cudaSuccess) return e;
-    cfg.gridDim = dim3(kPrefillCtas, 8);
+    cfg.gridDim = dim3(kMergeCtas);
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, paged_prefill_merge_kernel<HD>, p, BF16 ? 1 : 0, C::BN);
+    return cudaLaunchKernelEx(&cfg, paged_prefill_merge_kernel<HD>, p, BF16 ? 1 : 0);
 }
 template <bool BF16, bool F8>
 cudaError_t launch_hd(const PagedParams& p, int cache, const PrefillMaps& m, cudaStream_t s) {

@@ -149,6 +149,17 @@ def test_few_rows_over_one_long_sequence(dt, kind, hd, new):
     run(dt, kind, [12011], [new], 4, 1, hd, 16, seed=9 + new)
 
 
+def test_wide_heads_bound_by_memory():
+    """Many sequences of few rows at hd 256, whose tiles land late and out of their order, a few times over."""
+    new = [37 - (23 * b) // 36 for b in range(37)]
+    lengths = [1336 + (4907 * b) // 36 for b in range(37)]
+    c, q, cu, o, lse = run("bf16", "bf16", lengths, new, 4, 2, 256, 16, seed=61)
+    for _ in range(5):
+        again, _ = A.attn_paged_prefill(q, c.k, c.v, c.table_d, i32(lengths), i32(cu), H=4, **c.kw())
+        status_ok()
+        assert torch.equal(again[:int(cu[-1])], o[:int(cu[-1])])
+
+
 def test_split_rows_that_see_nothing_in_some_parts():
     run("bf16", "bf16", [9000], [200], 2, 1, 128, 16, seed=19, window=2000)
     run("bf16", "e4m3", [9000], [400], 1, 1, 64, 16, seed=20, window=700)
