@@ -35,13 +35,17 @@ constexpr int kItemCost = 2;
 // The least that a stretch holds.
 constexpr int kMinShare = 4;
 
-// p = 2^(x - ref): a row's reference is moved when its largest p would pass 2^top, or, before it has
-// seen anything, when it would stay below 2^(top - 10); it is then put at 2^(top - 8).  fp16 p have room up
-// to 2^8 and no more exponents to lose below; bf16 ones stay at most 1, so that P V passes fp32's range
-// no sooner than the sum of V does.
+// p = 2^x, x relative to a row's reference, which starts at `first` and stays while the sum over half a tile's p
+// is below `high` (so that every p is) and, in the first half of which the row sees anything, not below `low` (so
+// that its largest p is at least low / 64); a usual tile then needs no maximum.  Else the row's largest x
+// in the tile is taken and put at `put` if it is above x_high or, in a row that has seen nothing, below x_low, and
+// p formed again.  fp16 p reach up to 2^15 and have no exponents to lose below: the largest stays at 2^-2 or
+// more.  bf16 ones, whose exponent is fp32's, stay below 1, so that P V passes fp32's range no sooner than
+// the sum of V does.
 template <bool BF16>
 struct PRange {
-    static constexpr float top = BF16 ? 0.f : 8.f;
+    static constexpr float first = BF16 ? 24.f : -4.f, high = BF16 ? 1.f : 0x1p15f, low = BF16 ? 0x1p-60f : 0x1p4f,
+                           x_high = BF16 ? -7.f : 8.f, x_low = BF16 ? -60.f : -2.f, put = BF16 ? -24.f : 4.f;
 };
 
 template <int HD, bool F8>
@@ -64,17 +68,12 @@ struct Cfg {
                          MMA_DONE = 14, FULL = 15, EMPTY = FULL + kStages, V_OK = EMPTY + kStages, RAW_FULL = V_OK + kStages,
                          RAW_EMPTY = RAW_FULL + kRaw, kBars = RAW_EMPTY + kRaw;
     static constexpr int kBytes = kBarOff + kBars * 8 + 16 + 1024;  // (1024: alignment)
-    static_assert(kBytes <= 227 * 1024, "shared memory");
-    // Warpgroups: softmax of tile A; of tile B (at hd 256 the widening warps instead); loads and MMA
-    // issue; the widening warps beside two tiles.
-    static constexpr bool kWideB = F8 && NT == 1, kWide4 = F8 && NT == 2;
-    static constexpr int kThreads = kWide4 ? 512 : 384;
-    static constexpr int kWide0 = kWide4 ? 12 : 4;  // first widening warp
-    // registers: shares of what the launch holds (512 x 128, 384 x 168)
-    static constexpr int kRegsSoftmax = kWide4 ? 200 : 216, kRegsLoad = kWide4 ? 48 : 72, kRegsWide = kWide4 ? 64 : 120;
-    static constexpr int kRegsB = NT == 2 ? kRegsSoftmax : F8 ? kRegsWide : 168;
-    static_assert((kRegsSoftmax + kRegsB + kRegsLoad + (kWide4 ? kRegsWide : 0)) * 128 <= kThreads * (kWide4 ? 128 : 168),
-                  "register split exceeds the launch");
+    static_assert(kBytes + 1280 <= 227 * 1024, "shared memory");    // (1280: the kernel's own variables)
+    // Warpgroups: two of softmax, one that loads and issues, over 8-bit pools one that widens, with
+    // registers shared out from what the launch holds.
+    static constexpr int kThreads = F8 ? 512 : 384;
+    static constexpr int kRegsSoftmax = 168, kRegsLoad = 56, kRegsWide = 120;
+    static_assert((2 * kRegsSoftmax + kRegsLoad + kRegsWide) * 128 <= 512 * 128, "register split exceeds the launch");
 };
 
 // ------------------------------------------------------------------- the plan
@@ -281,23 +280,41 @@ __device__ __forceinline__ bool next_part(const Plan& plan, Walk& w, Part& p) {
     return false;
 }
 
-// Query tile u of a part: its tokens, and the tiles [t0, t0 + n) of the part that any of its rows sees.
-struct Tiles {
-    int ntok, pos, t0, n;
-};
-template <int BN>
-__device__ __forceinline__ Tiles tiles_of(const PagedParams& P, const Part& p, int u, int tm) {
-    Tiles t;
-    t.ntok = min(max(p.it.ntok - u * tm, 0), tm);
-    t.pos = p.it.pos + u * tm;
-    t.t0 = t.n = 0;
-    if (t.ntok > 0) {
-        int lo, hi;
-        key_range(P.wl, P.wr, p.it.len, t.pos, t.pos + t.ntok - 1, &lo, &hi);
-        const int a = max(lo / BN, p.it.t0 + p.begin), b = min((hi + BN - 1) / BN, p.it.t0 + p.end);
-        if (hi > lo && b > a) t.t0 = a, t.n = b - a;
+// What the query tiles of a part see.  Each has its rows (tokens from `pos` on) and sees key tiles [t0, t0 + n)
+// of the part.  An item with rows for one tile only is computed by both all the same (`solo`): the second
+// takes every other key tile of the same rows, and their results are joined at the end.
+struct Sight {
+    int t0[2], n[2], ntok[2];
+    bool solo;
+    __device__ bool has(int u, int t) const {
+        const int a = u ? t0[1] : t0[0], m = u ? n[1] : n[0];
+        return solo ? t >= a && ((t - a) & 1) == 0 && (t - a) >> 1 < m : t >= a && t < a + m;
     }
-    return t;
+    __device__ int index(int u, int t) const { return (t - (u ? t0[1] : t0[0])) >> (solo ? 1 : 0); }
+};
+template <int NT, int BN>
+__device__ __forceinline__ Sight sight_of(const PagedParams& P, const Part& p, int tm) {
+    Sight s;
+    s.solo = NT == 2 && p.it.ntok <= tm;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        s.ntok[u] = u < NT ? min(max(p.it.ntok - u * tm, 0), tm) : 0;
+        s.t0[u] = s.n[u] = 0;
+        if (s.ntok[u] > 0) {
+            int lo, hi;
+            const int pos = p.it.pos + u * tm;
+            key_range(P.wl, P.wr, p.it.len, pos, pos + s.ntok[u] - 1, &lo, &hi);
+            const int a = max(lo / BN, p.it.t0 + p.begin), b = min((hi + BN - 1) / BN, p.it.t0 + p.end);
+            if (hi > lo && b > a) s.t0[u] = a, s.n[u] = b - a;
+        }
+    }
+    if (s.solo) {
+        s.ntok[1] = s.ntok[0];
+        s.t0[1] = s.t0[0] + 1;
+        s.n[1] = s.n[0] / 2;
+        s.n[0] -= s.n[1];
+    }
+    return s;
 }
 
 __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
@@ -335,13 +352,25 @@ __device__ __forceinline__ void store_32(void* at, const uint32_t (&v)[8]) {
                  : "memory");
 }
 
+// Of two warps that share rows: whether either says so.  Both come here equally often whatever fails.
+__device__ __forceinline__ bool pair_any(int id, bool x) {
+    int r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.or.pred q, %2, 64, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"((int)x), "r"(id)
+                 : "memory");
+    return r != 0;
+}
+
 // ------------------------------------------------------------------ the kernel
-// Roles (warps): softmax of tile u, one thread to a row (0-3, 4-7); loads (8); MMA issue of tile u (9 + u); looking
-// V over (11); over 8-bit pools, widening (Cfg::kWide0 ...).  Two tiles take turns as in the dense forward: one tile's
-// softmax runs while the tensor cores work on the other's P V and next S; each has one S buffer, and a
-// completed S(n), issued after P(n-1) V(n-1), also means that O stands still.  With one tile (hd 256)
-// there are two S buffers instead, S(n+1) is issued before P(n) V(n), and the softmax may be done with P(n+1)
-// before that product is issued: S, P and the product have a barrier for each buffer.
+// Roles (warps): softmax (0-7); loads (8); MMA issue of tile u (9 + u); looking V over (11); over 8-bit pools,
+// widening (12-15).  All eight softmax warps work on one tile at a time, A(n), B(n), A(n+1), ..., while the
+// tensor cores make the other tile's P V and next S: warps w and w + 4 share 32 rows and take one half of the
+// keys each (one warp a scheduler reaches two thirds of the rates of exp2, fma and conversions that two do).
+// They know a row's reference alike; each sums its own half.  Each tile has one S buffer, and a completed S(n),
+// issued after P(n-1) V(n-1), also means that O stands still.  With one tile (hd 256) there are two S buffers
+// instead, S(n+1) is issued before P(n) V(n), and the softmax may be done with P(n+1) before that
+// product is issued: S, P and the product have a barrier for each buffer.
 //
 // What a row does not see has no effect on it.  Warp 11 looks over each tile of V before its product is
 // issued: rows of V that no row of the item sees (behind the sequence, in a page that does not exist) become
@@ -362,7 +391,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
     const uint32_t bar0 = smem_u32(bars);
     auto BAR = [&](int i) { return bar0 + 8u * (uint32_t)i; };
     __shared__ int abort_flag;
-    __shared__ int done_count[2];  // warps that have finished a softmax of tile u
+    __shared__ float half_s[2][kM];  // what two warps with the same rows tell each other
     __shared__ int bad_v[NS];      // of V tile n, at n mod NS, as its barrier: a value that not every row sees is not finite
     __shared__ int skip_pv[2][2];  // by the parity of the tile: the softmax warps make this product
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -372,14 +401,14 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
         for (int i = 0; i < C::kBars; ++i) {
             uint32_t n = 1;
             if ((i >= C::P_FULL && i < C::P_FULL + 2) || (i >= C::O_EMPTY && i < C::O_EMPTY + 2))
-                n = 4;  // softmax warps of a tile
+                n = 8;  // softmax warps
             if ((i >= C::EMPTY && i < C::EMPTY + NS) || i == C::MMA_DONE) n = NT;  // MMA issuers
             if (F8 && ((i >= C::FULL && i < C::FULL + NS) || (i >= C::RAW_EMPTY && i < C::RAW_EMPTY + C::kRaw)))
                 n = 4;  // widening warps
             mbar_init(BAR(i), n);
         }
         abort_flag = 0;
-        for (int u = 0; u < 2; ++u) done_count[u] = 0, skip_pv[u][0] = skip_pv[u][1] = 0;
+        for (int u = 0; u < 2; ++u) skip_pv[u][0] = skip_pv[u][1] = 0;
         fence_barrier_init();
     }
     if (warp == 9) {
@@ -408,7 +437,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
     };
 
     if (warp >= 8 && warp < 12) {
-        regs_dec<C::kRegsLoad>();
+        if constexpr (F8) regs_dec<C::kRegsLoad>();
         if (warp == 8) {
             // ------------------------------------------------------------ loads
             if (elect_one()) {
@@ -431,12 +460,11 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
             while (ok && next_part(plan, w, p)) {
                 int lo, hi;
                 key_span(p, lo, hi);
-                Tiles tu[2];
-                for (int u = 0; u < NT; ++u) tu[u] = tiles_of<BN>(P, p, u, tm);
+                const Sight st = sight_of<NT, BN>(P, p, tm);
                 const int tile0 = p.it.t0 + p.begin, n = p.end - p.begin;
                 int pg = n > 0 && col < kCols ? box_page(p, tile0 * BN + sub * box_rows, lo, hi) : -1;
                 for (int u = 0; ok && u < NT; ++u) {
-                    if (tu[u].n == 0) continue;
+                    if ((u ? st.n[1] : st.n[0]) == 0) continue;
                     if (qn[u] > 0 && !warp_wait(BAR(C::Q_EMPTY + u), (qn[u] - 1) & 1, P.status, ST_FWD_PRODUCER, &abort_flag)) {
                         ok = false;
                         break;
@@ -445,7 +473,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                     for (int bx = 0; bx < C::kBoxes; ++bx)
                         if (elect_one())
                             tma_load_3d(sbase + u * C::kQBytes + bx * (kM * 128), &tmQ, BAR(C::Q_FULL + u), bx * 64, p.h * P.G,
-                                        p.it.row + u * tm);
+                                        p.it.row + (st.solo ? 0 : u * tm));
                     ++qn[u];
                 }
                 for (int i = 0; ok && i < n; ++i) {
@@ -495,8 +523,9 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
             while (ok && next_part(plan, w, p)) {
                 const int n = p.end - p.begin, tile0 = p.it.t0 + p.begin;
                 if (n <= 0) continue;
-                const Tiles my = tiles_of<BN>(P, p, u, tm);
-                auto has = [&](int i) { return tile0 + i >= my.t0 && tile0 + i < my.t0 + my.n; };
+                const Sight st = sight_of<NT, BN>(P, p, tm);
+                const int mine = u ? st.n[1] : st.n[0];
+                auto has = [&](int i) { return st.has(u, tile0 + i); };
                 auto kst = [&](int i) { return (g + 2 * i) % NS; };
                 auto kph = [&](int i) { return ((g + 2 * i) / NS) & 1; };
                 auto vst = [&](int i) { return (g + 2 * i + 1) % NS; };
@@ -509,7 +538,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                                  kdesc + (((kk >> 2) * (BN * 128) + (kk & 3) * 32) >> 4), idS, kk > 0 ? 1u : 0u);
                     mma_commit_e(BAR(C::S_FULL + (NT == 2 ? u : (sc & 1))));
                     ++sc;
-                    if (tile0 + i == my.t0 + my.n - 1) mma_commit_e(BAR(C::Q_EMPTY + u));
+                    if (st.index(u, tile0 + i) == mine - 1) mma_commit_e(BAR(C::Q_EMPTY + u));
                 };
                 auto issue_pv = [&](int i, int k) {
                     const uint32_t tS = tbase + (NT == 2 ? u * 128 : ((pc - 1) & 1) * 64);
@@ -521,17 +550,17 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                             mma_ts_e(tO, tS + kk * 8, vdesc + ((kk * 16 * 128) >> 4), idPV, (k > 0 || kk > 0) ? 1u : 0u);
                     }
                     if constexpr (NT == 1) mma_commit_e(BAR(C::PV_DONE + ((pc - 1) & 1)));
-                    if (k == my.n - 1) mma_commit_e(BAR(C::O_DONE + u));
+                    if (k == mine - 1) mma_commit_e(BAR(C::O_DONE + u));
                 };
                 // A tile's release is committed only after the wait for its data, also for tiles that
                 // this query tile skips, so that no arrival belongs to a later use of the stage.
-                if (my.n > 0 && !wait(C::Q_FULL + u, act & 1)) break;
+                if (mine > 0 && !wait(C::Q_FULL + u, act & 1)) break;
                 if (!wait(C::FULL + kst(0), kph(0))) break;
                 tc_fence_after();
                 if (has(0)) issue_s(0);
                 mma_commit_e(BAR(C::EMPTY + kst(0)));
                 for (int i = 0; ok && i < n; ++i) {
-                    const int k = tile0 + i - my.t0;
+                    const int k = st.index(u, tile0 + i);
                     if constexpr (NT == 1) {
                         if (i + 1 < n) {
                             ok = wait(C::FULL + kst(i + 1), kph(i + 1));
@@ -559,7 +588,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                     if (NT == 2 && i + 1 < n) mma_commit_e(BAR(C::EMPTY + kst(i + 1)));
                 }
                 g += 2 * n;
-                if (my.n > 0) ++act;
+                if (mine > 0) ++act;
             }
             mma_commit_e(BAR(C::MMA_DONE));
             mbar_wait(BAR(C::MMA_DONE), 0, P.status, ST_TEARDOWN, nullptr);
@@ -638,11 +667,11 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
             }
             if (lane == 0) plan.split[blockIdx.x] = split;
         }
-    } else if (F8 && warp >= C::kWide0 && warp < C::kWide0 + 4) {
+    } else if (F8 && warp >= 12) {
         // ---------------------------------------------------------------- widening
         if constexpr (F8) {
             regs_dec<C::kRegsWide>();
-            const int ww = warp - C::kWide0;
+            const int ww = warp - 12;
             constexpr int kChunks = C::kRawRow / 16;            // 16-byte chunks of a box's row
             constexpr int kSteps = BN * HD / 16 / 128;          // chunks of a lane, of a tile
             const int sub = lane % subs;
@@ -720,28 +749,31 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                 }
             }
         }
-    } else if (warp < 4 * NT) {
-        regs_inc<C::kRegsSoftmax>();
-        // -------------------------------------------------- softmax, epilogue of tile u
-        const int u = warp >> 2, wq = warp & 3, r = wq * 32 + lane;
+    } else {
+        if constexpr (F8) regs_inc<C::kRegsSoftmax>();
+        // ------------------------------------------------------------ softmax, epilogue
+        const int wq = warp & 3, h = warp >> 2, r = wq * 32 + lane;  // row, and half of a tile's keys and of O's columns
         const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
-        const uint32_t tO = tbase + 256 + u * HD + lane_off;
         const int tok = r / P.G, head = r - tok * P.G;  // of this thread's row
         const float sl2 = P.scale * kLog2e;
         const uint64_t sl2_2 = f2_make(sl2, sl2);
         const float cap_in = P.scale / fmaxf(P.softcap, 1e-30f), cap_out = P.softcap * kLog2e;
-        constexpr float kTop = PRange<BF16>::top;
-        constexpr int NC = BN / 32;
+        using R = PRange<BF16>;
+        constexpr int NC = BN / 64, kCols = HD / 2;  // chunks of 32 keys of a half; columns of a half of O
         auto wait = [&](int bar, uint32_t parity) {
             return __all_sync(0xffffffffu, mbar_wait(BAR(bar), parity, P.status, ST_FWD_SOFTMAX, &abort_flag));
         };
+        // what the other warp of these rows put in its place of half_s
+        auto exchange = [&](float x) {
+            half_s[h][r] = x;
+            pair_any(1 + wq, false);
+            const float y = half_s[h ^ 1][r];
+            pair_any(1 + wq, false);
+            return y;
+        };
         bool ok = true;
-        int sc = 0, act = 0;  // tiles done, parts in which this tile was active
-        // (one tile) the product of the tile before this one is complete.  At most that one can still be on
-        // its way, since this tile's S was issued after the one before it, and it cannot be overtaken.
-        auto wait_pv = [&]() { return wait(C::PV_DONE + ((sc - 1) & 1), ((sc - 1) >> 1) & 1); };
-        int base[2] = {0, 0};         // softmaxes of both tiles in earlier parts
-        unsigned g = 0;               // ring position of the part's first K tile
+        int sc[2] = {0, 0}, act[2] = {0, 0};  // tiles done, parts in which the tile was active
+        unsigned g = 0;                       // ring position of the part's first K tile
         // x = score * log2(e) - m of a pair of raw scores; mode 0: plain; with a softcap 1: the fitted
         // polynomial, 2: by exp, 3: the short polynomial
         auto to_x = [&](auto modec, uint64_t rr, uint64_t nm) -> uint64_t {
@@ -776,319 +808,355 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
         Part p;
         while (ok && next_part(plan, w, p)) {
             const int n = p.end - p.begin, tile0 = p.it.t0 + p.begin;
-            const Tiles my = tiles_of<BN>(P, p, u, tm);
-            const Tiles other = NT == 2 ? tiles_of<BN>(P, p, 1 - u, tm) : my;
-            const int nA = u == 0 ? my.n : other.n, nB = u == 0 ? other.n : my.n, bA = base[0], bB = base[1];
-            // (a tile whose keys begin more than one tile before the other's would wait for a turn that needs a
-            // stage of the ring that only its own product frees; 128 rows apart they never do)
-            const bool alt = NT == 2 && abs(my.t0 - other.t0) <= 1;
-            base[0] += nA;
-            base[1] += nB;
-            const unsigned g0 = g;
+            const Sight st = sight_of<NT, BN>(P, p, tm);
+            const unsigned v0 = g / 2;  // V tiles before this part
             g += 2 * n;
-            if (my.ntok == 0) continue;
             int lo, hi;  // keys that any row of the item sees
             key_span(p, lo, hi);
-            const bool row_live = tok < my.ntok;
-            const int pos = my.pos + tok;
-            float m = 8.f - kTop, l = 0.f;
+            float m2[2] = {R::first, R::first}, l2[2] = {0.f, 0.f};  // of this row in both tiles
             const int sub = lane < subs ? lane : 0;
-            int pg = my.n > 0 ? box_page(p, my.t0 * BN + sub * box_rows, lo, hi) : -1;
-            for (int k = 0; k < my.n; ++k) {
-                const int j0 = (my.t0 + k) * BN;
+            int pg = n > 0 ? box_page(p, tile0 * BN + sub * box_rows, lo, hi) : -1;
+            for (int i = 0; ok && i < n; ++i) {
+                const int j0 = (tile0 + i) * BN;
                 // boxes of this tile that are there (bit = box)
                 const unsigned there = __ballot_sync(0xffffffffu, lane < subs && page_ok(pg));
-                if (k + 1 < my.n) pg = box_page(p, j0 + BN + sub * box_rows, lo, hi);
-                const bool full = there == (1u << subs) - 1u &&
-                                  tile_full(P.wl, P.wr, p.it.len, my.pos, my.pos + my.ntok - 1, j0, j0 + BN);
-                const int sbuf = NT == 2 ? u : (sc & 1);
-                const uint32_t tS = tbase + (NT == 2 ? u * 128 : (sc & 1) * 64) + lane_off;
-                if (!wait(C::S_FULL + sbuf, NT == 2 ? sc & 1 : (sc >> 1) & 1)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                uint32_t sv[NC][32];
+                if (i + 1 < n) pg = box_page(p, j0 + BN + sub * box_rows, lo, hi);
+                const bool all_there = there == (1u << subs) - 1u;
+#pragma unroll 1
+                for (int u = 0; ok && u < NT; ++u) {
+                    if (!st.has(u, tile0 + i)) continue;
+                    const int ntok = u ? st.ntok[1] : st.ntok[0], pos0 = p.it.pos + (st.solo ? 0 : u * tm);
+                    const bool first = st.index(u, tile0 + i) == 0;
+                    const int count = u ? sc[1] : sc[0];
+                    float m = u ? m2[1] : m2[0], l = u ? l2[1] : l2[0];
+                    const bool row_live = tok < ntok;
+                    const bool full = all_there && tile_full(P.wl, P.wr, p.it.len, pos0, pos0 + ntok - 1, j0, j0 + BN);
+                    const uint32_t tS = tbase + (NT == 2 ? u * 128 : (count & 1) * 64) + lane_off;  // S, and P over it
+                    const uint32_t tO = tbase + 256 + u * HD + h * kCols + lane_off;
+                    // (one tile) the product of the tile before this one is complete.  At most that one can still be
+                    // on its way, since this tile's S was issued after the one before it, and it cannot be overtaken.
+                    auto wait_pv = [&]() {
+                        return NT == 2 || wait(C::PV_DONE + ((count - 1) & 1), ((count - 1) >> 1) & 1);
+                    };
+                    uint32_t sv[NC][32];
+                    bool got = wait(C::S_FULL + (NT == 2 ? u : (count & 1)), (NT == 2 ? count : count >> 1) & 1);
+                    tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < NC; ++c) tmem_ld32(tS + c * 32, sv[c]);
-                if (alt && (u == 0 ? (k >= 1 && k - 1 < nB) : (k < nA))) {
-                    const int need = 4 * (u == 0 ? bB + k : bA + k + 1);
-                    const bool rr = count_wait(&done_count[u ^ 1], need, P.status, ST_FWD_SOFTMAX, &abort_flag);
-                    if (!__all_sync(0xffffffffu, rr)) {
+                    for (int c = 0; c < NC; ++c) tmem_ld32(tS + (h * NC + c) * 32, sv[c]);
+                    // ---- the keys of the tile that this row sees: [va, vb), in boxes that are there
+                    int va = 0, vb = BN;
+                    if (!full) {
+                        const long long pos = (long long)pos0 + tok;
+                        long long a = lo - j0, b = hi - j0;
+                        if (P.wl >= 0) a = max(a, pos - P.wl - j0);
+                        if (P.wr >= 0) b = min(b, pos + P.wr - j0 + 1);
+                        va = (int)min(max(a, 0ll), (long long)BN);
+                        vb = row_live ? (int)min(max(b, (long long)va), (long long)BN) : va;
+                    }
+                    auto mask = [&](uint32_t (&x32)[32], int c) {  // what the row does not see: -inf
+                        if (full) return;
+                        c += h * NC;
+                        const int c0 = min(max(va - 32 * c, 0), 32), c1 = min(max(vb - 32 * c, 0), 32);
+                        uint32_t x = bit_range(c0, c1 - c0);
+                        if (!all_there) {
+                            const int q = (32 * c) >> box_shift;
+                            uint32_t have = ((there >> q) & 1u) ? 0xffffffffu : 0u;
+                            if (box_rows == 16) have = (have & 0xffffu) | (((there >> (q + 1)) & 1u) ? 0xffff0000u : 0u);
+                            x &= have;
+                        }
+                        if (__all_sync(0xffffffffu, x == 0xffffffffu)) return;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x32[e] = (x >> e) & 1u ? x32[e] : 0xff800000u;
+                    };
+                    auto landed = [&]() {
                         tmem_ld_wait_only();
-                        ok = false;
-                        break;
-                    }
-                }
-                tmem_ld_wait_only();
 #pragma unroll
-                for (int c = 0; c < NC; ++c) tmem_pin(sv[c]);
-                bool accurate = false, shorter = false;
-                if constexpr (CAP) {
-                    float am[NC];
+                        for (int c = 0; c < NC; ++c) tmem_pin(sv[c]);
+                    };
+                    landed();
+                    // the form of the softcap: by exp where a raw score of the warp lies outside the fit's range
+                    bool accurate = false, shorter = false;
+                    if constexpr (CAP) {
+                        float am[NC];
 #pragma unroll
-                    for (int c = 0; c < NC; ++c) {
-                        am[c] = 0.f;
+                        for (int c = 0; c < NC; ++c) {
+                            am[c] = 0.f;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2)
-                            am[c] = max3f(am[c], fabsf(__uint_as_float(sv[c][e])), fabsf(__uint_as_float(sv[c][e + 1])));
-                    }
-                    float amax = fmaxf(am[0], am[1]);
-                    if constexpr (NC == 4) amax = fmaxf(amax, fmaxf(am[2], am[3]));
-                    const CapPoly cp = cap_poly(P.scale, P.softcap);
-                    accurate = __any_sync(0xffffffffu, !(amax <= cp.r_max)) || (!full && !cp.inf_ok);
-                    const CapShort cs = cap_short(P.scale, P.softcap);
-                    shorter = !accurate && __all_sync(0xffffffffu, amax <= cs.r_max) && (full || cs.inf_ok);
-                }
-                uint32_t seen[NC];  // the keys of the tile that this row sees
-                if (!full) {
-                    long long vlo = lo - j0, vhi = hi - j0;
-                    if (P.wl >= 0) vlo = max(vlo, (long long)pos - P.wl - j0);
-                    if (P.wr >= 0) vhi = min(vhi, (long long)pos + P.wr - j0 + 1);
-                    const int a = (int)min(max(vlo, 0ll), (long long)BN), b = row_live ? (int)min(max(vhi, (long long)a), (long long)BN) : a;
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) {
-                        const int c0 = min(max(a - 32 * c, 0), 32), c1 = min(max(b - 32 * c, 0), 32);
-                        seen[c] = bit_range(c0, c1 - c0);
-                    }
-                    if (there != (1u << subs) - 1u) {
-#pragma unroll
-                        for (int c = 0; c < NC; ++c) {  // boxes of 16, 32 or 64 keys
-                            const int x = 32 * c / box_rows;
-                            uint32_t have = ((there >> x) & 1u) ? 0xffffffffu : 0u;
-                            if (box_rows == 16) have = (have & 0xffffu) | (((there >> (x + 1)) & 1u) ? 0xffff0000u : 0u);
-                            seen[c] &= have;
+                            for (int e = 0; e < 32; e += 2)
+                                am[c] = max3f(am[c], fabsf(__uint_as_float(sv[c][e])), fabsf(__uint_as_float(sv[c][e + 1])));
                         }
+                        float amax = am[0];
+                        if constexpr (NC == 2) amax = fmaxf(amax, am[1]);
+                        const CapPoly cp = cap_poly(P.scale, P.softcap);
+                        accurate = __any_sync(0xffffffffu, !(amax <= cp.r_max)) || (!full && !cp.inf_ok);
+                        const CapShort cs = cap_short(P.scale, P.softcap);
+                        shorter = !accurate && __all_sync(0xffffffffu, amax <= cs.r_max) && (full || cs.inf_ok);
                     }
+                    // ---- p of the row's half, 16 bits each, and their sum
+                    uint32_t pk[NC * 16];
+                    auto p_pass = [&](auto modec) {
+                        const uint64_t nm = f2_make(-m, -m);
+                        uint64_t rs[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
 #pragma unroll
-                    for (int c = 0; c < NC; ++c)
-                        if (!__all_sync(0xffffffffu, seen[c] == 0xffffffffu)) {
+                        for (int c = 0; c < NC; ++c) {
+                            mask(sv[c], c);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) sv[c][e] = (seen[c] >> e) & 1u ? sv[c][e] : 0xff800000u;  // -inf
-                        }
-                }
-                // ---- the row's largest score, as x against its reference
-                float rm[NC];
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    rm[c] = -INFINITY;
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        rm[c] = max3f(rm[c], __uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1]));
-                }
-                float rmax = fmaxf(rm[0], rm[1]);
-                if constexpr (NC == 4) rmax = fmaxf(rmax, fmaxf(rm[2], rm[3]));
-                float xm, xm_;
-                {
-                    const uint64_t r2 = f2_make(rmax, rmax), n2 = f2_make(-m, -m);
-                    uint64_t x2;
-                    if (!CAP) x2 = to_x(M0(), r2, n2);
-                    else if (shorter) x2 = to_x(M3(), r2, n2);
-                    else if (!accurate) x2 = to_x(M1(), r2, n2);
-                    else x2 = to_x(M2(), r2, n2);
-                    f2_split(x2, xm, xm_);
-                }
-                if (rmax == -INFINITY) xm = -INFINITY;
-                const bool move = xm > kTop || (l == 0.f && xm < kTop - 10.f && xm != -INFINITY);
-                bool o_stands = NT == 2;  // the product of the tile before is complete
-                if (__any_sync(0xffffffffu, move)) {
-                    // rows that have seen nothing hold O = 0: their reference may move by any amount
-                    const float by = xm - (kTop - 8.f);
-                    const float alpha = fast_exp2(move && l > 0.f ? -by : 0.f);
-                    if (move) {
-                        m += by;
-                        l *= alpha;
-                    }
-                    if (k > 0) {
-                        if (!o_stands) {
-                            if (!wait_pv()) {
-                                ok = false;
-                                break;
+                            for (int e = 0; e < 16; ++e) {
+                                float x0, x1;
+                                f2_split(to_x(modec, f2_make(__uint_as_float(sv[c][2 * e]), __uint_as_float(sv[c][2 * e + 1])), nm), x0, x1);
+                                const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);  // 2^-inf = 0
+                                rs[e & 1] = f2_add(rs[e & 1], f2_make(p0, p1));
+                                pk[c * 16 + e] = pack2<BF16>(p0, p1);
                             }
-                            o_stands = true;
-                            tc_fence_after();
                         }
+                        float a0, a1, b0, b1;
+                        f2_split(rs[0], a0, a1);
+                        f2_split(rs[1], b0, b1);
+                        return (a0 + b0) + (a1 + b1);
+                    };
+                    const int ha = max(va, h * (BN / 2)), hb = min(vb, (h + 1) * (BN / 2));  // seen in this half
+                    float rs;
+                    bool again = false;
 #pragma unroll 1
-                        for (int c = 0; c < HD / 32; ++c) {
-                            uint32_t orr[32];
-                            tmem_ld32(tO + c * 32, orr);
-                            tmem_ld_wait(orr);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * alpha);
-                            tmem_st32(tO + c * 32, orr);
+                    while (true) {
+                        if (!CAP) rs = p_pass(M0());
+                        else if (shorter) rs = p_pass(M3());
+                        else if (!accurate) rs = p_pass(M1());
+                        else rs = p_pass(M2());
+                        if (again) break;
+                        // (the other half has loaded its scores too, which P is about to overwrite)
+                        const bool move = row_live && (!(rs < R::high) || (l == 0.f && rs < R::low && hb > ha));
+                        if (!pair_any(1 + wq, !got || move)) break;
+                        if (pair_any(1 + wq, !got)) {
+                            ok = false;
+                            break;
                         }
-                    }
-                }
-                // ---- p, chunk by chunk over S
-                auto p_pass = [&](auto modec) {
-                    const uint64_t nm = f2_make(-m, -m);
-                    uint64_t rs[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
+                        again = true;
+                        float rmax = -INFINITY;
+#pragma unroll 1
+                        for (int c = 0; c < NC; ++c) {
+                            uint32_t x[32];
+                            tmem_ld32(tS + (h * NC + c) * 32, x);
+                            tmem_ld_wait(x);
+                            mask(x, c);
+                            float am[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                    for (int c = 0; c < NC; ++c) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            float x0, x1;
-                            f2_split(to_x(modec, f2_make(__uint_as_float(sv[c][2 * e]), __uint_as_float(sv[c][2 * e + 1])), nm), x0, x1);
-                            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);  // 2^-inf = 0
-                            rs[e & 1] = f2_add(rs[e & 1], f2_make(p0, p1));
-                            pk[e] = pack2<BF16>(p0, p1);
+                            for (int e = 0; e < 32; e += 2)
+                                am[(e >> 1) & 1] = max3f(am[(e >> 1) & 1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                            rmax = max3f(rmax, am[0], am[1]);
                         }
-                        tmem_st16(tS + c * 16, pk);
-                    }
-                    float a0, a1, b0, b1;
-                    f2_split(rs[0], a0, a1);
-                    f2_split(rs[1], b0, b1);
-                    l += (a0 + b0) + (a1 + b1);
-                };
-                if (!CAP) p_pass(M0());
-                else if (shorter) p_pass(M3());
-                else if (!accurate) p_pass(M1());
-                else p_pass(M2());
-                // ---- a tile that is not whole: is all of V finite that some row does not see
-                bool by_row = false;
-                if (!full) {
-                    const int i = my.t0 + k - tile0;  // its place in the part
-                    const unsigned gv = g0 + 2 * i + 1, vn = g0 / 2 + i;
-                    if (!wait(C::V_OK + vn % NS, (vn / NS) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint8_t* vt = smem + C::kRingOff + (gv % NS) * C::kTileBytes;
-                    by_row = *static_cast<volatile int*>(&bad_v[vn % NS]) != 0;
-                    if (by_row) {
-                        tmem_st_wait();
-                        if (!o_stands && k > 0) {
-                            if (!wait_pv()) {
+                        rmax = fmaxf(rmax, exchange(rmax));
+                        const float l_other = exchange(l);
+                        float xm, xm_;  // (by exp under a softcap, so that both halves have the same)
+                        f2_split(CAP ? to_x(M2(), f2_make(rmax, rmax), f2_make(-m, -m)) : to_x(M0(), f2_make(rmax, rmax), f2_make(-m, -m)),
+                                 xm, xm_);
+                        const bool fresh = l == 0.f && l_other == 0.f;
+                        const bool moves = rmax != -INFINITY && (xm > R::x_high || (fresh && xm < R::x_low));
+                        const float by = xm - R::put;
+                        // (a row that has seen nothing holds O = 0: its reference may move by any amount)
+                        const float alpha = fast_exp2(moves && !fresh ? -by : 0.f);
+                        if (moves) {
+                            m += by;
+                            l *= alpha;
+                        }
+                        if (!first) {
+                            got = wait_pv();
+                            if (pair_any(1 + wq, !got)) {
                                 ok = false;
                                 break;
                             }
                             tc_fence_after();
-                        }
 #pragma unroll 1
-                        for (int c = 0; c < HD / 32; ++c) {
-                            uint32_t orr[32];
-                            if (k > 0) {
+                            for (int c = 0; c < kCols / 32; ++c) {
+                                uint32_t orr[32];
                                 tmem_ld32(tO + c * 32, orr);
                                 tmem_ld_wait(orr);
-                            } else {
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) orr[e] = 0u;
+                                for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * alpha);
+                                tmem_st32(tO + c * 32, orr);
                             }
-                            const uint8_t* col = vt + (c >> 1) * (BN * 128);
+                        }
+#pragma unroll
+                        for (int c = 0; c < NC; ++c) tmem_ld32(tS + (h * NC + c) * 32, sv[c]);
+                        landed();
+                    }
+                    if (again && ok) pair_any(1 + wq, false);  // (both have loaded their scores once more)
+                    if (!ok) break;
+                    l += rs;
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) tmem_st16(tS + (h * NC + c) * 16, pk + c * 16);
+                    // ---- a tile that is not whole: is all of V finite that some row does not see
+                    bool by_row = false;
+                    if (!full) {
+                        const unsigned vn = v0 + i, gv = 2 * vn + 1;
+                        got = wait(C::V_OK + vn % NS, (vn / NS) & 1);
+                        const uint8_t* vt = smem + C::kRingOff + (gv % NS) * C::kTileBytes;
+                        by_row = got && *static_cast<volatile int*>(&bad_v[vn % NS]) != 0;
+                        if (pair_any(1 + wq, !got || by_row)) {
+                            tmem_st_wait();
+                            tc_fence_before();
+                            got = got && (first || wait_pv());
+                            if (pair_any(1 + wq, !got)) {  // (and both halves of P are there)
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
 #pragma unroll 1
-                            for (int j = 0; j < BN; ++j) {
-                                uint32_t pw;
-                                asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(pw) : "r"(tS + (j >> 1)));
-                                asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(pw)::"memory");
-                                float p0, p1;
-                                if constexpr (BF16) {
-                                    p0 = __uint_as_float(pw << 16);
-                                    p1 = __uint_as_float(pw & 0xffff0000u);
+                            for (int c = 0; c < kCols / 32; ++c) {
+                                uint32_t orr[32];
+                                if (!first) {
+                                    tmem_ld32(tO + c * 32, orr);
+                                    tmem_ld_wait(orr);
                                 } else {
-                                    const float2 f = h2_to_f2(pw);
-                                    p0 = f.x, p1 = f.y;
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) orr[e] = 0u;
                                 }
-                                const float pj = (j & 1) ? p1 : p0;
-                                uint32_t sw = 0;
+                                const int col = h * kCols + c * 32;  // of O
+                                const uint8_t* vcol = vt + (col >> 6) * (BN * 128);
+#pragma unroll 1
+                                for (int j = 0; j < BN; ++j) {
+                                    uint32_t pw;
+                                    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(pw) : "r"(tS + (j >> 1)));
+                                    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(pw)::"memory");
+                                    float p0, p1;
+                                    if constexpr (BF16) {
+                                        p0 = __uint_as_float(pw << 16);
+                                        p1 = __uint_as_float(pw & 0xffff0000u);
+                                    } else {
+                                        const float2 f = h2_to_f2(pw);
+                                        p0 = f.x, p1 = f.y;
+                                    }
+                                    const float pj = (j & 1) ? p1 : p0;
+                                    const bool see = j >= va && j < vb && ((there >> (j >> box_shift)) & 1u);
 #pragma unroll
-                                for (int x = 0; x < NC; ++x) sw = (j >> 5) == x ? seen[x] : sw;
-                                const bool see = (sw >> (j & 31)) & 1u;
+                                    for (int q = 0; q < 4; ++q) {
+                                        const uint4 v = *reinterpret_cast<const uint4*>(vcol + j * 128 + (((((col >> 5) & 1) * 4 + q) ^ (j & 7)) << 4));
+                                        const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    const uint4 v = *reinterpret_cast<const uint4*>(col + j * 128 + ((((c & 1) * 4 + q) ^ (j & 7)) << 4));
-                                    const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e) {
-                                        float v0, v1;
-                                        if constexpr (BF16) {
-                                            v0 = __uint_as_float(vw[e] << 16);
-                                            v1 = __uint_as_float(vw[e] & 0xffff0000u);
-                                        } else {
-                                            const float2 f = h2_to_f2(vw[e]);
-                                            v0 = f.x, v1 = f.y;
-                                        }
-                                        uint32_t& o0 = orr[8 * q + 2 * e];
-                                        uint32_t& o1 = orr[8 * q + 2 * e + 1];
-                                        if (see) {
-                                            o0 = __float_as_uint(fmaf(pj, v0, __uint_as_float(o0)));
-                                            o1 = __float_as_uint(fmaf(pj, v1, __uint_as_float(o1)));
+                                        for (int e = 0; e < 4; ++e) {
+                                            float v0, v1;
+                                            if constexpr (BF16) {
+                                                v0 = __uint_as_float(vw[e] << 16);
+                                                v1 = __uint_as_float(vw[e] & 0xffff0000u);
+                                            } else {
+                                                const float2 f = h2_to_f2(vw[e]);
+                                                v0 = f.x, v1 = f.y;
+                                            }
+                                            uint32_t& o0 = orr[8 * q + 2 * e];
+                                            uint32_t& o1 = orr[8 * q + 2 * e + 1];
+                                            if (see) {
+                                                o0 = __float_as_uint(fmaf(pj, v0, __uint_as_float(o0)));
+                                                o1 = __float_as_uint(fmaf(pj, v1, __uint_as_float(o1)));
+                                            }
                                         }
                                     }
                                 }
+                                tmem_st32(tO + c * 32, orr);
                             }
-                            tmem_st32(tO + c * 32, orr);
                         }
                     }
+                    if (warp == 0 && lane == 0) *static_cast<volatile int*>(&skip_pv[u][count & 1]) = by_row ? 1 : 0;
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(BAR(C::P_FULL + (NT == 2 ? u : (count & 1))));
+                    if (u) m2[1] = m, l2[1] = l, ++sc[1];
+                    else m2[0] = m, l2[0] = l, ++sc[0];
                 }
-                if (wq == 0 && lane == 0) *static_cast<volatile int*>(&skip_pv[u][sc & 1]) = by_row ? 1 : 0;
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(BAR(C::P_FULL + (NT == 2 ? u : (sc & 1))));
-                    if constexpr (NT == 2) atomicAdd(&done_count[u], 1);
-                }
-                ++sc;
             }
             // ------------------------------------------------------------ epilogue
-            const bool have_o = ok && my.n > 0 && wait(C::O_DONE + u, act & 1);
-            if (my.n > 0) ++act;
-            if (!ok || (my.n > 0 && !have_o)) {
+            bool got = ok;
+            for (int u = 0; u < NT; ++u)
+                if ((u ? st.n[1] : st.n[0]) > 0) {
+                    got = got && wait(C::O_DONE + u, (u ? act[1] : act[0]) & 1);
+                    if (u) ++act[1];
+                    else ++act[0];
+                }
+            if (pair_any(1 + wq, !got)) {
                 ok = false;
                 break;
             }
-            if (have_o) tc_fence_after();
-            const bool whole = p.whole();
-            const bool none = l == 0.f, o32 = (reinterpret_cast<uintptr_t>(P.o) & 31u) == 0;
-            const float inv = none ? 0.f : 1.f / l;
+            tc_fence_after();
+            const bool whole = p.whole(), o32 = (reinterpret_cast<uintptr_t>(P.o) & 31u) == 0;
             const int slot = 2 * blockIdx.x + (p.begin == 0 ? 1 : 0), rows = NT * kM;
-            const long long orow = (long long)(p.it.row + u * tm + tok);
-            uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.o) + (orow * P.H + p.h * P.G + head) * HD);
-            float4* part = reinterpret_cast<float4*>(part_o(plan, slot, rows, HD) + (size_t)(u * kM + r) * HD);
 #pragma unroll 1
-            for (int c = 0; c < HD / 32; ++c) {
-                uint32_t orr[32];
-                if (have_o) {
-                    tmem_ld32(tO + c * 32, orr);
-                    tmem_ld_wait(orr);
-                }
-                if (row_live && whole) {
-                    uint32_t pk[2][8];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        pk[e >> 3][e & 7] = none ? 0u : pack2<BF16>(__uint_as_float(orr[2 * e]) * inv, __uint_as_float(orr[2 * e + 1]) * inv);
-                    // (a row's sector at a time, where O is aligned to them)
-                    if (o32) {
-                        store_32(out + c * 4, pk[0]);
-                        store_32(out + c * 4 + 2, pk[1]);
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            out[c * 4 + q] = make_uint4(pk[q >> 1][4 * (q & 1)], pk[q >> 1][4 * (q & 1) + 1], pk[q >> 1][4 * (q & 1) + 2],
-                                                        pk[q >> 1][4 * (q & 1) + 3]);
-                    }
-                } else if (row_live && !none) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const uint32_t f[8] = {orr[8 * q], orr[8 * q + 1], orr[8 * q + 2], orr[8 * q + 3],
-                                               orr[8 * q + 4], orr[8 * q + 5], orr[8 * q + 6], orr[8 * q + 7]};
-                        store_32(part + c * 8 + q * 2, f);
+            for (int u = 0; u < (st.solo ? 1 : NT); ++u) {
+                const int ntok = u ? st.ntok[1] : st.ntok[0];
+                if (ntok == 0) continue;
+                const bool have_a = (u ? st.n[1] : st.n[0]) > 0, have_b = st.solo && st.n[1] > 0;
+                float m = u ? m2[1] : m2[0], l = u ? l2[1] : l2[0];
+                l += exchange(l);
+                // (solo) the other tile's share of the same row
+                float fa = 1.f, fb = 0.f;
+                if (have_b) {
+                    const float lb = l2[1] + exchange(l2[1]);
+                    const float ma = l != 0.f ? m : -INFINITY, mb = lb != 0.f ? m2[1] : -INFINITY;
+                    const float top = fmaxf(ma, mb);
+                    if (top != -INFINITY) {
+                        fa = l != 0.f ? fast_exp2(ma - top) : 0.f;
+                        fb = lb != 0.f ? fast_exp2(mb - top) : 0.f;
+                        m = top;
+                        l = (l != 0.f ? fa * l : 0.f) + (lb != 0.f ? fb * lb : 0.f);
                     }
                 }
-                __syncwarp();
+                const bool none = l == 0.f, row_live = tok < ntok;
+                const float inv = none ? 0.f : 1.f / l, ga = whole ? fa * inv : fa, gb = whole ? fb * inv : fb;
+                const long long orow = (long long)(p.it.row + u * tm + tok);
+                uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.o) + (orow * P.H + p.h * P.G + head) * HD + h * kCols);
+                float4* part = reinterpret_cast<float4*>(part_o(plan, slot, rows, HD) + (size_t)(u * kM + r) * HD + h * kCols);
+#pragma unroll 1
+                for (int c = 0; c < kCols / 32; ++c) {
+                    const uint32_t tO = tbase + 256 + u * HD + h * kCols + lane_off + c * 32;
+                    uint32_t orr[32];
+                    if (have_a) {
+                        tmem_ld32(tO, orr);
+                        tmem_ld_wait(orr);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) orr[e] = none || fa == 0.f ? 0u : __float_as_uint(__uint_as_float(orr[e]) * ga);
+                    if (have_b) {
+                        uint32_t ob[32];
+                        tmem_ld32(tO + HD, ob);
+                        tmem_ld_wait(ob);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!none && fb != 0.f) orr[e] = __float_as_uint(fmaf(__uint_as_float(ob[e]), gb, __uint_as_float(orr[e])));
+                    }
+                    if (row_live && whole) {
+                        uint32_t pk[2][8];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) pk[e >> 3][e & 7] = pack2<BF16>(__uint_as_float(orr[2 * e]), __uint_as_float(orr[2 * e + 1]));
+                        // (a row's sector at a time, where O is aligned to them)
+                        if (o32) {
+                            store_32(out + c * 4, pk[0]);
+                            store_32(out + c * 4 + 2, pk[1]);
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                out[c * 4 + q] = make_uint4(pk[q >> 1][4 * (q & 1)], pk[q >> 1][4 * (q & 1) + 1],
+                                                            pk[q >> 1][4 * (q & 1) + 2], pk[q >> 1][4 * (q & 1) + 3]);
+                        }
+                    } else if (row_live && !none) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t f[8] = {orr[8 * q], orr[8 * q + 1], orr[8 * q + 2], orr[8 * q + 3],
+                                                   orr[8 * q + 4], orr[8 * q + 5], orr[8 * q + 6], orr[8 * q + 7]};
+                            store_32(part + c * 8 + q * 2, f);
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (row_live && h == 0) {
+                    if (!whole) part_ml(plan, slot, rows)[u * kM + r] = make_float2(m, l);
+                    else if (P.lse)
+                        P.lse[(long long)(p.h * P.G + head) * P.total + orow] = none ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+                }
             }
-            // O is in registers or out: the next part's first product may overwrite it
-            if (have_o) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(BAR(C::O_EMPTY + u));
-            }
-            if (row_live) {
-                if (!whole) part_ml(plan, slot, rows)[u * kM + r] = make_float2(m, l);
-                else if (P.lse)
-                    P.lse[(long long)(p.h * P.G + head) * P.total + orow] = none ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-            }
+            // O is in registers or out: the next part's first products may overwrite it
+            tc_fence_before();
+            __syncwarp();
+            for (int u = 0; u < NT; ++u)
+                if (lane == 0 && (u ? st.n[1] : st.n[0]) > 0) mbar_arrive(BAR(C::O_EMPTY + u));
         }
     }
     tc_fence_before();
@@ -1100,7 +1168,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
 }
 
 // ------------------------------------------------------------------- the merge
-// Joins the partial rows of the items that stretches cut, a warp to a row, in the order of the stretches.
+// Joins the partial rows of the items that stretches cut, a warp to a row or several, in a fixed order.
 constexpr int kMergeCtas = 8 * kPrefillCtas;
 template <int HD>
 __global__ void __launch_bounds__(256) paged_prefill_merge_kernel(const PagedParams P, const int bf16) {
@@ -1109,6 +1177,7 @@ __global__ void __launch_bounds__(256) paged_prefill_merge_kernel(const PagedPar
     __shared__ int4 split_s[kPrefillCtas];
     __shared__ int before_s[kPrefillCtas];  // rows of the items that earlier stretches cut
     __shared__ int sums[8];
+    __shared__ float acc_s[8][HD];
     const int tm = kM / P.G, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Plan plan = plan_of(P, NT * tm);
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1129,10 +1198,16 @@ __global__ void __launch_bounds__(256) paged_prefill_merge_kernel(const PagedPar
     }
     if (threadIdx.x < kPrefillCtas) split_s[threadIdx.x] = mine, before_s[threadIdx.x] = incl - count;
     __syncthreads();
-    for (int x = blockIdx.x * 8 + warp; x < all; x += kMergeCtas * 8) {
-        const int c = warp_last_le(kPrefillCtas, x, [&](int i) { return (long long)before_s[i]; });
+    // warps to a row, which take its parts in turn: as many as there are rows few
+    int wpr = 1;
+    while (wpr < 8 && all * wpr * 2 <= kMergeCtas * 8) wpr *= 2;
+    const int rpc = 8 / wpr, sub = warp % wpr;  // rows of a CTA at a time
+    for (int x0 = blockIdx.x * rpc; x0 < all; x0 += kMergeCtas * rpc) {
+        const int x = x0 + warp / wpr;
+        const bool live = x < all;
+        const int c = warp_last_le(kPrefillCtas, live ? x : x0, [&](int i) { return (long long)before_s[i]; });
         const int4 it = split_s[c];
-        const int y = x - before_s[c], n = it.w;
+        const int y = (live ? x : x0) - before_s[c], n = it.w;
         const int t = y / P.G, head = y - t * P.G, u = t / tm, r = u * kM + (t - u * tm) * P.G + head;
         auto slot = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); };
         float M = -INFINITY, L = 0.f;
@@ -1156,20 +1231,38 @@ __global__ void __launch_bounds__(256) paged_prefill_merge_kernel(const PagedPar
             for (int q = 0; q < kPer; ++q) acc[q] *= alpha;
             const int m = min(32, n - base);
 #pragma unroll 4
-            for (int j = 0; j < m; ++j) {
+            for (int j = sub; j < m; j += wpr) {
                 const float* src = part_o(plan, slot(base + j), rows, HD) + (size_t)r * HD + lane * kPer;
                 const float fj = __shfl_sync(0xffffffffu, f, j);
                 const bool has = (use >> j) & 1u;
+                float v[kPer];
+                if constexpr (kPer == 2) {
+                    const float2 w = *reinterpret_cast<const float2*>(src);
+                    v[0] = w.x, v[1] = w.y;
+                } else {
 #pragma unroll
-                for (int q = 0; q < kPer; q += 2) {
-                    const float2 v = *reinterpret_cast<const float2*>(src + q);
-                    acc[q] = has ? fmaf(fj, v.x, acc[q]) : acc[q];
-                    acc[q + 1] = has ? fmaf(fj, v.y, acc[q + 1]) : acc[q + 1];
+                    for (int q = 0; q < kPer; q += 4) {
+                        const float4 w = *reinterpret_cast<const float4*>(src + q);
+                        v[q] = w.x, v[q + 1] = w.y, v[q + 2] = w.z, v[q + 3] = w.w;
+                    }
                 }
+#pragma unroll
+                for (int q = 0; q < kPer; ++q) acc[q] = has ? fmaf(fj, v[q], acc[q]) : acc[q];
             }
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        if (wpr > 1) {
+            __syncthreads();  // (the sums of the rows before have been read)
+#pragma unroll
+            for (int q = 0; q < kPer; ++q) acc_s[warp][lane * kPer + q] = acc[q];
+            __syncthreads();
+            for (int i = 1; i < wpr; ++i)
+                if (sub == 0)
+#pragma unroll
+                    for (int q = 0; q < kPer; ++q) acc[q] += acc_s[warp + i][lane * kPer + q];
+        }
+        if (!live || sub != 0) continue;
         const bool none = M == -INFINITY;
         const float inv = none ? 0.f : 1.f / L;
         const long long orow = it.x + t;
