@@ -35,17 +35,13 @@ constexpr int kItemCost = 2;
 // The least that a stretch holds.
 constexpr int kMinShare = 4;
 
-// p = 2^x, x relative to a row's reference, which starts at `first` and stays while the sum over half a tile's p
-// is below `high` (so that every p is) and, in the first half of which the row sees anything, not below `low` (so
-// that its largest p is at least low / 64); a usual tile then needs no maximum.  Else the row's largest x
-// in the tile is taken and put at `put` if it is above x_high or, in a row that has seen nothing, below x_low, and
-// p formed again.  fp16 p reach up to 2^15 and have no exponents to lose below: the largest stays at 2^-2 or
-// more.  bf16 ones, whose exponent is fp32's, stay below 1, so that P V passes fp32's range no sooner than
-// the sum of V does.
+// p = 2^(x - ref): a row's reference is moved when its largest p would pass 2^top, or, before it has
+// seen anything, when it would stay below 2^(top - 10); it is then put at 2^(top - 8).  fp16 p have room up
+// to 2^8 and no more exponents to lose below; bf16 ones stay at most 1, so that P V passes fp32's range
+// no sooner than the sum of V does.
 template <bool BF16>
 struct PRange {
-    static constexpr float first = BF16 ? 24.f : -4.f, high = BF16 ? 1.f : 0x1p15f, low = BF16 ? 0x1p-60f : 0x1p4f,
-                           x_high = BF16 ? -7.f : 8.f, x_low = BF16 ? -60.f : -2.f, put = BF16 ? -24.f : 4.f;
+    static constexpr float top = BF16 ? 0.f : 8.f;
 };
 
 template <int HD, bool F8>
@@ -66,14 +62,21 @@ struct Cfg {
     // barriers, in this order
     static constexpr int Q_FULL = 0, Q_EMPTY = 2, S_FULL = 4, P_FULL = 6, O_DONE = 8, O_EMPTY = 10, PV_DONE = 12,
                          MMA_DONE = 14, FULL = 15, EMPTY = FULL + kStages, V_OK = EMPTY + kStages, RAW_FULL = V_OK + kStages,
-                         RAW_EMPTY = RAW_FULL + kRaw, kBars = RAW_EMPTY + kRaw;
-    static constexpr int kBytes = kBarOff + kBars * 8 + 16 + 1024;  // (1024: alignment)
-    static_assert(kBytes + 1280 <= 227 * 1024, "shared memory");    // (1280: the kernel's own variables)
-    // Warpgroups: two of softmax, one that loads and issues, over 8-bit pools one that widens, with
-    // registers shared out from what the launch holds.
-    static constexpr int kThreads = F8 ? 512 : 384;
-    static constexpr int kRegsSoftmax = 168, kRegsLoad = 56, kRegsWide = 120;
-    static_assert((2 * kRegsSoftmax + kRegsLoad + kRegsWide) * 128 <= 512 * 128, "register split exceeds the launch");
+                         RAW_EMPTY = RAW_FULL + kRaw, Q_WIDE = RAW_EMPTY + kRaw, kBars = Q_WIDE + (F8 ? 2 : 0);
+    // (8-bit pools) exponents that the rows of Q are held by, of two parts and both tiles
+    static constexpr int kQexpOff = kBarOff + kBars * 8 + 16, kQexpBytes = F8 ? 2 * 2 * kM * 2 : 0;
+    static constexpr int kBytes = kQexpOff + kQexpBytes + 1024;  // (1024: alignment)
+    static_assert(kBytes + 256 <= 227 * 1024, "shared memory");
+    // Warpgroups: softmax of tile A; of tile B (at hd 256 the widening warps instead); loads and MMA
+    // issue; the widening warps beside two tiles.
+    static constexpr bool kWideB = F8 && NT == 1, kWide4 = F8 && NT == 2;
+    static constexpr int kThreads = kWide4 ? 512 : 384;
+    static constexpr int kWide0 = kWide4 ? 12 : 4;  // first widening warp
+    // registers: shares of what the launch holds (512 x 128, 384 x 168)
+    static constexpr int kRegsSoftmax = kWide4 ? 200 : 216, kRegsLoad = kWide4 ? 48 : 72, kRegsWide = kWide4 ? 64 : 120;
+    static constexpr int kRegsB = NT == 2 ? kRegsSoftmax : F8 ? kRegsWide : 168;
+    static_assert((kRegsSoftmax + kRegsB + kRegsLoad + (kWide4 ? kRegsWide : 0)) * 128 <= kThreads * (kWide4 ? 128 : 168),
+                  "register split exceeds the launch");
 };
 
 // ------------------------------------------------------------------- the plan
@@ -280,41 +283,23 @@ __device__ __forceinline__ bool next_part(const Plan& plan, Walk& w, Part& p) {
     return false;
 }
 
-// What the query tiles of a part see.  Each has its rows (tokens from `pos` on) and sees key tiles [t0, t0 + n)
-// of the part.  An item with rows for one tile only is computed by both all the same (`solo`): the second
-// takes every other key tile of the same rows, and their results are joined at the end.
-struct Sight {
-    int t0[2], n[2], ntok[2];
-    bool solo;
-    __device__ bool has(int u, int t) const {
-        const int a = u ? t0[1] : t0[0], m = u ? n[1] : n[0];
-        return solo ? t >= a && ((t - a) & 1) == 0 && (t - a) >> 1 < m : t >= a && t < a + m;
-    }
-    __device__ int index(int u, int t) const { return (t - (u ? t0[1] : t0[0])) >> (solo ? 1 : 0); }
+// Query tile u of a part: its tokens, and the tiles [t0, t0 + n) of the part that any of its rows sees.
+struct Tiles {
+    int ntok, pos, t0, n;
 };
-template <int NT, int BN>
-__device__ __forceinline__ Sight sight_of(const PagedParams& P, const Part& p, int tm) {
-    Sight s;
-    s.solo = NT == 2 && p.it.ntok <= tm;
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        s.ntok[u] = u < NT ? min(max(p.it.ntok - u * tm, 0), tm) : 0;
-        s.t0[u] = s.n[u] = 0;
-        if (s.ntok[u] > 0) {
-            int lo, hi;
-            const int pos = p.it.pos + u * tm;
-            key_range(P.wl, P.wr, p.it.len, pos, pos + s.ntok[u] - 1, &lo, &hi);
-            const int a = max(lo / BN, p.it.t0 + p.begin), b = min((hi + BN - 1) / BN, p.it.t0 + p.end);
-            if (hi > lo && b > a) s.t0[u] = a, s.n[u] = b - a;
-        }
+template <int BN>
+__device__ __forceinline__ Tiles tiles_of(const PagedParams& P, const Part& p, int u, int tm) {
+    Tiles t;
+    t.ntok = min(max(p.it.ntok - u * tm, 0), tm);
+    t.pos = p.it.pos + u * tm;
+    t.t0 = t.n = 0;
+    if (t.ntok > 0) {
+        int lo, hi;
+        key_range(P.wl, P.wr, p.it.len, t.pos, t.pos + t.ntok - 1, &lo, &hi);
+        const int a = max(lo / BN, p.it.t0 + p.begin), b = min((hi + BN - 1) / BN, p.it.t0 + p.end);
+        if (hi > lo && b > a) t.t0 = a, t.n = b - a;
     }
-    if (s.solo) {
-        s.ntok[1] = s.ntok[0];
-        s.t0[1] = s.t0[0] + 1;
-        s.n[1] = s.n[0] / 2;
-        s.n[0] -= s.n[1];
-    }
-    return s;
+    return t;
 }
 
 __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
@@ -324,19 +309,50 @@ __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, ui
         : "memory");
 }
 
-// four codes as two words of two 16-bit values, times s in fp32, rounded once
-template <bool BF16, bool E4M3>
-__device__ __forceinline__ void widen4(uint32_t c, float s, uint32_t& w0, uint32_t& w1) {
-    uint32_t h0, h1;
+// ------------------------------------------------------------------ 8-bit pools
+// The products run in fp16, whose values hold both types' codes exactly.  Q becomes fp16 by a power of two for each
+// row that brings its largest element to 2^13 (exact for all that matters: 2^-38 of that element is kept).  A
+// key's scale multiplies its scores in fp32.  A value's enters its fp16 element as vs / vref, vref a power of two
+// beside the part's first usable scale, and O is multiplied by vref at the end: exact where the scale is a power
+// of two, else off by half a step of fp16 for the ratio and for the product.  A tile with a ratio outside
+// [2^-14, 2^7] (e5m2, whose codes reach fp16's end: [2^-14, 1]), zero but for, keeps its bare codes, and the softmax
+// warps make its product in fp32, as that of a tile with values that are not finite.
+struct VRef {
+    float ref, inv, most;  // vref, its inverse, and the largest ratio
+};
+// of the tile whose boxes' scales the first `subs` lanes hold: whether one is usable, and vref by it
+__device__ __forceinline__ bool vref_of(float vs, int subs, bool e4m3, VRef& v) {
+    const int lane = threadIdx.x & 31;
+    const float a = fabsf(vs);
+    const unsigned fit = __ballot_sync(0xffffffffu, lane < subs && a >= 0x1p-100f && a <= 0x1p90f);
+    v.ref = v.inv = 1.f;
+    v.most = e4m3 ? 0x1p7f : 1.f;
+    if (!fit) return false;
+    const float first = __shfl_sync(0xffffffffu, a, __ffs(fit) - 1);
+    const int e = (int)(__float_as_uint(first) >> 23) - 127 + (e4m3 ? 4 : 8);  // nominal ratios of 2^-4, 2^-8 .. 2 times that
+    v.ref = __uint_as_float((uint32_t)(e + 127) << 23);
+    v.inv = __uint_as_float((uint32_t)(127 - e) << 23);
+    return true;
+}
+// lanes (of the first `subs`) whose box's values do not fit in fp16 beside vref
+__device__ __forceinline__ unsigned odd_scales(float vs, int subs, const VRef& v) {
+    const float r = fabsf(vs * v.inv);
+    return __ballot_sync(0xffffffffu, (int)(threadIdx.x & 31) < subs && !(r == 0.f || (r >= 0x1p-14f && r <= v.most)));
+}
+// four codes as two words of two halves
+template <bool E4M3>
+__device__ __forceinline__ void widen4(uint32_t c, uint32_t& w0, uint32_t& w1) {
     if constexpr (E4M3)
         asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
-            : "=r"(h0), "=r"(h1)
+            : "=r"(w0), "=r"(w1)
             : "r"(c));
     else
-        h0 = __byte_perm(c, 0, 0x1404), h1 = __byte_perm(c, 0, 0x3424);  // an e5m2 code is its fp16's upper byte
-    const float2 a = h2_to_f2(h0), b = h2_to_f2(h1);
-    w0 = pack2<BF16>(a.x * s, a.y * s);
-    w1 = pack2<BF16>(b.x * s, b.y * s);
+        w0 = __byte_perm(c, 0, 0x1404), w1 = __byte_perm(c, 0, 0x3424);  // an e5m2 code is its fp16's upper byte
+}
+__device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
 
 // n bits from bit i on (i + n <= 32)
@@ -352,25 +368,13 @@ __device__ __forceinline__ void store_32(void* at, const uint32_t (&v)[8]) {
                  : "memory");
 }
 
-// Of two warps that share rows: whether either says so.  Both come here equally often whatever fails.
-__device__ __forceinline__ bool pair_any(int id, bool x) {
-    int r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.or.pred q, %2, 64, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
-                 : "=r"(r)
-                 : "r"((int)x), "r"(id)
-                 : "memory");
-    return r != 0;
-}
-
 // ------------------------------------------------------------------ the kernel
-// Roles (warps): softmax (0-7); loads (8); MMA issue of tile u (9 + u); looking V over (11); over 8-bit pools,
-// widening (12-15).  All eight softmax warps work on one tile at a time, A(n), B(n), A(n+1), ..., while the
-// tensor cores make the other tile's P V and next S: warps w and w + 4 share 32 rows and take one half of the
-// keys each (one warp a scheduler reaches two thirds of the rates of exp2, fma and conversions that two do).
-// They know a row's reference alike; each sums its own half.  Each tile has one S buffer, and a completed S(n),
-// issued after P(n-1) V(n-1), also means that O stands still.  With one tile (hd 256) there are two S buffers
-// instead, S(n+1) is issued before P(n) V(n), and the softmax may be done with P(n+1) before that
-// product is issued: S, P and the product have a barrier for each buffer.
+// Roles (warps): softmax of tile u, one thread to a row (0-3, 4-7); loads (8); MMA issue of tile u (9 + u); looking
+// V over (11); over 8-bit pools, widening (Cfg::kWide0 ...).  Two tiles take turns as in the dense forward: one tile's
+// softmax runs while the tensor cores work on the other's P V and next S; each has one S buffer, and a
+// completed S(n), issued after P(n-1) V(n-1), also means that O stands still.  With one tile (hd 256)
+// there are two S buffers instead, S(n+1) is issued before P(n) V(n), and the softmax may be done with P(n+1)
+// before that product is issued: S, P and the product have a barrier for each buffer.
 //
 // What a row does not see has no effect on it.  Warp 11 looks over each tile of V before its product is
 // issued: rows of V that no row of the item sees (behind the sequence, in a page that does not exist) become
@@ -383,6 +387,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                          const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
     using C = Cfg<HD, F8>;
     constexpr int NT = C::NT, BN = C::BN, NS = C::kStages;
+    constexpr bool MB = BF16 && !F8;  // the products' type is bfloat16
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -391,7 +396,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
     const uint32_t bar0 = smem_u32(bars);
     auto BAR = [&](int i) { return bar0 + 8u * (uint32_t)i; };
     __shared__ int abort_flag;
-    __shared__ float half_s[2][kM];  // what two warps with the same rows tell each other
+    __shared__ int done_count[2];  // warps that have finished a softmax of tile u
     __shared__ int bad_v[NS];      // of V tile n, at n mod NS, as its barrier: a value that not every row sees is not finite
     __shared__ int skip_pv[2][2];  // by the parity of the tile: the softmax warps make this product
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -401,14 +406,15 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
         for (int i = 0; i < C::kBars; ++i) {
             uint32_t n = 1;
             if ((i >= C::P_FULL && i < C::P_FULL + 2) || (i >= C::O_EMPTY && i < C::O_EMPTY + 2))
-                n = 8;  // softmax warps
+                n = 4;  // softmax warps of a tile
             if ((i >= C::EMPTY && i < C::EMPTY + NS) || i == C::MMA_DONE) n = NT;  // MMA issuers
             if (F8 && ((i >= C::FULL && i < C::FULL + NS) || (i >= C::RAW_EMPTY && i < C::RAW_EMPTY + C::kRaw)))
                 n = 4;  // widening warps
+            if (F8 && i >= C::Q_WIDE && i < C::Q_WIDE + 2) n = 4;
             mbar_init(BAR(i), n);
         }
         abort_flag = 0;
-        for (int u = 0; u < 2; ++u) skip_pv[u][0] = skip_pv[u][1] = 0;
+        for (int u = 0; u < 2; ++u) done_count[u] = 0, skip_pv[u][0] = skip_pv[u][1] = 0;
         fence_barrier_init();
     }
     if (warp == 9) {
@@ -436,8 +442,25 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
         key_range(P.wl, P.wr, p.it.len, p.it.pos, p.it.pos + p.it.ntok - 1, &lo, &hi);
     };
 
+    // (8-bit pools) the scales of a page's keys and values for the part's KV head; and vref of a part
+    auto scales_at = [&](const Part& p, int pg) {
+        if (!F8 || !page_ok(pg)) return make_float2(0.f, 0.f);
+        const long long i = (long long)pg * P.Hkv + p.h;
+        return make_float2(__ldg(P.k_scale + i), __ldg(P.v_scale + i));
+    };
+    auto first_vref = [&](const Part& p, int tile0, int n, int lo, int hi) {
+        VRef v = {1.f, 1.f, 1.f};
+        if constexpr (F8) {
+            const int sub = lane < subs ? lane : 0;
+#pragma unroll 1
+            for (int i = 0; i < n; ++i)
+                if (vref_of(scales_at(p, box_page(p, (tile0 + i) * BN + sub * box_rows, lo, hi)).y, subs, e4m3 != 0, v)) break;
+        }
+        return v;
+    };
+
     if (warp >= 8 && warp < 12) {
-        if constexpr (F8) regs_dec<C::kRegsLoad>();
+        regs_dec<C::kRegsLoad>();
         if (warp == 8) {
             // ------------------------------------------------------------ loads
             if (elect_one()) {
@@ -460,11 +483,12 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
             while (ok && next_part(plan, w, p)) {
                 int lo, hi;
                 key_span(p, lo, hi);
-                const Sight st = sight_of<NT, BN>(P, p, tm);
+                Tiles tu[2];
+                for (int u = 0; u < NT; ++u) tu[u] = tiles_of<BN>(P, p, u, tm);
                 const int tile0 = p.it.t0 + p.begin, n = p.end - p.begin;
                 int pg = n > 0 && col < kCols ? box_page(p, tile0 * BN + sub * box_rows, lo, hi) : -1;
                 for (int u = 0; ok && u < NT; ++u) {
-                    if ((u ? st.n[1] : st.n[0]) == 0) continue;
+                    if (tu[u].n == 0) continue;
                     if (qn[u] > 0 && !warp_wait(BAR(C::Q_EMPTY + u), (qn[u] - 1) & 1, P.status, ST_FWD_PRODUCER, &abort_flag)) {
                         ok = false;
                         break;
@@ -473,7 +497,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                     for (int bx = 0; bx < C::kBoxes; ++bx)
                         if (elect_one())
                             tma_load_3d(sbase + u * C::kQBytes + bx * (kM * 128), &tmQ, BAR(C::Q_FULL + u), bx * 64, p.h * P.G,
-                                        p.it.row + (st.solo ? 0 : u * tm));
+                                        p.it.row + u * tm);
                     ++qn[u];
                 }
                 for (int i = 0; ok && i < n; ++i) {
@@ -511,7 +535,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
         } else if (warp <= 8 + NT) {
             // -------------------------------------------------------- MMA issue
             const int u = warp - 9;
-            constexpr uint32_t idS = idesc_f16(BF16, kM, BN, false, false), idPV = idesc_f16(BF16, kM, HD, false, true);
+            constexpr uint32_t idS = idesc_f16(MB, kM, BN, false, false), idPV = idesc_f16(MB, kM, HD, false, true);
             const uint64_t qdesc = sdesc_sw128(sbase + u * C::kQBytes, 16, 1024);
             const uint32_t tO = tbase + 256 + u * HD;
             auto wait = [&](int bar, uint32_t parity) { return warp_wait(BAR(bar), parity, P.status, ST_FWD_MMA, &abort_flag); };
@@ -523,9 +547,8 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
             while (ok && next_part(plan, w, p)) {
                 const int n = p.end - p.begin, tile0 = p.it.t0 + p.begin;
                 if (n <= 0) continue;
-                const Sight st = sight_of<NT, BN>(P, p, tm);
-                const int mine = u ? st.n[1] : st.n[0];
-                auto has = [&](int i) { return st.has(u, tile0 + i); };
+                const Tiles my = tiles_of<BN>(P, p, u, tm);
+                auto has = [&](int i) { return tile0 + i >= my.t0 && tile0 + i < my.t0 + my.n; };
                 auto kst = [&](int i) { return (g + 2 * i) % NS; };
                 auto kph = [&](int i) { return ((g + 2 * i) / NS) & 1; };
                 auto vst = [&](int i) { return (g + 2 * i + 1) % NS; };
@@ -538,7 +561,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                                  kdesc + (((kk >> 2) * (BN * 128) + (kk & 3) * 32) >> 4), idS, kk > 0 ? 1u : 0u);
                     mma_commit_e(BAR(C::S_FULL + (NT == 2 ? u : (sc & 1))));
                     ++sc;
-                    if (st.index(u, tile0 + i) == mine - 1) mma_commit_e(BAR(C::Q_EMPTY + u));
+                    if (tile0 + i == my.t0 + my.n - 1) mma_commit_e(BAR(C::Q_EMPTY + u));
                 };
                 auto issue_pv = [&](int i, int k) {
                     const uint32_t tS = tbase + (NT == 2 ? u * 128 : ((pc - 1) & 1) * 64);
@@ -550,17 +573,17 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                             mma_ts_e(tO, tS + kk * 8, vdesc + ((kk * 16 * 128) >> 4), idPV, (k > 0 || kk > 0) ? 1u : 0u);
                     }
                     if constexpr (NT == 1) mma_commit_e(BAR(C::PV_DONE + ((pc - 1) & 1)));
-                    if (k == mine - 1) mma_commit_e(BAR(C::O_DONE + u));
+                    if (k == my.n - 1) mma_commit_e(BAR(C::O_DONE + u));
                 };
                 // A tile's release is committed only after the wait for its data, also for tiles that
                 // this query tile skips, so that no arrival belongs to a later use of the stage.
-                if (mine > 0 && !wait(C::Q_FULL + u, act & 1)) break;
+                if (my.n > 0 && !wait((F8 && BF16 ? C::Q_WIDE : C::Q_FULL) + u, act & 1)) break;
                 if (!wait(C::FULL + kst(0), kph(0))) break;
                 tc_fence_after();
                 if (has(0)) issue_s(0);
                 mma_commit_e(BAR(C::EMPTY + kst(0)));
                 for (int i = 0; ok && i < n; ++i) {
-                    const int k = st.index(u, tile0 + i);
+                    const int k = tile0 + i - my.t0;
                     if constexpr (NT == 1) {
                         if (i + 1 < n) {
                             ok = wait(C::FULL + kst(i + 1), kph(i + 1));
@@ -588,7 +611,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                     if (NT == 2 && i + 1 < n) mma_commit_e(BAR(C::EMPTY + kst(i + 1)));
                 }
                 g += 2 * n;
-                if (mine > 0) ++act;
+                if (my.n > 0) ++act;
             }
             mma_commit_e(BAR(C::MMA_DONE));
             mbar_wait(BAR(C::MMA_DONE), 0, P.status, ST_TEARDOWN, nullptr);
@@ -637,7 +660,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                                 for (int bx = 0; bx < C::kBoxes; ++bx) {
                                     const uint4 v = *reinterpret_cast<const uint4*>(vt + bx * (BN * 128) + x * 16);
                                     // an exponent of all ones carries into its sign's place
-                                    constexpr uint32_t kExp = BF16 ? 0x7f807f80u : 0x7c007c00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
+                                    constexpr uint32_t kExp = MB ? 0x7f807f80u : 0x7c007c00u, kOne = MB ? 0x00800080u : 0x04000400u;
                                     const uint32_t c = ((v.x & kExp) + kOne) | ((v.y & kExp) + kOne) | ((v.z & kExp) + kOne) | ((v.w & kExp) + kOne);
                                     bad = bad || (c & 0x80008000u);
                                 }
@@ -667,75 +690,122 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
             }
             if (lane == 0) plan.split[blockIdx.x] = split;
         }
-    } else if (F8 && warp >= 12) {
+    } else if (F8 && warp >= C::kWide0 && warp < C::kWide0 + 4) {
         // ---------------------------------------------------------------- widening
         if constexpr (F8) {
             regs_dec<C::kRegsWide>();
-            const int ww = warp - 12;
+            const int ww = warp - C::kWide0;
             constexpr int kChunks = C::kRawRow / 16;            // 16-byte chunks of a box's row
             constexpr int kSteps = BN * HD / 16 / 128;          // chunks of a lane, of a tile
             const int sub = lane % subs;
             bool ok = true;
             int stage = 0, phase = 1, raw = 0, raw_phase = 0;
-            auto scales = [&](const Part& p, int pg) {
-                if (!page_ok(pg)) return make_float2(0.f, 0.f);
-                const long long i = (long long)pg * P.Hkv + p.h;
-                return make_float2(__ldg(P.k_scale + i), __ldg(P.v_scale + i));
-            };
+            int qn[2] = {0, 0};  // parts in which a tile was active
             Walk w = walk_of(P, plan);
             Part p;
             while (ok && next_part(plan, w, p)) {
                 int lo, hi;
                 key_span(p, lo, hi);
                 const int tile0 = p.it.t0 + p.begin, n = p.end - p.begin;
+                // the rows of Q in fp16, a thread to a row
+                if constexpr (BF16) {
+                    for (int u = 0; ok && u < NT; ++u) {
+                        if (tiles_of<BN>(P, p, u, tm).n == 0) continue;
+                        const int at = u ? qn[1]++ : qn[0]++;
+                        ok = warp_wait(BAR(C::Q_FULL + u), at & 1, P.status, ST_FWD_PRODUCER, &abort_flag);
+                        if (!ok) break;
+                        const int r = ww * 32 + lane;
+                        uint8_t* row = smem + u * C::kQBytes + r * 128;
+                        float big = 0.f;
+#pragma unroll 2
+                        for (int c = 0; c < 8 * C::kBoxes; ++c) {
+                            const uint4 x = *reinterpret_cast<const uint4*>(row + (c >> 3) * (kM * 128) + (((c & 7) ^ (r & 7)) << 4));
+                            const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                big = max3f(big, fabsf(__uint_as_float(xw[e] << 16)), fabsf(__uint_as_float(xw[e] & 0xffff0000u)));
+                        }
+                        int ex = (int)(__float_as_uint(big) >> 23) - 127;
+                        ex = big > 0.f && big < INFINITY ? max(ex, -100) : 13;
+                        const float mul = __uint_as_float((uint32_t)(13 - ex + 127) << 23);
+#pragma unroll 2
+                        for (int c = 0; c < 8 * C::kBoxes; ++c) {
+                            uint4* q = reinterpret_cast<uint4*>(row + (c >> 3) * (kM * 128) + (((c & 7) ^ (r & 7)) << 4));
+                            const uint4 x = *q;
+                            auto half = [&](uint32_t v) {
+                                return pack2<false>(__uint_as_float(v << 16) * mul, __uint_as_float(v & 0xffff0000u) * mul);
+                            };
+                            *q = make_uint4(half(x.x), half(x.y), half(x.z), half(x.w));
+                        }
+                        reinterpret_cast<short*>(smem + C::kQexpOff)[((at & 1) * 2 + u) * kM + r] = (short)(ex - 13);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(BAR(C::Q_WIDE + u));
+                    }
+                }
                 auto page_at = [&](int i) { return i < n ? box_page(p, (tile0 + i) * BN + sub * box_rows, lo, hi) : -1; };
+                VRef vref = first_vref(p, tile0, n, lo, hi);
                 int pg = page_at(1);
-                float2 sc = scales(p, page_at(0));
+                float vs = scales_at(p, page_at(0)).y;
                 for (int i = 0; ok && i < n; ++i) {
-                    const float2 sc_next = scales(p, pg);
+                    const float vs_next = scales_at(p, pg).y;
                     pg = page_at(i + 2);
+                    const unsigned odd = odd_scales(vs, subs, vref);
+                    const float r = odd ? 1.f : vs * vref.inv;
+                    const uint32_t ratio = pack2<false>(r, r);  // of this lane's box
 #pragma unroll 1
                     for (int kv = 0; kv < 2; ++kv) {
-                        const float mine = kv ? sc.y : sc.x;
                         ok = warp_wait(BAR(C::RAW_FULL + raw), raw_phase, P.status, ST_FWD_PRODUCER, &abort_flag) &&
                              warp_wait(BAR(C::EMPTY + stage), phase, P.status, ST_FWD_PRODUCER, &abort_flag);
                         if (!ok) break;
                         const uint8_t* src = smem + C::kRawOff + raw * C::kRawBytes;
                         const uint32_t dst = sbase + C::kRingOff + stage * C::kTileBytes;
-                        auto widen = [&](auto e4m3c) {
-                        constexpr bool kE4m3 = decltype(e4m3c)::value;
-                        // consecutive lanes: the chunks of a row, then of the next; this warp's rows lie together
-                        uint4 x[kSteps];
+                        // consecutive lanes: the chunks of a row, then of the next; this warp's rows lie together.
+                        // Chunk c is columns 16c .. of the box: two chunks of a 128-byte column of the wide tile.  Lanes of
+                        // either half of a row store them in the other order, so that eight lanes meet no bank twice.
+                        auto widen = [&](auto e4m3c, auto valuec) {
+                            constexpr int kAhead = 4;
+#pragma unroll 1
+                            for (int t0 = 0; t0 < kSteps; t0 += kAhead) {
+                                uint4 x[kAhead];
 #pragma unroll
-                        for (int t = 0; t < kSteps; ++t) {
-                            const int at = ww * kSteps * 32 + t * 32 + lane;
-                            const int c = at % kChunks, row = at / kChunks % BN, box = at / kChunks / BN;
-                            x[t] = *reinterpret_cast<const uint4*>(
-                                src + box * (BN * C::kRawRow) + row * C::kRawRow +
-                                (C::kRawRow == 128 ? (c ^ (row & 7)) << 4 : (c ^ ((row >> 1) & 3)) << 4));
-                        }
+                                for (int t = 0; t < kAhead; ++t) {
+                                    const int at = (ww * kSteps + t0 + t) * 32 + lane;
+                                    const int c = at % kChunks, row = at / kChunks % BN, box = at / kChunks / BN;
+                                    x[t] = *reinterpret_cast<const uint4*>(
+                                        src + box * (BN * C::kRawRow) + row * C::kRawRow +
+                                        (C::kRawRow == 128 ? (c ^ (row & 7)) << 4 : (c ^ ((row >> 1) & 3)) << 4));
+                                }
 #pragma unroll
-                        for (int t = 0; t < kSteps; ++t) {
-                            const int at = ww * kSteps * 32 + t * 32 + lane;
-                            const int c = at % kChunks, row = at / kChunks % BN, box = at / kChunks / BN;
-                            const float s = __shfl_sync(0xffffffffu, mine, row >> box_shift);
-                            uint32_t o[8];
-                            widen4<BF16, kE4m3>(x[t].x, s, o[0], o[1]);
-                            widen4<BF16, kE4m3>(x[t].y, s, o[2], o[3]);
-                            widen4<BF16, kE4m3>(x[t].z, s, o[4], o[5]);
-                            widen4<BF16, kE4m3>(x[t].w, s, o[6], o[7]);
-                            // columns 16c .. of the box: two chunks of a 128-byte column of the wide tile.  Lanes of
-                            // either half of a row store them in the other order, so that eight lanes meet no bank twice.
-                            const int wide = box * (kChunks / 4) + (c >> 2), c2 = (2 * c) & 7;
-                            const uint32_t to = dst + wide * (BN * 128) + row * 128;
-                            const bool swap = (c >> 2) & 1;
-                            const uint32_t a0 = to + ((c2 ^ (row & 7)) << 4), a1 = to + (((c2 + 1) ^ (row & 7)) << 4);
-                            st_shared_v4(swap ? a1 : a0, swap ? o[4] : o[0], swap ? o[5] : o[1], swap ? o[6] : o[2], swap ? o[7] : o[3]);
-                            st_shared_v4(swap ? a0 : a1, swap ? o[0] : o[4], swap ? o[1] : o[5], swap ? o[2] : o[6], swap ? o[3] : o[7]);
-                        }
+                                for (int t = 0; t < kAhead; ++t) {
+                                    const int at = (ww * kSteps + t0 + t) * 32 + lane;
+                                    const int c = at % kChunks, row = at / kChunks % BN, box = at / kChunks / BN;
+                                    const bool swap = (c >> 2) & 1;
+                                    uint32_t o[8];
+                                    widen4<decltype(e4m3c)::value>(swap ? x[t].z : x[t].x, o[0], o[1]);
+                                    widen4<decltype(e4m3c)::value>(swap ? x[t].w : x[t].y, o[2], o[3]);
+                                    widen4<decltype(e4m3c)::value>(swap ? x[t].x : x[t].z, o[4], o[5]);
+                                    widen4<decltype(e4m3c)::value>(swap ? x[t].y : x[t].w, o[6], o[7]);
+                                    if constexpr (decltype(valuec)::value) {
+                                        const uint32_t f = __shfl_sync(0xffffffffu, ratio, row >> box_shift);
+#pragma unroll
+                                        for (int e = 0; e < 8; ++e) o[e] = mul_h2(o[e], f);
+                                    }
+                                    const int wide = box * (kChunks / 4) + (c >> 2), c2 = (2 * c) & 7;
+                                    const uint32_t to = dst + wide * (BN * 128) + row * 128;
+                                    const uint32_t a0 = to + ((c2 ^ (row & 7)) << 4), a1 = to + (((c2 + 1) ^ (row & 7)) << 4);
+                                    st_shared_v4(swap ? a1 : a0, o[0], o[1], o[2], o[3]);
+                                    st_shared_v4(swap ? a0 : a1, o[4], o[5], o[6], o[7]);
+                                }
+                            }
                         };
-                        if (e4m3) widen(std::true_type());
-                        else widen(std::false_type());
+                        if (e4m3) {
+                            if (kv) widen(std::true_type(), std::true_type());
+                            else widen(std::true_type(), std::false_type());
+                        } else {
+                            if (kv) widen(std::false_type(), std::true_type());
+                            else widen(std::false_type(), std::false_type());
+                        }
                         fence_proxy_async_smem();  // the tensor cores read the tile through the async proxy
                         __syncwarp();
                         if (lane == 0) {
@@ -745,35 +815,32 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                         if (++stage == NS) stage = 0, phase ^= 1;
                         if (++raw == C::kRaw) raw = 0, raw_phase ^= 1;
                     }
-                    sc = sc_next;
+                    vs = vs_next;
                 }
             }
         }
-    } else {
-        if constexpr (F8) regs_inc<C::kRegsSoftmax>();
-        // ------------------------------------------------------------ softmax, epilogue
-        const int wq = warp & 3, h = warp >> 2, r = wq * 32 + lane;  // row, and half of a tile's keys and of O's columns
+    } else if (warp < 4 * NT) {
+        regs_inc<C::kRegsSoftmax>();
+        // -------------------------------------------------- softmax, epilogue of tile u
+        const int u = warp >> 2, wq = warp & 3, r = wq * 32 + lane;
         const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
+        const uint32_t tO = tbase + 256 + u * HD + lane_off;
         const int tok = r / P.G, head = r - tok * P.G;  // of this thread's row
         const float sl2 = P.scale * kLog2e;
         const uint64_t sl2_2 = f2_make(sl2, sl2);
         const float cap_in = P.scale / fmaxf(P.softcap, 1e-30f), cap_out = P.softcap * kLog2e;
-        using R = PRange<BF16>;
-        constexpr int NC = BN / 64, kCols = HD / 2;  // chunks of 32 keys of a half; columns of a half of O
+        constexpr float kTop = PRange<MB>::top;
+        constexpr int NC = BN / 32;
         auto wait = [&](int bar, uint32_t parity) {
             return __all_sync(0xffffffffu, mbar_wait(BAR(bar), parity, P.status, ST_FWD_SOFTMAX, &abort_flag));
         };
-        // what the other warp of these rows put in its place of half_s
-        auto exchange = [&](float x) {
-            half_s[h][r] = x;
-            pair_any(1 + wq, false);
-            const float y = half_s[h ^ 1][r];
-            pair_any(1 + wq, false);
-            return y;
-        };
         bool ok = true;
-        int sc[2] = {0, 0}, act[2] = {0, 0};  // tiles done, parts in which the tile was active
-        unsigned g = 0;                       // ring position of the part's first K tile
+        int sc = 0, act = 0;  // tiles done, parts in which this tile was active
+        // (one tile) the product of the tile before this one is complete.  At most that one can still be on
+        // its way, since this tile's S was issued after the one before it, and it cannot be overtaken.
+        auto wait_pv = [&]() { return wait(C::PV_DONE + ((sc - 1) & 1), ((sc - 1) >> 1) & 1); };
+        int base[2] = {0, 0};         // softmaxes of both tiles in earlier parts
+        unsigned g = 0;               // ring position of the part's first K tile
         // x = score * log2(e) - m of a pair of raw scores; mode 0: plain; with a softcap 1: the fitted
         // polynomial, 2: by exp, 3: the short polynomial
         auto to_x = [&](auto modec, uint64_t rr, uint64_t nm) -> uint64_t {
@@ -808,355 +875,356 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
         Part p;
         while (ok && next_part(plan, w, p)) {
             const int n = p.end - p.begin, tile0 = p.it.t0 + p.begin;
-            const Sight st = sight_of<NT, BN>(P, p, tm);
-            const unsigned v0 = g / 2;  // V tiles before this part
+            const Tiles my = tiles_of<BN>(P, p, u, tm);
+            const Tiles other = NT == 2 ? tiles_of<BN>(P, p, 1 - u, tm) : my;
+            const int nA = u == 0 ? my.n : other.n, nB = u == 0 ? other.n : my.n, bA = base[0], bB = base[1];
+            // (a tile whose keys begin more than one tile before the other's would wait for a turn that needs a
+            // stage of the ring that only its own product frees; 128 rows apart they never do)
+            const bool alt = NT == 2 && abs(my.t0 - other.t0) <= 1;
+            base[0] += nA;
+            base[1] += nB;
+            const unsigned g0 = g;
             g += 2 * n;
+            if (my.ntok == 0) continue;
             int lo, hi;  // keys that any row of the item sees
             key_span(p, lo, hi);
-            float m2[2] = {R::first, R::first}, l2[2] = {0.f, 0.f};  // of this row in both tiles
+            const bool row_live = tok < my.ntok;
+            const int pos = my.pos + tok;
+            float m = 8.f - kTop, l = 0.f;
             const int sub = lane < subs ? lane : 0;
-            int pg = n > 0 ? box_page(p, tile0 * BN + sub * box_rows, lo, hi) : -1;
-            for (int i = 0; ok && i < n; ++i) {
-                const int j0 = (tile0 + i) * BN;
+            int pg = my.n > 0 ? box_page(p, my.t0 * BN + sub * box_rows, lo, hi) : -1;
+            // (8-bit pools) vref, the scales of the tile's boxes, those of the next, and this row's factor
+            const VRef vref = first_vref(p, tile0, n, lo, hi);
+            float2 scale = scales_at(p, pg), scale_next = make_float2(0.f, 0.f);
+            int pg_next = my.n > 1 ? box_page(p, (my.t0 + 1) * BN + sub * box_rows, lo, hi) : -1;
+            float qf = 1.f;
+            for (int k = 0; k < my.n; ++k) {
+                const int j0 = (my.t0 + k) * BN;
                 // boxes of this tile that are there (bit = box)
                 const unsigned there = __ballot_sync(0xffffffffu, lane < subs && page_ok(pg));
-                if (i + 1 < n) pg = box_page(p, j0 + BN + sub * box_rows, lo, hi);
-                const bool all_there = there == (1u << subs) - 1u;
-#pragma unroll 1
-                for (int u = 0; ok && u < NT; ++u) {
-                    if (!st.has(u, tile0 + i)) continue;
-                    const int ntok = u ? st.ntok[1] : st.ntok[0], pos0 = p.it.pos + (st.solo ? 0 : u * tm);
-                    const bool first = st.index(u, tile0 + i) == 0;
-                    const int count = u ? sc[1] : sc[0];
-                    float m = u ? m2[1] : m2[0], l = u ? l2[1] : l2[0];
-                    const bool row_live = tok < ntok;
-                    const bool full = all_there && tile_full(P.wl, P.wr, p.it.len, pos0, pos0 + ntok - 1, j0, j0 + BN);
-                    const uint32_t tS = tbase + (NT == 2 ? u * 128 : (count & 1) * 64) + lane_off;  // S, and P over it
-                    const uint32_t tO = tbase + 256 + u * HD + h * kCols + lane_off;
-                    // (one tile) the product of the tile before this one is complete.  At most that one can still be
-                    // on its way, since this tile's S was issued after the one before it, and it cannot be overtaken.
-                    auto wait_pv = [&]() {
-                        return NT == 2 || wait(C::PV_DONE + ((count - 1) & 1), ((count - 1) >> 1) & 1);
-                    };
-                    uint32_t sv[NC][32];
-                    bool got = wait(C::S_FULL + (NT == 2 ? u : (count & 1)), (NT == 2 ? count : count >> 1) & 1);
-                    tc_fence_after();
+                const unsigned odd = F8 ? odd_scales(scale.y, subs, vref) : 0u;
+                if constexpr (F8) {
+                    pg = pg_next;
+                    scale_next = scales_at(p, pg);
+                    if (k + 2 < my.n) pg_next = box_page(p, j0 + 2 * BN + sub * box_rows, lo, hi);
+                } else {
+                    if (k + 1 < my.n) pg = box_page(p, j0 + BN + sub * box_rows, lo, hi);
+                }
+                const bool full = there == (1u << subs) - 1u &&
+                                  tile_full(P.wl, P.wr, p.it.len, my.pos, my.pos + my.ntok - 1, j0, j0 + BN);
+                const int sbuf = NT == 2 ? u : (sc & 1);
+                const uint32_t tS = tbase + (NT == 2 ? u * 128 : (sc & 1) * 64) + lane_off;
+                if (!wait(C::S_FULL + sbuf, NT == 2 ? sc & 1 : (sc >> 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                uint32_t sv[NC][32];
 #pragma unroll
-                    for (int c = 0; c < NC; ++c) tmem_ld32(tS + (h * NC + c) * 32, sv[c]);
-                    // ---- the keys of the tile that this row sees: [va, vb), in boxes that are there
-                    int va = 0, vb = BN;
-                    if (!full) {
-                        const long long pos = (long long)pos0 + tok;
-                        long long a = lo - j0, b = hi - j0;
-                        if (P.wl >= 0) a = max(a, pos - P.wl - j0);
-                        if (P.wr >= 0) b = min(b, pos + P.wr - j0 + 1);
-                        va = (int)min(max(a, 0ll), (long long)BN);
-                        vb = row_live ? (int)min(max(b, (long long)va), (long long)BN) : va;
-                    }
-                    auto mask = [&](uint32_t (&x32)[32], int c) {  // what the row does not see: -inf
-                        if (full) return;
-                        c += h * NC;
-                        const int c0 = min(max(va - 32 * c, 0), 32), c1 = min(max(vb - 32 * c, 0), 32);
-                        uint32_t x = bit_range(c0, c1 - c0);
-                        if (!all_there) {
-                            const int q = (32 * c) >> box_shift;
-                            uint32_t have = ((there >> q) & 1u) ? 0xffffffffu : 0u;
-                            if (box_rows == 16) have = (have & 0xffffu) | (((there >> (q + 1)) & 1u) ? 0xffff0000u : 0u);
-                            x &= have;
-                        }
-                        if (__all_sync(0xffffffffu, x == 0xffffffffu)) return;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) x32[e] = (x >> e) & 1u ? x32[e] : 0xff800000u;
-                    };
-                    auto landed = [&]() {
+                for (int c = 0; c < NC; ++c) tmem_ld32(tS + c * 32, sv[c]);
+                if (alt && (u == 0 ? (k >= 1 && k - 1 < nB) : (k < nA))) {
+                    const int need = 4 * (u == 0 ? bB + k : bA + k + 1);
+                    const bool rr = count_wait(&done_count[u ^ 1], need, P.status, ST_FWD_SOFTMAX, &abort_flag);
+                    if (!__all_sync(0xffffffffu, rr)) {
                         tmem_ld_wait_only();
-#pragma unroll
-                        for (int c = 0; c < NC; ++c) tmem_pin(sv[c]);
-                    };
-                    landed();
-                    // the form of the softcap: by exp where a raw score of the warp lies outside the fit's range
-                    bool accurate = false, shorter = false;
-                    if constexpr (CAP) {
-                        float am[NC];
-#pragma unroll
-                        for (int c = 0; c < NC; ++c) {
-                            am[c] = 0.f;
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2)
-                                am[c] = max3f(am[c], fabsf(__uint_as_float(sv[c][e])), fabsf(__uint_as_float(sv[c][e + 1])));
-                        }
-                        float amax = am[0];
-                        if constexpr (NC == 2) amax = fmaxf(amax, am[1]);
-                        const CapPoly cp = cap_poly(P.scale, P.softcap);
-                        accurate = __any_sync(0xffffffffu, !(amax <= cp.r_max)) || (!full && !cp.inf_ok);
-                        const CapShort cs = cap_short(P.scale, P.softcap);
-                        shorter = !accurate && __all_sync(0xffffffffu, amax <= cs.r_max) && (full || cs.inf_ok);
+                        ok = false;
+                        break;
                     }
-                    // ---- p of the row's half, 16 bits each, and their sum
-                    uint32_t pk[NC * 16];
-                    auto p_pass = [&](auto modec) {
-                        const uint64_t nm = f2_make(-m, -m);
-                        uint64_t rs[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
+                }
+                tmem_ld_wait_only();
 #pragma unroll
-                        for (int c = 0; c < NC; ++c) {
-                            mask(sv[c], c);
+                for (int c = 0; c < NC; ++c) tmem_pin(sv[c]);
+                if constexpr (F8) {
+                    // raw scores in units of 1: the scale of the keys' page, and the power of two of the row of Q
+                    if (BF16 && k == 0) {
+                        const int ex = reinterpret_cast<const volatile short*>(smem + C::kQexpOff)[((act & 1) * 2 + u) * kM + r];
+                        qf = __uint_as_float((uint32_t)(ex + 127) << 23);
+                    }
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                float x0, x1;
-                                f2_split(to_x(modec, f2_make(__uint_as_float(sv[c][2 * e]), __uint_as_float(sv[c][2 * e + 1])), nm), x0, x1);
-                                const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);  // 2^-inf = 0
-                                rs[e & 1] = f2_add(rs[e & 1], f2_make(p0, p1));
-                                pk[c * 16 + e] = pack2<BF16>(p0, p1);
+                    for (int c = 0; c < NC; ++c) {
+                        const float f0 = __shfl_sync(0xffffffffu, scale.x, (32 * c) >> box_shift) * qf;
+                        const float f1 = __shfl_sync(0xffffffffu, scale.x, (32 * c + 16) >> box_shift) * qf;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const float f = e < 16 ? f0 : f1;
+                            float x, y;
+                            f2_split(f2_mul(f2_make(__uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1])), f2_make(f, f)), x, y);
+                            sv[c][e] = __float_as_uint(x);
+                            sv[c][e + 1] = __float_as_uint(y);
+                        }
+                    }
+                }
+                bool accurate = false, shorter = false;
+                if constexpr (CAP) {
+                    float am[NC];
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        am[c] = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2)
+                            am[c] = max3f(am[c], fabsf(__uint_as_float(sv[c][e])), fabsf(__uint_as_float(sv[c][e + 1])));
+                    }
+                    float amax = fmaxf(am[0], am[1]);
+                    if constexpr (NC == 4) amax = fmaxf(amax, fmaxf(am[2], am[3]));
+                    const CapPoly cp = cap_poly(P.scale, P.softcap);
+                    accurate = __any_sync(0xffffffffu, !(amax <= cp.r_max)) || (!full && !cp.inf_ok);
+                    const CapShort cs = cap_short(P.scale, P.softcap);
+                    shorter = !accurate && __all_sync(0xffffffffu, amax <= cs.r_max) && (full || cs.inf_ok);
+                }
+                uint32_t seen[NC];  // the keys of the tile that this row sees
+#pragma unroll
+                for (int c = 0; c < NC; ++c) seen[c] = 0xffffffffu;
+                if (!full) {
+                    long long vlo = lo - j0, vhi = hi - j0;
+                    if (P.wl >= 0) vlo = max(vlo, (long long)pos - P.wl - j0);
+                    if (P.wr >= 0) vhi = min(vhi, (long long)pos + P.wr - j0 + 1);
+                    const int a = (int)min(max(vlo, 0ll), (long long)BN), b = row_live ? (int)min(max(vhi, (long long)a), (long long)BN) : a;
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        const int c0 = min(max(a - 32 * c, 0), 32), c1 = min(max(b - 32 * c, 0), 32);
+                        seen[c] = bit_range(c0, c1 - c0);
+                    }
+                    if (there != (1u << subs) - 1u) {
+#pragma unroll
+                        for (int c = 0; c < NC; ++c) {  // boxes of 16, 32 or 64 keys
+                            const int x = 32 * c / box_rows;
+                            uint32_t have = ((there >> x) & 1u) ? 0xffffffffu : 0u;
+                            if (box_rows == 16) have = (have & 0xffffu) | (((there >> (x + 1)) & 1u) ? 0xffff0000u : 0u);
+                            seen[c] &= have;
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < NC; ++c)
+                        if (!__all_sync(0xffffffffu, seen[c] == 0xffffffffu)) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) sv[c][e] = (seen[c] >> e) & 1u ? sv[c][e] : 0xff800000u;  // -inf
+                        }
+                }
+                // ---- the row's largest score, as x against its reference
+                float rm[NC];
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    rm[c] = -INFINITY;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2)
+                        rm[c] = max3f(rm[c], __uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1]));
+                }
+                float rmax = fmaxf(rm[0], rm[1]);
+                if constexpr (NC == 4) rmax = fmaxf(rmax, fmaxf(rm[2], rm[3]));
+                float xm, xm_;
+                {
+                    const uint64_t r2 = f2_make(rmax, rmax), n2 = f2_make(-m, -m);
+                    uint64_t x2;
+                    if (!CAP) x2 = to_x(M0(), r2, n2);
+                    else if (shorter) x2 = to_x(M3(), r2, n2);
+                    else if (!accurate) x2 = to_x(M1(), r2, n2);
+                    else x2 = to_x(M2(), r2, n2);
+                    f2_split(x2, xm, xm_);
+                }
+                if (rmax == -INFINITY) xm = -INFINITY;
+                const bool move = xm > kTop || (l == 0.f && xm < kTop - 10.f && xm != -INFINITY);
+                bool o_stands = NT == 2;  // the product of the tile before is complete
+                if (__any_sync(0xffffffffu, move)) {
+                    // rows that have seen nothing hold O = 0: their reference may move by any amount
+                    const float by = xm - (kTop - 8.f);
+                    const float alpha = fast_exp2(move && l > 0.f ? -by : 0.f);
+                    if (move) {
+                        m += by;
+                        l *= alpha;
+                    }
+                    if (k > 0) {
+                        if (!o_stands) {
+                            if (!wait_pv()) {
+                                ok = false;
+                                break;
                             }
+                            o_stands = true;
+                            tc_fence_after();
                         }
-                        float a0, a1, b0, b1;
-                        f2_split(rs[0], a0, a1);
-                        f2_split(rs[1], b0, b1);
-                        return (a0 + b0) + (a1 + b1);
-                    };
-                    const int ha = max(va, h * (BN / 2)), hb = min(vb, (h + 1) * (BN / 2));  // seen in this half
-                    float rs;
-                    bool again = false;
 #pragma unroll 1
-                    while (true) {
-                        if (!CAP) rs = p_pass(M0());
-                        else if (shorter) rs = p_pass(M3());
-                        else if (!accurate) rs = p_pass(M1());
-                        else rs = p_pass(M2());
-                        if (again) break;
-                        // (the other half has loaded its scores too, which P is about to overwrite)
-                        const bool move = row_live && (!(rs < R::high) || (l == 0.f && rs < R::low && hb > ha));
-                        if (!pair_any(1 + wq, !got || move)) break;
-                        if (pair_any(1 + wq, !got)) {
-                            ok = false;
-                            break;
-                        }
-                        again = true;
-                        float rmax = -INFINITY;
-#pragma unroll 1
-                        for (int c = 0; c < NC; ++c) {
-                            uint32_t x[32];
-                            tmem_ld32(tS + (h * NC + c) * 32, x);
-                            tmem_ld_wait(x);
-                            mask(x, c);
-                            float am[2] = {-INFINITY, -INFINITY};
+                        for (int c = 0; c < HD / 32; ++c) {
+                            uint32_t orr[32];
+                            tmem_ld32(tO + c * 32, orr);
+                            tmem_ld_wait(orr);
 #pragma unroll
-                            for (int e = 0; e < 32; e += 2)
-                                am[(e >> 1) & 1] = max3f(am[(e >> 1) & 1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-                            rmax = max3f(rmax, am[0], am[1]);
+                            for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * alpha);
+                            tmem_st32(tO + c * 32, orr);
                         }
-                        rmax = fmaxf(rmax, exchange(rmax));
-                        const float l_other = exchange(l);
-                        float xm, xm_;  // (by exp under a softcap, so that both halves have the same)
-                        f2_split(CAP ? to_x(M2(), f2_make(rmax, rmax), f2_make(-m, -m)) : to_x(M0(), f2_make(rmax, rmax), f2_make(-m, -m)),
-                                 xm, xm_);
-                        const bool fresh = l == 0.f && l_other == 0.f;
-                        const bool moves = rmax != -INFINITY && (xm > R::x_high || (fresh && xm < R::x_low));
-                        const float by = xm - R::put;
-                        // (a row that has seen nothing holds O = 0: its reference may move by any amount)
-                        const float alpha = fast_exp2(moves && !fresh ? -by : 0.f);
-                        if (moves) {
-                            m += by;
-                            l *= alpha;
+                    }
+                }
+                // ---- p, chunk by chunk over S
+                auto p_pass = [&](auto modec) {
+                    const uint64_t nm = f2_make(-m, -m);
+                    uint64_t rs[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float x0, x1;
+                            f2_split(to_x(modec, f2_make(__uint_as_float(sv[c][2 * e]), __uint_as_float(sv[c][2 * e + 1])), nm), x0, x1);
+                            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);  // 2^-inf = 0
+                            rs[e & 1] = f2_add(rs[e & 1], f2_make(p0, p1));
+                            pk[e] = pack2<MB>(p0, p1);
                         }
-                        if (!first) {
-                            got = wait_pv();
-                            if (pair_any(1 + wq, !got)) {
+                        tmem_st16(tS + c * 16, pk);
+                    }
+                    float a0, a1, b0, b1;
+                    f2_split(rs[0], a0, a1);
+                    f2_split(rs[1], b0, b1);
+                    l += (a0 + b0) + (a1 + b1);
+                };
+                if (!CAP) p_pass(M0());
+                else if (shorter) p_pass(M3());
+                else if (!accurate) p_pass(M1());
+                else p_pass(M2());
+                // ---- a tile that is not whole: is all of V finite that some row does not see
+                bool by_row = false;
+                if (!full || odd) {
+                    const int i = my.t0 + k - tile0;  // its place in the part
+                    const unsigned gv = g0 + 2 * i + 1, vn = g0 / 2 + i;
+                    if (!wait(C::V_OK + vn % NS, (vn / NS) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint8_t* vt = smem + C::kRingOff + (gv % NS) * C::kTileBytes;
+                    by_row = (!full && *static_cast<volatile int*>(&bad_v[vn % NS]) != 0) || odd;
+                    if (by_row) {
+                        tmem_st_wait();
+                        if (!o_stands && k > 0) {
+                            if (!wait_pv()) {
                                 ok = false;
                                 break;
                             }
                             tc_fence_after();
+                        }
 #pragma unroll 1
-                            for (int c = 0; c < kCols / 32; ++c) {
-                                uint32_t orr[32];
+                        for (int c = 0; c < HD / 32; ++c) {
+                            uint32_t orr[32];
+                            if (k > 0) {
                                 tmem_ld32(tO + c * 32, orr);
                                 tmem_ld_wait(orr);
+                            } else {
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * alpha);
-                                tmem_st32(tO + c * 32, orr);
+                                for (int e = 0; e < 32; ++e) orr[e] = 0u;
                             }
-                        }
-#pragma unroll
-                        for (int c = 0; c < NC; ++c) tmem_ld32(tS + (h * NC + c) * 32, sv[c]);
-                        landed();
-                    }
-                    if (again && ok) pair_any(1 + wq, false);  // (both have loaded their scores once more)
-                    if (!ok) break;
-                    l += rs;
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) tmem_st16(tS + (h * NC + c) * 16, pk + c * 16);
-                    // ---- a tile that is not whole: is all of V finite that some row does not see
-                    bool by_row = false;
-                    if (!full) {
-                        const unsigned vn = v0 + i, gv = 2 * vn + 1;
-                        got = wait(C::V_OK + vn % NS, (vn / NS) & 1);
-                        const uint8_t* vt = smem + C::kRingOff + (gv % NS) * C::kTileBytes;
-                        by_row = got && *static_cast<volatile int*>(&bad_v[vn % NS]) != 0;
-                        if (pair_any(1 + wq, !got || by_row)) {
-                            tmem_st_wait();
-                            tc_fence_before();
-                            got = got && (first || wait_pv());
-                            if (pair_any(1 + wq, !got)) {  // (and both halves of P are there)
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
+                            const uint8_t* col = vt + (c >> 1) * (BN * 128);
 #pragma unroll 1
-                            for (int c = 0; c < kCols / 32; ++c) {
-                                uint32_t orr[32];
-                                if (!first) {
-                                    tmem_ld32(tO + c * 32, orr);
-                                    tmem_ld_wait(orr);
+                            for (int j = 0; j < BN; ++j) {
+                                uint32_t pw;
+                                asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(pw) : "r"(tS + (j >> 1)));
+                                asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(pw)::"memory");
+                                float p0, p1;
+                                if constexpr (MB) {
+                                    p0 = __uint_as_float(pw << 16);
+                                    p1 = __uint_as_float(pw & 0xffff0000u);
                                 } else {
-#pragma unroll
-                                    for (int e = 0; e < 32; ++e) orr[e] = 0u;
+                                    const float2 f = h2_to_f2(pw);
+                                    p0 = f.x, p1 = f.y;
                                 }
-                                const int col = h * kCols + c * 32;  // of O
-                                const uint8_t* vcol = vt + (col >> 6) * (BN * 128);
-#pragma unroll 1
-                                for (int j = 0; j < BN; ++j) {
-                                    uint32_t pw;
-                                    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(pw) : "r"(tS + (j >> 1)));
-                                    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(pw)::"memory");
-                                    float p0, p1;
-                                    if constexpr (BF16) {
-                                        p0 = __uint_as_float(pw << 16);
-                                        p1 = __uint_as_float(pw & 0xffff0000u);
-                                    } else {
-                                        const float2 f = h2_to_f2(pw);
-                                        p0 = f.x, p1 = f.y;
-                                    }
-                                    const float pj = (j & 1) ? p1 : p0;
-                                    const bool see = j >= va && j < vb && ((there >> (j >> box_shift)) & 1u);
+                                float pj = (j & 1) ? p1 : p0;
+                                if (F8 && odd) pj *= __shfl_sync(0xffffffffu, scale.y * vref.inv, j >> box_shift);
+                                uint32_t sw = 0;
 #pragma unroll
-                                    for (int q = 0; q < 4; ++q) {
-                                        const uint4 v = *reinterpret_cast<const uint4*>(vcol + j * 128 + (((((col >> 5) & 1) * 4 + q) ^ (j & 7)) << 4));
-                                        const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+                                for (int x = 0; x < NC; ++x) sw = (j >> 5) == x ? seen[x] : sw;
+                                const bool see = (sw >> (j & 31)) & 1u;
 #pragma unroll
-                                        for (int e = 0; e < 4; ++e) {
-                                            float v0, v1;
-                                            if constexpr (BF16) {
-                                                v0 = __uint_as_float(vw[e] << 16);
-                                                v1 = __uint_as_float(vw[e] & 0xffff0000u);
-                                            } else {
-                                                const float2 f = h2_to_f2(vw[e]);
-                                                v0 = f.x, v1 = f.y;
-                                            }
-                                            uint32_t& o0 = orr[8 * q + 2 * e];
-                                            uint32_t& o1 = orr[8 * q + 2 * e + 1];
-                                            if (see) {
-                                                o0 = __float_as_uint(fmaf(pj, v0, __uint_as_float(o0)));
-                                                o1 = __float_as_uint(fmaf(pj, v1, __uint_as_float(o1)));
-                                            }
+                                for (int q = 0; q < 4; ++q) {
+                                    const uint4 v = *reinterpret_cast<const uint4*>(col + j * 128 + ((((c & 1) * 4 + q) ^ (j & 7)) << 4));
+                                    const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        float v0, v1;
+                                        if constexpr (MB) {
+                                            v0 = __uint_as_float(vw[e] << 16);
+                                            v1 = __uint_as_float(vw[e] & 0xffff0000u);
+                                        } else {
+                                            const float2 f = h2_to_f2(vw[e]);
+                                            v0 = f.x, v1 = f.y;
+                                        }
+                                        uint32_t& o0 = orr[8 * q + 2 * e];
+                                        uint32_t& o1 = orr[8 * q + 2 * e + 1];
+                                        if (see) {
+                                            o0 = __float_as_uint(fmaf(pj, v0, __uint_as_float(o0)));
+                                            o1 = __float_as_uint(fmaf(pj, v1, __uint_as_float(o1)));
                                         }
                                     }
                                 }
-                                tmem_st32(tO + c * 32, orr);
                             }
+                            tmem_st32(tO + c * 32, orr);
                         }
                     }
-                    if (warp == 0 && lane == 0) *static_cast<volatile int*>(&skip_pv[u][count & 1]) = by_row ? 1 : 0;
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(BAR(C::P_FULL + (NT == 2 ? u : (count & 1))));
-                    if (u) m2[1] = m, l2[1] = l, ++sc[1];
-                    else m2[0] = m, l2[0] = l, ++sc[0];
                 }
+                if (wq == 0 && lane == 0) *static_cast<volatile int*>(&skip_pv[u][sc & 1]) = by_row ? 1 : 0;
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(BAR(C::P_FULL + (NT == 2 ? u : (sc & 1))));
+                    if constexpr (NT == 2) atomicAdd(&done_count[u], 1);
+                }
+                ++sc;
+                scale = scale_next;
             }
             // ------------------------------------------------------------ epilogue
-            bool got = ok;
-            for (int u = 0; u < NT; ++u)
-                if ((u ? st.n[1] : st.n[0]) > 0) {
-                    got = got && wait(C::O_DONE + u, (u ? act[1] : act[0]) & 1);
-                    if (u) ++act[1];
-                    else ++act[0];
-                }
-            if (pair_any(1 + wq, !got)) {
+            const bool have_o = ok && my.n > 0 && wait(C::O_DONE + u, act & 1);
+            if (my.n > 0) ++act;
+            if (!ok || (my.n > 0 && !have_o)) {
                 ok = false;
                 break;
             }
-            tc_fence_after();
-            const bool whole = p.whole(), o32 = (reinterpret_cast<uintptr_t>(P.o) & 31u) == 0;
+            if (have_o) tc_fence_after();
+            const bool whole = p.whole();
+            const bool none = l == 0.f, o32 = (reinterpret_cast<uintptr_t>(P.o) & 31u) == 0;
+            const float inv = (none ? 0.f : 1.f / l) * vref.ref;
             const int slot = 2 * blockIdx.x + (p.begin == 0 ? 1 : 0), rows = NT * kM;
+            const long long orow = (long long)(p.it.row + u * tm + tok);
+            uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.o) + (orow * P.H + p.h * P.G + head) * HD);
+            float4* part = reinterpret_cast<float4*>(part_o(plan, slot, rows, HD) + (size_t)(u * kM + r) * HD);
 #pragma unroll 1
-            for (int u = 0; u < (st.solo ? 1 : NT); ++u) {
-                const int ntok = u ? st.ntok[1] : st.ntok[0];
-                if (ntok == 0) continue;
-                const bool have_a = (u ? st.n[1] : st.n[0]) > 0, have_b = st.solo && st.n[1] > 0;
-                float m = u ? m2[1] : m2[0], l = u ? l2[1] : l2[0];
-                l += exchange(l);
-                // (solo) the other tile's share of the same row
-                float fa = 1.f, fb = 0.f;
-                if (have_b) {
-                    const float lb = l2[1] + exchange(l2[1]);
-                    const float ma = l != 0.f ? m : -INFINITY, mb = lb != 0.f ? m2[1] : -INFINITY;
-                    const float top = fmaxf(ma, mb);
-                    if (top != -INFINITY) {
-                        fa = l != 0.f ? fast_exp2(ma - top) : 0.f;
-                        fb = lb != 0.f ? fast_exp2(mb - top) : 0.f;
-                        m = top;
-                        l = (l != 0.f ? fa * l : 0.f) + (lb != 0.f ? fb * lb : 0.f);
+            for (int c = 0; c < HD / 32; ++c) {
+                uint32_t orr[32];
+                if (have_o) {
+                    tmem_ld32(tO + c * 32, orr);
+                    tmem_ld_wait(orr);
+                }
+                if (row_live && whole) {
+                    uint32_t pk[2][8];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        pk[e >> 3][e & 7] = none ? 0u : pack2<BF16>(__uint_as_float(orr[2 * e]) * inv, __uint_as_float(orr[2 * e + 1]) * inv);
+                    // (a row's sector at a time, where O is aligned to them)
+                    if (o32) {
+                        store_32(out + c * 4, pk[0]);
+                        store_32(out + c * 4 + 2, pk[1]);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            out[c * 4 + q] = make_uint4(pk[q >> 1][4 * (q & 1)], pk[q >> 1][4 * (q & 1) + 1], pk[q >> 1][4 * (q & 1) + 2],
+                                                        pk[q >> 1][4 * (q & 1) + 3]);
+                    }
+                } else if (row_live && !none) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t f[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[e] = F8 ? __float_as_uint(__uint_as_float(orr[8 * q + e]) * vref.ref) : orr[8 * q + e];
+                        store_32(part + c * 8 + q * 2, f);
                     }
                 }
-                const bool none = l == 0.f, row_live = tok < ntok;
-                const float inv = none ? 0.f : 1.f / l, ga = whole ? fa * inv : fa, gb = whole ? fb * inv : fb;
-                const long long orow = (long long)(p.it.row + u * tm + tok);
-                uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.o) + (orow * P.H + p.h * P.G + head) * HD + h * kCols);
-                float4* part = reinterpret_cast<float4*>(part_o(plan, slot, rows, HD) + (size_t)(u * kM + r) * HD + h * kCols);
-#pragma unroll 1
-                for (int c = 0; c < kCols / 32; ++c) {
-                    const uint32_t tO = tbase + 256 + u * HD + h * kCols + lane_off + c * 32;
-                    uint32_t orr[32];
-                    if (have_a) {
-                        tmem_ld32(tO, orr);
-                        tmem_ld_wait(orr);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) orr[e] = none || fa == 0.f ? 0u : __float_as_uint(__uint_as_float(orr[e]) * ga);
-                    if (have_b) {
-                        uint32_t ob[32];
-                        tmem_ld32(tO + HD, ob);
-                        tmem_ld_wait(ob);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!none && fb != 0.f) orr[e] = __float_as_uint(fmaf(__uint_as_float(ob[e]), gb, __uint_as_float(orr[e])));
-                    }
-                    if (row_live && whole) {
-                        uint32_t pk[2][8];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) pk[e >> 3][e & 7] = pack2<BF16>(__uint_as_float(orr[2 * e]), __uint_as_float(orr[2 * e + 1]));
-                        // (a row's sector at a time, where O is aligned to them)
-                        if (o32) {
-                            store_32(out + c * 4, pk[0]);
-                            store_32(out + c * 4 + 2, pk[1]);
-                        } else {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                out[c * 4 + q] = make_uint4(pk[q >> 1][4 * (q & 1)], pk[q >> 1][4 * (q & 1) + 1],
-                                                            pk[q >> 1][4 * (q & 1) + 2], pk[q >> 1][4 * (q & 1) + 3]);
-                        }
-                    } else if (row_live && !none) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const uint32_t f[8] = {orr[8 * q], orr[8 * q + 1], orr[8 * q + 2], orr[8 * q + 3],
-                                                   orr[8 * q + 4], orr[8 * q + 5], orr[8 * q + 6], orr[8 * q + 7]};
-                            store_32(part + c * 8 + q * 2, f);
-                        }
-                    }
-                    __syncwarp();
-                }
-                if (row_live && h == 0) {
-                    if (!whole) part_ml(plan, slot, rows)[u * kM + r] = make_float2(m, l);
-                    else if (P.lse)
-                        P.lse[(long long)(p.h * P.G + head) * P.total + orow] = none ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-                }
+                __syncwarp();
             }
-            // O is in registers or out: the next part's first products may overwrite it
-            tc_fence_before();
-            __syncwarp();
-            for (int u = 0; u < NT; ++u)
-                if (lane == 0 && (u ? st.n[1] : st.n[0]) > 0) mbar_arrive(BAR(C::O_EMPTY + u));
+            // O is in registers or out: the next part's first product may overwrite it
+            if (have_o) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(BAR(C::O_EMPTY + u));
+            }
+            if (row_live) {
+                if (!whole) part_ml(plan, slot, rows)[u * kM + r] = make_float2(m, l);
+                else if (P.lse)
+                    P.lse[(long long)(p.h * P.G + head) * P.total + orow] = none ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+            }
         }
     }
     tc_fence_before();
@@ -1168,7 +1236,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
 }
 
 // ------------------------------------------------------------------- the merge
-// Joins the partial rows of the items that stretches cut, a warp to a row or several, in a fixed order.
+// Joins the partial rows of the items that stretches cut, a warp to a row, in the order of the stretches.
 constexpr int kMergeCtas = 8 * kPrefillCtas;
 template <int HD>
 __global__ void __launch_bounds__(256) paged_prefill_merge_kernel(const PagedParams P, const int bf16) {
@@ -1177,7 +1245,6 @@ __global__ void __launch_bounds__(256) paged_prefill_merge_kernel(const PagedPar
     __shared__ int4 split_s[kPrefillCtas];
     __shared__ int before_s[kPrefillCtas];  // rows of the items that earlier stretches cut
     __shared__ int sums[8];
-    __shared__ float acc_s[8][HD];
     const int tm = kM / P.G, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Plan plan = plan_of(P, NT * tm);
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1198,16 +1265,10 @@ __global__ void __launch_bounds__(256) paged_prefill_merge_kernel(const PagedPar
     }
     if (threadIdx.x < kPrefillCtas) split_s[threadIdx.x] = mine, before_s[threadIdx.x] = incl - count;
     __syncthreads();
-    // warps to a row, which take its parts in turn: as many as there are rows few
-    int wpr = 1;
-    while (wpr < 8 && all * wpr * 2 <= kMergeCtas * 8) wpr *= 2;
-    const int rpc = 8 / wpr, sub = warp % wpr;  // rows of a CTA at a time
-    for (int x0 = blockIdx.x * rpc; x0 < all; x0 += kMergeCtas * rpc) {
-        const int x = x0 + warp / wpr;
-        const bool live = x < all;
-        const int c = warp_last_le(kPrefillCtas, live ? x : x0, [&](int i) { return (long long)before_s[i]; });
+    for (int x = blockIdx.x * 8 + warp; x < all; x += kMergeCtas * 8) {
+        const int c = warp_last_le(kPrefillCtas, x, [&](int i) { return (long long)before_s[i]; });
         const int4 it = split_s[c];
-        const int y = (live ? x : x0) - before_s[c], n = it.w;
+        const int y = x - before_s[c], n = it.w;
         const int t = y / P.G, head = y - t * P.G, u = t / tm, r = u * kM + (t - u * tm) * P.G + head;
         auto slot = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); };
         float M = -INFINITY, L = 0.f;
@@ -1231,38 +1292,20 @@ __global__ void __launch_bounds__(256) paged_prefill_merge_kernel(const PagedPar
             for (int q = 0; q < kPer; ++q) acc[q] *= alpha;
             const int m = min(32, n - base);
 #pragma unroll 4
-            for (int j = sub; j < m; j += wpr) {
+            for (int j = 0; j < m; ++j) {
                 const float* src = part_o(plan, slot(base + j), rows, HD) + (size_t)r * HD + lane * kPer;
                 const float fj = __shfl_sync(0xffffffffu, f, j);
                 const bool has = (use >> j) & 1u;
-                float v[kPer];
-                if constexpr (kPer == 2) {
-                    const float2 w = *reinterpret_cast<const float2*>(src);
-                    v[0] = w.x, v[1] = w.y;
-                } else {
 #pragma unroll
-                    for (int q = 0; q < kPer; q += 4) {
-                        const float4 w = *reinterpret_cast<const float4*>(src + q);
-                        v[q] = w.x, v[q + 1] = w.y, v[q + 2] = w.z, v[q + 3] = w.w;
-                    }
+                for (int q = 0; q < kPer; q += 2) {
+                    const float2 v = *reinterpret_cast<const float2*>(src + q);
+                    acc[q] = has ? fmaf(fj, v.x, acc[q]) : acc[q];
+                    acc[q + 1] = has ? fmaf(fj, v.y, acc[q + 1]) : acc[q + 1];
                 }
-#pragma unroll
-                for (int q = 0; q < kPer; ++q) acc[q] = has ? fmaf(fj, v[q], acc[q]) : acc[q];
             }
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-        if (wpr > 1) {
-            __syncthreads();  // (the sums of the rows before have been read)
-#pragma unroll
-            for (int q = 0; q < kPer; ++q) acc_s[warp][lane * kPer + q] = acc[q];
-            __syncthreads();
-            for (int i = 1; i < wpr; ++i)
-                if (sub == 0)
-#pragma unroll
-                    for (int q = 0; q < kPer; ++q) acc[q] += acc_s[warp + i][lane * kPer + q];
-        }
-        if (!live || sub != 0) continue;
         const bool none = M == -INFINITY;
         const float inv = none ? 0.f : 1.f / L;
         const long long orow = it.x + t;

@@ -2,11 +2,12 @@
 with the rotation and the writer as a serving program makes them.  Every call goes through the C ABI.
 
 Tolerances as for decode (test_paged_gpu.py): u(t) half a step of type t relative to the value; P is rounded to
-the rows' type before P V: u(P) sum p|v| / l; fp16 p below 2^-14 by 2^-25 a key, where the largest p of a row is
-2^-2 at least: 2^-23 a key relative to l; a score error ds changes every p by a factor of at most 1 + 2 ds; O is
-rounded once.  ds: fp32 sums of hd products and the hardware exponential, at most 2^-18 of the largest
-|scale q.k| sum of magnitudes, and 2^-19 of the softcap.  8-bit elements are compared as they are read: their
-fp32 product with the scale rounded to the rows' type.
+16 bits before P V (the rows' type over 16-bit pages, fp16 over 8-bit ones): u(P) sum p|v| / l; fp16 p below 2^-14 by
+2^-25 a key, where the largest p of a row is 2^-2 at least: 2^-23 a key relative to l; a score error ds changes
+every p by a factor of at most 1 + 2 ds; O is rounded once.  ds: fp32 sums of hd products and the hardware
+exponential, at most 2^-18 of the largest |scale q.k| sum of magnitudes, and 2^-19 of the softcap.  A value of an
+8-bit page enters as an fp16 number whose scale (relative to a power of two) and product are rounded, 2 u(fp16),
+where the scale is no power of two; below 2^-14 by 2^-25 of that power, at most 2^8 times a scale.
 """
 import math
 
@@ -23,31 +24,11 @@ pytestmark = pytest.mark.gpu
 TYPES = [("bf16", "bf16"), ("f16", "f16"), ("bf16", "e4m3"), ("f16", "e4m3"), ("bf16", "e5m2"), ("f16", "e5m2")]
 
 
-def read_tokens(c, lengths):
-    """Each sequence's tokens as the kernels read them (a page outside the pool: NaN)."""
-    if not is8(c.kind):
-        return c.tokens(lengths)
-    out = []
-    k, v, ks, vs = c.host()
-    for b, n in enumerate(lengths):
-        pair = []
-        for cache, scale in ((k, ks), (v, vs)):
-            x = np.full((n, c.Hkv, c.hd), np.nan)
-            for j in range((n + c.page - 1) // c.page):
-                pg, m = int(c.table[b, j]), min(c.page, n - j * c.page)
-                if 0 <= pg < len(cache):
-                    val = oracle.f8_values(c.kind).astype(np.float32)[cache[pg, :, :m]] * scale[pg].astype(np.float32)[:, None, None]
-                    x[j * c.page:j * c.page + m] = torch.from_numpy(val).to(T[c.dt]).double().numpy().transpose(1, 0, 2)
-            pair.append(x.reshape(n, c.Hkv * c.hd))
-        out.append(tuple(pair))
-    return out
-
-
 def check(c, q, lengths, cu, o, lse, tokens=None, rows=None, **flags):
     H, hd = q.shape[1] // c.hd, c.hd
     kw = dict(H=H, Hkv=c.Hkv, scale=1.0 / math.sqrt(hd))
     kw.update(flags)
-    tok = read_tokens(c, lengths) if tokens is None else tokens
+    tok = c.tokens(lengths) if tokens is None else tokens
     ro, rl = oracle.paged_prefill(f64(q), tok, lengths, cu, **kw)
     ra, _ = oracle.paged_prefill(f64(q), tok, lengths, cu, absolute=True, **kw)
     og, lg = f64(o), f64(lse)
@@ -60,8 +41,12 @@ def check(c, q, lengths, cu, o, lse, tokens=None, rows=None, **flags):
         qa = np.abs(f64(q)[r]).reshape(len(r), H, hd)
         smax = kw["scale"] * qa.max() * np.abs(k).reshape(n, c.Hkv, hd).sum(2).max(initial=0.0)
         ds = 2.0 ** -18 * smax + 2.0 ** -19 * kw.get("softcap", 0.0)
-        flush = n * 2.0 ** -23 * np.abs(v).max(initial=0.0) if c.dt == "f16" else 0.0
-        tol = U[c.dt] * np.abs(ro[r]) + (U[c.dt] + 2 * ds + 2.0 ** -16) * 1.02 * ra[r] + flush + TINY[c.dt]
+        up = 3 * U["f16"] if is8(c.kind) else U[c.dt]
+        flush = n * 2.0 ** -23 * np.abs(v).max(initial=0.0) if is8(c.kind) or c.dt == "f16" else 0.0
+        if is8(c.kind):
+            vs = f64(c.vs)
+            flush += 2.0 ** -25 * 2.0 ** 8 * np.abs(vs[np.isfinite(vs)]).max(initial=0.0)
+        tol = U[c.dt] * np.abs(ro[r]) + (up + 2 * ds + 2.0 ** -16) * 1.02 * ra[r] + flush + TINY[c.dt]
         assert np.isfinite(og[r]).all(), "sequence %d: not finite" % b
         bad = np.abs(og[r] - ro[r]) > tol
         assert not bad.any(), "sequence %d, %d rows of %d tokens: O off by %.3g where %.3g is allowed, first at row %d" % (
@@ -188,7 +173,7 @@ def test_what_a_row_does_not_see_has_no_effect(dt, kind, hd):
     cu = np.cumsum([0] + new)
     q = queries(int(cu[-1]), 4 * hd, dt, 4)
     kw = dict(H=4, window=50, **c.kw())
-    tokens = read_tokens(c, lengths)
+    tokens = c.tokens(lengths)
     bad = [NAN[kind], 0x7f] if is8(kind) else [float("nan"), float("inf")]
     wild = {0: [290, 329, 260], 1: [33, 69], 2: [497, 448]}
     for w, pool in enumerate((c.k, c.v)):
@@ -333,7 +318,7 @@ def test_pages_before_every_window_are_not_read():
     lengths, new = [900, 400], [33, 20]
     c = Cache("bf16", "e4m3", lengths, 2, 64, 16, seed=16)
     c.fill(lengths, 16)
-    tokens = read_tokens(c, lengths)
+    tokens = c.tokens(lengths)
     c.table[0, :(900 - 33 - 99) // 16] = -1
     c.table[1, :(400 - 20 - 99) // 16] = 10 ** 9
     c.table_d = i32(c.table)
@@ -370,7 +355,7 @@ def test_prefix_sums_out_of_range(cu, whole):
         assert (o[:10] == 7).all() and (o[50:] == 7).all()
     else:
         expect_flag()
-    tok = read_tokens(c, lengths)
+    tok = c.tokens(lengths)
     for b in whole:
         if cu == [0, 40, 30, 60] and b == 0:
             continue  # (its last rows are the third sequence's too)
