@@ -302,6 +302,38 @@ __device__ __forceinline__ Tiles tiles_of(const PagedParams& P, const Part& p, i
     return t;
 }
 
+// Bounded waits as mbar_wait and warp_wait, but a waiting warp sleeps until the phase completes (for up to a
+// millisecond at a time) instead of asking again and again: the others' asking took 40 % of the issue slots.
+__device__ __forceinline__ bool sleep_wait(uint32_t bar, uint32_t parity, unsigned int* status, unsigned int code,
+                                           volatile int* abort_flag) {
+    if (mbar_test_wait(bar, parity)) return true;
+    unsigned long long t0 = 0;
+#pragma unroll 1
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(1000000u)
+            : "memory");
+        if (ok) return true;
+        if (abort_flag && *abort_flag) return false;
+        const unsigned long long t = globaltimer();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > kWaitLimitNs) {
+            atomicOr(status, code);
+            if (abort_flag) *abort_flag = 1;
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool warp_sleep_wait(uint32_t bar, uint32_t parity, unsigned int* status, unsigned int code,
+                                                volatile int* abort_flag) {
+    return __all_sync(0xffffffffu, sleep_wait(bar, parity, status, code, abort_flag));
+}
+
 __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
@@ -489,7 +521,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                 int pg = n > 0 && col < kCols ? box_page(p, tile0 * BN + sub * box_rows, lo, hi) : -1;
                 for (int u = 0; ok && u < NT; ++u) {
                     if (tu[u].n == 0) continue;
-                    if (qn[u] > 0 && !warp_wait(BAR(C::Q_EMPTY + u), (qn[u] - 1) & 1, P.status, ST_FWD_PRODUCER, &abort_flag)) {
+                    if (qn[u] > 0 && !warp_sleep_wait(BAR(C::Q_EMPTY + u), (qn[u] - 1) & 1, P.status, ST_FWD_PRODUCER, &abort_flag)) {
                         ok = false;
                         break;
                     }
@@ -509,7 +541,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                     const int y = load ? ((pg * P.Hkv + p.h) << P.page_shift) + (key & (P.page_size - 1)) : 0;
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv) {
-                        if (!warp_wait(BAR(kEmpty + stage), phase, P.status, ST_FWD_PRODUCER, &abort_flag)) {
+                        if (!warp_sleep_wait(BAR(kEmpty + stage), phase, P.status, ST_FWD_PRODUCER, &abort_flag)) {
                             ok = false;
                             break;
                         }
@@ -527,94 +559,106 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
             }
             // every copy in flight lands before the CTA ends
             for (int u = 0; u < NT; ++u)
-                if (qn[u] > 0) mbar_wait(BAR(C::Q_FULL + u), (qn[u] - 1) & 1, P.status, ST_TEARDOWN, nullptr);
+                if (qn[u] > 0) sleep_wait(BAR(C::Q_FULL + u), (qn[u] - 1) & 1, P.status, ST_TEARDOWN, nullptr);
             for (int i = 0; i < made; ++i) {
                 if (--stage < 0) stage = kDepth - 1, phase ^= 1;
-                mbar_wait(BAR(kFull + stage), phase ^ 1, P.status, ST_TEARDOWN, nullptr);
+                sleep_wait(BAR(kFull + stage), phase ^ 1, P.status, ST_TEARDOWN, nullptr);
             }
         } else if (warp <= 8 + NT) {
             // -------------------------------------------------------- MMA issue
+            // (its loops are rolled up: a product takes longer than the loop's turn, and the fewer instructions all
+            // roles' loops have, the fewer are fetched again and again)
             const int u = warp - 9;
             constexpr uint32_t idS = idesc_f16(MB, kM, BN, false, false), idPV = idesc_f16(MB, kM, HD, false, true);
             const uint64_t qdesc = sdesc_sw128(sbase + u * C::kQBytes, 16, 1024);
+            const uint64_t kdesc0 = sdesc_sw128(sbase + C::kRingOff, 16, 1024);
+            const uint64_t vdesc0 = sdesc_sw128(sbase + C::kRingOff, BN * 128, 1024);
             const uint32_t tO = tbase + 256 + u * HD;
-            auto wait = [&](int bar, uint32_t parity) { return warp_wait(BAR(bar), parity, P.status, ST_FWD_MMA, &abort_flag); };
+            auto wait = [&](int bar, uint32_t parity) { return warp_sleep_wait(BAR(bar), parity, P.status, ST_FWD_MMA, &abort_flag); };
             bool ok = true;
-            unsigned g = 0;            // ring position of the part's first K tile
+            int rs = 0, vs = 0;           // stage of the ring that comes next, and V tile's place among the looked over
+            uint32_t rph = 0, vph = 0;    // their phases
             int sc = 0, pc = 0, act = 0;  // S issued, P taken, parts in which this tile was active
+            auto advance = [&]() {
+                if (++rs == NS) rs = 0, rph ^= 1;
+            };
+            // (by the one elected lane, as the rest of the issue)
+            auto issue_s = [&](int stage, bool last) {
+                const int buf = NT == 2 ? 0 : (sc & 1);
+                uint64_t qd = qdesc, kd = kdesc0 + (uint32_t)(stage * C::kTileBytes >> 4);
+#pragma unroll 1
+                for (int kk = 0; kk < HD / 16; ++kk) {
+                    mma_ss(tbase + (NT == 2 ? u * 128 : buf * 64), qd, kd, idS, kk > 0 ? 1u : 0u);
+                    const bool box = (kk & 3) == 3;  // the next 64 columns
+                    qd += box ? (kM * 128 - 96) >> 4 : 2;
+                    kd += box ? (BN * 128 - 96) >> 4 : 2;
+                }
+                mma_commit(BAR(C::S_FULL + (NT == 2 ? u : buf)));
+                if (last) mma_commit(BAR(C::Q_EMPTY + u));
+            };
             Walk w = walk_of(P, plan);
             Part p;
             while (ok && next_part(plan, w, p)) {
                 const int n = p.end - p.begin, tile0 = p.it.t0 + p.begin;
                 if (n <= 0) continue;
                 const Tiles my = tiles_of<BN>(P, p, u, tm);
-                auto has = [&](int i) { return tile0 + i >= my.t0 && tile0 + i < my.t0 + my.n; };
-                auto kst = [&](int i) { return (g + 2 * i) % NS; };
-                auto kph = [&](int i) { return ((g + 2 * i) / NS) & 1; };
-                auto vst = [&](int i) { return (g + 2 * i + 1) % NS; };
-                auto issue_s = [&](int i) {
-                    const uint32_t tS = tbase + (NT == 2 ? u * 128 : (sc & 1) * 64);
-                    const uint64_t kdesc = sdesc_sw128(sbase + C::kRingOff + kst(i) * C::kTileBytes, 16, 1024);
-#pragma unroll
-                    for (int kk = 0; kk < HD / 16; ++kk)
-                        mma_ss_e(tS, qdesc + (((kk >> 2) * (kM * 128) + (kk & 3) * 32) >> 4),
-                                 kdesc + (((kk >> 2) * (BN * 128) + (kk & 3) * 32) >> 4), idS, kk > 0 ? 1u : 0u);
-                    mma_commit_e(BAR(C::S_FULL + (NT == 2 ? u : (sc & 1))));
-                    ++sc;
-                    if (tile0 + i == my.t0 + my.n - 1) mma_commit_e(BAR(C::Q_EMPTY + u));
-                };
-                auto issue_pv = [&](int i, int k) {
-                    const uint32_t tS = tbase + (NT == 2 ? u * 128 : ((pc - 1) & 1) * 64);
-                    const uint64_t vdesc = sdesc_sw128(sbase + C::kRingOff + vst(i) * C::kTileBytes, BN * 128, 1024);
-                    const int skip = *static_cast<volatile int*>(&skip_pv[u][(pc - 1) & 1]);
-                    if (!skip) {
-#pragma unroll
-                        for (int kk = 0; kk < BN / 16; ++kk)
-                            mma_ts_e(tO, tS + kk * 8, vdesc + ((kk * 16 * 128) >> 4), idPV, (k > 0 || kk > 0) ? 1u : 0u);
-                    }
-                    if constexpr (NT == 1) mma_commit_e(BAR(C::PV_DONE + ((pc - 1) & 1)));
-                    if (k == my.n - 1) mma_commit_e(BAR(C::O_DONE + u));
-                };
+                const int i0 = my.t0 - tile0, i1 = i0 + my.n;  // the tiles of the part that this query tile takes
                 // A tile's release is committed only after the wait for its data, also for tiles that
                 // this query tile skips, so that no arrival belongs to a later use of the stage.
                 if (my.n > 0 && !wait((F8 && BF16 ? C::Q_WIDE : C::Q_FULL) + u, act & 1)) break;
-                if (!wait(C::FULL + kst(0), kph(0))) break;
-                tc_fence_after();
-                if (has(0)) issue_s(0);
-                mma_commit_e(BAR(C::EMPTY + kst(0)));
-                for (int i = 0; ok && i < n; ++i) {
-                    const int k = tile0 + i - my.t0;
-                    if constexpr (NT == 1) {
-                        if (i + 1 < n) {
-                            ok = wait(C::FULL + kst(i + 1), kph(i + 1));
-                            if (!ok) break;
-                            tc_fence_after();
-                            if (has(i + 1)) issue_s(i + 1);
-                            mma_commit_e(BAR(C::EMPTY + kst(i + 1)));
+                for (int i = -1; i < n; ++i) {
+                    // tile i's product with V, and S of tile i + 1: after it, or (one tile) before
+                    const bool now = i >= i0 && i < i1 && i >= 0, more = i + 1 < n, next = more && i + 1 >= i0 && i + 1 < i1;
+                    const bool first = i == i0, last = i == i1 - 1, next_last = i + 1 == i1 - 1;
+                    int vstage = 0;
+                    if (i >= 0) {
+                        vstage = rs;
+                        advance();
+                    }
+                    if (more && !(ok = wait(C::FULL + rs, rph))) break;
+                    if (NT == 1 || i < 0) {
+                        tc_fence_after();
+                        if (more && elect_one()) {
+                            if (next) issue_s(rs, next_last);
+                            mma_commit(BAR(C::EMPTY + rs));
                         }
+                        __syncwarp();
+                        if (next) ++sc;
                     }
-                    ok = wait(C::V_OK + (g / 2 + i) % NS, ((g / 2 + i) / NS) & 1);
-                    if (NT == 2 && ok && i + 1 < n) ok = wait(C::FULL + kst(i + 1), kph(i + 1));
-                    if (ok && has(i)) {
-                        ok = NT == 2 ? wait(C::P_FULL + u, pc & 1) : wait(C::P_FULL + (pc & 1), (pc >> 1) & 1);
-                        ++pc;
+                    if (i >= 0) {
+                        if (!(ok = wait(C::V_OK + vs, vph))) break;
+                        if (++vs == NS) vs = 0, vph ^= 1;
                         // the first product overwrites O: the last part's epilogue must have read it
-                        if (ok && k == 0 && act > 0) ok = wait(C::O_EMPTY + u, (act - 1) & 1);
+                        if (now && first && act > 0 && !(ok = wait(C::O_EMPTY + u, (act - 1) & 1))) break;
+                        const int pb = NT == 2 ? u : (pc & 1);
+                        if (now && !(ok = wait(C::P_FULL + pb, (NT == 2 ? pc : pc >> 1) & 1))) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            if (now) {
+                                if (!*static_cast<volatile int*>(&skip_pv[u][pc & 1])) {
+                                    const uint32_t tS = tbase + (NT == 2 ? u * 128 : (pc & 1) * 64);
+                                    const uint64_t vd = vdesc0 + (uint32_t)(vstage * C::kTileBytes >> 4);
+#pragma unroll 1
+                                    for (int kk = 0; kk < BN / 16; ++kk)
+                                        mma_ts(tO, tS + kk * 8, vd + kk * 128, idPV, (!first || kk > 0) ? 1u : 0u);
+                                }
+                                if constexpr (NT == 1) mma_commit(BAR(C::PV_DONE + (pc & 1)));
+                                if (last) mma_commit(BAR(C::O_DONE + u));
+                            }
+                            if (NT == 2 && next) issue_s(rs, next_last);
+                            mma_commit(BAR(C::EMPTY + vstage));
+                            if (NT == 2 && more) mma_commit(BAR(C::EMPTY + rs));
+                        }
+                        __syncwarp();
+                        if (now) ++pc;
+                        if (NT == 2 && next) ++sc;
                     }
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (has(i)) issue_pv(i, k);
-                    if constexpr (NT == 2) {
-                        if (i + 1 < n && has(i + 1)) issue_s(i + 1);
-                    }
-                    mma_commit_e(BAR(C::EMPTY + vst(i)));
-                    if (NT == 2 && i + 1 < n) mma_commit_e(BAR(C::EMPTY + kst(i + 1)));
+                    if (more) advance();
                 }
-                g += 2 * n;
                 if (my.n > 0) ++act;
             }
             mma_commit_e(BAR(C::MMA_DONE));
-            mbar_wait(BAR(C::MMA_DONE), 0, P.status, ST_TEARDOWN, nullptr);
+            sleep_wait(BAR(C::MMA_DONE), 0, P.status, ST_TEARDOWN, nullptr);
         } else if (warp == 11) {
             // ------------------------------------------------------ V looked over
             const int sub = lane < subs ? lane : 0;
@@ -641,8 +685,8 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                     // (the K tile too, though it is not looked at: a stage's uses are waited for one by one, since a
                     // phase that has not begun looks like one that is over)
                     const unsigned gk = g + 2 * i, gv = gk + 1, stage = gv % NS;
-                    ok = warp_wait(BAR(C::FULL + gk % NS), (gk / NS) & 1, P.status, ST_FWD_PRODUCER, &abort_flag) &&
-                         warp_wait(BAR(C::FULL + stage), (gv / NS) & 1, P.status, ST_FWD_PRODUCER, &abort_flag);
+                    ok = warp_sleep_wait(BAR(C::FULL + gk % NS), (gk / NS) & 1, P.status, ST_FWD_PRODUCER, &abort_flag) &&
+                         warp_sleep_wait(BAR(C::FULL + stage), (gv / NS) & 1, P.status, ST_FWD_PRODUCER, &abort_flag);
                     if (!ok) break;
                     bool bad = false;
                     if (j0 < all_lo || j0 + BN > all_hi || there != (1u << subs) - 1u) {
@@ -712,7 +756,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                     for (int u = 0; ok && u < NT; ++u) {
                         if (tiles_of<BN>(P, p, u, tm).n == 0) continue;
                         const int at = u ? qn[1]++ : qn[0]++;
-                        ok = warp_wait(BAR(C::Q_FULL + u), at & 1, P.status, ST_FWD_PRODUCER, &abort_flag);
+                        ok = warp_sleep_wait(BAR(C::Q_FULL + u), at & 1, P.status, ST_FWD_PRODUCER, &abort_flag);
                         if (!ok) break;
                         const int r = ww * 32 + lane;
                         uint8_t* row = smem + u * C::kQBytes + r * 128;
@@ -755,57 +799,41 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                     const uint32_t ratio = pack2<false>(r, r);  // of this lane's box
 #pragma unroll 1
                     for (int kv = 0; kv < 2; ++kv) {
-                        ok = warp_wait(BAR(C::RAW_FULL + raw), raw_phase, P.status, ST_FWD_PRODUCER, &abort_flag) &&
-                             warp_wait(BAR(C::EMPTY + stage), phase, P.status, ST_FWD_PRODUCER, &abort_flag);
+                        ok = warp_sleep_wait(BAR(C::RAW_FULL + raw), raw_phase, P.status, ST_FWD_PRODUCER, &abort_flag) &&
+                             warp_sleep_wait(BAR(C::EMPTY + stage), phase, P.status, ST_FWD_PRODUCER, &abort_flag);
                         if (!ok) break;
                         const uint8_t* src = smem + C::kRawOff + raw * C::kRawBytes;
                         const uint32_t dst = sbase + C::kRingOff + stage * C::kTileBytes;
                         // consecutive lanes: the chunks of a row, then of the next; this warp's rows lie together.
                         // Chunk c is columns 16c .. of the box: two chunks of a 128-byte column of the wide tile.  Lanes of
                         // either half of a row store them in the other order, so that eight lanes meet no bank twice.
-                        auto widen = [&](auto e4m3c, auto valuec) {
-                            constexpr int kAhead = 4;
-#pragma unroll 1
-                            for (int t0 = 0; t0 < kSteps; t0 += kAhead) {
-                                uint4 x[kAhead];
+                        const uint32_t factor = kv ? ratio : pack2<false>(1.f, 1.f);
+                        auto widen = [&](auto e4m3c) {
+#pragma unroll 2
+                            for (int t = 0; t < kSteps; ++t) {
+                                const int at = (ww * kSteps + t) * 32 + lane;
+                                const int c = at % kChunks, row = at / kChunks % BN, box = at / kChunks / BN;
+                                const uint4 x = *reinterpret_cast<const uint4*>(
+                                    src + box * (BN * C::kRawRow) + row * C::kRawRow +
+                                    (C::kRawRow == 128 ? (c ^ (row & 7)) << 4 : (c ^ ((row >> 1) & 3)) << 4));
+                                const bool swap = (c >> 2) & 1;
+                                uint32_t o[8];
+                                widen4<decltype(e4m3c)::value>(swap ? x.z : x.x, o[0], o[1]);
+                                widen4<decltype(e4m3c)::value>(swap ? x.w : x.y, o[2], o[3]);
+                                widen4<decltype(e4m3c)::value>(swap ? x.x : x.z, o[4], o[5]);
+                                widen4<decltype(e4m3c)::value>(swap ? x.y : x.w, o[6], o[7]);
+                                const uint32_t f = __shfl_sync(0xffffffffu, factor, row >> box_shift);
 #pragma unroll
-                                for (int t = 0; t < kAhead; ++t) {
-                                    const int at = (ww * kSteps + t0 + t) * 32 + lane;
-                                    const int c = at % kChunks, row = at / kChunks % BN, box = at / kChunks / BN;
-                                    x[t] = *reinterpret_cast<const uint4*>(
-                                        src + box * (BN * C::kRawRow) + row * C::kRawRow +
-                                        (C::kRawRow == 128 ? (c ^ (row & 7)) << 4 : (c ^ ((row >> 1) & 3)) << 4));
-                                }
-#pragma unroll
-                                for (int t = 0; t < kAhead; ++t) {
-                                    const int at = (ww * kSteps + t0 + t) * 32 + lane;
-                                    const int c = at % kChunks, row = at / kChunks % BN, box = at / kChunks / BN;
-                                    const bool swap = (c >> 2) & 1;
-                                    uint32_t o[8];
-                                    widen4<decltype(e4m3c)::value>(swap ? x[t].z : x[t].x, o[0], o[1]);
-                                    widen4<decltype(e4m3c)::value>(swap ? x[t].w : x[t].y, o[2], o[3]);
-                                    widen4<decltype(e4m3c)::value>(swap ? x[t].x : x[t].z, o[4], o[5]);
-                                    widen4<decltype(e4m3c)::value>(swap ? x[t].y : x[t].w, o[6], o[7]);
-                                    if constexpr (decltype(valuec)::value) {
-                                        const uint32_t f = __shfl_sync(0xffffffffu, ratio, row >> box_shift);
-#pragma unroll
-                                        for (int e = 0; e < 8; ++e) o[e] = mul_h2(o[e], f);
-                                    }
-                                    const int wide = box * (kChunks / 4) + (c >> 2), c2 = (2 * c) & 7;
-                                    const uint32_t to = dst + wide * (BN * 128) + row * 128;
-                                    const uint32_t a0 = to + ((c2 ^ (row & 7)) << 4), a1 = to + (((c2 + 1) ^ (row & 7)) << 4);
-                                    st_shared_v4(swap ? a1 : a0, o[0], o[1], o[2], o[3]);
-                                    st_shared_v4(swap ? a0 : a1, o[4], o[5], o[6], o[7]);
-                                }
+                                for (int e = 0; e < 8; ++e) o[e] = mul_h2(o[e], f);
+                                const int wide = box * (kChunks / 4) + (c >> 2), c2 = (2 * c) & 7;
+                                const uint32_t to = dst + wide * (BN * 128) + row * 128;
+                                const uint32_t a0 = to + ((c2 ^ (row & 7)) << 4), a1 = to + (((c2 + 1) ^ (row & 7)) << 4);
+                                st_shared_v4(swap ? a1 : a0, o[0], o[1], o[2], o[3]);
+                                st_shared_v4(swap ? a0 : a1, o[4], o[5], o[6], o[7]);
                             }
                         };
-                        if (e4m3) {
-                            if (kv) widen(std::true_type(), std::true_type());
-                            else widen(std::true_type(), std::false_type());
-                        } else {
-                            if (kv) widen(std::false_type(), std::true_type());
-                            else widen(std::false_type(), std::false_type());
-                        }
+                        if (e4m3) widen(std::true_type());
+                        else widen(std::false_type());
                         fence_proxy_async_smem();  // the tensor cores read the tile through the async proxy
                         __syncwarp();
                         if (lane == 0) {
@@ -832,7 +860,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
         constexpr float kTop = PRange<MB>::top;
         constexpr int NC = BN / 32;
         auto wait = [&](int bar, uint32_t parity) {
-            return __all_sync(0xffffffffu, mbar_wait(BAR(bar), parity, P.status, ST_FWD_SOFTMAX, &abort_flag));
+            return __all_sync(0xffffffffu, sleep_wait(BAR(bar), parity, P.status, ST_FWD_SOFTMAX, &abort_flag));
         };
         bool ok = true;
         int sc = 0, act = 0;  // tiles done, parts in which this tile was active
@@ -919,98 +947,92 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                uint32_t sv[NC][32];
-#pragma unroll
-                for (int c = 0; c < NC; ++c) tmem_ld32(tS + c * 32, sv[c]);
                 if (alt && (u == 0 ? (k >= 1 && k - 1 < nB) : (k < nA))) {
                     const int need = 4 * (u == 0 ? bB + k : bA + k + 1);
                     const bool rr = count_wait(&done_count[u ^ 1], need, P.status, ST_FWD_SOFTMAX, &abort_flag);
                     if (!__all_sync(0xffffffffu, rr)) {
-                        tmem_ld_wait_only();
                         ok = false;
                         break;
                     }
                 }
-                tmem_ld_wait_only();
-#pragma unroll
-                for (int c = 0; c < NC; ++c) tmem_pin(sv[c]);
-                if constexpr (F8) {
-                    // raw scores in units of 1: the scale of the keys' page, and the power of two of the row of Q
-                    if (BF16 && k == 0) {
-                        const int ex = reinterpret_cast<const volatile short*>(smem + C::kQexpOff)[((act & 1) * 2 + u) * kM + r];
-                        qf = __uint_as_float((uint32_t)(ex + 127) << 23);
-                    }
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) {
-                        const float f0 = __shfl_sync(0xffffffffu, scale.x, (32 * c) >> box_shift) * qf;
-                        const float f1 = __shfl_sync(0xffffffffu, scale.x, (32 * c + 16) >> box_shift) * qf;
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const float f = e < 16 ? f0 : f1;
-                            float x, y;
-                            f2_split(f2_mul(f2_make(__uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1])), f2_make(f, f)), x, y);
-                            sv[c][e] = __float_as_uint(x);
-                            sv[c][e + 1] = __float_as_uint(y);
-                        }
-                    }
+                if (F8 && BF16 && k == 0) {
+                    const int ex = reinterpret_cast<const volatile short*>(smem + C::kQexpOff)[((act & 1) * 2 + u) * kM + r];
+                    qf = __uint_as_float((uint32_t)(ex + 127) << 23);
                 }
+                // ---- the keys of the tile that this row sees: [va, vb), in boxes that are there
+                int va = 0, vb = BN;
+                if (!full) {
+                    long long x = lo - j0, y = hi - j0;
+                    if (P.wl >= 0) x = max(x, (long long)pos - P.wl - j0);
+                    if (P.wr >= 0) y = min(y, (long long)pos + P.wr - j0 + 1);
+                    va = (int)min(max(x, 0ll), (long long)BN);
+                    vb = row_live ? (int)min(max(y, (long long)va), (long long)BN) : va;
+                }
+                // The row's scores chunk by chunk out of TMEM, the next chunk on its way, in two passes: the maximum, then p.
+                // Rolled up, the loops take a few kilobytes of instructions; with the 128 scores held in registers and
+                // everything unrolled, warps waited for their instructions a fifth of the time (over 8-bit pages,
+                // with the widening warps' besides, half of it).
+                auto chunks = [&](bool masked, auto fn) {
+                    uint32_t xa[32];
+                    auto prepare = [&](uint32_t (&x)[32], int c) {
+                        if constexpr (F8) {
+                            // raw scores in units of 1: the scale of the keys' page, and the power of two of the row of Q
+                            const float f0 = __shfl_sync(0xffffffffu, scale.x, (32 * c) >> box_shift) * qf;
+                            const float f1 = __shfl_sync(0xffffffffu, scale.x, (32 * c + 16) >> box_shift) * qf;
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) {
+                                const float f = e < 16 ? f0 : f1;
+                                float y, z;
+                                f2_split(f2_mul(f2_make(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), f2_make(f, f)), y, z);
+                                x[e] = __float_as_uint(y);
+                                x[e + 1] = __float_as_uint(z);
+                            }
+                        }
+                        if (masked && __builtin_expect(!full, 0)) {
+                            const int c0 = min(max(va - 32 * c, 0), 32), c1 = min(max(vb - 32 * c, 0), 32);
+                            uint32_t see = bit_range(c0, c1 - c0);
+                            if (there != (1u << subs) - 1u) {  // boxes of 16, 32 or 64 keys
+                                const int q = (32 * c) >> box_shift;
+                                uint32_t have = ((there >> q) & 1u) ? 0xffffffffu : 0u;
+                                if (box_rows == 16) have = (have & 0xffffu) | (((there >> (q + 1)) & 1u) ? 0xffff0000u : 0u);
+                                see &= have;
+                            }
+                            if (!__all_sync(0xffffffffu, see == 0xffffffffu)) {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) x[e] = (see >> e) & 1u ? x[e] : 0xff800000u;  // -inf
+                            }
+                        }
+                    };
+#pragma unroll 1
+                    for (int c = 0; c < NC; ++c) {
+                        tmem_ld32(tS + c * 32, xa);
+                        tmem_ld_wait(xa);
+                        prepare(xa, c);
+                        fn(xa, c);
+                    }
+                };
+                auto largest = [&](const uint32_t (&x)[32], bool magnitude) {
+                    float y[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float x0 = __uint_as_float(x[e]), x1 = __uint_as_float(x[e + 1]);
+                        y[(e >> 1) & 1] = max3f(y[(e >> 1) & 1], magnitude ? fabsf(x0) : x0, magnitude ? fabsf(x1) : x1);
+                    }
+                    return fmaxf(y[0], y[1]);
+                };
+                // the form of the softcap: by exp where a raw score of the warp lies outside the fit's range
                 bool accurate = false, shorter = false;
                 if constexpr (CAP) {
-                    float am[NC];
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) {
-                        am[c] = 0.f;
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2)
-                            am[c] = max3f(am[c], fabsf(__uint_as_float(sv[c][e])), fabsf(__uint_as_float(sv[c][e + 1])));
-                    }
-                    float amax = fmaxf(am[0], am[1]);
-                    if constexpr (NC == 4) amax = fmaxf(amax, fmaxf(am[2], am[3]));
+                    float amax = 0.f;
+                    chunks(false, [&](uint32_t (&x)[32], int) { amax = fmaxf(amax, largest(x, true)); });
                     const CapPoly cp = cap_poly(P.scale, P.softcap);
                     accurate = __any_sync(0xffffffffu, !(amax <= cp.r_max)) || (!full && !cp.inf_ok);
                     const CapShort cs = cap_short(P.scale, P.softcap);
                     shorter = !accurate && __all_sync(0xffffffffu, amax <= cs.r_max) && (full || cs.inf_ok);
                 }
-                uint32_t seen[NC];  // the keys of the tile that this row sees
-#pragma unroll
-                for (int c = 0; c < NC; ++c) seen[c] = 0xffffffffu;
-                if (!full) {
-                    long long vlo = lo - j0, vhi = hi - j0;
-                    if (P.wl >= 0) vlo = max(vlo, (long long)pos - P.wl - j0);
-                    if (P.wr >= 0) vhi = min(vhi, (long long)pos + P.wr - j0 + 1);
-                    const int a = (int)min(max(vlo, 0ll), (long long)BN), b = row_live ? (int)min(max(vhi, (long long)a), (long long)BN) : a;
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) {
-                        const int c0 = min(max(a - 32 * c, 0), 32), c1 = min(max(b - 32 * c, 0), 32);
-                        seen[c] = bit_range(c0, c1 - c0);
-                    }
-                    if (there != (1u << subs) - 1u) {
-#pragma unroll
-                        for (int c = 0; c < NC; ++c) {  // boxes of 16, 32 or 64 keys
-                            const int x = 32 * c / box_rows;
-                            uint32_t have = ((there >> x) & 1u) ? 0xffffffffu : 0u;
-                            if (box_rows == 16) have = (have & 0xffffu) | (((there >> (x + 1)) & 1u) ? 0xffff0000u : 0u);
-                            seen[c] &= have;
-                        }
-                    }
-#pragma unroll
-                    for (int c = 0; c < NC; ++c)
-                        if (!__all_sync(0xffffffffu, seen[c] == 0xffffffffu)) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) sv[c][e] = (seen[c] >> e) & 1u ? sv[c][e] : 0xff800000u;  // -inf
-                        }
-                }
                 // ---- the row's largest score, as x against its reference
-                float rm[NC];
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    rm[c] = -INFINITY;
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        rm[c] = max3f(rm[c], __uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1]));
-                }
-                float rmax = fmaxf(rm[0], rm[1]);
-                if constexpr (NC == 4) rmax = fmaxf(rmax, fmaxf(rm[2], rm[3]));
+                float rmax = -INFINITY;
+                chunks(true, [&](uint32_t (&x)[32], int) { rmax = fmaxf(rmax, largest(x, false)); });
                 float xm, xm_;
                 {
                     const uint64_t r2 = f2_make(rmax, rmax), n2 = f2_make(-m, -m);
@@ -1022,9 +1044,9 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                     f2_split(x2, xm, xm_);
                 }
                 if (rmax == -INFINITY) xm = -INFINITY;
-                const bool move = xm > kTop || (l == 0.f && xm < kTop - 10.f && xm != -INFINITY);
+                const bool move = row_live && (xm > kTop || (l == 0.f && xm < kTop - 10.f && xm != -INFINITY));
                 bool o_stands = NT == 2;  // the product of the tile before is complete
-                if (__any_sync(0xffffffffu, move)) {
+                if (__builtin_expect(__any_sync(0xffffffffu, move), 0)) {
                     // rows that have seen nothing hold O = 0: their reference may move by any amount
                     const float by = xm - (kTop - 8.f);
                     const float alpha = fast_exp2(move && l > 0.f ? -by : 0.f);
@@ -1052,26 +1074,26 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                         }
                     }
                 }
-                // ---- p, chunk by chunk over S
+                // ---- p over S, behind the chunks that have been loaded
                 auto p_pass = [&](auto modec) {
                     const uint64_t nm = f2_make(-m, -m);
-                    uint64_t rs[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) {
+                    uint64_t rs0 = f2_make(0.f, 0.f), rs1 = f2_make(0.f, 0.f);
+                    chunks(true, [&](uint32_t (&x)[32], int c) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             float x0, x1;
-                            f2_split(to_x(modec, f2_make(__uint_as_float(sv[c][2 * e]), __uint_as_float(sv[c][2 * e + 1])), nm), x0, x1);
+                            f2_split(to_x(modec, f2_make(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), nm), x0, x1);
                             const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);  // 2^-inf = 0
-                            rs[e & 1] = f2_add(rs[e & 1], f2_make(p0, p1));
+                            if (e & 1) rs1 = f2_add(rs1, f2_make(p0, p1));
+                            else rs0 = f2_add(rs0, f2_make(p0, p1));
                             pk[e] = pack2<MB>(p0, p1);
                         }
                         tmem_st16(tS + c * 16, pk);
-                    }
+                    });
                     float a0, a1, b0, b1;
-                    f2_split(rs[0], a0, a1);
-                    f2_split(rs[1], b0, b1);
+                    f2_split(rs0, a0, a1);
+                    f2_split(rs1, b0, b1);
                     l += (a0 + b0) + (a1 + b1);
                 };
                 if (!CAP) p_pass(M0());
@@ -1124,10 +1146,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                                 }
                                 float pj = (j & 1) ? p1 : p0;
                                 if (F8 && odd) pj *= __shfl_sync(0xffffffffu, scale.y * vref.inv, j >> box_shift);
-                                uint32_t sw = 0;
-#pragma unroll
-                                for (int x = 0; x < NC; ++x) sw = (j >> 5) == x ? seen[x] : sw;
-                                const bool see = (sw >> (j & 31)) & 1u;
+                                const bool see = j >= va && j < vb && ((there >> (j >> box_shift)) & 1u);
 #pragma unroll
                                 for (int q = 0; q < 4; ++q) {
                                     const uint4 v = *reinterpret_cast<const uint4*>(col + j * 128 + ((((c & 1) * 4 + q) ^ (j & 7)) << 4));
