@@ -744,6 +744,22 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
             const int sub = lane % subs;
             bool ok = true;
             int stage = 0, phase = 1, raw = 0, raw_phase = 0;
+            // This lane's chunk of 16 codes (columns 16c .. of a box's row) in steps of kRowsStep rows, the warp's 32 rows
+            // together: where it lies, and the two chunks of a 128-byte column of the wide tile that it becomes, by the
+            // step's parity.  Lanes of either half of a row store those in the other order, so that eight lanes
+            // meet no bank twice.
+            constexpr int kRowsStep = 32 / kChunks, kStepRaw = kRowsStep * C::kRawRow;
+            const int c = lane % kChunks, row0 = ww * 32 % BN, box = ww * 32 / BN;
+            const bool swap = (c >> 2) & 1;
+            uint32_t from[2], to0[2], to1[2];
+#pragma unroll
+            for (int o2 = 0; o2 < 2; ++o2) {
+                const int row = row0 + o2 * kRowsStep + lane / kChunks, c2 = (2 * c) & 7;
+                from[o2] = box * (BN * C::kRawRow) + row * C::kRawRow + (C::kRawRow == 128 ? (c ^ (row & 7)) << 4 : (c ^ ((row >> 1) & 3)) << 4);
+                const uint32_t to = (box * (kChunks / 4) + (c >> 2)) * (BN * 128) + row * 128;
+                to0[o2] = to + (((c2 + (swap ? 1 : 0)) ^ (row & 7)) << 4);
+                to1[o2] = to + (((c2 + (swap ? 0 : 1)) ^ (row & 7)) << 4);
+            }
             int qn[2] = {0, 0};  // parts in which a tile was active
             Walk w = walk_of(P, plan);
             Part p;
@@ -809,27 +825,22 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                         // either half of a row store them in the other order, so that eight lanes meet no bank twice.
                         const uint32_t factor = kv ? ratio : pack2<false>(1.f, 1.f);
                         auto widen = [&](auto e4m3c) {
-#pragma unroll 2
-                            for (int t = 0; t < kSteps; ++t) {
-                                const int at = (ww * kSteps + t) * 32 + lane;
-                                const int c = at % kChunks, row = at / kChunks % BN, box = at / kChunks / BN;
-                                const uint4 x = *reinterpret_cast<const uint4*>(
-                                    src + box * (BN * C::kRawRow) + row * C::kRawRow +
-                                    (C::kRawRow == 128 ? (c ^ (row & 7)) << 4 : (c ^ ((row >> 1) & 3)) << 4));
-                                const bool swap = (c >> 2) & 1;
-                                uint32_t o[8];
-                                widen4<decltype(e4m3c)::value>(swap ? x.z : x.x, o[0], o[1]);
-                                widen4<decltype(e4m3c)::value>(swap ? x.w : x.y, o[2], o[3]);
-                                widen4<decltype(e4m3c)::value>(swap ? x.x : x.z, o[4], o[5]);
-                                widen4<decltype(e4m3c)::value>(swap ? x.y : x.w, o[6], o[7]);
-                                const uint32_t f = __shfl_sync(0xffffffffu, factor, row >> box_shift);
+#pragma unroll 1
+                            for (int t = 0; t < kSteps; t += 2) {
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) o[e] = mul_h2(o[e], f);
-                                const int wide = box * (kChunks / 4) + (c >> 2), c2 = (2 * c) & 7;
-                                const uint32_t to = dst + wide * (BN * 128) + row * 128;
-                                const uint32_t a0 = to + ((c2 ^ (row & 7)) << 4), a1 = to + (((c2 + 1) ^ (row & 7)) << 4);
-                                st_shared_v4(swap ? a1 : a0, o[0], o[1], o[2], o[3]);
-                                st_shared_v4(swap ? a0 : a1, o[4], o[5], o[6], o[7]);
+                                for (int o2 = 0; o2 < 2; ++o2) {
+                                    const uint4 x = *reinterpret_cast<const uint4*>(src + from[o2] + t * kStepRaw);
+                                    const uint32_t f = __shfl_sync(0xffffffffu, factor, (row0 + (t + o2) * kRowsStep) >> box_shift);
+                                    uint32_t o[8];
+                                    widen4<decltype(e4m3c)::value>(swap ? x.z : x.x, o[0], o[1]);
+                                    widen4<decltype(e4m3c)::value>(swap ? x.w : x.y, o[2], o[3]);
+                                    widen4<decltype(e4m3c)::value>(swap ? x.x : x.z, o[4], o[5]);
+                                    widen4<decltype(e4m3c)::value>(swap ? x.y : x.w, o[6], o[7]);
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e) o[e] = mul_h2(o[e], f);
+                                    st_shared_v4(dst + to0[o2] + t * (kRowsStep * 128), o[0], o[1], o[2], o[3]);
+                                    st_shared_v4(dst + to1[o2] + t * (kRowsStep * 128), o[4], o[5], o[6], o[7]);
+                                }
                             }
                         };
                         if (e4m3) widen(std::true_type());
@@ -908,7 +919,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
             const int nA = u == 0 ? my.n : other.n, nB = u == 0 ? other.n : my.n, bA = base[0], bB = base[1];
             // (a tile whose keys begin more than one tile before the other's would wait for a turn that needs a
             // stage of the ring that only its own product frees; 128 rows apart they never do)
-            const bool alt = NT == 2 && abs(my.t0 - other.t0) <= 1;
+            const bool alt = NT == 2 && !F8 && abs(my.t0 - other.t0) <= 1;
             base[0] += nA;
             base[1] += nB;
             const unsigned g0 = g;
@@ -919,6 +930,9 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
             const bool row_live = tok < my.ntok;
             const int pos = my.pos + tok;
             float m = 8.f - kTop, l = 0.f;
+            // the first keys of the tiles that every row sees whole: from full_lo to full_hi
+            const int full_lo = P.wl >= 0 ? (int)max((long long)my.pos + my.ntok - 1 - P.wl, 0ll) : 0;
+            const int full_hi = (P.wr >= 0 ? (int)min((long long)p.it.len, max((long long)my.pos + P.wr + 1, 0ll)) : p.it.len) - BN;
             const int sub = lane < subs ? lane : 0;
             int pg = my.n > 0 ? box_page(p, my.t0 * BN + sub * box_rows, lo, hi) : -1;
             // (8-bit pools) vref, the scales of the tile's boxes, those of the next, and this row's factor
@@ -938,8 +952,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                 } else {
                     if (k + 1 < my.n) pg = box_page(p, j0 + BN + sub * box_rows, lo, hi);
                 }
-                const bool full = there == (1u << subs) - 1u &&
-                                  tile_full(P.wl, P.wr, p.it.len, my.pos, my.pos + my.ntok - 1, j0, j0 + BN);
+                const bool full = there == (1u << subs) - 1u && j0 >= full_lo && j0 <= full_hi;
                 const int sbuf = NT == 2 ? u : (sc & 1);
                 const uint32_t tS = tbase + (NT == 2 ? u * 128 : (sc & 1) * 64) + lane_off;
                 if (!wait(C::S_FULL + sbuf, NT == 2 ? sc & 1 : (sc >> 1) & 1)) {
@@ -947,13 +960,26 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                     break;
                 }
                 tc_fence_after();
+                // 16-bit pools keep the row's scores in registers; with the widening's instructions besides, over 8-bit ones
+                // they are loaded chunk by chunk
+                constexpr bool kHold = !F8 && NT == 2;
+                uint32_t sv[kHold ? NC : 1][32];
+                if constexpr (kHold)
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) tmem_ld32(tS + c * 32, sv[c]);
                 if (alt && (u == 0 ? (k >= 1 && k - 1 < nB) : (k < nA))) {
                     const int need = 4 * (u == 0 ? bB + k : bA + k + 1);
                     const bool rr = count_wait(&done_count[u ^ 1], need, P.status, ST_FWD_SOFTMAX, &abort_flag);
                     if (!__all_sync(0xffffffffu, rr)) {
+                        if constexpr (kHold) tmem_ld_wait_only();
                         ok = false;
                         break;
                     }
+                }
+                if constexpr (kHold) {
+                    tmem_ld_wait_only();
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) tmem_pin(sv[c]);
                 }
                 if (F8 && BF16 && k == 0) {
                     const int ex = reinterpret_cast<const volatile short*>(smem + C::kQexpOff)[((act & 1) * 2 + u) * kM + r];
@@ -972,43 +998,52 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                 // Rolled up, the loops take a few kilobytes of instructions; with the 128 scores held in registers and
                 // everything unrolled, warps waited for their instructions a fifth of the time (over 8-bit pages,
                 // with the widening warps' besides, half of it).
+                // (8-bit pools) a raw score in units of 1: the scale of the keys' page, and the power of two of the row of Q
+                // (applied as the scores are loaded where a softcap or a mask follows, else with the factor log2(e) scale)
+                const bool scale_first = CAP || !full;
+                auto page_unit = [&](int c, int half) { return __shfl_sync(0xffffffffu, scale.x, (32 * c + 16 * half) >> box_shift) * qf; };
+                auto unit = [&](int c, int half) { return scale_first ? 1.f : page_unit(c, half); };
+                auto scaled = [&](uint32_t (&x)[32], int c) {
+                    const float f0 = page_unit(c, 0), f1 = page_unit(c, 1);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float f = e < 16 ? f0 : f1;
+                        float y, z;
+                        f2_split(f2_mul(f2_make(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), f2_make(f, f)), y, z);
+                        x[e] = __float_as_uint(y);
+                        x[e + 1] = __float_as_uint(z);
+                    }
+                };
+                auto prepare = [&](uint32_t (&x)[32], int c, bool masked) {
+                    if (F8 && scale_first) scaled(x, c);
+                    if (masked && __builtin_expect(!full, 0)) {
+                        const int c0 = min(max(va - 32 * c, 0), 32), c1 = min(max(vb - 32 * c, 0), 32);
+                        uint32_t see = bit_range(c0, c1 - c0);
+                        if (there != (1u << subs) - 1u) {  // boxes of 16, 32 or 64 keys
+                            const int q = (32 * c) >> box_shift;
+                            uint32_t have = ((there >> q) & 1u) ? 0xffffffffu : 0u;
+                            if (box_rows == 16) have = (have & 0xffffu) | (((there >> (q + 1)) & 1u) ? 0xffff0000u : 0u);
+                            see &= have;
+                        }
+                        if (!__all_sync(0xffffffffu, see == 0xffffffffu)) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[e] = (see >> e) & 1u ? x[e] : 0xff800000u;  // -inf
+                        }
+                    }
+                };
                 auto chunks = [&](bool masked, auto fn) {
-                    uint32_t xa[32];
-                    auto prepare = [&](uint32_t (&x)[32], int c) {
-                        if constexpr (F8) {
-                            // raw scores in units of 1: the scale of the keys' page, and the power of two of the row of Q
-                            const float f0 = __shfl_sync(0xffffffffu, scale.x, (32 * c) >> box_shift) * qf;
-                            const float f1 = __shfl_sync(0xffffffffu, scale.x, (32 * c + 16) >> box_shift) * qf;
+                    if constexpr (kHold) {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                const float f = e < 16 ? f0 : f1;
-                                float y, z;
-                                f2_split(f2_mul(f2_make(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), f2_make(f, f)), y, z);
-                                x[e] = __float_as_uint(y);
-                                x[e + 1] = __float_as_uint(z);
-                            }
-                        }
-                        if (masked && __builtin_expect(!full, 0)) {
-                            const int c0 = min(max(va - 32 * c, 0), 32), c1 = min(max(vb - 32 * c, 0), 32);
-                            uint32_t see = bit_range(c0, c1 - c0);
-                            if (there != (1u << subs) - 1u) {  // boxes of 16, 32 or 64 keys
-                                const int q = (32 * c) >> box_shift;
-                                uint32_t have = ((there >> q) & 1u) ? 0xffffffffu : 0u;
-                                if (box_rows == 16) have = (have & 0xffffu) | (((there >> (q + 1)) & 1u) ? 0xffff0000u : 0u);
-                                see &= have;
-                            }
-                            if (!__all_sync(0xffffffffu, see == 0xffffffffu)) {
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) x[e] = (see >> e) & 1u ? x[e] : 0xff800000u;  // -inf
-                            }
-                        }
-                    };
+                        for (int c = 0; c < NC; ++c) fn(sv[c], c);
+                    } else {
 #pragma unroll 1
-                    for (int c = 0; c < NC; ++c) {
-                        tmem_ld32(tS + c * 32, xa);
-                        tmem_ld_wait(xa);
-                        prepare(xa, c);
-                        fn(xa, c);
+                        for (int c = 0; c < NC; ++c) {
+                            uint32_t x[32];
+                            tmem_ld32(tS + c * 32, x);
+                            tmem_ld_wait(x);
+                            prepare(x, c, masked);
+                            fn(x, c);
+                        }
                     }
                 };
                 auto largest = [&](const uint32_t (&x)[32], bool magnitude) {
@@ -1030,9 +1065,30 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                     const CapShort cs = cap_short(P.scale, P.softcap);
                     shorter = !accurate && __all_sync(0xffffffffu, amax <= cs.r_max) && (full || cs.inf_ok);
                 }
+                if (kHold && !full) {
+#pragma unroll
+                    for (int c = 0; c < (kHold ? NC : 0); ++c) prepare(sv[c], c, true);
+                }
                 // ---- the row's largest score, as x against its reference
                 float rmax = -INFINITY;
-                chunks(true, [&](uint32_t (&x)[32], int) { rmax = fmaxf(rmax, largest(x, false)); });
+                chunks(true, [&](uint32_t (&x)[32], int c) {
+                    if constexpr (F8 && !CAP) {
+                        const float f0 = unit(c, 0), f1 = unit(c, 1);
+                        float y[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) y[e >> 4] = max3f(y[e >> 4], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                        if (__builtin_expect(f0 < 0.f || f1 < 0.f, 0)) {  // (the same for all of a warp's rows)
+                            float z[2] = {INFINITY, INFINITY};
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) z[e >> 4] = fminf(z[e >> 4], __uint_as_float(x[e]));
+                            if (f0 < 0.f) y[0] = z[0];
+                            if (f1 < 0.f) y[1] = z[1];
+                        }
+                        rmax = max3f(rmax, y[0] * f0, y[1] * f1);
+                    } else {
+                        rmax = fmaxf(rmax, largest(x, false));
+                    }
+                });
                 float xm, xm_;
                 {
                     const uint64_t r2 = f2_make(rmax, rmax), n2 = f2_make(-m, -m);
@@ -1080,10 +1136,17 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                     uint64_t rs0 = f2_make(0.f, 0.f), rs1 = f2_make(0.f, 0.f);
                     chunks(true, [&](uint32_t (&x)[32], int c) {
                         uint32_t pk[16];
+                        uint64_t f2[2] = {sl2_2, sl2_2};
+                        if constexpr (F8 && !CAP) {
+                            const float f0 = unit(c, 0) * sl2, f1 = unit(c, 1) * sl2;
+                            f2[0] = f2_make(f0, f0);
+                            f2[1] = f2_make(f1, f1);
+                        }
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             float x0, x1;
-                            f2_split(to_x(modec, f2_make(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), nm), x0, x1);
+                            const uint64_t rr = f2_make(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+                            f2_split(F8 && !CAP ? f2_fma(rr, f2[e >> 3], nm) : to_x(modec, rr, nm), x0, x1);
                             const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);  // 2^-inf = 0
                             if (e & 1) rs1 = f2_add(rs1, f2_make(p0, p1));
                             else rs0 = f2_add(rs0, f2_make(p0, p1));
