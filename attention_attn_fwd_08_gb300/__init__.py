@@ -1003,8 +1003,9 @@ def attn_paged_gather(k_cache, v_cache, page_table, cu_seqlens, total, *, Hkv, d
                       k_out=None, v_out=None, stream=None):
     """Reads a paged cache back: token i of sequence b into row cu_seqlens[b] + i of
     (k_out, v_out), [total, Hkv*hd] of dtype (torch.float16 or torch.bfloat16), made if not
-    given.  For attention of long query blocks over cached tokens: attn_fwd with q_offset
-    takes one sequence's rows.  Rows in no sequence are left as they were."""
+    given, for calls that take no pages (attn_fwd with q_offset takes one sequence's rows;
+    attn_paged_prefill attends long query blocks over the pages).  Rows in no sequence are left
+    as they were."""
     torch = _torch()
     rd, cd, num_pages, page_size, hd, B, max_pages = _pools(k_cache, v_cache, k_scale, v_scale, page_table, Hkv, dtype)
     dev, shape = k_cache.device, (int(total), Hkv * hd)

@@ -15,6 +15,14 @@
 //   rows load every SM alike; the launch depends on none of them.  An item cut by a stretch's end leaves
 //   partial (m, l, O) rows in the workspace.
 //   paged_prefill_merge_kernel joins those in a fixed order.
+//
+// What bounds it: with many rows the chain S, softmax, P V of two tiles that share an SM (the scores' tensor work
+// is 561 us of the 821 that 2048 tokens over 32768 take, 32 heads of 128 on 8 in bf16: 1.32 PFLOP/s; with nearly all of the
+// softmax left out 640 remain).  Beside that the instructions themselves: all roles together fit the
+// instruction cache only where their loops are rolled up, and over 8-bit pages, whose widening warps
+// issue beside the softmax, that was worth more than anything else (the same chunk over e4m3 pages: 2537 us with the
+// softmax and the issue unrolled, 1472 rolled, 1437 now).  With few rows the launches: of the 24.5 us that 64 tokens
+// over 777 take, the plan is 4.5, the merge 6.6, and a CTA's first fetch of each path some of the rest.
 #pragma once
 
 #include <math.h>
@@ -32,8 +40,9 @@ constexpr int kM = 128;  // rows of a query tile
 constexpr float kLog2e = 1.4426950408889634f;
 // What an item costs beside its key tiles, in tiles, dealt out at its beginning.
 constexpr int kItemCost = 2;
-// The least that a stretch holds.
-constexpr int kMinShare = 4;
+// The least that a stretch holds.  (64 new tokens over 777, 32 heads on 8: 35.2 us at 8, 27.5 at 4, 24.5 at 2; larger
+// calls have more than that in each stretch anyway.)
+constexpr int kMinShare = 2;
 
 // p = 2^(x - ref): a row's reference is moved when its largest p would pass 2^top, or, before it has
 // seen anything, when it would stay below 2^(top - 10); it is then put at 2^(top - 8).  fp16 p have room up
@@ -402,9 +411,11 @@ __device__ __forceinline__ void store_32(void* at, const uint32_t (&v)[8]) {
 
 // ------------------------------------------------------------------ the kernel
 // Roles (warps): softmax of tile u, one thread to a row (0-3, 4-7); loads (8); MMA issue of tile u (9 + u); looking
-// V over (11); over 8-bit pools, widening (Cfg::kWide0 ...).  Two tiles take turns as in the dense forward: one tile's
-// softmax runs while the tensor cores work on the other's P V and next S; each has one S buffer, and a
-// completed S(n), issued after P(n-1) V(n-1), also means that O stands still.  With one tile (hd 256)
+// V over (11); over 8-bit pools, widening (Cfg::kWide0 ...).  With two tiles one's softmax runs while the tensor cores
+// work on the other's P V and next S; each has one S buffer, and a completed S(n), issued after
+// P(n-1) V(n-1), also means that O stands still.  Over 16-bit pages the softmaxes take turns, so that they do not end
+// up in step with the tensor cores idle behind both (long chunks 819 us, 1056 without turns); over 8-bit ones the
+// widening warps' rate spaces them and a turn only waits (ragged chunks 1267 us, 1395 with turns).  With one tile (hd 256)
 // there are two S buffers instead, S(n+1) is issued before P(n) V(n), and the softmax may be done with P(n+1)
 // before that product is issued: S, P and the product have a barrier for each buffer.
 //
@@ -820,9 +831,6 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                         if (!ok) break;
                         const uint8_t* src = smem + C::kRawOff + raw * C::kRawBytes;
                         const uint32_t dst = sbase + C::kRingOff + stage * C::kTileBytes;
-                        // consecutive lanes: the chunks of a row, then of the next; this warp's rows lie together.
-                        // Chunk c is columns 16c .. of the box: two chunks of a 128-byte column of the wide tile.  Lanes of
-                        // either half of a row store them in the other order, so that eight lanes meet no bank twice.
                         const uint32_t factor = kv ? ratio : pack2<false>(1.f, 1.f);
                         auto widen = [&](auto e4m3c) {
 #pragma unroll 1
@@ -960,8 +968,10 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                // 16-bit pools keep the row's scores in registers; with the widening's instructions besides, over 8-bit ones
-                // they are loaded chunk by chunk
+                // Two tiles over 16-bit pages hold a row's 128 scores in registers, with the chunks unrolled; elsewhere they are
+                // loaded chunk by chunk in rolled loops, twice.  Held, the loops take three times the instructions:
+                // alone they still fit the instruction cache (long chunks 821 us, rolled 990), beside the widening's they do
+                // not (2048 tokens over 8192 of e4m3: 428 us, rolled 365).
                 constexpr bool kHold = !F8 && NT == 2;
                 uint32_t sv[kHold ? NC : 1][32];
                 if constexpr (kHold)
@@ -994,10 +1004,6 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                     va = (int)min(max(x, 0ll), (long long)BN);
                     vb = row_live ? (int)min(max(y, (long long)va), (long long)BN) : va;
                 }
-                // The row's scores chunk by chunk out of TMEM, the next chunk on its way, in two passes: the maximum, then p.
-                // Rolled up, the loops take a few kilobytes of instructions; with the 128 scores held in registers and
-                // everything unrolled, warps waited for their instructions a fifth of the time (over 8-bit pages,
-                // with the widening warps' besides, half of it).
                 // (8-bit pools) a raw score in units of 1: the scale of the keys' page, and the power of two of the row of Q
                 // (applied as the scores are loaded where a softcap or a mask follows, else with the factor log2(e) scale)
                 const bool scale_first = CAP || !full;
@@ -1130,7 +1136,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                         }
                     }
                 }
-                // ---- p over S, behind the chunks that have been loaded
+                // ---- p over S, behind the scores that have been loaded: rounded to the products' type, summed in fp32 before
                 auto p_pass = [&](auto modec) {
                     const uint64_t nm = f2_make(-m, -m);
                     uint64_t rs0 = f2_make(0.f, 0.f), rs1 = f2_make(0.f, 0.f);

@@ -445,7 +445,7 @@ ATTN_API attn_status attn_bwd_rope(attn_dtype dt, const void* q, const void* k, 
                         long long key_mask_bstride, int rope_pos, float rope_theta, void* stream);
 
 /*
- * A paged key/value cache: its writer, decode over it, and reading it back.
+ * A paged key/value cache: its writer, decode and prompt chunks over it, and reading it back.
  *
  * The pages lie in two pools, k_cache and v_cache, [num_pages][Hkv][page_size][hd] each;
  * page_table [B][max_pages] (int32, device) names the pages of sequence b in order, so that
@@ -540,10 +540,17 @@ ATTN_API attn_status attn_paged_decode(attn_dtype dt, attn_dtype cache_dt, const
  *               aligned; contents on entry are ignored.  Calls that may run at the same time
  *               need one each.
  * What a row does not see has no effect on it, whatever bytes it holds.  Table entries of which no row
- * sees a token (behind a sequence, before every row's window) are not read.  Over 8-bit pages an
- * element is read as attn_paged_gather reads it, its product with its scale rounded once to dt (exact
- * for scales that are powers of two, while the product stays in dt's range).  Sums are fp32, over
- * weights of at most 1 in bf16 and 2^8 in fp16.
+ * sees a token (behind a sequence, before every row's window) are not read.  Sums are fp32, over weights
+ * rounded to the products' type: bf16 ones of at most 1, or fp16 ones of at most 2^8.
+ *   Over 16-bit pages the products are in dt.  Over 8-bit pages they are in fp16, which holds every
+ * code exactly, for either dt: a bf16 query row enters by a power of two, so that 2^-38 of its
+ * largest element is kept; a page's scale multiplies its keys' scores in fp32; its values enter
+ * as code times the ratio of its scale to a power of two near the scales of the rows' other pages, which is
+ * exact for scales that are powers of two and otherwise off by half a step of fp16 for the ratio
+ * and for the product.  Pages whose ratio fp16 does not hold (scales some 2^10 apart within a
+ * sequence) are multiplied in fp32, right and several times as slow.
+ *   The order of the sums depends on the device arrays (lengths and prefix sums), not on the time at which
+ * CTAs run: the same call gives the same bits.
  */
 ATTN_API size_t attn_paged_prefill_workspace_size(int total_new, int batch, int H, int Hkv, int hd);
 ATTN_API attn_status attn_paged_prefill(attn_dtype dt, attn_dtype cache_dt, const void* q, long long q_stride,
@@ -555,10 +562,10 @@ ATTN_API attn_status attn_paged_prefill(attn_dtype dt, attn_dtype cache_dt, cons
 /*
  * Reads pages back: token i of sequence b into row cu_seqlens[b] + i of k_out and v_out
  * [total][Hkv*hd] (type dt), for i < cu_seqlens[b+1] - cu_seqlens[b]; 8-bit elements are
- * multiplied by their scale and rounded once.  For query blocks longer than the decode's 16
- * rows (the next chunk of a prompt over its cached prefix): attn_fwd takes the rows of one
- * sequence as k and v, with q_offset the position of the first query row.  Rows in no
- * sequence are not written.
+ * multiplied by their scale and rounded once.  For calls over the tokens that take no pages (attn_fwd takes
+ * the rows of one sequence as k and v, with q_offset the position of the first query row; attention of
+ * query blocks longer than the decode's 16 rows is attn_paged_prefill).  Rows in no sequence are
+ * not written.
  */
 ATTN_API attn_status attn_paged_gather(attn_dtype dt, attn_dtype cache_dt, const void* k_cache, const void* v_cache,
                         const float* k_scale, const float* v_scale, void* k_out, void* v_out,
