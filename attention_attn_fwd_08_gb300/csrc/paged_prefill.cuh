@@ -65,6 +65,7 @@ struct Cfg {
     static constexpr int kRawBytes = F8 ? BN * HD : 0;
     static constexpr int kStages = F8 ? (HD == 64 ? 4 : 3) : (HD == 64 ? 8 : 5);
     static constexpr int kRaw = F8 ? (HD == 64 ? 8 : 4) : 0;
+    static_assert(!F8 || kStages == 3 || kStages % 2 == 0, "which use of a stage comes before a V tile's");
     static constexpr int kRingOff = NT * kQBytes;
     static constexpr int kRawOff = kRingOff + kStages * kTileBytes;
     static constexpr int kBarOff = kRawOff + kRaw * kRawBytes;
@@ -441,6 +442,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
     __shared__ int abort_flag;
     __shared__ int done_count[2];  // warps that have finished a softmax of tile u
     __shared__ int bad_v[NS];      // of V tile n, at n mod NS, as its barrier: a value that not every row sees is not finite
+    __shared__ int v_loads;        // (16-bit pools) V tiles whose load has been asked for
     __shared__ int skip_pv[2][2];  // by the parity of the tile: the softmax warps make this product
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tm = kM / P.G;  // tokens of a query tile
@@ -456,7 +458,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
             if (F8 && i >= C::Q_WIDE && i < C::Q_WIDE + 2) n = 4;
             mbar_init(BAR(i), n);
         }
-        abort_flag = 0;
+        abort_flag = v_loads = 0;
         for (int u = 0; u < 2; ++u) done_count[u] = 0, skip_pv[u][0] = skip_pv[u][1] = 0;
         fence_barrier_init();
     }
@@ -556,7 +558,10 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                             ok = false;
                             break;
                         }
-                        if (lane == 0) mbar_expect_tx(BAR(kFull + stage), bytes);
+                        if (lane == 0) {
+                            mbar_expect_tx(BAR(kFull + stage), bytes);
+                            if (!F8 && kv) atomicAdd(&v_loads, 1);
+                        }
                         __syncwarp();
                         if (load)
                             load_2d(sbase + kOff + stage * kBytes + col * (BN * kRowBytes) + sub * box_rows * kRowBytes,
@@ -693,11 +698,17 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                     const int j0 = (tile0 + i) * BN;
                     const unsigned there = __ballot_sync(0xffffffffu, lane < subs && page_ok(pg));
                     if (i + 1 < n) pg = box_page(p, j0 + BN + sub * box_rows, lo, hi);
-                    // (the K tile too, though it is not looked at: a stage's uses are waited for one by one, since a
-                    // phase that has not begun looks like one that is over)
-                    const unsigned gk = g + 2 * i, gv = gk + 1, stage = gv % NS;
-                    ok = warp_sleep_wait(BAR(C::FULL + gk % NS), (gk / NS) & 1, P.status, ST_FWD_PRODUCER, &abort_flag) &&
-                         warp_sleep_wait(BAR(C::FULL + stage), (gv / NS) & 1, P.status, ST_FWD_PRODUCER, &abort_flag);
+                    // A phase that has not begun looks like one that is over, so V's is asked for only when the stage's use
+                    // before it is known to be: over 8-bit pages the tiles come in order and that was a V tile, or the
+                    // K tile before one that has been seen; over 16-bit ones V's load, once asked for, shows it.  K tiles are
+                    // not waited for: their stages are filled again without a look at V, so that a late wait could
+                    // find its phase two uses back, which looks like one that is still to come.
+                    const unsigned gv = g + 2 * i + 1, stage = gv % NS;
+                    if (!F8) {
+                        ok = count_wait(&v_loads, (int)(g / 2 + i + 1), P.status, ST_FWD_PRODUCER, &abort_flag);
+                        ok = __all_sync(0xffffffffu, ok);
+                    }
+                    ok = ok && warp_sleep_wait(BAR(C::FULL + stage), (gv / NS) & 1, P.status, ST_FWD_PRODUCER, &abort_flag);
                     if (!ok) break;
                     bool bad = false;
                     if (j0 < all_lo || j0 + BN > all_hi || there != (1u << subs) - 1u) {

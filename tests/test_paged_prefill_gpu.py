@@ -9,6 +9,7 @@ exponential, at most 2^-18 of the largest |scale q.k| sum of magnitudes, and 2^-
 8-bit page enters as an fp16 number whose scale (relative to a power of two) and product are rounded, 2 u(fp16),
 where the scale is no power of two; below 2^-14 by 2^-25 of that power, at most 2^8 times a scale.
 """
+import itertools
 import math
 
 import numpy as np
@@ -543,3 +544,44 @@ def test_pages_past_four_gigabytes():
         check(c, q, [100], [0, 40], o, lse, tokens=[(f64(ko), f64(vo))])
         del c
         torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hd", [64, 128, 256])
+def test_many_short_parts_behind_values_that_are_looked_over(kind, hd):
+    """Chunks whose every tile is cut by the causal mask or has values that are not finite, so that looking V
+    over lags behind the tiles that come after it: each call ends, and two give the same bits."""
+    H, Hkv, page = 8, 2, 16
+    dt = torch.bfloat16
+    cd = torch.float8_e4m3fn if kind == "e4m3" else dt
+    g = torch.Generator(device="cuda").manual_seed(hd)
+    new = [1 + (37 * i) % 190 for i in range(40)]
+    lengths = [n + (53 * i) % 300 for i, n in enumerate(new)]
+    per = [-(-n // page) for n in lengths]
+    order = torch.randperm(sum(per), generator=torch.Generator().manual_seed(1)).int()
+    table = torch.full((len(new), max(per)), -1, dtype=torch.int32)
+    at = 0
+    for b, n in enumerate(per):
+        table[b, :n] = order[at:at + n]
+        at += n
+    k = torch.randn((sum(per), Hkv, page, hd), device="cuda", generator=g).to(dt)
+    v = torch.randn((sum(per), Hkv, page, hd), device="cuda", generator=g).to(dt)
+    kw = dict(H=H, Hkv=Hkv, causal=True)
+    if kind == "e4m3":
+        kw.update(k_scale=torch.ones(sum(per), Hkv, device="cuda"), v_scale=torch.ones(sum(per), Hkv, device="cuda"))
+    k, v = k.to(cd), v.to(cd)
+    last = [int(table[b, n - 1]) for b, n in enumerate(per)]
+    v8 = v.view(torch.uint8) if kind == "e4m3" else v
+    for b, n in enumerate(lengths):  # the last key is seen by the last row alone
+        v8[last[b], :, (n - 1) % page] = 0x7f if kind == "e4m3" else float("nan")
+    q = torch.randn((sum(new), H * hd), device="cuda", generator=g).to(dt)
+    cu = torch.tensor([0] + list(itertools.accumulate(new)), dtype=torch.int32, device="cuda")
+    args = (q, k, v, table.cuda(), torch.tensor(lengths, dtype=torch.int32, device="cuda"), cu)
+    first = A.attn_paged_prefill(*args, **kw)
+    for _ in range(20):
+        again = A.attn_paged_prefill(*args, **kw)
+    assert A.attn_get_device_status()[0] == A.OK
+    rows = torch.ones(sum(new), dtype=torch.bool)
+    rows[(cu[1:] - 1).cpu().long()] = False
+    assert torch.isfinite(first[0][rows.cuda()].float()).all() and torch.isnan(first[0][~rows.cuda()].float()).all()
+    assert torch.equal(first[0].view(torch.int16), again[0].view(torch.int16)) and torch.equal(first[1], again[1])
