@@ -21,7 +21,8 @@
 // softmax left out 640 remain).  Beside that the instructions themselves: all roles together fit the
 // instruction cache only where their loops are rolled up, and over 8-bit pages, whose widening warps
 // issue beside the softmax, that was worth more than anything else (the same chunk over e4m3 pages: 2537 us with the
-// softmax and the issue unrolled, 1472 rolled, 1437 now).  With few rows the launches: of the 24.5 us that 64 tokens
+// softmax and the issue unrolled, 1472 rolled, 1302 now; with a quarter of the widening it would be 5 % less, with a quarter of
+// the softmax 970).  With few rows the launches: of the 24.5 us that 64 tokens
 // over 777 take, the plan is 4.5, the merge 6.6, and a CTA's first fetch of each path some of the rest.
 #pragma once
 
@@ -60,11 +61,12 @@ struct Cfg {
     static constexpr int kBoxes = HD / 64;           // 128-byte columns of a 16-bit tile
     static constexpr int kQBytes = kM * HD * 2, kTileBytes = BN * HD * 2;
     // K and V tiles in turn go through one ring, 16 bits to an element; 8-bit tiles come into a
-    // ring of their own and are widened into it
+    // ring of their own and are widened into it (room for 4 wide and 2 bare ones: 2048 over 32768 e4m3 tokens 1302 us, with
+    // 3 and 4 1316)
     static constexpr int kRawRow = HD < 128 ? HD : 128, kRawBoxes = HD / kRawRow;
     static constexpr int kRawBytes = F8 ? BN * HD : 0;
-    static constexpr int kStages = F8 ? (HD == 64 ? 4 : 3) : (HD == 64 ? 8 : 5);
-    static constexpr int kRaw = F8 ? (HD == 64 ? 8 : 4) : 0;
+    static constexpr int kStages = F8 ? (HD == 64 ? 6 : 4) : (HD == 64 ? 8 : 5);
+    static constexpr int kRaw = F8 ? (HD == 64 ? 4 : 2) : 0;
     static_assert(!F8 || kStages == 3 || kStages % 2 == 0, "which use of a stage comes before a V tile's");
     static constexpr int kRingOff = NT * kQBytes;
     static constexpr int kRawOff = kRingOff + kStages * kTileBytes;
@@ -980,7 +982,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                 }
                 tc_fence_after();
                 // Two tiles over 16-bit pages hold a row's 128 scores in registers, with the chunks unrolled; elsewhere they are
-                // loaded chunk by chunk in rolled loops, twice.  Held, the loops take three times the instructions:
+                // loaded chunk by chunk in rolled loops.  Held, the loops take three times the instructions:
                 // alone they still fit the instruction cache (long chunks 821 us, rolled 990), beside the widening's they do
                 // not (2048 tokens over 8192 of e4m3: 428 us, rolled 365).
                 constexpr bool kHold = !F8 && NT == 2;
@@ -1017,9 +1019,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                 }
                 // (8-bit pools) a raw score in units of 1: the scale of the keys' page, and the power of two of the row of Q
                 // (applied as the scores are loaded where a softcap or a mask follows, else with the factor log2(e) scale)
-                const bool scale_first = CAP || !full;
                 auto page_unit = [&](int c, int half) { return __shfl_sync(0xffffffffu, scale.x, (32 * c + 16 * half) >> box_shift) * qf; };
-                auto unit = [&](int c, int half) { return scale_first ? 1.f : page_unit(c, half); };
                 auto scaled = [&](uint32_t (&x)[32], int c) {
                     const float f0 = page_unit(c, 0), f1 = page_unit(c, 1);
 #pragma unroll
@@ -1032,7 +1032,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                     }
                 };
                 auto prepare = [&](uint32_t (&x)[32], int c, bool masked) {
-                    if (F8 && scale_first) scaled(x, c);
+                    if (F8) scaled(x, c);
                     if (masked && __builtin_expect(!full, 0)) {
                         const int c0 = min(max(va - 32 * c, 0), 32), c1 = min(max(vb - 32 * c, 0), 32);
                         uint32_t see = bit_range(c0, c1 - c0);
@@ -1072,114 +1072,201 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                     }
                     return fmaxf(y[0], y[1]);
                 };
-                // the form of the softcap: by exp where a raw score of the warp lies outside the fit's range
-                bool accurate = false, shorter = false;
-                if constexpr (CAP) {
-                    float amax = 0.f;
-                    chunks(false, [&](uint32_t (&x)[32], int) { amax = fmaxf(amax, largest(x, true)); });
-                    const CapPoly cp = cap_poly(P.scale, P.softcap);
-                    accurate = __any_sync(0xffffffffu, !(amax <= cp.r_max)) || (!full && !cp.inf_ok);
-                    const CapShort cs = cap_short(P.scale, P.softcap);
-                    shorter = !accurate && __all_sync(0xffffffffu, amax <= cs.r_max) && (full || cs.inf_ok);
-                }
-                if (kHold && !full) {
-#pragma unroll
-                    for (int c = 0; c < (kHold ? NC : 0); ++c) prepare(sv[c], c, true);
-                }
-                // ---- the row's largest score, as x against its reference
-                float rmax = -INFINITY;
-                chunks(true, [&](uint32_t (&x)[32], int c) {
-                    if constexpr (F8 && !CAP) {
-                        const float f0 = unit(c, 0), f1 = unit(c, 1);
-                        float y[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) y[e >> 4] = max3f(y[e >> 4], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-                        if (__builtin_expect(f0 < 0.f || f1 < 0.f, 0)) {  // (the same for all of a warp's rows)
-                            float z[2] = {INFINITY, INFINITY};
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) z[e >> 4] = fminf(z[e >> 4], __uint_as_float(x[e]));
-                            if (f0 < 0.f) y[0] = z[0];
-                            if (f1 < 0.f) y[1] = z[1];
-                        }
-                        rmax = max3f(rmax, y[0] * f0, y[1] * f1);
-                    } else {
-                        rmax = fmaxf(rmax, largest(x, false));
-                    }
-                });
-                float xm, xm_;
-                {
-                    const uint64_t r2 = f2_make(rmax, rmax), n2 = f2_make(-m, -m);
-                    uint64_t x2;
-                    if (!CAP) x2 = to_x(M0(), r2, n2);
-                    else if (shorter) x2 = to_x(M3(), r2, n2);
-                    else if (!accurate) x2 = to_x(M1(), r2, n2);
-                    else x2 = to_x(M2(), r2, n2);
-                    f2_split(x2, xm, xm_);
-                }
-                if (rmax == -INFINITY) xm = -INFINITY;
-                const bool move = row_live && (xm > kTop || (l == 0.f && xm < kTop - 10.f && xm != -INFINITY));
                 bool o_stands = NT == 2;  // the product of the tile before is complete
-                if (__builtin_expect(__any_sync(0xffffffffu, move), 0)) {
-                    // rows that have seen nothing hold O = 0: their reference may move by any amount
-                    const float by = xm - (kTop - 8.f);
-                    const float alpha = fast_exp2(move && l > 0.f ? -by : 0.f);
-                    if (move) {
-                        m += by;
-                        l *= alpha;
-                    }
-                    if (k > 0) {
-                        if (!o_stands) {
-                            if (!wait_pv()) {
-                                ok = false;
-                                break;
-                            }
-                            o_stands = true;
-                            tc_fence_after();
-                        }
+                // ---- (8-bit pools) the scores in one pass, 32 kAt keys at a time: their maximum, then their p over S.  A move
+                // of the reference, rare after the first keys, also scales the P of the tile's earlier keys, by a power of two.
+                // 2048 tokens over 32768 e4m3 ones take 1314 us with 64 keys at a time, 1320 with 32, 1664 with the whole tile
+                // (more instructions than stay in their cache), and 1410 in two passes of 32.
+                auto one_pass = [&](auto wholec) {
+                    constexpr bool kWhole = decltype(wholec)::value;
+                    constexpr int kAt = 2;
+                    float low = l == 0.f && row_live ? kTop - 10.f : -INFINITY;
+                    uint64_t nm = f2_make(-m, -m), rs0 = f2_make(0.f, 0.f), rs1 = rs0;
+                    const float top = row_live ? kTop : INFINITY;
+                    auto add_up = [&]() {
+                        float a0, a1, b0, b1;
+                        f2_split(rs0, a0, a1);
+                        f2_split(rs1, b0, b1);
+                        l += (a0 + b0) + (a1 + b1);
+                        rs0 = rs1 = f2_make(0.f, 0.f);
+                    };
 #pragma unroll 1
-                        for (int c = 0; c < HD / 32; ++c) {
-                            uint32_t orr[32];
-                            tmem_ld32(tO + c * 32, orr);
-                            tmem_ld_wait(orr);
+                    for (int c = 0; c < NC; c += kAt) {
+                        uint32_t x[kAt][32];
+                        float f[kAt][2];
+                        float xm = -INFINITY;
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * alpha);
-                            tmem_st32(tO + c * 32, orr);
+                        for (int d = 0; d < kAt; ++d) tmem_ld32(tS + (c + d) * 32, x[d]);
+                        tmem_ld_wait_only();
+#pragma unroll
+                        for (int d = 0; d < kAt; ++d) {
+                            tmem_pin(x[d]);
+                            if constexpr (!kWhole) prepare(x[d], c + d, true);
+                            f[d][0] = (kWhole ? page_unit(c + d, 0) : 1.f) * sl2;
+                            f[d][1] = (kWhole ? page_unit(c + d, 1) : 1.f) * sl2;
+                            float y[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) y[e >> 4] = max3f(y[e >> 4], __uint_as_float(x[d][e]), __uint_as_float(x[d][e + 1]));
+                            if (__builtin_expect(f[d][0] < 0.f || f[d][1] < 0.f, 0)) {  // (the same for all of a warp's rows)
+                                float z[2] = {INFINITY, INFINITY};
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) z[e >> 4] = fminf(z[e >> 4], __uint_as_float(x[d][e]));
+                                if (f[d][0] < 0.f) y[0] = z[0];
+                                if (f[d][1] < 0.f) y[1] = z[1];
+                            }
+                            // (nothing seen is -inf also where the page's scale is 0)
+                            xm = max3f(xm, y[0] == -INFINITY ? y[0] : fmaf(y[0], f[d][0], -m), y[1] == -INFINITY ? y[1] : fmaf(y[1], f[d][1], -m));
+                        }
+                        const bool move = xm > top || (xm < low && xm != -INFINITY);
+                        if (__builtin_expect(__any_sync(0xffffffffu, move), 0)) {
+                            add_up();
+                            // rows that have seen nothing hold O = 0: their reference may move by any amount
+                            const float by = ceilf(xm - (kTop - 8.f));
+                            const float alpha = fast_exp2(move && l > 0.f ? -by : 0.f);
+                            if (move) {
+                                m += by;
+                                l *= alpha;
+                            }
+                            nm = f2_make(-m, -m);
+                            if (c > 0) tmem_st_wait();
+#pragma unroll 1
+                            for (int q = 0; q < c / 2; ++q) {
+                                uint32_t pk[32];
+                                tmem_ld32(tS + q * 32, pk);
+                                tmem_ld_wait(pk);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) {
+                                    const float2 h = h2_to_f2(pk[e]);
+                                    pk[e] = pack2<false>(h.x * alpha, h.y * alpha);
+                                }
+                                tmem_st32(tS + q * 32, pk);
+                            }
+                            if (k > 0) {
+                                if (!o_stands) {
+                                    ok = wait_pv() && ok;
+                                    o_stands = true;
+                                    tc_fence_after();
+                                }
+#pragma unroll 1
+                                for (int q = 0; q < HD / 32; ++q) {
+                                    uint32_t orr[32];
+                                    tmem_ld32(tO + q * 32, orr);
+                                    tmem_ld_wait(orr);
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * alpha);
+                                    tmem_st32(tO + q * 32, orr);
+                                }
+                            }
+                        }
+                        if (xm != -INFINITY) low = -INFINITY;
+#pragma unroll
+                        for (int d = 0; d < kAt; ++d) {
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                float x0, x1;
+                                const float g = f[d][e >> 3];
+                                f2_split(f2_fma(f2_make(__uint_as_float(x[d][2 * e]), __uint_as_float(x[d][2 * e + 1])), f2_make(g, g), nm), x0, x1);
+                                const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);  // 2^-inf = 0
+                                if (e & 1) rs1 = f2_add(rs1, f2_make(p0, p1));
+                                else rs0 = f2_add(rs0, f2_make(p0, p1));
+                                pk[e] = pack2<false>(p0, p1);
+                            }
+                            tmem_st16(tS + (c + d) * 16, pk);
                         }
                     }
-                }
-                // ---- p over S, behind the scores that have been loaded: rounded to the products' type, summed in fp32 before
-                auto p_pass = [&](auto modec) {
-                    const uint64_t nm = f2_make(-m, -m);
-                    uint64_t rs0 = f2_make(0.f, 0.f), rs1 = f2_make(0.f, 0.f);
-                    chunks(true, [&](uint32_t (&x)[32], int c) {
-                        uint32_t pk[16];
-                        uint64_t f2[2] = {sl2_2, sl2_2};
-                        if constexpr (F8 && !CAP) {
-                            const float f0 = unit(c, 0) * sl2, f1 = unit(c, 1) * sl2;
-                            f2[0] = f2_make(f0, f0);
-                            f2[1] = f2_make(f1, f1);
-                        }
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            float x0, x1;
-                            const uint64_t rr = f2_make(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
-                            f2_split(F8 && !CAP ? f2_fma(rr, f2[e >> 3], nm) : to_x(modec, rr, nm), x0, x1);
-                            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);  // 2^-inf = 0
-                            if (e & 1) rs1 = f2_add(rs1, f2_make(p0, p1));
-                            else rs0 = f2_add(rs0, f2_make(p0, p1));
-                            pk[e] = pack2<MB>(p0, p1);
-                        }
-                        tmem_st16(tS + c * 16, pk);
-                    });
-                    float a0, a1, b0, b1;
-                    f2_split(rs0, a0, a1);
-                    f2_split(rs1, b0, b1);
-                    l += (a0 + b0) + (a1 + b1);
+                    add_up();
                 };
-                if (!CAP) p_pass(M0());
-                else if (shorter) p_pass(M3());
-                else if (!accurate) p_pass(M1());
-                else p_pass(M2());
+                auto two_passes = [&]() {
+                    // the form of the softcap: by exp where a raw score of the warp lies outside the fit's range
+                    bool accurate = false, shorter = false;
+                    if constexpr (CAP) {
+                        float amax = 0.f;
+                        chunks(false, [&](uint32_t (&x)[32], int) { amax = fmaxf(amax, largest(x, true)); });
+                        const CapPoly cp = cap_poly(P.scale, P.softcap);
+                        accurate = __any_sync(0xffffffffu, !(amax <= cp.r_max)) || (!full && !cp.inf_ok);
+                        const CapShort cs = cap_short(P.scale, P.softcap);
+                        shorter = !accurate && __all_sync(0xffffffffu, amax <= cs.r_max) && (full || cs.inf_ok);
+                    }
+                    if (kHold && !full) {
+#pragma unroll
+                        for (int c = 0; c < (kHold ? NC : 0); ++c) prepare(sv[c], c, true);
+                    }
+                    // ---- the row's largest score, as x against its reference
+                    float rmax = -INFINITY;
+                    chunks(true, [&](uint32_t (&x)[32], int) { rmax = fmaxf(rmax, largest(x, false)); });
+                    float xm, xm_;
+                    {
+                        const uint64_t r2 = f2_make(rmax, rmax), n2 = f2_make(-m, -m);
+                        uint64_t x2;
+                        if (!CAP) x2 = to_x(M0(), r2, n2);
+                        else if (shorter) x2 = to_x(M3(), r2, n2);
+                        else if (!accurate) x2 = to_x(M1(), r2, n2);
+                        else x2 = to_x(M2(), r2, n2);
+                        f2_split(x2, xm, xm_);
+                    }
+                    if (rmax == -INFINITY) xm = -INFINITY;
+                    const bool move = row_live && (xm > kTop || (l == 0.f && xm < kTop - 10.f && xm != -INFINITY));
+                    if (__builtin_expect(__any_sync(0xffffffffu, move), 0)) {
+                        // rows that have seen nothing hold O = 0: their reference may move by any amount
+                        const float by = xm - (kTop - 8.f);
+                        const float alpha = fast_exp2(move && l > 0.f ? -by : 0.f);
+                        if (move) {
+                            m += by;
+                            l *= alpha;
+                        }
+                        if (k > 0) {
+                            if (!o_stands) {
+                                ok = wait_pv() && ok;
+                                o_stands = true;
+                                tc_fence_after();
+                            }
+#pragma unroll 1
+                            for (int c = 0; c < HD / 32; ++c) {
+                                uint32_t orr[32];
+                                tmem_ld32(tO + c * 32, orr);
+                                tmem_ld_wait(orr);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * alpha);
+                                tmem_st32(tO + c * 32, orr);
+                            }
+                        }
+                    }
+                    // ---- p over S, behind the scores that have been loaded: rounded to the products' type, summed in fp32 before
+                    auto p_pass = [&](auto modec) {
+                        const uint64_t nm = f2_make(-m, -m);
+                        uint64_t rs0 = f2_make(0.f, 0.f), rs1 = f2_make(0.f, 0.f);
+                        chunks(true, [&](uint32_t (&x)[32], int c) {
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                float x0, x1;
+                                const uint64_t rr = f2_make(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+                                f2_split(to_x(modec, rr, nm), x0, x1);
+                                const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);  // 2^-inf = 0
+                                if (e & 1) rs1 = f2_add(rs1, f2_make(p0, p1));
+                                else rs0 = f2_add(rs0, f2_make(p0, p1));
+                                pk[e] = pack2<MB>(p0, p1);
+                            }
+                            tmem_st16(tS + c * 16, pk);
+                        });
+                        float a0, a1, b0, b1;
+                        f2_split(rs0, a0, a1);
+                        f2_split(rs1, b0, b1);
+                        l += (a0 + b0) + (a1 + b1);
+                    };
+                    if (!CAP) p_pass(M0());
+                    else if (shorter) p_pass(M3());
+                    else if (!accurate) p_pass(M1());
+                    else p_pass(M2());
+                };
+                if constexpr (F8 && !CAP) {
+                    if (full) one_pass(std::true_type());
+                    else one_pass(std::false_type());
+                } else {
+                    two_passes();
+                }
+                if (!ok) break;
                 // ---- a tile that is not whole: is all of V finite that some row does not see
                 bool by_row = false;
                 if (!full || odd) {

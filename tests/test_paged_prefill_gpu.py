@@ -240,6 +240,27 @@ def test_scores_that_climb(dt, kind, hd, softcap):
     check(c, q, lengths, cu, o, lse, **kw)
 
 
+@pytest.mark.parametrize("kind", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("window", [0, 77])
+def test_scores_that_climb_inside_a_tile(kind, hd, window):
+    """Pages whose scales rise and fall, and change sign, from one to the next: references move in the middle of a tile, whose
+    earlier weights are then scaled too (a power of two; weights below 2^-14 are rounded by 2^-25 twice, where l is 2^-1
+    at least: 2^-23 a key relative to l as before)."""
+    lengths, new = [700, 333, 90], [200, 333, 5]
+    c = Cache("bf16", kind, lengths, 2, hd, 16, seed=47)
+    c.fill(lengths, 47, unequal=False)
+    for b, n in enumerate(lengths):
+        for j in range((n + 15) // 16):
+            c.ks[int(c.table[b, j])] *= (0.25, 1.0, -3.0, 12.0, 0.0, 40.0, -2.0, 60.0, 5.0)[j % 9]
+    cu = np.cumsum([0] + new)
+    q = queries(int(cu[-1]), 8 * hd, "bf16", 17)
+    kw = dict(scale=0.5 / math.sqrt(hd), window=window)
+    o, lse = A.attn_paged_prefill(q, c.k, c.v, c.table_d, i32(lengths), i32(cu), H=8, **c.kw(), **kw)
+    status_ok()
+    check(c, q, lengths, cu, o, lse, **kw)
+
+
 @pytest.mark.parametrize("hd", [64, 128, 256])
 @pytest.mark.parametrize("climb", [False, True])
 def test_values_near_the_end_of_bf16(hd, climb):
