@@ -12,8 +12,9 @@
 // moves chunks of up to 16 bytes, several in flight.  16-bit elements take the hardware sine and
 // cosine (2^-20 of the pair's length, under the 2^-12 at least of the rounding that follows),
 // fp32 ones sincospif of the angle's distance to the nearest quarter turn (2^-22).
-// 4 x 2048 rows of 32 heads of 128 in bf16 (134 MB) take 25.4 us, 0.78 of the copy rate, in either layout and direction;
-// 5003 rows of 16 heads of 256 in fp32, 64 elements turned, 30.9 (0.78 too).  64 rows of 40 heads: 2.5 us.
+// 4 x 2048 rows of 32 heads of 128 in bf16 (134 MB) take 22.8 us, 0.87 of the copy rate, in either layout and direction
+// (25.4 with CTAs of 256 threads and 1024 items, of which fewer are in different stages at a time); 5003 rows of 16
+// heads of 256 in fp32, 64 elements turned, 32.1 (30.9).  64 rows of 40 heads: 2.6 us.
 #include <math.h>
 
 #include "kernels.h"
@@ -22,7 +23,7 @@
 namespace attn {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kSms = 152;
 constexpr int kTableBytes = 20 * 1024;
 constexpr int kMaxRows = 8;       // of a CTA
@@ -175,9 +176,9 @@ cudaError_t rope_ex_typed(RopeExArgs a, bool interleaved, cudaStream_t s) {
     a.lo_step = !kPair && interleaved ? 2 : V;
     a.hi_off = interleaved ? 1 : a.rd / 2;
     a.inv_slots = inverse(a.slots);
-    // About 1024 items to a CTA: as few rows as hold them, or, where there are few rows, as few of
+    // About 512 items to a CTA: as few rows as hold them, or, where there are few rows, as few of
     // a row's heads as leave two CTAs to an SM, down to one item a thread.
-    constexpr int kItems = 1024;
+    constexpr int kItems = 512;
     const long long row_items = (long long)a.H * a.slots;
     long long rows = kItems / row_items;
     rows = rows < 1 ? 1 : rows > kMaxRows ? kMaxRows : rows;

@@ -530,7 +530,8 @@ ATTN_API attn_status attn_paged_decode(attn_dtype dt, attn_dtype cache_dt, const
  * length, prompts beside single tokens.  Source: brotensor ops/flash_attention.h, flash_attention_decode_len
  * (query rows at the end of a cache of device-held length), without a limit on the rows.
  *   q         : packed rows [total_new][H*hd], q_stride elements apart (a multiple of 8, at least
- *               H*hd).  o : [total_new][H*hd] (contiguous).  lse : [H][total_new] fp32, or NULL.
+ *               H*hd).  o : [total_new][H*hd] (contiguous).  lse : [H][total_new] fp32, or NULL.  Neither
+ *               overlaps an input.
  *   cu_new, lengths, page_table : as for attn_paged_append: rows [cu_new[b], cu_new[b+1]) are sequence b's
  *               last tokens, at positions L_b - n_b .. L_b - 1, L_b = min(max(lengths[b], 0), max_pages *
  *               page_size).  A row that sees no key (one at a negative position under the causal mask)
