@@ -12,9 +12,8 @@
 // moves chunks of up to 16 bytes, several in flight.  16-bit elements take the hardware sine and
 // cosine (2^-20 of the pair's length, under the 2^-12 at least of the rounding that follows),
 // fp32 ones sincospif of the angle's distance to the nearest quarter turn (2^-22).
-// 4 x 2048 rows of 32 heads of 128 in bf16 (134 MB) take 22.8 us, 0.87 of the copy rate, in either layout and direction
-// (25.4 with CTAs of 256 threads and 1024 items, of which fewer are in different stages at a time); 5003 rows of 16
-// heads of 256 in fp32, 64 elements turned, 32.1 (30.9).  64 rows of 40 heads: 2.6 us.
+// 4 x 2048 rows of 32 heads of 128 in bf16 (134 MB) take 22.8 us, 0.87 of the copy rate, in either layout and
+// direction; 5003 rows of 16 heads of 256 in fp32, 64 elements turned, 30.9 (0.78).  64 rows of 40 heads: 2.6 us.
 #include <math.h>
 
 #include "kernels.h"
@@ -23,7 +22,10 @@
 namespace attn {
 namespace {
 
-constexpr int kThreads = 128;
+// of a CTA, which takes about four items a thread: 16-bit rows gain from more and smaller CTAs in different stages at a time
+// (4 x 2048 rows of 32 heads in bf16 22.7 us, 25.4 with 256), fp32 rows, whose sines take longer, do not (32.0, and 30.9 with 256)
+template <typename T>
+constexpr int kThreadsOf = sizeof(T) == 4 ? 256 : 128;
 constexpr int kSms = 152;
 constexpr int kTableBytes = 20 * 1024;
 constexpr int kMaxRows = 8;       // of a CTA
@@ -78,7 +80,8 @@ template <> struct Chunk<2> { using U = uint16_t; };
 // kPair: a chunk's pairs lie inside it (interleaved); otherwise an item is two chunks, the first
 // and the second elements of its pairs (with one element to a chunk, of either layout).
 template <typename T, int kBytes, bool kPair>
-__global__ void __launch_bounds__(kThreads) rope_ex_kernel(const __grid_constant__ RopeExArgs P) {
+__global__ void __launch_bounds__(kThreadsOf<T>) rope_ex_kernel(const __grid_constant__ RopeExArgs P) {
+    constexpr int kThreads = kThreadsOf<T>;
     constexpr int V = kBytes / (int)sizeof(T);  // elements of a chunk
     constexpr int kAngles = kPair ? V / 2 : V;  // of an item
     constexpr int kAhead = kPair ? 4 : 2;       // items of a thread in flight
@@ -176,9 +179,9 @@ cudaError_t rope_ex_typed(RopeExArgs a, bool interleaved, cudaStream_t s) {
     a.lo_step = !kPair && interleaved ? 2 : V;
     a.hi_off = interleaved ? 1 : a.rd / 2;
     a.inv_slots = inverse(a.slots);
-    // About 512 items to a CTA: as few rows as hold them, or, where there are few rows, as few of
+    // About four items a thread to a CTA: as few rows as hold them, or, where there are few rows, as few of
     // a row's heads as leave two CTAs to an SM, down to one item a thread.
-    constexpr int kItems = 512;
+    constexpr int kThreads = kThreadsOf<T>, kItems = 4 * kThreads;
     const long long row_items = (long long)a.H * a.slots;
     long long rows = kItems / row_items;
     rows = rows < 1 ? 1 : rows > kMaxRows ? kMaxRows : rows;
