@@ -1180,7 +1180,8 @@ size_t attn_paged_prefill_workspace_size(int total, int batch, int H, int Hkv, i
     if (total <= 0 || batch <= 0 || batch > 65535 || H <= 0 || Hkv <= 0 || H % Hkv || H / Hkv > 128 || total > INT32_MAX - 512 ||
         (hd != 64 && hd != 128 && hd != 256))
         return 0;
-    return paged_prefill_workspace(total, batch, H / Hkv, hd);
+    // (room to begin on a multiple of kPrefillAlign wherever the caller's bytes begin)
+    return paged_prefill_workspace(total, batch, H / Hkv, hd) + kPrefillAlign;
 }
 
 attn_status attn_paged_prefill(attn_dtype dt, attn_dtype cache_dt, const void* q, long long q_stride, const void* k_cache,
@@ -1207,7 +1208,8 @@ attn_status attn_paged_prefill(attn_dtype dt, attn_dtype cache_dt, const void* q
         return ATTN_ERR_INVALID_ARG;
     p.status = status_ptr();
     if (!p.status) return ATTN_ERR_CUDA;
-    p.q = q; p.q_stride = q_stride; p.o = o; p.lse = lse; p.ws = static_cast<float*>(workspace);
+    p.q = q; p.q_stride = q_stride; p.o = o; p.lse = lse;
+    p.ws = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(workspace) + kPrefillAlign - 1) / kPrefillAlign * kPrefillAlign);
     p.cu = cu_new; p.lengths = lengths; p.total = total_new;
     if (num_pages == 0) p.max_pages = 0;  // no token anywhere: no key tile, and no map is read
     p.scale = scale; p.softcap = softcap;

@@ -128,6 +128,8 @@ inline cudaError_t launch_paged_prefill(const PagedParams& p, bool bf16, int cac
     if (cache == CACHE_16) return bf16 ? launch_paged_prefill_bf16(p, cache, maps, s) : launch_paged_prefill_f16(p, cache, maps, s);
     return bf16 ? launch_paged_prefill_bf16_f8(p, cache, maps, s) : launch_paged_prefill_f16_f8(p, cache, maps, s);
 }
+// The layout of PagedParams::ws, whose partial rows are stored 32 bytes at a time, begins on a multiple of kPrefillAlign.
+constexpr size_t kPrefillAlign = 256;
 size_t paged_prefill_workspace(int total, int B, int G, int hd);
 
 }  // namespace attn

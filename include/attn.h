@@ -538,8 +538,8 @@ ATTN_API attn_status attn_paged_decode(attn_dtype dt, attn_dtype cache_dt, const
  *               gets O = 0 and LSE = -inf; rows in no sequence are not written.
  *   scale, causal, window, softcap : as for attn_decode.  H/Hkv is at most 128.
  *   workspace : at least attn_paged_prefill_workspace_size() bytes of device scratch, 16-byte
- *               aligned; contents on entry are ignored.  Calls that may run at the same time
- *               need one each.
+ *               aligned (the size has room to begin on a multiple of 256 inside it); contents on entry are
+ *               ignored.  Calls that may run at the same time need one each.
  * What a row does not see has no effect on it, whatever bytes it holds.  Table entries of which no row
  * sees a token (behind a sequence, before every row's window) are not read.  Sums are fp32, over weights
  * rounded to the products' type: bf16 ones of at most 1, or fp16 ones of at most 2^8.

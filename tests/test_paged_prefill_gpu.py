@@ -421,6 +421,34 @@ def test_twice_is_the_same_bits_and_leaves_its_inputs():
     np.testing.assert_array_equal(before[1], bits(c.v))
 
 
+@pytest.mark.parametrize("dt,kind,hd", [("bf16", "bf16", 64), ("bf16", "bf16", 128), ("f16", "f16", 256), ("bf16", "e4m3", 128)])
+def test_workspaces_and_outputs_that_begin_anywhere(dt, kind, hd):
+    """A workspace 16 bytes and more into a larger tensor, and an O at 16 modulo 32: the same bits, for a sequence whose items are cut
+    and one whose item is not, and nothing outside is touched."""
+    lengths, new, H = [5003, 40], [29, 40], 8
+    c = Cache(dt, kind, lengths, 2, hd, 16, seed=52)
+    c.fill(lengths, 52)
+    cu, n = np.cumsum([0] + new), sum(new)
+    q = queries(n, H * hd, dt, 53)
+    args = (q, c.k, c.v, c.table_d, i32(lengths), i32(cu))
+    size = A.attn_paged_prefill_workspace_size(n, 2, H, 2, hd)
+    buf = torch.empty(size + 1024, dtype=torch.uint8, device=DEV)
+    rows = torch.empty(n * H * hd + 64, dtype=T[dt], device=DEV)
+    assert buf.data_ptr() % 256 == 0 and rows.data_ptr() % 256 == 0
+    ref, lse = A.attn_paged_prefill(*args, H=H, workspace=buf[:size], **c.kw())
+    status_ok()
+    check(c, q, lengths, cu, ref, lse)
+    for at, o_at in ((16, 0), (48, 8), (240, 8), (256, 24), (336, 0)):
+        buf.fill_(0x5a)
+        rows.fill_(7.0)
+        o = rows[o_at:o_at + n * H * hd].view(n, H * hd)
+        got, l2 = A.attn_paged_prefill(*args, H=H, workspace=buf[at:at + size], o=o, **c.kw())
+        status_ok()
+        assert torch.equal(got, ref) and torch.equal(l2, lse)
+        assert (buf[:at] == 0x5a).all() and (buf[at + size:] == 0x5a).all()
+        assert (rows[:o_at] == 7).all() and (rows[o_at + n * H * hd:] == 7).all()
+
+
 def test_two_calls_at_once():
     calls = []
     for i, (lengths, new) in enumerate((([3000, 17, 900], [200, 17, 1]), ([64, 2100, 5], [64, 300, 2]))):

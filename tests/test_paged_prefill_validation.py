@@ -69,6 +69,20 @@ def test_workspace_size():
                     assert prefill(wsb=n - 1, **kw) == A.ERR_INVALID_ARG
 
 
+def test_workspace_size_has_room_for_any_beginning():
+    """The layout begins on a multiple of 256 inside a workspace that begins on any multiple of 16: 240 bytes at most lie
+    before it.  What it holds: the plan's lists, and 304 slots of partial rows, (m, l) and fp32 O each."""
+    up = lambda n: -(-n // 256) * 256
+    for total in (1, 29, 4096, 70001):
+        for B in (1, 37, 1500):
+            for G in (1, 3, 4, 128):
+                for hd in (64, 128, 256):
+                    rows = 128 if hd == 256 else 256
+                    n = total // (rows // 128 * (128 // G)) + B  # items
+                    lists = 256 + up(152 * 16) + up((B + 1) * 4) + up(n * 32) + up((n + 1) * 8)
+                    assert A.attn_paged_prefill_workspace_size(total, B, G, 1, hd) >= 240 + lists + 304 * rows * (8 + 4 * hd)
+
+
 # ------------------------------------------------------------------ the binding
 B, Hkv, H, hd, page, P, most = 3, 2, 4, 64, 16, 9, 4
 
