@@ -901,36 +901,30 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
         auto wait_pv = [&]() { return wait(C::PV_DONE + ((sc - 1) & 1), ((sc - 1) >> 1) & 1); };
         int base[2] = {0, 0};         // softmaxes of both tiles in earlier parts
         unsigned g = 0;               // ring position of the part's first K tile
-        // x = score * log2(e) - m of a pair of raw scores; mode 0: plain; with a softcap 1: the fitted
-        // polynomial, 2: by exp, 3: the short polynomial
+        // x = score * log2(e) - m of a pair of raw scores; mode 0: plain; with a softcap 1: the fitted polynomial, for
+        // scores in its range; 2: by exp outside it.  A score's form is its own, so that no other's bytes change its bits.
+        const CapPoly cp = cap_poly(P.scale, P.softcap);
         auto to_x = [&](auto modec, uint64_t rr, uint64_t nm) -> uint64_t {
             constexpr int kMode = decltype(modec)::value;
-            if constexpr (kMode == 2) {
-                float r0, r1, m0, m1;
-                f2_split(rr, r0, r1);
-                f2_split(nm, m0, m1);
-                // a masked score is -inf, and softcap * tanh(-inf) would be finite
-                return f2_make(r0 == -INFINITY ? -INFINITY : fmaf(cap_out, tanh_accurate(r0 * cap_in), m0),
-                               r1 == -INFINITY ? -INFINITY : fmaf(cap_out, tanh_accurate(r1 * cap_in), m1));
-            } else if constexpr (kMode == 1) {
-                const CapPoly cp = cap_poly(P.scale, P.softcap);
-                const uint64_t uu = f2_mul(rr, rr);
-                uint64_t sp = f2_fma(uu, f2_mul(cp.s3, sl2_2), f2_mul(cp.s2, sl2_2));
-                sp = f2_fma(uu, sp, f2_mul(cp.s1, sl2_2));
-                sp = f2_fma(uu, sp, f2_mul(cp.s0, sl2_2));
-                return f2_fma(rr, f2_fma(uu, sp, sl2_2), nm);
-            } else if constexpr (kMode == 3) {
-                const CapShort cs = cap_short(P.scale, P.softcap);
-                const uint64_t uu = f2_mul(rr, rr);
-                return f2_fma(rr, f2_fma(uu, f2_fma(uu, f2_mul(cs.s1, sl2_2), f2_mul(cs.s0, sl2_2)), sl2_2), nm);
-            } else {
-                return f2_fma(rr, sl2_2, nm);
-            }
+            if constexpr (kMode == 0) return f2_fma(rr, sl2_2, nm);
+            const uint64_t uu = f2_mul(rr, rr);
+            uint64_t sp = f2_fma(uu, f2_mul(cp.s3, sl2_2), f2_mul(cp.s2, sl2_2));
+            sp = f2_fma(uu, sp, f2_mul(cp.s1, sl2_2));
+            sp = f2_fma(uu, sp, f2_mul(cp.s0, sl2_2));
+            const uint64_t fit = f2_fma(rr, f2_fma(uu, sp, sl2_2), nm);
+            if constexpr (kMode == 1) return fit;
+            float r0, r1, m0, m1, x0, x1;
+            f2_split(rr, r0, r1);
+            f2_split(nm, m0, m1);
+            f2_split(fit, x0, x1);
+            // a masked score is -inf, and softcap * tanh(-inf) would be finite
+            const float y0 = r0 == -INFINITY ? -INFINITY : fmaf(cap_out, tanh_accurate(r0 * cap_in), m0);
+            const float y1 = r1 == -INFINITY ? -INFINITY : fmaf(cap_out, tanh_accurate(r1 * cap_in), m1);
+            return f2_make(fabsf(r0) <= cp.r_max ? x0 : y0, fabsf(r1) <= cp.r_max ? x1 : y1);
         };
         using M0 = std::integral_constant<int, 0>;
         using M1 = std::integral_constant<int, 1>;
         using M2 = std::integral_constant<int, 2>;
-        using M3 = std::integral_constant<int, 3>;
         Walk w = walk_of(P, plan);
         Part p;
         while (ok && next_part(plan, w, p)) {
@@ -984,8 +978,9 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                 // Two tiles over 16-bit pages hold a row's 128 scores in registers, with the chunks unrolled; elsewhere they are
                 // loaded chunk by chunk in rolled loops.  Held, the loops take three times the instructions:
                 // alone they still fit the instruction cache (long chunks 821 us, rolled 990), beside the widening's they do
-                // not (2048 tokens over 8192 of e4m3: 428 us, rolled 365).
-                constexpr bool kHold = !F8 && NT == 2;
+                // not (2048 tokens over 8192 of e4m3: 428 us, rolled 365), nor with both forms of a softcap (of 50, the
+                // same over bf16 pages: 507 us, rolled 400).
+                constexpr bool kHold = !F8 && NT == 2 && !CAP;
                 uint32_t sv[kHold ? NC : 1][32];
                 if constexpr (kHold)
 #pragma unroll
@@ -1031,9 +1026,9 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                         x[e + 1] = __float_as_uint(z);
                     }
                 };
-                auto prepare = [&](uint32_t (&x)[32], int c, bool masked) {
+                auto prepare = [&](uint32_t (&x)[32], int c) {
                     if (F8) scaled(x, c);
-                    if (masked && __builtin_expect(!full, 0)) {
+                    if (__builtin_expect(!full, 0)) {
                         const int c0 = min(max(va - 32 * c, 0), 32), c1 = min(max(vb - 32 * c, 0), 32);
                         uint32_t see = bit_range(c0, c1 - c0);
                         if (there != (1u << subs) - 1u) {  // boxes of 16, 32 or 64 keys
@@ -1048,7 +1043,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                         }
                     }
                 };
-                auto chunks = [&](bool masked, auto fn) {
+                auto chunks = [&](auto fn) {
                     if constexpr (kHold) {
 #pragma unroll
                         for (int c = 0; c < NC; ++c) fn(sv[c], c);
@@ -1058,18 +1053,22 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                             uint32_t x[32];
                             tmem_ld32(tS + c * 32, x);
                             tmem_ld_wait(x);
-                            prepare(x, c, masked);
+                            prepare(x, c);
                             fn(x, c);
                         }
                     }
                 };
-                auto largest = [&](const uint32_t (&x)[32], bool magnitude) {
+                auto largest = [&](const uint32_t (&x)[32]) {
                     float y[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float x0 = __uint_as_float(x[e]), x1 = __uint_as_float(x[e + 1]);
-                        y[(e >> 1) & 1] = max3f(y[(e >> 1) & 1], magnitude ? fabsf(x0) : x0, magnitude ? fabsf(x1) : x1);
-                    }
+                    for (int e = 0; e < 32; e += 2) y[(e >> 1) & 1] = max3f(y[(e >> 1) & 1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                    return fmaxf(y[0], y[1]);
+                };
+                auto largest_abs = [&](const uint32_t (&x)[32]) {
+                    float y[2] = {0.f, 0.f};
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2)
+                        y[(e >> 1) & 1] = max3f(y[(e >> 1) & 1], fabsf(__uint_as_float(x[e])), fabsf(__uint_as_float(x[e + 1])));
                     return fmaxf(y[0], y[1]);
                 };
                 bool o_stands = NT == 2;  // the product of the tile before is complete
@@ -1101,7 +1100,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
 #pragma unroll
                         for (int d = 0; d < kAt; ++d) {
                             tmem_pin(x[d]);
-                            if constexpr (!kWhole) prepare(x[d], c + d, true);
+                            if constexpr (!kWhole) prepare(x[d], c + d);
                             f[d][0] = (kWhole ? page_unit(c + d, 0) : 1.f) * sl2;
                             f[d][1] = (kWhole ? page_unit(c + d, 1) : 1.f) * sl2;
                             float y[2] = {-INFINITY, -INFINITY};
@@ -1178,30 +1177,18 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                     add_up();
                 };
                 auto two_passes = [&]() {
-                    // the form of the softcap: by exp where a raw score of the warp lies outside the fit's range
-                    bool accurate = false, shorter = false;
-                    if constexpr (CAP) {
-                        float amax = 0.f;
-                        chunks(false, [&](uint32_t (&x)[32], int) { amax = fmaxf(amax, largest(x, true)); });
-                        const CapPoly cp = cap_poly(P.scale, P.softcap);
-                        accurate = __any_sync(0xffffffffu, !(amax <= cp.r_max)) || (!full && !cp.inf_ok);
-                        const CapShort cs = cap_short(P.scale, P.softcap);
-                        shorter = !accurate && __all_sync(0xffffffffu, amax <= cs.r_max) && (full || cs.inf_ok);
-                    }
                     if (kHold && !full) {
 #pragma unroll
-                        for (int c = 0; c < (kHold ? NC : 0); ++c) prepare(sv[c], c, true);
+                        for (int c = 0; c < (kHold ? NC : 0); ++c) prepare(sv[c], c);
                     }
                     // ---- the row's largest score, as x against its reference
                     float rmax = -INFINITY;
-                    chunks(true, [&](uint32_t (&x)[32], int) { rmax = fmaxf(rmax, largest(x, false)); });
+                    chunks([&](uint32_t (&x)[32], int) { rmax = fmaxf(rmax, largest(x)); });
                     float xm, xm_;
                     {
                         const uint64_t r2 = f2_make(rmax, rmax), n2 = f2_make(-m, -m);
                         uint64_t x2;
                         if (!CAP) x2 = to_x(M0(), r2, n2);
-                        else if (shorter) x2 = to_x(M3(), r2, n2);
-                        else if (!accurate) x2 = to_x(M1(), r2, n2);
                         else x2 = to_x(M2(), r2, n2);
                         f2_split(x2, xm, xm_);
                     }
@@ -1232,33 +1219,43 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                             }
                         }
                     }
-                    // ---- p over S, behind the scores that have been loaded: rounded to the products' type, summed in fp32 before
-                    auto p_pass = [&](auto modec) {
-                        const uint64_t nm = f2_make(-m, -m);
-                        uint64_t rs0 = f2_make(0.f, 0.f), rs1 = f2_make(0.f, 0.f);
-                        chunks(true, [&](uint32_t (&x)[32], int c) {
+                    // ---- p over S, behind the scores that have been loaded: rounded to the products' type, summed in fp32 before.
+                    // With a softcap, 32 keys at a time that the warp's rows see within the fit's range take the fit alone (2048 tokens
+                    // over 8192 of bf16, softcap 50: 387 us; of 8, which a score in 16 000 passes by half: 616, 2: 1302).
+                    const uint64_t nm = f2_make(-m, -m);
+                    uint64_t rs0 = f2_make(0.f, 0.f), rs1 = f2_make(0.f, 0.f);
+                    chunks([&](uint32_t (&x)[32], int c) {
+                        auto put = [&](auto modec) {
                             uint32_t pk[16];
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
                                 float x0, x1;
-                                const uint64_t rr = f2_make(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
-                                f2_split(to_x(modec, rr, nm), x0, x1);
+                                f2_split(to_x(modec, f2_make(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), nm), x0, x1);
                                 const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);  // 2^-inf = 0
                                 if (e & 1) rs1 = f2_add(rs1, f2_make(p0, p1));
                                 else rs0 = f2_add(rs0, f2_make(p0, p1));
                                 pk[e] = pack2<MB>(p0, p1);
                             }
                             tmem_st16(tS + c * 16, pk);
-                        });
-                        float a0, a1, b0, b1;
-                        f2_split(rs0, a0, a1);
-                        f2_split(rs1, b0, b1);
-                        l += (a0 + b0) + (a1 + b1);
-                    };
-                    if (!CAP) p_pass(M0());
-                    else if (shorter) p_pass(M3());
-                    else if (!accurate) p_pass(M1());
-                    else p_pass(M2());
+                        };
+                        if constexpr (!CAP) {
+                            put(M0());
+                        } else {
+                            float amax = 0.f;
+                            if (full) {
+                                amax = largest_abs(x);
+                            } else {  // (-inf: not seen)
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) amax = fmaxf(amax, x[e] == 0xff800000u ? 0.f : fabsf(__uint_as_float(x[e])));
+                            }
+                            if (__all_sync(0xffffffffu, amax <= cp.r_max || !row_live) && (full || cp.inf_ok)) put(M1());
+                            else put(M2());
+                        }
+                    });
+                    float a0, a1, b0, b1;
+                    f2_split(rs0, a0, a1);
+                    f2_split(rs1, b0, b1);
+                    l += (a0 + b0) + (a1 + b1);
                 };
                 if constexpr (F8 && !CAP) {
                     if (full) one_pass(std::true_type());

@@ -540,7 +540,9 @@ ATTN_API attn_status attn_paged_decode(attn_dtype dt, attn_dtype cache_dt, const
  *   workspace : at least attn_paged_prefill_workspace_size() bytes of device scratch, 16-byte
  *               aligned (the size has room to begin on a multiple of 256 inside it); contents on entry are
  *               ignored.  Calls that may run at the same time need one each.
- * What a row does not see has no effect on it, whatever bytes it holds.  Table entries of which no row
+ * What a row does not see has no effect on it, whatever bytes it holds, but for one in the roundings: where values that
+ * are not finite, or (8-bit pages) scales too far apart, make a tile's product be formed in fp32, that is so for all of
+ * the tile's rows.  Table entries of which no row
  * sees a token (behind a sequence, before every row's window) are not read.  Sums are fp32, over weights
  * rounded to the products' type: bf16 ones of at most 1, or fp16 ones of at most 2^8.
  *   Over 16-bit pages the products are in dt.  Over 8-bit pages they are in fp16, which holds every

@@ -634,3 +634,91 @@ def test_many_short_parts_behind_values_that_are_looked_over(kind, hd):
     rows[(cu[1:] - 1).cpu().long()] = False
     assert torch.isfinite(first[0][rows.cuda()].float()).all() and torch.isnan(first[0][~rows.cuda()].float()).all()
     assert torch.equal(first[0].view(torch.int16), again[0].view(torch.int16)) and torch.equal(first[1], again[1])
+
+
+SOFT = [("bf16", "bf16", 128), ("f16", "f16", 64), ("bf16", "bf16", 256), ("bf16", "e4m3", 128), ("f16", "e5m2", 256)]
+
+
+def same_rows(got, ref, rows):
+    return torch.equal(got[0][rows], ref[0][rows]) and torch.equal(got[1][:, rows], ref[1][:, rows])
+
+
+@pytest.mark.parametrize("dt,kind,hd", SOFT)
+@pytest.mark.parametrize("window", [0, 90])
+def test_softcapped_rows_take_nothing_from_what_they_do_not_see(dt, kind, hd, window):
+    """The same bits whatever finite keys and values lie behind the sequences, whatever keys lie ahead of a row or before
+    its window, and whatever the query rows beside it hold; and rows of scores unlike each other side by side."""
+    lengths, new, H = [330, 70, 500], [80, 70, 33], 7
+    c = Cache(dt, kind, lengths, 1, hd, 16, seed=71)
+    c.fill(lengths, 71)
+    # every byte 0x7b: 6.1e4, 1.3e36, 352 or 5.7e4
+    unused = torch.ones(c.k.shape[0], 16, dtype=torch.bool, device=DEV)
+    for b, n in enumerate(lengths):
+        for j in range((n + 15) // 16):
+            unused[int(c.table[b, j]), :min(16, n - 16 * j)] = False
+
+    def put(pool, where, byte):
+        raw = pool.view(torch.uint8) if is8(kind) else pool.view(torch.int16)
+        raw.masked_fill_(where[:, None, :, None], byte if is8(kind) else byte * 257)
+
+    put(c.k, unused, 0), put(c.v, unused, 0)
+    cu = np.cumsum([0] + new)
+    q = queries(int(cu[-1]) + 9, H * hd, dt, 72)
+    flags = dict(softcap=50.0, window=window)
+
+    def call(q=q, k=c.k, v=c.v):
+        out = A.attn_paged_prefill(q, k, v, c.table_d, i32(lengths), i32(cu), H=H, **c.kw(), **flags)
+        status_ok()
+        return out
+
+    ref, every = call(), np.arange(cu[-1])
+    check(c, q, lengths, cu, *ref, **flags)
+    k, v = c.k.clone(), c.v.clone()
+    put(k, unused, 0x7b), put(v, unused, 0x7b)
+    assert same_rows(call(k=k, v=v), ref, every)
+    # rows behind the sequences, a whole sequence's, and a few amid one's
+    loud = q.clone()
+    other = np.concatenate([np.arange(cu[1], cu[2]), [5, 17, 18, 40, 64], np.arange(cu[3], len(q))])
+    loud[other] *= 64
+    got = call(q=loud)
+    assert same_rows(got, ref, np.setdiff1d(every, other))
+    check(c, loud, lengths, cu, *got, **flags)
+    # keys that the rows behind the first 33 alone see, or (in a window) those before them alone
+    for b in (0, 2):
+        at = lengths[b] - new[b] + 33 - (2 if b else 0)
+        for before in (False, True):
+            if before and not window:
+                continue
+            t = np.arange(0, at - window + 1) if before else np.arange(at, lengths[b])
+            where = torch.zeros_like(unused)
+            where[c.table[b, t // 16], t % 16] = True
+            k = c.k.clone()
+            put(k, where, 0x57)  # 117, 2.4e14, 120 or 120
+            i = at - (lengths[b] - new[b])
+            rows = np.arange(cu[b] + i, cu[b + 1]) if before else np.arange(cu[b], cu[b] + i)
+            assert len(rows) and same_rows(call(k=k), ref, rows)
+
+
+def test_softcapped_calls_repeat_their_bits_after_others():
+    """Groups of 7 heads leave rows of the tensor cores' tile unused: what other calls left in their place changes nothing."""
+    lengths, new = [700, 129], [150, 129]
+    cu = np.cumsum([0] + new)
+    calls = []
+    for dt, kind, hd in SOFT:
+        c = Cache(dt, kind, lengths, 1, hd, 16, seed=73)
+        c.fill(lengths, 73)
+        for H, factor in ((7, 1.0), (8, 100.0)):
+            calls.append((c, queries(int(cu[-1]), H * hd, dt, 74) * factor, H))
+
+    def call(c, q, H):
+        out = A.attn_paged_prefill(q, c.k, c.v, c.table_d, i32(lengths), i32(cu), H=H, softcap=50.0, **c.kw())
+        status_ok()
+        return out
+
+    quiet, loud = calls[0::2], calls[1::2]
+    ref = [call(*x) for x in quiet]
+    for x in loud:
+        call(*x)
+        for y, r in zip(quiet, ref):
+            assert same_rows(call(*y), r, np.arange(cu[-1]))
+            call(*x)
