@@ -1,7 +1,8 @@
 // turns.cuh -- angles of rotary positions as fractions of a turn in 64-bit fixed point: the
 // frequency of a pair is held as the fraction of a turn that it adds from one position to the
 // next, in units of 2^-64 turns, and its product with the position modulo 2^64 is the angle's
-// fraction of a turn, right to p * 2^-65 at position p.
+// fraction of a turn, right to p * 2^-64 at position p (a rounding to half a unit, and less than another
+// quarter from the arithmetic before it).
 #pragma once
 
 #include <math.h>
@@ -35,9 +36,11 @@ inline Two two_sqrt(Two a) {  // a Newton step from the double's root
 }
 
 constexpr Two kTurnsPerRadian = {0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};  // 1 / (2 pi)
-// the fraction of a turn (at least 0) of `turns` >= 0, below 2^53
+// the fraction of a turn (at least 0) of `turns` >= 0, below 2^53: rounded once, what the upper part holds
+// below 2^-64 together with the lower one
 inline unsigned long long turn_fraction(Two turns) {
-    return (unsigned long long)ldexp(turns.hi - floor(turns.hi), 64) + (unsigned long long)(long long)rint(ldexp(turns.lo, 64));
+    const double upper = ldexp(turns.hi - floor(turns.hi), 64), whole = floor(upper);
+    return (unsigned long long)whole + (unsigned long long)(long long)rint((upper - whole) + ldexp(turns.lo, 64));
 }
 
 // Sine and cosine of p turns of f: the upper 32 bits of the product become an angle in
