@@ -662,7 +662,8 @@ def attn_rope_freqs(rotary_dim, theta=10000.0, *, scaling=None, factor=1.0, orig
       "base"    theta grown to theta * factor^(rotary_dim/(rotary_dim - 2)): the first pair stays, the last
                 is divided by factor
       "ramp"    f_i (1 - r_i) + f_i / factor * r_i, r_i rising from 0 to 1 along i between the pairs that make
-                `fast` (32) and `slow` (1) turns in original_length (rounded outwards to whole i);
+                `fast` (32) and `slow` (1) turns in original_length (rounded outwards to whole i, and kept
+                from 0 to rotary_dim - 1);
                 amplitude 0.1 ln(factor) + 1 unless given
       "bands"   f_i where it makes at least `fast` (4) turns in original_length, f_i / factor where it makes at
                 most `slow` (1), between them (1 - s) f_i / factor + s f_i with s linear in the turns
@@ -695,7 +696,8 @@ def attn_rope_freqs(rotary_dim, theta=10000.0, *, scaling=None, factor=1.0, orig
             pair = lambda t: d * math.log(original_length / (2 * math.pi * t)) / (2 * math.log(theta))
             lo, hi = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), d - 1)
             for i in range(d // 2):
-                r = min(max((i - lo) / max(hi - lo, 0.001), 0.0), 1.0)
+                # (no room between the borders: all pairs lie behind the slow one, or all before the fast one)
+                r = min(max((i - lo) / (hi - lo), 0.0), 1.0) if hi > lo else float(hi <= 0)
                 f[i] = f[i] * (1 - r) + f[i] / factor * r
             amplitude = 0.1 * math.log(factor) + 1 if amplitude is None and factor > 1 else amplitude
         else:

@@ -116,6 +116,22 @@ def test_frequencies_ramp():
     assert A.attn_rope_freqs(d, scaling="ramp", factor=s, original_length=L, amplitude=1.0).amplitude == 1.0
 
 
+@pytest.mark.parametrize("L,slow,fast", [(4, 1.0, 32.0), (6.28, 1.0, 32.0), (100, 32.0, 64.0), (2, 0.1, 0.2), (10, 1.0, 32.0)])
+def test_frequencies_ramp_where_pairs_turn_slowly(L, slow, fast):
+    """Pairs that make at most `slow` turns are scaled whole, also where no pair makes more."""
+    f = 10000.0 ** (-np.arange(32) / 32)
+    got = np.array(A.attn_rope_freqs(64, scaling="ramp", factor=8.0, original_length=L, slow=slow, fast=fast).inv_freq)
+    turns = L * f / (2 * math.pi)
+    behind = np.flatnonzero(turns <= slow)
+    behind = behind if turns[0] <= slow else behind[1:]  # (the border is rounded outwards to a whole pair)
+    assert len(behind) and near(got[behind], f[behind] / 8)
+
+
+def test_frequencies_ramp_where_all_turn_fast():
+    f = 10000.0 ** (-np.arange(32) / 32)
+    assert near(A.attn_rope_freqs(64, scaling="ramp", factor=8.0, original_length=10 ** 12).inv_freq, f)
+
+
 def test_frequencies_bands():
     d, theta, L, s = 128, 500000.0, 8192, 8.0
     f = theta ** (-2.0 * np.arange(d // 2) / d)
