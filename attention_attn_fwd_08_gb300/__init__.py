@@ -681,7 +681,12 @@ def attn_rope_freqs(rotary_dim, theta=10000.0, *, scaling=None, factor=1.0, orig
     if scaling == "base":
         if d == 2:
             raise ValueError("'base' needs two pairs at least")
-        theta *= factor ** (d / (d - 2))
+        try:
+            theta *= factor ** (d / (d - 2))
+        except OverflowError:
+            theta = math.inf
+        if not (theta > 0 and math.isfinite(theta)):
+            raise ValueError("no double holds the base that a factor of %g gives" % factor)
     f = [theta ** (-2.0 * i / d) for i in range(d // 2)]
     if scaling == "linear":
         f = [x / factor for x in f]
@@ -692,6 +697,8 @@ def attn_rope_freqs(rotary_dim, theta=10000.0, *, scaling=None, factor=1.0, orig
         if scaling == "ramp":
             if not theta > 1:
                 raise ValueError("'ramp' needs theta > 1")
+            if not original_length < math.inf or not fast < math.inf:
+                raise ValueError("'ramp' needs a finite original_length and a finite fast")
             # the (fractional) pair that makes t turns in original_length
             pair = lambda t: d * math.log(original_length / (2 * math.pi * t)) / (2 * math.log(theta))
             lo, hi = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), d - 1)

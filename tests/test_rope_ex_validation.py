@@ -80,6 +80,14 @@ def test_frequencies_refuse(kw):
         A.attn_rope_freqs(**dict(dict(rotary_dim=64), **kw))
 
 
+@pytest.mark.parametrize("kw", [
+    dict(scaling="ramp", original_length=float("inf")), dict(scaling="ramp", original_length=100, fast=float("inf")),
+    dict(scaling="base", rotary_dim=4, factor=1e300), dict(scaling="base", rotary_dim=4, factor=1e-300)])
+def test_frequencies_refuse_what_is_not_finite(kw):
+    with pytest.raises(ValueError, match="finite|no double"):
+        A.attn_rope_freqs(**dict(dict(rotary_dim=64, factor=2.0), **kw))
+
+
 def test_raw_frequencies():
     f = A.RopeFreqs([1.0, -0.25], 2.0)
     assert f.rotary_dim == 4 and f.inv_freq == (1.0, -0.25) and f.amplitude == 2.0
