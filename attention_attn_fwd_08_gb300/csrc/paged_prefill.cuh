@@ -904,6 +904,8 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
         // x = score * log2(e) - m of a pair of raw scores; mode 0: plain; with a softcap 1: the fitted polynomial, for
         // scores in its range; 2: by exp outside it.  A score's form is its own, so that no other's bytes change its bits.
         const CapPoly cp = cap_poly(P.scale, P.softcap);
+        // (the fit's highest coefficient is an eighth power of scale / softcap: where fp32 might not hold it, nothing fits, not even 0)
+        const float fit_max = P.scale <= 1e4f * P.softcap ? cp.r_max : -1.f;
         auto to_x = [&](auto modec, uint64_t rr, uint64_t nm) -> uint64_t {
             constexpr int kMode = decltype(modec)::value;
             if constexpr (kMode == 0) return f2_fma(rr, sl2_2, nm);
@@ -920,7 +922,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
             // a masked score is -inf, and softcap * tanh(-inf) would be finite
             const float y0 = r0 == -INFINITY ? -INFINITY : fmaf(cap_out, tanh_accurate(r0 * cap_in), m0);
             const float y1 = r1 == -INFINITY ? -INFINITY : fmaf(cap_out, tanh_accurate(r1 * cap_in), m1);
-            return f2_make(fabsf(r0) <= cp.r_max ? x0 : y0, fabsf(r1) <= cp.r_max ? x1 : y1);
+            return f2_make(fabsf(r0) <= fit_max ? x0 : y0, fabsf(r1) <= fit_max ? x1 : y1);
         };
         using M0 = std::integral_constant<int, 0>;
         using M1 = std::integral_constant<int, 1>;
@@ -1248,7 +1250,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
 #pragma unroll
                                 for (int e = 0; e < 32; ++e) amax = fmaxf(amax, x[e] == 0xff800000u ? 0.f : fabsf(__uint_as_float(x[e])));
                             }
-                            if (__all_sync(0xffffffffu, amax <= cp.r_max || !row_live) && (full || cp.inf_ok)) put(M1());
+                            if (__all_sync(0xffffffffu, amax <= fit_max || !row_live) && (full || cp.inf_ok)) put(M1());
                             else put(M2());
                         }
                     });

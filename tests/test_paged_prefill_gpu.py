@@ -722,3 +722,23 @@ def test_softcapped_calls_repeat_their_bits_after_others():
         for y, r in zip(quiet, ref):
             assert same_rows(call(*y), r, np.arange(cu[-1]))
             call(*x)
+
+
+@pytest.mark.parametrize("dt,kind,hd", SOFT)
+@pytest.mark.parametrize("softcap", [1e-7, 1e-3])
+def test_scores_of_zero_under_a_small_softcap(dt, kind, hd, softcap):
+    """Keys of zeros, some and a sequence's all, and a query row of zeros, under a softcap so small that the scores' ratio to it has
+    an eighth power which fp32 does not hold."""
+    lengths, new, H = [330, 70], [80, 70], 4
+    c = Cache(dt, kind, lengths, 2, hd, 16, seed=75)
+    c.fill(lengths, 75)
+    raw = c.k.view(torch.uint8) if is8(kind) else c.k
+    for b, ts in ((0, range(20, 290, 3)), (1, range(70))):
+        for t in ts:
+            raw[int(c.table[b, t // 16]), :, t % 16] = 0
+    cu = np.cumsum([0] + new)
+    q = queries(int(cu[-1]), H * hd, dt, 76)
+    q[11] = 0
+    o, lse = A.attn_paged_prefill(q, c.k, c.v, c.table_d, i32(lengths), i32(cu), H=H, softcap=softcap, **c.kw())
+    status_ok()
+    check(c, q, lengths, cu, o, lse, softcap=softcap)
