@@ -740,7 +740,7 @@ def attn_rope_ex(x, freqs, *, H, positions=None, pos=0, layout="half", rotary_st
     not given; out=x turns in place."""
     torch = _torch()
     dev, dtype, shape = x.device, x.dtype, x.shape
-    if len(shape) not in (2, 3) or shape[-1] % H or not shape[-1]:
+    if len(shape) not in (2, 3) or H < 1 or shape[-1] % H or not shape[-1]:
         raise ValueError("x must be [rows, H*hd] or [B, T, H*hd] with H = %d (got %s)" % (H, tuple(shape)))
     if layout not in ("half", "interleaved"):
         raise ValueError("layout must be 'half' or 'interleaved' (got %r)" % (layout,))

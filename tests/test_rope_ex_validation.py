@@ -69,6 +69,12 @@ def test_binding_refuses():
         A.attn_rope_ex(x.long(), f, H=4)
 
 
+@pytest.mark.parametrize("H", [0, -4])
+def test_binding_refuses_no_heads(H):
+    with pytest.raises(ValueError, match="H = "):
+        A.attn_rope_ex(torch.zeros(6, 512, dtype=torch.bfloat16), A.attn_rope_freqs(64), H=H)
+
+
 @pytest.mark.parametrize("kw", [
     dict(rotary_dim=0), dict(rotary_dim=3), dict(rotary_dim=258), dict(theta=0.0), dict(theta=float("inf")), dict(factor=2.0),
     dict(scaling="wide", factor=2.0), dict(scaling="linear", factor=0.0), dict(scaling="base", rotary_dim=2, factor=2.0),
