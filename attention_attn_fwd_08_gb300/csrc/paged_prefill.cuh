@@ -16,13 +16,14 @@
 //   partial (m, l, O) rows in the workspace.
 //   paged_prefill_merge_kernel joins those in a fixed order.
 //
-// What bounds it: with many rows the chain S, softmax, P V of two tiles that share an SM (the scores' tensor work
-// is 561 us of the 821 that 2048 tokens over 32768 take, 32 heads of 128 on 8 in bf16: 1.32 PFLOP/s; with nearly all of the
+// What bounds it: with many rows the chain S, softmax, P V of two tiles that share an SM (the tensor work of both products
+// is 561 us of the 816 that 2048 tokens over 32768 take, 32 heads of 128 on 8 in bf16: 1.32 PFLOP/s; with nearly all of the
 // softmax left out 640 remain).  Beside that the instructions themselves: all roles together fit the
 // instruction cache only where their loops are rolled up, and over 8-bit pages, whose widening warps
 // issue beside the softmax, that was worth more than anything else (the same chunk over e4m3 pages: 2537 us with the
-// softmax and the issue unrolled, 1472 rolled, 1302 now; with a quarter of the widening it would be 5 % less, with a quarter of
-// the softmax 970).  With few rows the launches: of the 24.5 us that 64 tokens
+// softmax and the issue unrolled, 1472 rolled, 1299 now; with a quarter of the widening it would be 5 % less, with a quarter of
+// the softmax 970).  The widening keeps up: of 4460 cycles that a K and a V tile take it, 1730 are waits for a free
+// stage, while a softmax works 3000 of a tile's 4600.  With few rows the launches: of the 24.6 us that 64 tokens
 // over 777 take, the plan is 4.5, the merge 6.6, and a CTA's first fetch of each path some of the rest.
 #pragma once
 
@@ -360,7 +361,8 @@ __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, ui
 // beside the part's first usable scale, and O is multiplied by vref at the end: exact where the scale is a power
 // of two, else off by half a step of fp16 for the ratio and for the product.  A tile with a ratio outside
 // [2^-14, 2^7] (e5m2, whose codes reach fp16's end: [2^-14, 1]), zero but for, keeps its bare codes, and the softmax
-// warps make its product in fp32, as that of a tile with values that are not finite.
+// warps make its product in fp32, as that of a tile with values that are not finite.  (A load of P and its wait for each
+// key and 32 columns: 2048 tokens over 8192 take 335 us, with a tile in four like that 2880, with all 10200.)
 struct VRef {
     float ref, inv, most;  // vref, its inverse, and the largest ratio
 };

@@ -540,18 +540,18 @@ ATTN_API attn_status attn_paged_decode(attn_dtype dt, attn_dtype cache_dt, const
  *   workspace : at least attn_paged_prefill_workspace_size() bytes of device scratch, 16-byte
  *               aligned (the size has room to begin on a multiple of 256 inside it); contents on entry are
  *               ignored.  Calls that may run at the same time need one each.
- * What a row does not see has no effect on it, whatever bytes it holds, but for one in the roundings: where values that
- * are not finite, or (8-bit pages) scales too far apart, make a tile's product be formed in fp32, that is so for all of
- * the tile's rows.  Table entries of which no row
- * sees a token (behind a sequence, before every row's window) are not read.  Sums are fp32, over weights
- * rounded to the products' type: bf16 ones of at most 1, or fp16 ones of at most 2^8.
+ * What a row does not see has no effect on it, whatever bytes it holds, but for two in the roundings, which are
+ * chosen for a tile of rows and keys together: where values are not finite, or scales of 8-bit pages lie too far
+ * apart, its product is formed in fp32; and 8-bit values enter relative to one power of two.  Table entries of
+ * which no row sees a token (behind a sequence, before every row's window) are not read.  Sums are fp32, over
+ * weights rounded to the products' type: bf16 ones of at most 1, or fp16 ones of at most 2^8.
  *   Over 16-bit pages the products are in dt.  Over 8-bit pages they are in fp16, which holds every
  * code exactly, for either dt: a bf16 query row enters by a power of two, so that 2^-38 of its
  * largest element is kept; a page's scale multiplies its keys' scores in fp32; its values enter
  * as code times the ratio of its scale to a power of two near the scales of the rows' other pages, which is
  * exact for scales that are powers of two and otherwise off by half a step of fp16 for the ratio
- * and for the product.  Pages whose ratio fp16 does not hold (scales some 2^10 apart within a
- * sequence) are multiplied in fp32, right and several times as slow.
+ * and for the product.  Tiles of keys with a page whose ratio fp16 does not hold (scales that lie 2^10 apart within a
+ * sequence, 2^6 over e5m2 pages) are multiplied in fp32, right and some 30 times as slow.
  *   The order of the sums depends on the device arrays (lengths and prefix sums), not on the time at which
  * CTAs run: the same call gives the same bits.
  */
