@@ -908,6 +908,9 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
         const CapPoly cp = cap_poly(P.scale, P.softcap);
         // (the fit's highest coefficient is an eighth power of scale / softcap: where fp32 might not hold it, nothing fits, not even 0)
         const float fit_max = P.scale <= 1e4f * P.softcap ? cp.r_max : -1.f;
+        float lead, lead_;  // the coefficient as it enters: where it is 0, a masked -inf would become NaN
+        f2_split(f2_mul(cp.s3, sl2_2), lead, lead_);
+        const bool inf_fits = lead > 0.f;
         auto to_x = [&](auto modec, uint64_t rr, uint64_t nm) -> uint64_t {
             constexpr int kMode = decltype(modec)::value;
             if constexpr (kMode == 0) return f2_fma(rr, sl2_2, nm);
@@ -1225,7 +1228,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
                     }
                     // ---- p over S, behind the scores that have been loaded: rounded to the products' type, summed in fp32 before.
                     // With a softcap, 32 keys at a time that the warp's rows see within the fit's range take the fit alone (2048 tokens
-                    // over 8192 of bf16, softcap 50: 387 us; of 8, which a score in 16 000 passes by half: 616, 2: 1302).
+                    // over 8192 of bf16, softcap 50: 382 us; of 8, half of which a score in 16 000 passes: 612, 2: 1300).
                     const uint64_t nm = f2_make(-m, -m);
                     uint64_t rs0 = f2_make(0.f, 0.f), rs1 = f2_make(0.f, 0.f);
                     chunks([&](uint32_t (&x)[32], int c) {
@@ -1252,7 +1255,7 @@ __global__ void __launch_bounds__(Cfg<HD, F8>::kThreads, 1)
 #pragma unroll
                                 for (int e = 0; e < 32; ++e) amax = fmaxf(amax, x[e] == 0xff800000u ? 0.f : fabsf(__uint_as_float(x[e])));
                             }
-                            if (__all_sync(0xffffffffu, amax <= fit_max || !row_live) && (full || cp.inf_ok)) put(M1());
+                            if (__all_sync(0xffffffffu, amax <= fit_max || !row_live) && (full || inf_fits)) put(M1());
                             else put(M2());
                         }
                     });

@@ -742,3 +742,12 @@ def test_scores_of_zero_under_a_small_softcap(dt, kind, hd, softcap):
     o, lse = A.attn_paged_prefill(q, c.k, c.v, c.table_d, i32(lengths), i32(cu), H=H, softcap=softcap, **c.kw())
     status_ok()
     check(c, q, lengths, cu, o, lse, softcap=softcap)
+
+
+@pytest.mark.parametrize("dt,kind,hd", SOFT)
+@pytest.mark.parametrize("scale,softcap", [(1e-6, 0.1), (1e-4, 30.0), (1e-9, 1e-3)])
+def test_small_scales_under_a_softcap(dt, kind, hd, scale, softcap):
+    """The fit's highest coefficient is near or below fp32's smallest number: keys that are not seen stay unseen."""
+    lengths, new = [330, 70], [80, 70]
+    run(dt, kind, lengths, new, 4, 2, hd, 16, seed=78, scale=scale, softcap=softcap)
+    run(dt, kind, lengths, new, 4, 2, hd, 16, seed=79, scale=scale, softcap=softcap, window=40)
